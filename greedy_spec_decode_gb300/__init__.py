@@ -27,6 +27,7 @@ LIB_PATH = os.path.join(_PKG, "_build", "libsga.so")
 SGA_F32, SGA_BF16 = 0, 1
 SGA_MAX_K = 15
 SGA_MAX_VOCAB = 1 << 24
+SGA_MAX_TOP = 32
 SGA_DEVERR_K_RANGE, SGA_DEVERR_D2T_RANGE, SGA_DEVERR_TIMEOUT, SGA_DEVERR_LAYOUT = 1, 2, 4, 8
 
 _lib = None
@@ -70,6 +71,12 @@ def lib():
             "sga_lmhead_argmax": ([vp, i64, i64, vp, i64, i64, i64, vp, vp, sz, vp], i32),
             "sga_lmhead_argmax_fp8": ([vp, vp, i64, i64, vp, ctypes.c_float, i64, i64, i64, vp,
                                        vp, sz, vp], i32),
+            "sga_token_logprobs": ([vp, i32, i64, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp,
+                                    vp], i32),
+            "sga_local_logprobs": ([vp, i32, i64, i64, i64, i64, i64, vp, i32, vp, vp, vp], i32),
+            "sga_logprob_reduce": ([vp, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp], i32),
+            "sga_token_logprobs_grad": ([vp, i32, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp,
+                                         i32, vp, vp, vp, i64, vp], i32),
             "sga_device_error": ([ctypes.POINTER(ctypes.c_uint32)], i32),
             "sga_clear_device_error": ([], i32),
             "sga_selftest_wait_timeout": ([ctypes.c_uint64, vp, vp], i32),
@@ -341,6 +348,112 @@ def sga_lmhead_argmax_shards_fp8(hidden_q, hidden_scale, weight_q, weight_scale,
         starts, widths, int(org_vocab), _ptr(out_stats), _ptr(workspace), nbytes,
         _stream(stream)))
     return out_stats
+
+
+def _check_out(t, dtype, numel, name):
+    """A contiguous CUDA tensor of `dtype` with `numel` elements, or None."""
+    if t is not None and not (t.dtype == dtype and t.numel() == numel and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements")
+
+
+def _logits_2d(logits):
+    if logits.dim() != 2 or (logits.size(1) > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be 2-D with unit stride along the vocab")
+    rows, width = logits.shape
+    return rows, width, logits.stride(0) if rows > 1 else max(logits.stride(0), width)
+
+
+def _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids, out_top_logprobs):
+    """Checks the per-row tensors of the log-probability calls; returns top_k."""
+    _check_out(tokens, torch.int32, rows, "tokens")
+    _check_out(out_logprob, torch.float32, rows, "out_logprob")
+    _check_out(out_entropy, torch.float32, rows, "out_entropy")
+    _check_out(out_lse, torch.float32, rows, "out_lse")
+    top = out_top_ids if out_top_ids is not None else out_top_logprobs
+    k = 0 if top is None else top.size(-1)
+    _check_out(out_top_ids, torch.int32, rows * k, "out_top_ids")
+    _check_out(out_top_logprobs, torch.float32, rows * k, "out_top_logprobs")
+    return k
+
+
+def sga_token_logprobs(logits, org_vocab, tokens=None, out_logprob=None, out_entropy=None,
+                       out_lse=None, out_top_ids=None, out_top_logprobs=None, stream=None):
+    """Log probability of each row's token (int32 [rows]) over a whole
+    vocabulary, with the row's entropy, log-sum-exp and the top_k best ids with
+    their log probabilities.  logits: 2-D, unit stride along the vocab; outputs
+    are contiguous CUDA tensors or None: float32 [rows], and int32 / float32
+    [rows, top_k], whose last size is top_k (see include/sga.h)."""
+    rows, width, ld = _logits_2d(logits)
+    k = _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
+                     out_top_logprobs)
+    _check("sga_token_logprobs", lib().sga_token_logprobs(
+        _ptr(logits), _dtype_code(logits), rows, ld, width, int(org_vocab), _ptr(tokens), k,
+        _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse), _ptr(out_top_ids),
+        _ptr(out_top_logprobs), _stream(stream)))
+
+
+def sga_local_logprobs(logits, shard_start, shard_width, org_vocab, tokens, out_parts,
+                       out_top=None, stream=None):
+    """One vocab shard's part of sga_token_logprobs.  logits: 2-D, column 0 =
+    global id shard_start; out_parts: float32 [rows, 4]; out_top: int32 [rows,
+    top_k, 2] stats, or None (pass slices of the gathered buffers to emulate
+    all_gather on dim 0)."""
+    rows, width, ld = _logits_2d(logits)
+    if width < shard_width:
+        raise ValueError("logits has fewer columns than the shard")
+    k = 0 if out_top is None else out_top.size(-2)
+    _check_out(tokens, torch.int32, rows, "tokens")
+    _check_out(out_parts, torch.float32, 4 * rows, "out_parts")
+    _check_out(out_top, torch.int32, 2 * k * rows, "out_top")
+    _check("sga_local_logprobs", lib().sga_local_logprobs(
+        _ptr(logits), _dtype_code(logits), rows, ld, int(shard_start), int(shard_width),
+        int(org_vocab), _ptr(tokens), k, _ptr(out_parts), _ptr(out_top), _stream(stream)))
+    return out_parts
+
+
+def sga_logprob_reduce(parts, tops, num_shards, tokens=None, out_logprob=None, out_entropy=None,
+                       out_lse=None, out_top_ids=None, out_top_logprobs=None, stream=None):
+    """Results of sga_token_logprobs from the gathered parts (float32
+    [num_shards, rows, 4]) and lists (int32 [num_shards, rows, top_k, 2] or
+    None)."""
+    rows = parts.numel() // (4 * int(num_shards))
+    k = _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
+                     out_top_logprobs)
+    _check_out(parts, torch.float32, 4 * rows * num_shards, "parts")
+    if k and tops is None:
+        raise ValueError("alternatives are asked for without tops")
+    if k:
+        _check_out(tops, torch.int32, 2 * k * rows * num_shards, "tops")
+    _check("sga_logprob_reduce", lib().sga_logprob_reduce(
+        _ptr(parts), _ptr(tops) if k else None, int(num_shards), rows, k, _ptr(tokens),
+        _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse), _ptr(out_top_ids),
+        _ptr(out_top_logprobs), _stream(stream)))
+
+
+def sga_token_logprobs_grad(logits, shard_start, org_vocab, tokens, lse, entropy, grad_logprob,
+                            out_grad, grad_entropy=None, top_ids=None, grad_top=None,
+                            stream=None):
+    """Gradient of sga_token_logprobs' log probabilities, entropy and
+    alternatives with respect to the logits (a whole vocabulary, shard_start 0,
+    or one shard).  lse, entropy: the forward results; the upstream gradients
+    are float32 or None; out_grad: like logits, or logits itself."""
+    rows, width, ld = _logits_2d(logits)
+    if out_grad.dtype != logits.dtype or out_grad.shape != logits.shape or (
+            width > 1 and out_grad.stride(1) != 1):
+        raise ValueError("out_grad must match logits, unit stride along the vocab")
+    ldg = out_grad.stride(0) if rows > 1 else max(out_grad.stride(0), width)
+    k = 0 if top_ids is None else top_ids.size(-1)
+    _check_out(tokens, torch.int32, rows, "tokens")
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob"),
+                    (grad_entropy, "grad_entropy")):
+        _check_out(t, torch.float32, rows, name)
+    _check_out(top_ids, torch.int32, rows * k, "top_ids")
+    _check_out(grad_top, torch.float32, rows * k, "grad_top")
+    _check("sga_token_logprobs_grad", lib().sga_token_logprobs_grad(
+        _ptr(logits), _dtype_code(logits), rows, ld, int(shard_start), width, int(org_vocab),
+        _ptr(tokens), _ptr(lse), _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), k,
+        _ptr(top_ids), _ptr(grad_top), _ptr(out_grad), ldg, _stream(stream)))
+    return out_grad
 
 
 def sga_device_error():

@@ -105,6 +105,24 @@ cudaError_t launch_lmhead_decode(bool fp8, const void *hidden, int64_t M, int64_
                                  const float *row_scale, float w_scale, int num_sms,
                                  uint32_t *err, cudaStream_t stream, bool *launched);
 
+// Token log probabilities (logprobs.cu) of ids [shard_start, shard_start +
+// valid): the final results, or with `part` set the shard's parts and lists.
+cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld,
+                            int64_t shard_start, int64_t valid, const int32_t *tokens, int top_k,
+                            float *logprob, float *entropy, float *lse, int32_t *top_ids,
+                            float *top_logprobs, sga_logprob_part *part, sga_stat *top,
+                            int num_sms, cudaStream_t stream);
+cudaError_t launch_logprob_reduce(const sga_logprob_part *parts, const sga_stat *tops,
+                                  int num_shards, int64_t rows, int top_k, const int32_t *tokens,
+                                  float *logprob, float *entropy, float *lse, int32_t *top_ids,
+                                  float *top_logprobs, cudaStream_t stream);
+cudaError_t launch_logprobs_grad(const void *logits, int dtype, int64_t rows, int64_t ld,
+                                 int64_t shard_start, int64_t width, int64_t valid,
+                                 const int32_t *tokens, const float *lse, const float *entropy,
+                                 const float *g_logprob, const float *g_entropy, int top_k,
+                                 const int32_t *top_ids, const float *g_top, void *grad,
+                                 int64_t ldg, int num_sms, cudaStream_t stream);
+
 // Bounded-wait self-test (lmhead.cu).
 cudaError_t launch_selftest_timeout(unsigned long long limit_ns, uint32_t *err,
                                     unsigned long long *waited_ns, cudaStream_t stream);

@@ -464,6 +464,108 @@ int sga_lmhead_argmax_noalloc(const void *hidden, int64_t M, int64_t H,
   return launch_status(e);
 }
 
+int sga_token_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+                       int64_t org_vocab, const int32_t *tokens, int top_k, float *out_logprob,
+                       float *out_entropy, float *out_lse, int32_t *out_top_ids,
+                       float *out_top_logprobs, sga_stream stream) {
+  if (dtype != SGA_F32 && dtype != SGA_BF16) return SGA_ERR_DTYPE;
+  if (rows < 0 || rows > (int64_t(1) << 28)) return SGA_ERR_SIZE;
+  if (top_k < 0 || top_k > SGA_MAX_TOP) return SGA_ERR_SIZE;
+  int st = check_shard(0, vocab, org_vocab);
+  if (st != SGA_OK) return st;
+  if (ld < vocab) return SGA_ERR_SHARD;
+  if (rows == 0) return SGA_OK;
+  if (logits == nullptr) return SGA_ERR_NULL;
+  if (misaligned(logits, dtype == SGA_BF16 ? 2 : 4) || misaligned(tokens, 4) ||
+      misaligned(out_logprob, 4) || misaligned(out_entropy, 4) || misaligned(out_lse, 4) ||
+      misaligned(out_top_ids, 4) || misaligned(out_top_logprobs, 4))
+    return SGA_ERR_ALIGN;
+  if (out_top_ids == nullptr && out_top_logprobs == nullptr) top_k = 0;
+  DeviceInfo d;
+  if ((st = current_device(&d)) != SGA_OK) return st;
+  return launch_status(sga::launch_logprobs(
+      logits, dtype, rows, ld, 0, valid_ids(0, vocab, org_vocab), tokens, top_k, out_logprob,
+      out_entropy, out_lse, out_top_ids, out_top_logprobs, nullptr, nullptr, d.num_sms,
+      static_cast<cudaStream_t>(stream)));
+}
+
+int sga_local_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld,
+                       int64_t shard_start, int64_t shard_width, int64_t org_vocab,
+                       const int32_t *tokens, int top_k, sga_logprob_part *out_parts,
+                       sga_stat *out_top, sga_stream stream) {
+  if (dtype != SGA_F32 && dtype != SGA_BF16) return SGA_ERR_DTYPE;
+  if (rows < 0 || rows > (int64_t(1) << 28)) return SGA_ERR_SIZE;
+  if (top_k < 0 || top_k > SGA_MAX_TOP) return SGA_ERR_SIZE;
+  int st = check_shard(shard_start, shard_width, org_vocab);
+  if (st != SGA_OK) return st;
+  if (ld < shard_width) return SGA_ERR_SHARD;
+  if (rows == 0) return SGA_OK;
+  if (logits == nullptr || out_parts == nullptr || (top_k > 0 && out_top == nullptr))
+    return SGA_ERR_NULL;
+  if (misaligned(logits, dtype == SGA_BF16 ? 2 : 4) || misaligned(tokens, 4) ||
+      misaligned(out_parts, 4) || misaligned(out_top, 8))
+    return SGA_ERR_ALIGN;
+  DeviceInfo d;
+  if ((st = current_device(&d)) != SGA_OK) return st;
+  return launch_status(sga::launch_logprobs(
+      logits, dtype, rows, ld, shard_start, valid_ids(shard_start, shard_width, org_vocab), tokens,
+      top_k, nullptr, nullptr, nullptr, nullptr, nullptr, out_parts, out_top, d.num_sms,
+      static_cast<cudaStream_t>(stream)));
+}
+
+int sga_logprob_reduce(const sga_logprob_part *parts, const sga_stat *tops, int num_shards,
+                       int64_t rows, int top_k, const int32_t *tokens, float *out_logprob,
+                       float *out_entropy, float *out_lse, int32_t *out_top_ids,
+                       float *out_top_logprobs, sga_stream stream) {
+  if (num_shards < 1 || num_shards > 4096) return SGA_ERR_SIZE;
+  if (rows < 0 || rows > (int64_t(1) << 28)) return SGA_ERR_SIZE;
+  if (top_k < 0 || top_k > SGA_MAX_TOP) return SGA_ERR_SIZE;
+  if (rows == 0) return SGA_OK;
+  if (parts == nullptr || (top_k > 0 && tops == nullptr)) return SGA_ERR_NULL;
+  if (misaligned(parts, 4) || misaligned(tops, 8) || misaligned(tokens, 4) ||
+      misaligned(out_logprob, 4) || misaligned(out_entropy, 4) || misaligned(out_lse, 4) ||
+      misaligned(out_top_ids, 4) || misaligned(out_top_logprobs, 4))
+    return SGA_ERR_ALIGN;
+  if (out_top_ids == nullptr && out_top_logprobs == nullptr) top_k = 0;
+  DeviceInfo d;
+  const int st = current_device(&d);
+  if (st != SGA_OK) return st;
+  return launch_status(sga::launch_logprob_reduce(
+      parts, tops, num_shards, rows, top_k, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
+      out_top_logprobs, static_cast<cudaStream_t>(stream)));
+}
+
+int sga_token_logprobs_grad(const void *logits, int dtype, int64_t rows, int64_t ld,
+                            int64_t shard_start, int64_t shard_width, int64_t org_vocab,
+                            const int32_t *tokens, const float *lse, const float *entropy,
+                            const float *grad_logprob, const float *grad_entropy, int top_k,
+                            const int32_t *top_ids, const float *grad_top, void *out_grad,
+                            int64_t ldg, sga_stream stream) {
+  if (dtype != SGA_F32 && dtype != SGA_BF16) return SGA_ERR_DTYPE;
+  if (rows < 0 || rows > (int64_t(1) << 28)) return SGA_ERR_SIZE;
+  if (top_k < 0 || top_k > SGA_MAX_TOP) return SGA_ERR_SIZE;
+  int st = check_shard(shard_start, shard_width, org_vocab);
+  if (st != SGA_OK) return st;
+  if (ld < shard_width || ldg < shard_width) return SGA_ERR_SHARD;
+  if (rows == 0) return SGA_OK;
+  if (logits == nullptr || lse == nullptr || out_grad == nullptr ||
+      (grad_entropy != nullptr && entropy == nullptr) ||
+      (top_k > 0 && (top_ids == nullptr || grad_top == nullptr)))
+    return SGA_ERR_NULL;
+  const uintptr_t elt = dtype == SGA_BF16 ? 2 : 4;
+  if (misaligned(logits, elt) || misaligned(out_grad, elt) || misaligned(tokens, 4) ||
+      misaligned(lse, 4) || misaligned(entropy, 4) || misaligned(grad_logprob, 4) ||
+      misaligned(grad_entropy, 4) || misaligned(top_ids, 4) || misaligned(grad_top, 4))
+    return SGA_ERR_ALIGN;
+  DeviceInfo d;
+  if ((st = current_device(&d)) != SGA_OK) return st;
+  return launch_status(sga::launch_logprobs_grad(
+      logits, dtype, rows, ld, shard_start, shard_width,
+      valid_ids(shard_start, shard_width, org_vocab), tokens, lse, entropy, grad_logprob,
+      grad_entropy, top_k, top_ids, grad_top, out_grad, ldg, d.num_sms,
+      static_cast<cudaStream_t>(stream)));
+}
+
 int sga_selftest_wait_timeout(uint64_t limit_ns, uint64_t *waited_ns, sga_stream stream) {
   if (limit_ns < 1000 || limit_ns > 1000000000ull) return SGA_ERR_SIZE;
   if (misaligned(waited_ns, 8)) return SGA_ERR_ALIGN;

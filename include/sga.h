@@ -457,6 +457,117 @@ int sga_lmhead_argmax_noalloc(const void *hidden, int64_t M, int64_t H,
                               sga_stream stream);
 
 /*
+ * sga_token_logprobs -- log probabilities of given tokens over a whole
+ * vocabulary, with each row's entropy and best alternatives: what a server
+ * reports beside the greedy ids, and the loss of a draft model in training.
+ * (The pages stop at the ids; this is the library's extension, on the same
+ * row, shard and padding conventions.)
+ *
+ * With x the row's logits of ids below org_vocab, lse = log sum_j e^x_j:
+ *   logprob = x_token - lse,   entropy = lse - sum_j e^(x_j - lse) x_j,
+ *   alternatives: the top_k best ids in the argmax order, each with x - lse.
+ * Sums are kept in fp32 relative to the row's maximum.
+ *
+ *   logits       as sga_local_argmax, column 0 = global id 0.
+ *   vocab        columns of a row, 1 .. SGA_MAX_VOCAB; ld >= vocab.
+ *   org_vocab    1 .. SGA_MAX_VOCAB; ids >= org_vocab are padding, not read.
+ *   tokens       device int32 [rows] or NULL.  A negative token is no token:
+ *                its log probability is 0.  A token >= org_vocab (or one whose
+ *                logit is -inf) has log probability -inf.
+ *   top_k        0 .. SGA_MAX_TOP.
+ *   out_logprob, out_entropy, out_lse   device fp32 [rows], each nullable.
+ *   out_top_ids, out_top_logprobs   device int32 / fp32 [rows, top_k], each
+ *                nullable: best first, equal logits by ascending id (-inf
+ *                logits included); with fewer than top_k ids below org_vocab
+ *                the rest are id -1, log probability -inf.
+ * A row with no logit above -inf has lse -inf, entropy 0 and every log
+ * probability -inf (a negative token's stays 0).  A row holding a NaN or +inf
+ * has NaN for lse, entropy and every log probability (a negative token's stays
+ * 0); its alternatives' ids keep the argmax order.
+ * fp32 and int32 pointers must be 4-byte aligned.  One kernel launch.
+ * Errors: SGA_ERR_DTYPE, SGA_ERR_SIZE (rows or top_k), SGA_ERR_VOCAB,
+ * SGA_ERR_SHARD (ld < vocab), SGA_ERR_NULL (logits), SGA_ERR_ALIGN.
+ */
+#define SGA_MAX_TOP 32
+int sga_token_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+                       int64_t org_vocab, const int32_t *tokens, int top_k, float *out_logprob,
+                       float *out_entropy, float *out_lse, int32_t *out_top_ids,
+                       float *out_top_logprobs, sga_stream stream);
+
+/* A row's statistics over one vocab shard: the maximum, sum_j e^(x_j - max),
+ * sum_j (x_j - max) log2(e) e^(x_j - max), and the token's logit (-inf when
+ * the token is not an id of the shard).  A shard with no logit above -inf has
+ * max -inf (its sums are not used). */
+typedef struct sga_logprob_part {
+  float max, sum, wsum, token;
+} sga_logprob_part;
+
+/*
+ * sga_local_logprobs -- the part of sga_token_logprobs that one vocab shard
+ * (one tensor-parallel rank) contributes; the parts of all shards, gathered
+ * on dim 0, go to sga_logprob_reduce.
+ *
+ *   logits, dtype, rows, ld, shard_start, shard_width, org_vocab
+ *                as sga_local_argmax.
+ *   tokens       device int32 [rows] GLOBAL ids, or NULL, as above.
+ *   out_parts    device [rows], 4-byte aligned.
+ *   out_top      device [rows, top_k], 8-byte aligned: the shard's best
+ *                (logit, GLOBAL id), best first; entries past the shard's
+ *                non-padding ids are (-inf, 0x7fffffff).  NULL iff top_k is 0.
+ */
+int sga_local_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld,
+                       int64_t shard_start, int64_t shard_width, int64_t org_vocab,
+                       const int32_t *tokens, int top_k, sga_logprob_part *out_parts,
+                       sga_stat *out_top, sga_stream stream);
+
+/*
+ * sga_logprob_reduce -- joins the gathered parts of all shards into the
+ * results of sga_token_logprobs.
+ *
+ *   parts        device, num_shards * rows entries, shard-major.
+ *   tops         device, num_shards * rows * top_k entries, shard-major (NULL
+ *                iff top_k is 0); shards in ascending id order.
+ *   num_shards   1 .. 4096.
+ *   tokens       the tokens given to sga_local_logprobs (they tell a row
+ *                without a token from one whose token has no probability).
+ * Outputs as sga_token_logprobs.
+ */
+int sga_logprob_reduce(const sga_logprob_part *parts, const sga_stat *tops, int num_shards,
+                       int64_t rows, int top_k, const int32_t *tokens, float *out_logprob,
+                       float *out_entropy, float *out_lse, int32_t *out_top_ids,
+                       float *out_top_logprobs, sga_stream stream);
+
+/*
+ * sga_token_logprobs_grad -- gradient of the log probabilities, the entropy
+ * and the alternatives' log probabilities with respect to the logits, over
+ * the whole vocabulary or one shard of it (no exchange: the row's lse and
+ * entropy carry what the other shards hold).  With p_j = e^(x_j - lse):
+ *   grad_j = [j = token] g_logprob + sum_i [j = top_ids_i] g_top_i
+ *            - p_j (g_logprob + sum_i g_top_i) - g_entropy p_j (x_j - lse + entropy)
+ *
+ *   logits, dtype, rows, ld, shard_start, shard_width, org_vocab
+ *                as sga_local_argmax.
+ *   tokens       device int32 [rows] or NULL: global ids, as above (a negative
+ *                token has no gradient).
+ *   lse, entropy device fp32 [rows] from the forward pass; entropy may be NULL
+ *                iff grad_entropy is.
+ *   grad_logprob, grad_entropy   device fp32 [rows], nullable (no gradient).
+ *   top_ids, grad_top   device [rows, top_k]; NULL iff top_k is 0.  Ids may
+ *                repeat and may be the token; a negative id is skipped.
+ *   out_grad     device, rows x shard_width elements of `dtype`, row stride
+ *                ldg >= shard_width elements, aligned to the element; padding
+ *                ids get 0.  May be the logits buffer itself (ldg == ld); any
+ *                other overlap is not allowed.
+ * A row whose lse is -inf gets 0 everywhere.
+ */
+int sga_token_logprobs_grad(const void *logits, int dtype, int64_t rows, int64_t ld,
+                            int64_t shard_start, int64_t shard_width, int64_t org_vocab,
+                            const int32_t *tokens, const float *lse, const float *entropy,
+                            const float *grad_logprob, const float *grad_entropy, int top_k,
+                            const int32_t *top_ids, const float *grad_top, void *out_grad,
+                            int64_t ldg, sga_stream stream);
+
+/*
  * Device error word of the current device.  Kernels OR bits into it instead
  * of trapping: SGA_DEVERR_K_RANGE (a request's K_i outside [0, max_k]),
  * SGA_DEVERR_D2T_RANGE (a winning id outside the d2t table),
