@@ -28,6 +28,7 @@ SGA_F32, SGA_BF16 = 0, 1
 SGA_MAX_K = 15
 SGA_MAX_VOCAB = 1 << 24
 SGA_MAX_TOP = 32
+SGA_ACT_NONE, SGA_ACT_RELU, SGA_ACT_SILU, SGA_ACT_GELU, SGA_ACT_GELU_TANH = 0, 1, 2, 3, 4
 SGA_DEVERR_K_RANGE, SGA_DEVERR_D2T_RANGE, SGA_DEVERR_TIMEOUT, SGA_DEVERR_LAYOUT = 1, 2, 4, 8
 
 _lib = None
@@ -71,6 +72,11 @@ def lib():
             "sga_lmhead_argmax": ([vp, i64, i64, vp, i64, i64, i64, vp, vp, sz, vp], i32),
             "sga_lmhead_argmax_fp8": ([vp, vp, i64, i64, vp, ctypes.c_float, i64, i64, i64, vp,
                                        vp, sz, vp], i32),
+            "sga_linear": ([vp, i64, i64, i64, vp, i64, i64, vp, i32, i32, vp, i64, vp, i64, vp,
+                            i64, vp], i32),
+            "sga_linear_grad_workspace": ([i64, i64, i64], sz),
+            "sga_linear_grad": ([vp, i64, i64, i64, vp, i64, i32, vp, i64, i64, vp, i64, vp, i64,
+                                 vp, i64, vp, i32, vp, sz, vp], i32),
             "sga_token_logprobs": ([vp, i32, i64, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp,
                                     vp], i32),
             "sga_local_logprobs": ([vp, i32, i64, i64, i64, i64, i64, vp, i32, vp, vp, vp], i32),
@@ -348,6 +354,66 @@ def sga_lmhead_argmax_shards_fp8(hidden_q, hidden_scale, weight_q, weight_scale,
         starts, widths, int(org_vocab), _ptr(out_stats), _ptr(workspace), nbytes,
         _stream(stream)))
     return out_stats
+
+
+def _bf16_rows(t, rows, cols, name):
+    """Row stride of a bf16 [rows, cols] tensor with unit column stride."""
+    if t.dtype != torch.bfloat16 or t.shape != (rows, cols) or (
+            cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be bf16 [{rows}, {cols}] with unit column stride")
+    return t.stride(0) if rows > 1 else cols  # the stride of a single row is never used
+
+
+def _bias_code(t, n, name):
+    if t is None:
+        return SGA_F32
+    if t.dtype not in (torch.float32, torch.bfloat16) or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 or bf16 tensor of {n} elements")
+    return SGA_F32 if t.dtype == torch.float32 else SGA_BF16
+
+
+def sga_linear(x, weight, out, bias=None, act=SGA_ACT_NONE, residual=None, out_preact=None,
+               stream=None):
+    """out = act(x . weight^T + bias) + residual.  x: bf16 [M, K], weight: bf16
+    [N, K], out / residual / out_preact: bf16 [M, N] (unit column stride, any
+    row stride; x and weight rows 16-byte aligned), bias: float32 or bf16 [N].
+    out may be residual itself; out_preact receives x . weight^T + bias, which
+    sga_linear_grad needs when there is an activation (see include/sga.h)."""
+    M, K = x.shape
+    N = weight.size(0)
+    ldx, ldw = _bf16_rows(x, M, K, "x"), _bf16_rows(weight, N, K, "weight")
+    ldo = _bf16_rows(out, M, N, "out")
+    ldr = 0 if residual is None else _bf16_rows(residual, M, N, "residual")
+    ldp = 0 if out_preact is None else _bf16_rows(out_preact, M, N, "out_preact")
+    code = _bias_code(bias, N, "bias")
+    _check("sga_linear", lib().sga_linear(
+        _ptr(x), M, K, ldx, _ptr(weight), N, ldw, _ptr(bias), code, int(act), _ptr(residual), ldr,
+        _ptr(out_preact), ldp, _ptr(out), ldo, _stream(stream)))
+    return out
+
+
+def sga_linear_grad_workspace(M, N, K):
+    return int(lib().sga_linear_grad_workspace(int(M), int(N), int(K)))
+
+
+def sga_linear_grad(grad_out, x, weight, workspace, act=SGA_ACT_NONE, preact=None, grad_x=None,
+                    grad_weight=None, grad_bias=None, stream=None):
+    """Gradient of sga_linear with respect to x, weight and bias (each output
+    bf16 like its operand, grad_bias float32 or bf16, or None); the residual's
+    gradient is grad_out itself.  preact: sga_linear's out_preact; workspace: a
+    CUDA tensor of at least sga_linear_grad_workspace(M, N, K) bytes."""
+    M, K = x.shape
+    N = weight.size(0)
+    ldx, ldw = _bf16_rows(x, M, K, "x"), _bf16_rows(weight, N, K, "weight")
+    ldg = _bf16_rows(grad_out, M, N, "grad_out")
+    ldp = 0 if preact is None else _bf16_rows(preact, M, N, "preact")
+    ldgx = 0 if grad_x is None else _bf16_rows(grad_x, M, K, "grad_x")
+    ldgw = 0 if grad_weight is None else _bf16_rows(grad_weight, N, K, "grad_weight")
+    code = _bias_code(grad_bias, N, "grad_bias")
+    _check("sga_linear_grad", lib().sga_linear_grad(
+        _ptr(grad_out), M, N, ldg, _ptr(preact), ldp, int(act), _ptr(x), K, ldx, _ptr(weight),
+        ldw, _ptr(grad_x), ldgx, _ptr(grad_weight), ldgw, _ptr(grad_bias), code, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def _check_out(t, dtype, numel, name):

@@ -105,6 +105,20 @@ cudaError_t launch_lmhead_decode(bool fp8, const void *hidden, int64_t M, int64_
                                  const float *row_scale, float w_scale, int num_sms,
                                  uint32_t *err, cudaStream_t stream, bool *launched);
 
+// Matrix product with bias, activation and residual, and its gradient
+// (linear.cu); strides in elements.
+cudaError_t launch_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const void *weight,
+                          int64_t N, int64_t ldw, const void *bias, int bias_dtype, int act,
+                          const void *residual, int64_t ldr, void *preact, int64_t ldp, void *out,
+                          int64_t ldo, int num_sms, uint32_t *err, cudaStream_t stream);
+size_t linear_grad_workspace_bytes(int64_t M, int64_t N);
+cudaError_t launch_linear_grad(const void *grad_out, int64_t M, int64_t N, int64_t ldg,
+                               const void *preact, int64_t ldp, int act, const void *x, int64_t K,
+                               int64_t ldx, const void *weight, int64_t ldw, void *grad_x,
+                               int64_t ldgx, void *grad_weight, int64_t ldgw, void *grad_bias,
+                               int bias_dtype, void *workspace, int num_sms, uint32_t *err,
+                               cudaStream_t stream);
+
 // Token log probabilities (logprobs.cu) of ids [shard_start, shard_start +
 // valid): the final results, or with `part` set the shard's parts and lists.
 cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld,

@@ -1,0 +1,999 @@
+// linear.cu -- matrix product with bias, activation and residual in its
+// epilogue, and its gradient, in bf16 on the tcgen05 tensor cores:
+//   y  = act(z) + residual,  z = x . W^T + b         x [M, K], W [N, K]
+//   dz = g * act'(z),  dx = dz . W,  dW = dz^T . x,  db = sum over rows of dz
+// A draft head's residual block and its LM head are this product; sums are
+// held in fp32 (tensor memory) and each result is rounded once.
+//
+// Three products, one kernel: the operands of D[r, c] = sum_k A[r, k] B[c, k]
+// are read where they lie, the summed dimension contiguous (x and W of the
+// forward product, dz of dx) or strided (W of dx, dz and x of dW); TMA brings
+// either into 128-byte swizzled tiles and the matrix descriptor tells the
+// tensor core which way they run, so nothing is transposed in memory.
+//   gemm_kernel      CTA pairs (cta_group::2), 256 x kBN tiles, persistent.
+//   few_rows_kernel  M <= 128: the weight is the 128-row operand, streamed
+//                    once; a cluster splits the summed dimension and joins
+//                    through distributed shared memory.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "tcgen05.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace sga {
+namespace {
+
+// ------------------------------------------------------------- activations
+
+__device__ __forceinline__ float sigmoid_times(float z, float u) {  // z / (1 + e^-u)
+  return __fdividef(z, 1.0f + __expf(-u));
+}
+
+constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+__device__ __forceinline__ float activate(float z, int act) {
+  switch (act) {
+    case SGA_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case SGA_ACT_SILU: return sigmoid_times(z, z);
+    case SGA_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.7071067811865476f));
+    case SGA_ACT_GELU_TANH:  // z (1 + tanh u) / 2 = z / (1 + e^-2u)
+      return sigmoid_times(z, 2.0f * kGeluA * fmaf(kGeluB * z * z, z, z));
+    default: return z;
+  }
+}
+
+__device__ __forceinline__ float activate_grad(float z, int act) {
+  switch (act) {
+    case SGA_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case SGA_ACT_SILU: {
+      const float q = sigmoid_times(1.0f, z);
+      return q * fmaf(z, 1.0f - q, 1.0f);
+    }
+    case SGA_ACT_GELU:
+      return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z),
+                  0.5f * (1.0f + erff(z * 0.7071067811865476f)));
+    case SGA_ACT_GELU_TANH: {
+      const float q = sigmoid_times(1.0f, 2.0f * kGeluA * fmaf(kGeluB * z * z, z, z));
+      const float du = 2.0f * kGeluA * fmaf(3.0f * kGeluB * z, z, 1.0f);
+      return fmaf(z * q * (1.0f - q), du, q);
+    }
+    default: return 1.0f;
+  }
+}
+
+__device__ __forceinline__ float ld_bf16(const __nv_bfloat16 *p) {
+  return __uint_as_float(
+      static_cast<uint32_t>(*reinterpret_cast<const unsigned short *>(p)) << 16);
+}
+
+__device__ __forceinline__ float ld_bias(const void *bias, int f32, int64_t c) {
+  if (bias == nullptr) return 0.0f;
+  return f32 ? static_cast<const float *>(bias)[c]
+             : ld_bf16(static_cast<const __nv_bfloat16 *>(bias) + c);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// What happens to an accumulator: out[r, c] = act(acc + bias[c]) + res[r, c],
+// pre[r, c] = acc + bias[c] (each of bias, res, pre nullable).
+struct Epilogue {
+  __nv_bfloat16 *out, *pre;
+  const __nv_bfloat16 *res;
+  const void *bias;
+  int64_t ldo, ldp, ldr;
+  int bias_f32, act;
+};
+
+// ------------------------------------------------------------- descriptors
+
+// Shared-memory descriptor of an operand tile with the 128-byte swizzle.
+// Summed dimension contiguous: rows of 128 bytes, 8-row groups 1024 B apart.
+// Summed dimension strided: rows of 64 elements of the other dimension, one
+// row per summed index, 8-row groups 1024 B apart (stride offset) and the next
+// 64 elements of the other dimension one 64-row box (8192 B) on (leading
+// offset).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool strided) {
+  return smem_desc_sw128(addr) + (strided ? static_cast<uint64_t>((8192 >> 4) - 1) << 16 : 0);
+}
+
+// Instruction descriptor (bf16 x bf16 -> fp32) with the operands' directions.
+__device__ __forceinline__ uint32_t operand_idesc(uint32_t m, uint32_t n, bool a_strided,
+                                                  bool b_strided) {
+  return instr_desc<false>(m, n) | (a_strided ? 1u << 15 : 0u) | (b_strided ? 1u << 16 : 0u);
+}
+
+// 16-byte descriptor units between the 16-deep K steps of a 64-deep block.
+__device__ __forceinline__ uint32_t k_step(bool strided) { return strided ? 2048 >> 4 : 32 >> 4; }
+
+__device__ __forceinline__ void mma_pair_rt(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_one_rt(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// gemm_kernel: warp 0 TMA producer, warp 1 MMA issuer (leader CTA of the
+// pair), warps 2..5 epilogue; the same roles and barriers as the LM-head
+// kernel of lmhead.cu.  A launch runs one or two products (dx and dW of one
+// gradient): their tiles form one list, so the second fills the SMs that the
+// first one's last wave leaves idle.
+// ---------------------------------------------------------------------------
+constexpr int kMaxProducts = 2;
+
+struct Product {
+  int rows, cols, num_kb;       // D's size; 64-deep blocks of the summed dimension
+  int tiles_r, tiles_c;         // 256 x kBN tiles
+  int a_strided, b_strided;
+  Epilogue ep;
+};
+
+struct Products {
+  int n;
+  int tile0[kMaxProducts + 1];  // first tile number of each product
+  Product p[kMaxProducts];
+};
+
+struct Maps {
+  CUtensorMap a[kMaxProducts], b[kMaxProducts];
+};
+
+constexpr int kTileA = 128 * ROW_BYTES;  // 16 KB: this CTA's 128 rows of A
+template <int kBN>
+constexpr int tile_b = kBN / 2 * ROW_BYTES;  // this CTA's half of B
+template <int kBN>
+constexpr int gemm_stage = kTileA + tile_b<kBN>;
+constexpr int kEpiPitch = 33;                               // floats; conflict-free both ways
+constexpr int kEpiBytes = 4 * 32 * kEpiPitch * 4;           // one 32 x 32 square per warp
+template <int kBN>
+constexpr int gemm_stages = (227 * 1024 - 2048 - kEpiBytes) / gemm_stage<kBN>;
+template <int kBN>
+constexpr int gemm_smem = 1024 + gemm_stages<kBN> * gemm_stage<kBN> + kEpiBytes + 512;
+
+template <int kBN>
+struct SharedGemm {
+  uint64_t full[gemm_stages<kBN>];
+  uint64_t empty[gemm_stages<kBN>];
+  uint64_t tmem_full[2];
+  uint64_t tmem_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ void raise_abort(int *flag, uint32_t *err) {
+  *reinterpret_cast<volatile int *>(flag) = 1;
+  atomicOr(err, SGA_DEVERR_TIMEOUT);
+}
+
+// Tile t of a product: bands of 8 row tiles, row tiles fastest, so that the
+// pairs at work share a few A and B panels through L2.
+__device__ __forceinline__ void tile_at(const Product &p, int t, int &tr, int &tc) {
+  constexpr int kBand = 8;
+  const int band = t / (kBand * p.tiles_c);
+  const int height = min(kBand, p.tiles_r - band * kBand);
+  const int in = t - band * kBand * p.tiles_c;
+  tc = in / height;
+  tr = band * kBand + in - tc * height;
+}
+
+// The epilogue of one 32-row x 32-column square whose accumulators lie in
+// `sq` (row-major, pitch kEpiPitch): half a warp per row, two columns a lane,
+// so that global rows are read and written in 64-byte runs.
+__device__ __forceinline__ void square_epilogue(const Epilogue &ep, const float *sq, int64_t row0,
+                                                int rows, int64_t col0, int cols, int lane) {
+  const int c = 2 * (lane & 15);
+  const int64_t col = col0 + c;
+  const bool has0 = c < cols, has1 = c + 1 < cols;
+  const float b0 = has0 ? ld_bias(ep.bias, ep.bias_f32, col) : 0.0f;
+  const float b1 = has1 ? ld_bias(ep.bias, ep.bias_f32, col + 1) : 0.0f;
+  const bool wide_out = has1 && ((reinterpret_cast<uintptr_t>(ep.out) | (2 * ep.ldo)) & 3) == 0;
+  const bool wide_pre = has1 && ((reinterpret_cast<uintptr_t>(ep.pre) | (2 * ep.ldp)) & 3) == 0;
+  const bool wide_res = has1 && ((reinterpret_cast<uintptr_t>(ep.res) | (2 * ep.ldr)) & 3) == 0;
+  float r0[16], r1[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + (lane >> 4);
+    r0[i] = r1[i] = 0.0f;
+    if (ep.res != nullptr && r < rows && has0) {
+      const __nv_bfloat16 *q = ep.res + (row0 + r) * ep.ldr + col;
+      if (wide_res) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(q);
+        r0[i] = bf16_lo(w);
+        r1[i] = bf16_hi(w);
+      } else {
+        r0[i] = ld_bf16(q);
+        if (has1) r1[i] = ld_bf16(q + 1);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int r = 2 * i + (lane >> 4);
+    if (r < rows && has0) {
+      const float z0 = sq[r * kEpiPitch + c] + b0, z1 = sq[r * kEpiPitch + c + 1] + b1;
+      if (ep.pre != nullptr) {
+        __nv_bfloat16 *q = ep.pre + (row0 + r) * ep.ldp + col;
+        if (wide_pre) {
+          *reinterpret_cast<uint32_t *>(q) = pack2(z0, z1);
+        } else {
+          q[0] = __float2bfloat16_rn(z0);
+          if (has1) q[1] = __float2bfloat16_rn(z1);
+        }
+      }
+      const float y0 = activate(z0, ep.act) + r0[i], y1 = activate(z1, ep.act) + r1[i];
+      __nv_bfloat16 *q = ep.out + (row0 + r) * ep.ldo + col;
+      if (wide_out) {
+        *reinterpret_cast<uint32_t *>(q) = pack2(y0, y1);
+      } else {
+        q[0] = __float2bfloat16_rn(y0);
+        if (has1) q[1] = __float2bfloat16_rn(y1);
+      }
+    }
+  }
+}
+
+template <int kBN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Products prods,
+                uint32_t *err) {
+  constexpr int kStages = gemm_stages<kBN>;
+  constexpr int kStageB = gemm_stage<kBN>;
+  constexpr int kCols = 2 * kBN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float *epi = reinterpret_cast<float *>(base + kStages * kStageB);
+  SharedGemm<kBN> *sh =
+      reinterpret_cast<SharedGemm<kBN> *>(base + kStages * kStageB + kEpiBytes);
+  const volatile int *abort_flag = &sh->abort;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int num_pairs = static_cast<int>(gridDim.x >> 1);
+  const int total = prods.tile0[prods.n];
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&sh->full[s]), 1);
+      mbar_init(smem_u32(&sh->empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sh->tmem_full[b]), 1);
+      mbar_init(smem_u32(&sh->tmem_empty[b]), 8);
+    }
+    mbar_init(smem_u32(&sh->drain), 1);
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sh->tmem_base)),
+                 "r"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  tc_fence_after();
+  const uint32_t tmem_base = sh->tmem_base;
+  pdl_wait();
+
+  int prod_stage = 0;
+  uint32_t prod_phase = 0;
+  long long issued = 0;
+
+  if (warp == 0 && lane == 0) {
+    // -------------------------------------------------- producer (both CTAs)
+    int pi = 0;
+    for (int t = pair; t < total && !*abort_flag; t += num_pairs) {
+      while (t >= prods.tile0[pi + 1]) ++pi;
+      const Product &p = prods.p[pi];
+      int tr, tc;
+      tile_at(p, t - prods.tile0[pi], tr, tc);
+      const int row = tr * 256 + static_cast<int>(rank) * 128;
+      const int col = tc * kBN + static_cast<int>(rank) * (kBN / 2);
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!mbar_wait(smem_u32(&sh->empty[prod_stage]), prod_phase ^ 1, abort_flag)) {
+          raise_abort(&sh->abort, err);
+          break;
+        }
+        const uint32_t full = map_to_rank(smem_u32(&sh->full[prod_stage]), 0);
+        if (leader) mbar_expect_tx(smem_u32(&sh->full[prod_stage]), 2 * kStageB);
+        const uint32_t a = smem_u32(base + prod_stage * kStageB);
+        if (p.a_strided) {
+          tma_load_2d_pair(a, &maps.a[pi], row, kb * 64, full);
+          tma_load_2d_pair(a + 8192, &maps.a[pi], row + 64, kb * 64, full);
+        } else {
+          tma_load_2d_pair(a, &maps.a[pi], kb * 64, row, full);
+        }
+        if (p.b_strided) {
+#pragma unroll
+          for (int i = 0; i < kBN / 128; ++i)
+            tma_load_2d_pair(a + kTileA + i * 8192, &maps.b[pi], col + i * 64, kb * 64, full);
+        } else {
+          tma_load_2d_pair(a + kTileA, &maps.b[pi], kb * 64, col, full);
+        }
+        ++issued;
+        if (++prod_stage == kStages) {
+          prod_stage = 0;
+          prod_phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1 && lane == 0 && leader) {
+    // --------------------------------------------------- MMA issuer (leader)
+    int stage = 0, acc = 0, pi = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = pair; t < total && ok && !*abort_flag; t += num_pairs) {
+      while (t >= prods.tile0[pi + 1]) ++pi;
+      const Product &p = prods.p[pi];
+      const uint32_t idesc = operand_idesc(256, kBN, p.a_strided, p.b_strided);
+      const uint32_t step_a = k_step(p.a_strided), step_b = k_step(p.b_strided);
+      if (!mbar_wait(smem_u32(&sh->tmem_empty[acc]), acc_phase ^ 1, abort_flag)) {
+        raise_abort(&sh->abort, err);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + acc * kBN;
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!mbar_wait(smem_u32(&sh->full[stage]), phase, abort_flag)) {
+          raise_abort(&sh->abort, err);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a = smem_u32(base + stage * kStageB);
+        const uint64_t a_desc = operand_desc(a, p.a_strided);
+        const uint64_t b_desc = operand_desc(a + kTileA, p.b_strided);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_pair_rt(d_tmem, a_desc + step_a * kk, b_desc + step_b * kk, idesc, (kb | kk) != 0);
+        mma_commit_pair(smem_u32(&sh->empty[stage]));
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      mma_commit_pair(smem_u32(&sh->tmem_full[acc]));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  } else if (warp >= 2) {
+    // -------------------------------------------------- epilogue (both CTAs)
+    const int quarter = warp & 3;
+    float *sq = epi + quarter * 32 * kEpiPitch;
+    const uint32_t empty_leader[2] = {map_to_rank(smem_u32(&sh->tmem_empty[0]), 0),
+                                      map_to_rank(smem_u32(&sh->tmem_empty[1]), 0)};
+    int acc = 0, pi = 0;
+    uint32_t acc_phase = 0;
+    for (int t = pair; t < total; t += num_pairs) {
+      while (t >= prods.tile0[pi + 1]) ++pi;
+      const Product &p = prods.p[pi];
+      int tr, tc;
+      tile_at(p, t - prods.tile0[pi], tr, tc);
+      const bool ok = __all_sync(
+          0xffffffffu, mbar_wait(smem_u32(&sh->tmem_full[acc]), acc_phase, abort_flag));
+      if (!ok) {
+        if (lane == 0) raise_abort(&sh->abort, err);
+        break;
+      }
+      tc_fence_after();
+      const int64_t row0 = tr * 256 + static_cast<int>(rank) * 128 + quarter * 32;
+      const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.rows - row0));
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN;
+#pragma unroll 1
+      for (int q = 0; q < kBN / 32; ++q) {
+        uint32_t r[32];
+        tmem_ld32(taddr + q * 32, r);
+        tmem_ld_wait();
+        if (q == kBN / 32 - 1) {
+          // the accumulator is in registers: the MMA may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              mbar_arrive(smem_u32(&sh->tmem_empty[acc]));
+            else
+              mbar_arrive_remote(empty_leader[acc]);
+          }
+        }
+        const int64_t col0 = static_cast<int64_t>(tc) * kBN + q * 32;
+        if (rows > 0 && col0 < p.cols) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sq[lane * kEpiPitch + i] = __uint_as_float(r[i]);
+          __syncwarp();
+          square_epilogue(p.ep, sq, row0, rows, col0,
+                          static_cast<int>(min(static_cast<int64_t>(32), p.cols - col0)), lane);
+          __syncwarp();
+        }
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  }
+
+  pdl_launch_dependents();
+  __syncthreads();
+  if (*abort_flag) {
+    const int zero = 0;
+    if (warp == 0 && lane == 0) {
+      if (leader) {
+        // the leader's full barriers count the copies of both CTAs
+        const long long outstanding = issued < kStages ? issued : kStages;
+        for (long long i = 1; i <= outstanding; ++i) {
+          int s = prod_stage - static_cast<int>(i);
+          uint32_t ph = prod_phase;
+          if (s < 0) {
+            s += kStages;
+            ph ^= 1;
+          }
+          mbar_wait(smem_u32(&sh->full[s]), ph, &zero);
+        }
+      } else if (issued > 0) {
+        // the follower's copies complete on the leader's barriers, which it
+        // cannot wait on: give them a bounded 1 ms to land
+        const unsigned long long t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+      }
+    }
+    if (warp == 1 && lane == 0 && leader) {
+      mma_commit_pair(smem_u32(&sh->drain));
+      mbar_wait(smem_u32(&sh->drain), 0, &zero);
+    }
+  }
+  // the peer may still read this CTA's shared memory or write its TMEM
+  tc_fence_before();
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(kCols)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// few_rows_kernel, M <= 128: out[m, r] = act(sum_k A[r, k] x[m, k] + bias[r])
+// + res[m, r] with A the weight (128 rows r per CTA, its TMEM lanes) and the M
+// rows of x the MMA's kN columns.  The weight is read once and sets the pace.
+// A cluster of `splits` CTAs shares a tile: each sums its range of K blocks,
+// stores its fp32 partial tile in its own shared memory, and adds up
+// 128 / splits of the rows from every CTA's, in rank order (a fixed order:
+// results do not vary from run to run).
+// ---------------------------------------------------------------------------
+template <int kN>
+constexpr int few_stage = kTileA + kN * ROW_BYTES;
+template <int kN>
+constexpr int few_stages = (110 * 1024) / few_stage<kN>;  // two CTAs per SM
+template <int kN>
+constexpr int few_cols = kN < 32 ? 32 : kN;  // TMEM columns (a power of two, at least 32)
+
+template <int kN>
+struct SharedFew {
+  uint64_t full[few_stages<kN>];
+  uint64_t empty[few_stages<kN>];
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int kN>
+constexpr int few_smem = 1024 + few_stages<kN> * few_stage<kN> + static_cast<int>(sizeof(SharedFew<kN>));
+static_assert(few_stages<128> * few_stage<128> >= 128 * 128 * 4, "a partial tile fits the ring");
+
+template <int kN>
+__global__ void __launch_bounds__(THREADS, 2)
+    few_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
+                    const __grid_constant__ CUtensorMap tmap_x, int M, int rows, int num_kb,
+                    int splits, int strided, const Epilogue ep, uint32_t *err) {
+  constexpr int kStages = few_stages<kN>;
+  constexpr int kStageB = few_stage<kN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  SharedFew<kN> *sh = reinterpret_cast<SharedFew<kN> *>(base + kStages * kStageB);
+  const volatile int *abort_flag = &sh->abort;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int tile = static_cast<int>(blockIdx.x) / splits;
+  const int split = static_cast<int>(blockIdx.x) - tile * splits;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * split / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (split + 1) / splits);
+  const int row0 = tile * 128;
+
+  if (threadIdx.x == 64) {
+    // Warm L2 with the first ring of the weight while the previous kernel
+    // drains: a prefetch only fills L2, which stays coherent with any later
+    // write, so it may precede the dependency wait.
+    for (int kb = kb0; kb < kb1 && kb < kb0 + kStages; ++kb) {
+      if (strided) {
+        tma_prefetch_2d(&tmap_w, row0, kb * 64);
+        tma_prefetch_2d(&tmap_w, row0 + 64, kb * 64);
+      } else {
+        tma_prefetch_2d(&tmap_w, kb * 64, row0);
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&sh->full[s]), 1);
+      mbar_init(smem_u32(&sh->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sh->done), 1);
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sh->tmem_base)),
+                 "r"(few_cols<kN>)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = sh->tmem_base;
+  pdl_wait();
+
+  int prod_stage = 0;
+  uint32_t prod_phase = 0;
+  int issued = 0;
+  bool good = true;
+  float *part = reinterpret_cast<float *>(base);  // [kN][128], once the ring has been read
+  if (warp == 0 && lane == 0) {
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(smem_u32(&sh->empty[prod_stage]), prod_phase ^ 1, abort_flag)) {
+        raise_abort(&sh->abort, err);
+        break;
+      }
+      const uint32_t full = smem_u32(&sh->full[prod_stage]);
+      const uint32_t a = smem_u32(base + prod_stage * kStageB);
+      mbar_expect_tx(full, kStageB);
+      if (strided) {
+        tma_load_2d(a, &tmap_w, row0, kb * 64, full);
+        tma_load_2d(a + 8192, &tmap_w, row0 + 64, kb * 64, full);
+      } else {
+        tma_load_2d(a, &tmap_w, kb * 64, row0, full);
+      }
+      tma_load_2d(a + kTileA, &tmap_x, kb * 64, 0, full);
+      ++issued;
+      if (++prod_stage == kStages) {
+        prod_stage = 0;
+        prod_phase ^= 1;
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    int stage = 0;
+    uint32_t phase = 0;
+    const uint32_t idesc = operand_idesc(128, kN, strided, false);
+    const uint32_t step_a = k_step(strided);
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(smem_u32(&sh->full[stage]), phase, abort_flag)) {
+        raise_abort(&sh->abort, err);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t a = smem_u32(base + stage * kStageB);
+      const uint64_t a_desc = operand_desc(a, strided);
+      const uint64_t b_desc = smem_desc_sw128(a + kTileA);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_one_rt(tmem_base, a_desc + step_a * kk, b_desc + 2 * kk, idesc,
+                   (kb != kb0) || kk != 0);
+      mma_commit(smem_u32(&sh->empty[stage]));
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (ok) mma_commit(smem_u32(&sh->done));
+  } else if (warp >= 2) {
+    good = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->done), 0, abort_flag));
+    if (!good && lane == 0) raise_abort(&sh->abort, err);
+    if (good) {
+      tc_fence_after();
+      const int quarter = warp & 3;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+      for (int m0 = 0; m0 < M; m0 += 16) {
+        uint32_t r[16];
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr + m0));
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          part[(m0 + i) * 128 + quarter * 32 + lane] = __uint_as_float(r[i]);
+      }
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (*abort_flag) {
+    // let this CTA's own copies and MMAs land before its memory is released
+    const int zero = 0;
+    if (warp == 0 && lane == 0) {
+      const int outstanding = issued < kStages ? issued : kStages;
+      for (int i = 1; i <= outstanding; ++i) {
+        int s = prod_stage - i;
+        uint32_t ph = prod_phase;
+        if (s < 0) {
+          s += kStages;
+          ph ^= 1;
+        }
+        mbar_wait(smem_u32(&sh->full[s]), ph, &zero);
+      }
+    }
+    if (warp == 1 && lane == 0) {
+      mma_commit(smem_u32(&sh->done));
+      mbar_wait(smem_u32(&sh->done), 0, &zero);
+    }
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  pdl_launch_dependents();
+  // this CTA's share of the tile's rows, for every m; rows fastest
+  const int share = 128 / splits;
+  const int mine = split * share;
+  const float *src[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    src[i] = i < splits ? cluster.map_shared_rank(part, i) : nullptr;
+  for (int e = threadIdx.x; e < share * M; e += THREADS) {
+    const int m = e / share;
+    const int r = mine + e - m * share;
+    if (row0 + r >= rows) continue;
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < splits) z += src[i][m * 128 + r];
+    const int64_t col = row0 + r;
+    z += ld_bias(ep.bias, ep.bias_f32, col);
+    if (ep.pre != nullptr) ep.pre[m * ep.ldp + col] = __float2bfloat16_rn(z);
+    float y = activate(z, ep.act);
+    if (ep.res != nullptr) y += ld_bf16(ep.res + m * ep.ldr + col);
+    ep.out[m * ep.ldo + col] = __float2bfloat16_rn(y);
+  }
+  cluster.sync();  // partial tiles stay alive until every CTA has read them
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(few_cols<kN>)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dz = g * act'(z) in bf16 and the partial column sums of dz (fp32, before the
+// rounding).  A CTA covers 64 columns x kDzRows rows: a warp per row, two
+// columns a lane.
+// ---------------------------------------------------------------------------
+constexpr int kDzRows = 128;
+constexpr int kDzThreads = 256;
+
+__global__ void __launch_bounds__(kDzThreads)
+    dz_kernel(const __nv_bfloat16 *__restrict__ g, int64_t ldg,
+              const __nv_bfloat16 *__restrict__ z, int64_t ldz, int act, int M, int N,
+              __nv_bfloat16 *__restrict__ dz, int64_t lddz, float *__restrict__ partial) {
+  __shared__ float2 sums[kDzThreads / 32][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x * 64 + 2 * lane;
+  const int m0 = blockIdx.y * kDzRows, m1 = min(M, m0 + kDzRows);
+  pdl_wait();
+  float2 s = {0.0f, 0.0f};
+  for (int m = m0 + warp; m < m1; m += kDzThreads / 32) {
+    float d[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (c + i < N) {
+        d[i] = ld_bf16(g + m * ldg + c + i);
+        if (act != SGA_ACT_NONE) d[i] *= activate_grad(ld_bf16(z + m * ldz + c + i), act);
+        if (dz != nullptr) dz[m * lddz + c + i] = __float2bfloat16_rn(d[i]);
+      }
+    }
+    s.x += d[0];
+    s.y += d[1];
+  }
+  pdl_launch_dependents();
+  if (partial == nullptr) return;
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < kDzThreads / 32; ++w) {
+      s.x += sums[w][lane].x;
+      s.y += sums[w][lane].y;
+    }
+    float *q = partial + static_cast<int64_t>(blockIdx.y) * N + c;
+    if (c < N) q[0] = s.x;
+    if (c + 1 < N) q[1] = s.y;
+  }
+}
+
+__global__ void bias_grad_kernel(const float *__restrict__ partial, int n, int N,
+                                 void *__restrict__ db, int f32) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= N) return;
+  float s = 0.0f;
+  for (int i = 0; i < n; ++i) s += partial[static_cast<int64_t>(i) * N + c];
+  if (f32)
+    static_cast<float *>(db)[c] = s;
+  else
+    static_cast<__nv_bfloat16 *>(db)[c] = __float2bfloat16_rn(s);
+}
+
+// ------------------------------------------------------------------ host
+
+// Tensor map over a row-major bf16 [rows, cols] matrix with row stride ld;
+// box = box_rows x 64 columns (one 128-byte swizzled row), zero fill outside.
+bool make_map_ld(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld,
+                 int box_rows) {
+  auto encode = get_encode_fn();
+  if (encode == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * 2)};
+  cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides,
+                box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// One operand of a product: `other` (rows of D, or columns) x `summed`.
+struct Operand {
+  const void *ptr;
+  int64_t ld;
+  bool strided;  // the summed dimension is the strided one
+};
+
+struct Mat {  // D[rows, cols] = sum over `summed` of A B
+  Operand a, b;
+  int64_t rows, cols, summed;
+  Epilogue ep;
+};
+
+bool operand_map(CUtensorMap *map, const Operand &o, int64_t other, int64_t summed, int box) {
+  return o.strided ? make_map_ld(map, o.ptr, summed, other, o.ld, 64)
+                   : make_map_ld(map, o.ptr, other, summed, o.ld, box);
+}
+
+template <int kBN>
+cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cudaStream_t stream) {
+  Maps maps;
+  Products prods = {};
+  prods.n = n;
+  for (int i = 0; i < n; ++i) {
+    const Mat &m = mats[i];
+    Product &p = prods.p[i];
+    p.rows = static_cast<int>(m.rows);
+    p.cols = static_cast<int>(m.cols);
+    p.num_kb = static_cast<int>((m.summed + 63) / 64);
+    p.tiles_r = static_cast<int>((m.rows + 255) / 256);
+    p.tiles_c = static_cast<int>((m.cols + kBN - 1) / kBN);
+    p.a_strided = m.a.strided;
+    p.b_strided = m.b.strided;
+    p.ep = m.ep;
+    prods.tile0[i + 1] = prods.tile0[i] + p.tiles_r * p.tiles_c;
+    if (!operand_map(&maps.a[i], m.a, m.rows, m.summed, 128) ||
+        !operand_map(&maps.b[i], m.b, m.cols, m.summed, kBN / 2))
+      return cudaErrorNotSupported;
+  }
+  for (int i = n; i < kMaxProducts; ++i) {
+    maps.a[i] = maps.a[0];
+    maps.b[i] = maps.b[0];
+  }
+  auto kern = gemm_kernel<kBN>;
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), gemm_smem<kBN>,
+                                      kBN == 256 ? 0 : (kBN == 128 ? 1 : 2));
+  if (e != cudaSuccess) return e;
+  const int pairs = num_sms / 2 < prods.tile0[n] ? num_sms / 2 : prods.tile0[n];
+  return launch_pdl(kern, 2 * pairs, gemm_smem<kBN>, stream, maps, prods, err);
+}
+
+// Columns of a tile: the widest that does not leave SMs idle.  Cost of a
+// width: the waves of pairs times the time of a tile, kBN columns plus about
+// 32 columns' worth of filling and draining the pipeline.
+cudaError_t launch_products(const Mat *mats, int n, int num_sms, uint32_t *err,
+                            cudaStream_t stream) {
+  bool strided = false;
+  int64_t tiles[3] = {0, 0, 0};
+  constexpr int widths[3] = {256, 128, 64};
+  for (int i = 0; i < n; ++i) {
+    strided = strided || mats[i].b.strided;
+    for (int w = 0; w < 3; ++w)
+      tiles[w] += (mats[i].rows + 255) / 256 * ((mats[i].cols + widths[w] - 1) / widths[w]);
+  }
+  int best = 0;
+  int64_t cost = 0;
+  for (int w = 0; w < (strided ? 2 : 3); ++w) {
+    const int64_t pairs = num_sms / 2;
+    const int64_t c = (tiles[w] + pairs - 1) / pairs * (widths[w] + 32);
+    if (w == 0 || c < cost) {
+      best = w;
+      cost = c;
+    }
+  }
+  if (best == 0) return launch_gemm<256>(mats, n, num_sms, err, stream);
+  if (best == 1) return launch_gemm<128>(mats, n, num_sms, err, stream);
+  return launch_gemm<64>(mats, n, num_sms, err, stream);
+}
+
+template <int kN>
+cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream_t stream) {
+  // m: D^T, rows = weight rows, cols = M
+  CUtensorMap map_w, map_x;
+  if (!operand_map(&map_w, m.a, m.rows, m.summed, 128) ||
+      !operand_map(&map_x, m.b, m.cols, m.summed, kN))
+    return cudaErrorNotSupported;
+  const int64_t tiles = (m.rows + 127) / 128;
+  const int num_kb = static_cast<int>((m.summed + 63) / 64);
+  // splits: while every CTA is resident (two per SM) and keeps a few K blocks
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= 2 * num_sms && num_kb >= 4 * splits) splits *= 2;
+  auto kern = few_rows_kernel<kN>;
+  const cudaError_t e =
+      set_smem_once(reinterpret_cast<const void *>(kern), few_smem<kN>,
+                    kN == 16 ? 3 : (kN == 32 ? 4 : (kN == 64 ? 5 : 6)));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = few_smem<kN>;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, static_cast<int>(m.cols),
+                            static_cast<int>(m.rows), num_kb, splits,
+                            static_cast<int>(m.a.strided), m.ep, err);
+}
+
+// out[M, cols] of few rows: the weight becomes the row operand.
+cudaError_t launch_product(const Mat &m, int num_sms, uint32_t *err, cudaStream_t stream) {
+  if (m.rows > 128 || m.a.strided) return launch_products(&m, 1, num_sms, err, stream);
+  const Mat t = {m.b, m.a, m.cols, m.rows, m.summed, m.ep};
+  if (m.rows <= 16) return launch_few_rows<16>(t, num_sms, err, stream);
+  if (m.rows <= 32) return launch_few_rows<32>(t, num_sms, err, stream);
+  if (m.rows <= 64) return launch_few_rows<64>(t, num_sms, err, stream);
+  return launch_few_rows<128>(t, num_sms, err, stream);
+}
+
+int64_t dz_ld(int64_t N) { return (N + 7) / 8 * 8; }
+
+}  // namespace
+
+cudaError_t launch_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const void *weight,
+                          int64_t N, int64_t ldw, const void *bias, int bias_dtype, int act,
+                          const void *residual, int64_t ldr, void *preact, int64_t ldp, void *out,
+                          int64_t ldo, int num_sms, uint32_t *err, cudaStream_t stream) {
+  Mat m = {};
+  m.a = {x, ldx, false};
+  m.b = {weight, ldw, false};
+  m.rows = M;
+  m.cols = N;
+  m.summed = K;
+  m.ep = {static_cast<__nv_bfloat16 *>(out), static_cast<__nv_bfloat16 *>(preact),
+          static_cast<const __nv_bfloat16 *>(residual), bias, ldo, ldp, ldr,
+          bias_dtype == SGA_F32, act};
+  return launch_product(m, num_sms, err, stream);
+}
+
+size_t linear_grad_workspace_bytes(int64_t M, int64_t N) {
+  const int64_t blocks = (M + kDzRows - 1) / kDzRows;
+  return static_cast<size_t>((M * dz_ld(N) * 2 + 15) / 16 * 16 + blocks * N * 4);
+}
+
+cudaError_t launch_linear_grad(const void *grad_out, int64_t M, int64_t N, int64_t ldg,
+                               const void *preact, int64_t ldp, int act, const void *x, int64_t K,
+                               int64_t ldx, const void *weight, int64_t ldw, void *grad_x,
+                               int64_t ldgx, void *grad_weight, int64_t ldgw, void *grad_bias,
+                               int bias_dtype, void *workspace, int num_sms, uint32_t *err,
+                               cudaStream_t stream) {
+  // dz lies where g lies when there is nothing to multiply and TMA can read it
+  const bool direct =
+      act == SGA_ACT_NONE && ldg % 8 == 0 && reinterpret_cast<uintptr_t>(grad_out) % 16 == 0;
+  const int64_t blocks = (M + kDzRows - 1) / kDzRows;
+  auto *dz = static_cast<__nv_bfloat16 *>(workspace);
+  float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                             (M * dz_ld(N) * 2 + 15) / 16 * 16);
+  cudaError_t e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (!direct || grad_bias != nullptr) {
+    cfg.gridDim = dim3(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kDzThreads);
+    e = cudaLaunchKernelEx(&cfg, dz_kernel, static_cast<const __nv_bfloat16 *>(grad_out), ldg,
+                           static_cast<const __nv_bfloat16 *>(preact), ldp, act,
+                           static_cast<int>(M), static_cast<int>(N),
+                           direct ? static_cast<__nv_bfloat16 *>(nullptr) : dz, dz_ld(N),
+                           grad_bias != nullptr ? partial : static_cast<float *>(nullptr));
+    if (e != cudaSuccess) return e;
+  }
+  if (grad_bias != nullptr) {
+    cfg.gridDim = dim3(static_cast<unsigned>((N + 127) / 128));
+    cfg.blockDim = dim3(128);
+    e = cudaLaunchKernelEx(&cfg, bias_grad_kernel, static_cast<const float *>(partial),
+                           static_cast<int>(blocks), static_cast<int>(N), grad_bias,
+                           static_cast<int>(bias_dtype == SGA_F32));
+    if (e != cudaSuccess) return e;
+  }
+  const Operand d = direct ? Operand{grad_out, ldg, false} : Operand{dz, dz_ld(N), false};
+  Mat mats[2] = {};
+  int n = 0;
+  if (grad_x != nullptr) {
+    Mat &m = mats[n++];
+    m.a = d;
+    m.b = {weight, ldw, true};
+    m.rows = M;
+    m.cols = K;
+    m.summed = N;
+    m.ep.out = static_cast<__nv_bfloat16 *>(grad_x);
+    m.ep.ldo = ldgx;
+    if (M <= 128) {
+      e = launch_product(m, num_sms, err, stream);
+      if (e != cudaSuccess) return e;
+      n = 0;
+    }
+  }
+  if (grad_weight != nullptr) {
+    Mat &m = mats[n++];
+    m = Mat{};
+    m.a = {d.ptr, d.ld, true};
+    m.b = {x, ldx, true};
+    m.rows = N;
+    m.cols = K;
+    m.summed = M;
+    m.ep.out = static_cast<__nv_bfloat16 *>(grad_weight);
+    m.ep.ldo = ldgw;
+  }
+  return n > 0 ? launch_products(mats, n, num_sms, err, stream) : cudaSuccess;
+}
+
+}  // namespace sga

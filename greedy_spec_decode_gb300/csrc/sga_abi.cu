@@ -464,6 +464,88 @@ int sga_lmhead_argmax_noalloc(const void *hidden, int64_t M, int64_t H,
   return launch_status(e);
 }
 
+// Checks that sga_linear and its gradient share.
+static int check_linear(int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw, int act,
+                        const void *bias, int bias_dtype) {
+  if (M < 0 || M > (int64_t(1) << 20) || N < 1 || N > SGA_MAX_VOCAB) return SGA_ERR_SIZE;
+  if (K < 8 || K % 8 != 0 || K > (int64_t(1) << 20)) return SGA_ERR_SIZE;
+  if (ldx < K || ldx % 8 != 0 || ldw < K || ldw % 8 != 0) return SGA_ERR_SIZE;
+  if (act < SGA_ACT_NONE || act > SGA_ACT_GELU_TANH) return SGA_ERR_UNSUPPORTED;
+  if (bias != nullptr && bias_dtype != SGA_F32 && bias_dtype != SGA_BF16) return SGA_ERR_DTYPE;
+  return SGA_OK;
+}
+
+static uintptr_t bias_align(int bias_dtype) { return bias_dtype == SGA_F32 ? 4 : 2; }
+
+int sga_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const void *weight, int64_t N,
+               int64_t ldw, const void *bias, int bias_dtype, int act, const void *residual,
+               int64_t ldr, void *out_preact, int64_t ldp, void *out, int64_t ldo,
+               sga_stream stream) {
+  int st = check_linear(M, N, K, ldx, ldw, act, bias, bias_dtype);
+  if (st != SGA_OK) return st;
+  if (ldo < N || (residual != nullptr && ldr < N) || (out_preact != nullptr && ldp < N))
+    return SGA_ERR_SIZE;
+  if (M == 0) return SGA_OK;
+  if (x == nullptr || weight == nullptr || out == nullptr) return SGA_ERR_NULL;
+  if (misaligned(x, 16) || misaligned(weight, 16) || misaligned(residual, 2) ||
+      misaligned(out_preact, 2) || misaligned(out, 2) ||
+      misaligned(bias, bias_align(bias_dtype)))
+    return SGA_ERR_ALIGN;
+  DeviceInfo d;
+  if ((st = current_device(&d)) != SGA_OK) return st;
+  const cudaError_t e = sga::launch_linear(x, M, K, ldx, weight, N, ldw, bias, bias_dtype, act,
+                                           residual, ldr, out_preact, ldp, out, ldo, d.num_sms,
+                                           d.err, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return SGA_ERR_UNSUPPORTED;
+  return launch_status(e);
+}
+
+size_t sga_linear_grad_workspace(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return sga::linear_grad_workspace_bytes(M, N);
+}
+
+int sga_linear_grad(const void *grad_out, int64_t M, int64_t N, int64_t ldg, const void *preact,
+                    int64_t ldp, int act, const void *x, int64_t K, int64_t ldx,
+                    const void *weight, int64_t ldw, void *grad_x, int64_t ldgx,
+                    void *grad_weight, int64_t ldgw, void *grad_bias, int bias_dtype,
+                    void *workspace, size_t workspace_bytes, sga_stream stream) {
+  int st = check_linear(M, N, K, ldx, ldw, act, grad_bias, bias_dtype);
+  if (st != SGA_OK) return st;
+  if (ldg < N || (preact != nullptr && ldp < N) || (grad_x != nullptr && ldgx < K) ||
+      (grad_weight != nullptr && ldgw < K))
+    return SGA_ERR_SIZE;
+  if (misaligned(grad_x, 2) || misaligned(grad_weight, 2) ||
+      misaligned(grad_bias, bias_align(bias_dtype)))
+    return SGA_ERR_ALIGN;
+  DeviceInfo d;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {  // sums over no rows
+    if (grad_weight == nullptr && grad_bias == nullptr) return SGA_OK;
+    if ((st = current_device(&d)) != SGA_OK) return st;
+    if (grad_weight != nullptr &&
+        cudaMemset2DAsync(grad_weight, ldgw * 2, 0, K * 2, N, s) != cudaSuccess)
+      return SGA_ERR_CUDA;
+    if (grad_bias != nullptr &&
+        cudaMemsetAsync(grad_bias, 0, N * bias_align(bias_dtype), s) != cudaSuccess)
+      return SGA_ERR_CUDA;
+    return SGA_OK;
+  }
+  if (grad_out == nullptr || x == nullptr || weight == nullptr || workspace == nullptr ||
+      (act != SGA_ACT_NONE && preact == nullptr))
+    return SGA_ERR_NULL;
+  if (misaligned(grad_out, 2) || misaligned(preact, 2) || misaligned(x, 16) ||
+      misaligned(weight, 16) || misaligned(workspace, 16))
+    return SGA_ERR_ALIGN;
+  if (workspace_bytes < sga::linear_grad_workspace_bytes(M, N)) return SGA_ERR_WORKSPACE;
+  if ((st = current_device(&d)) != SGA_OK) return st;
+  const cudaError_t e = sga::launch_linear_grad(
+      grad_out, M, N, ldg, preact, ldp, act, x, K, ldx, weight, ldw, grad_x, ldgx, grad_weight,
+      ldgw, grad_bias, bias_dtype, workspace, d.num_sms, d.err, s);
+  if (e == cudaErrorNotSupported) return SGA_ERR_UNSUPPORTED;
+  return launch_status(e);
+}
+
 int sga_token_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
                        int64_t org_vocab, const int32_t *tokens, int top_k, float *out_logprob,
                        float *out_entropy, float *out_lse, int32_t *out_top_ids,

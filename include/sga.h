@@ -457,6 +457,71 @@ int sga_lmhead_argmax_noalloc(const void *hidden, int64_t M, int64_t H,
                               sga_stream stream);
 
 /*
+ * sga_linear -- matrix product with bias, activation and residual in its
+ * epilogue, on the tensor cores (bf16 operands, fp32 accumulation):
+ *   z = x . weight^T + bias,   out = act(z) + residual.
+ * A draft head is out = x + act(weight x + bias) in front of the LM head;
+ * the LM head's logits themselves are the product alone.  (The pages take
+ * hidden states and logits as given; this is the library's extension.)
+ *
+ *   x            device bf16 [M, K], row stride ldx >= K elements.
+ *   weight       device bf16 [N, K], row stride ldw >= K elements.
+ *                x and weight 16-byte aligned, ldx, ldw and K multiples of 8.
+ *   M            0 .. 1048576 (0: nothing enqueued).
+ *   N            1 .. SGA_MAX_VOCAB.    K   8 .. 1048576.
+ *   bias         device fp32 or bf16 [N] (bias_dtype), nullable.
+ *   act          one of enum sga_act.
+ *   residual     device bf16 [M, N], row stride ldr >= N, nullable.
+ *   out_preact   device bf16 [M, N], row stride ldp >= N, nullable: z, which
+ *                sga_linear_grad needs when there is an activation.
+ *   out          device bf16 [M, N], row stride ldo >= N.  May be the residual
+ *                buffer itself (ldo == ldr); any other overlap is not allowed.
+ * residual, out_preact, out: 2-byte aligned, any stride.  z is rounded to bf16
+ * for out_preact only; out is rounded once.  Errors: SGA_ERR_SIZE (sizes and
+ * strides), SGA_ERR_UNSUPPORTED (act), SGA_ERR_DTYPE (bias_dtype),
+ * SGA_ERR_NULL, SGA_ERR_ALIGN.  One kernel launch, no workspace.
+ */
+enum sga_act {
+  SGA_ACT_NONE = 0,
+  SGA_ACT_RELU = 1,
+  SGA_ACT_SILU = 2,     /* z / (1 + e^-z) */
+  SGA_ACT_GELU = 3,     /* z (1 + erf(z / sqrt 2)) / 2 */
+  SGA_ACT_GELU_TANH = 4 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+};
+int sga_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const void *weight, int64_t N,
+               int64_t ldw, const void *bias, int bias_dtype, int act, const void *residual,
+               int64_t ldr, void *out_preact, int64_t ldp, void *out, int64_t ldo,
+               sga_stream stream);
+
+/*
+ * sga_linear_grad -- gradient of sga_linear: with g the gradient of out,
+ *   dz = g act'(z),  grad_x = dz . weight,  grad_weight = dz^T . x,
+ *   grad_bias = sum over rows of dz          (the residual's gradient is g).
+ * relu's slope at 0 is 0.
+ *
+ *   grad_out     device bf16 [M, N], row stride ldg >= N, 2-byte aligned.
+ *   preact       device bf16 [M, N], row stride ldp >= N, 2-byte aligned: z
+ *                from the forward pass; may be NULL iff act is SGA_ACT_NONE.
+ *   x, weight    as sga_linear (both are always given).
+ *   grad_x       device bf16 [M, K], row stride ldgx >= K, nullable.
+ *   grad_weight  device bf16 [N, K], row stride ldgw >= K, nullable.
+ *   grad_bias    device fp32 or bf16 [N] (bias_dtype), nullable; summed in
+ *                fp32 from unrounded dz, in a fixed order.
+ *   workspace    device, >= sga_linear_grad_workspace(M, N, K) bytes, 16-byte
+ *                aligned; contents on entry are ignored; not to be used by two
+ *                calls at once.
+ * dz is rounded to bf16 as the products' operand.  M = 0 writes zeros to
+ * grad_weight and grad_bias.  No output may overlap an input.  Errors as
+ * sga_linear, and SGA_ERR_WORKSPACE.
+ */
+size_t sga_linear_grad_workspace(int64_t M, int64_t N, int64_t K);
+int sga_linear_grad(const void *grad_out, int64_t M, int64_t N, int64_t ldg, const void *preact,
+                    int64_t ldp, int act, const void *x, int64_t K, int64_t ldx,
+                    const void *weight, int64_t ldw, void *grad_x, int64_t ldgx,
+                    void *grad_weight, int64_t ldgw, void *grad_bias, int bias_dtype,
+                    void *workspace, size_t workspace_bytes, sga_stream stream);
+
+/*
  * sga_token_logprobs -- log probabilities of given tokens over a whole
  * vocabulary, with each row's entropy and best alternatives: what a server
  * reports beside the greedy ids, and the loss of a draft model in training.
