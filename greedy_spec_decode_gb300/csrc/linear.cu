@@ -24,6 +24,48 @@ namespace cg = cooperative_groups;
 namespace sga {
 namespace {
 
+// mbar_wait that sleeps in the barrier unit (try_wait with a time hint)
+// between looks at the clock and the abort flag.
+__device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity,
+                                          const volatile int *abort_flag) {
+  unsigned long long t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    const unsigned long long t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// True in one lane of a converged warp.  The producer and MMA warps run their
+// loops with all lanes and elect one around each issue: the operands of TMA
+// and MMA instructions then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The abort flag as the whole warp sees it.
+__device__ __forceinline__ bool aborted(const volatile int *abort_flag) {
+  return __any_sync(0xffffffffu, *abort_flag != 0) != 0;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // ------------------------------------------------------------- activations
 
 __device__ __forceinline__ float sigmoid_times(float z, float u) {  // z / (1 + e^-u)
@@ -88,6 +130,7 @@ struct Epilogue {
   const void *bias;
   int64_t ldo, ldp, ldr;
   int bias_f32, act;
+  int tma_out, tma_pre, tma_res;  // gemm_kernel: TMA can reach the matrix
 };
 
 // ------------------------------------------------------------- descriptors
@@ -133,7 +176,7 @@ __device__ __forceinline__ void mma_one_rt(uint32_t d_tmem, uint64_t a_desc, uin
 
 // ---------------------------------------------------------------------------
 // gemm_kernel: warp 0 TMA producer, warp 1 MMA issuer (leader CTA of the
-// pair), warps 2..5 epilogue; the same roles and barriers as the LM-head
+// pair), warps 2..9 epilogue; the roles and barriers are those of the LM-head
 // kernel of lmhead.cu.  A launch runs one or two products (dx and dW of one
 // gradient): their tiles form one list, so the second fills the SMs that the
 // first one's last wave leaves idle.
@@ -155,19 +198,22 @@ struct Products {
 
 struct Maps {
   CUtensorMap a[kMaxProducts], b[kMaxProducts];
+  CUtensorMap out[kMaxProducts], pre[kMaxProducts], res[kMaxProducts];  // 32 x 64 boxes
 };
 
+constexpr int kGemmThreads = 320;        // producer, MMA, eight epilogue warps
+constexpr int kEpiWarps = 8;
 constexpr int kTileA = 128 * ROW_BYTES;  // 16 KB: this CTA's 128 rows of A
 template <int kBN>
 constexpr int tile_b = kBN / 2 * ROW_BYTES;  // this CTA's half of B
 template <int kBN>
 constexpr int gemm_stage = kTileA + tile_b<kBN>;
-constexpr int kEpiPitch = 33;                               // floats; conflict-free both ways
-constexpr int kEpiBytes = 4 * 32 * kEpiPitch * 4;           // one 32 x 32 square per warp
+constexpr int kBox = 32 * ROW_BYTES;         // 32 rows x 64 columns of results
+constexpr int kEpiBytes = kEpiWarps * kBox;  // one box per epilogue warp
 template <int kBN>
-constexpr int gemm_stages = (227 * 1024 - 2048 - kEpiBytes) / gemm_stage<kBN>;
+constexpr int gemm_stages = (227 * 1024 - 2560 - kEpiBytes) / gemm_stage<kBN>;
 template <int kBN>
-constexpr int gemm_smem = 1024 + gemm_stages<kBN> * gemm_stage<kBN> + kEpiBytes + 512;
+constexpr int gemm_smem = 1024 + gemm_stages<kBN> * gemm_stage<kBN> + kEpiBytes + 1536;
 
 template <int kBN>
 struct SharedGemm {
@@ -175,10 +221,13 @@ struct SharedGemm {
   uint64_t empty[gemm_stages<kBN>];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
+  uint64_t res_full[kEpiWarps];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  alignas(16) float bias[kBN];  // the tile's
 };
+static_assert(sizeof(SharedGemm<256>) <= 1536 && sizeof(SharedGemm<64>) <= 1536, "shared block");
 
 __device__ __forceinline__ void raise_abort(int *flag, uint32_t *err) {
   *reinterpret_cast<volatile int *>(flag) = 1;
@@ -196,64 +245,122 @@ __device__ __forceinline__ void tile_at(const Product &p, int t, int &tr, int &t
   tr = band * kBand + in - tc * height;
 }
 
-// The epilogue of one 32-row x 32-column square whose accumulators lie in
-// `sq` (row-major, pitch kEpiPitch): half a warp per row, two columns a lane,
-// so that global rows are read and written in 64-byte runs.
-__device__ __forceinline__ void square_epilogue(const Epilogue &ep, const float *sq, int64_t row0,
-                                                int rows, int64_t col0, int cols, int lane) {
-  const int c = 2 * (lane & 15);
-  const int64_t col = col0 + c;
-  const bool has0 = c < cols, has1 = c + 1 < cols;
-  const float b0 = has0 ? ld_bias(ep.bias, ep.bias_f32, col) : 0.0f;
-  const float b1 = has1 ? ld_bias(ep.bias, ep.bias_f32, col + 1) : 0.0f;
-  const bool wide_out = has1 && ((reinterpret_cast<uintptr_t>(ep.out) | (2 * ep.ldo)) & 3) == 0;
-  const bool wide_pre = has1 && ((reinterpret_cast<uintptr_t>(ep.pre) | (2 * ep.ldp)) & 3) == 0;
-  const bool wide_res = has1 && ((reinterpret_cast<uintptr_t>(ep.res) | (2 * ep.ldr)) & 3) == 0;
-  float r0[16], r1[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = 2 * i + (lane >> 4);
-    r0[i] = r1[i] = 0.0f;
-    if (ep.res != nullptr && r < rows && has0) {
-      const __nv_bfloat16 *q = ep.res + (row0 + r) * ep.ldr + col;
-      if (wide_res) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(q);
-        r0[i] = bf16_lo(w);
-        r1[i] = bf16_hi(w);
-      } else {
-        r0[i] = ld_bf16(q);
-        if (has1) r1[i] = ld_bf16(q + 1);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = 2 * i + (lane >> 4);
-    if (r < rows && has0) {
-      const float z0 = sq[r * kEpiPitch + c] + b0, z1 = sq[r * kEpiPitch + c + 1] + b1;
-      if (ep.pre != nullptr) {
-        __nv_bfloat16 *q = ep.pre + (row0 + r) * ep.ldp + col;
-        if (wide_pre) {
-          *reinterpret_cast<uint32_t *>(q) = pack2(z0, z1);
-        } else {
-          q[0] = __float2bfloat16_rn(z0);
-          if (has1) q[1] = __float2bfloat16_rn(z1);
-        }
-      }
-      const float y0 = activate(z0, ep.act) + r0[i], y1 = activate(z1, ep.act) + r1[i];
-      __nv_bfloat16 *q = ep.out + (row0 + r) * ep.ldo + col;
-      if (wide_out) {
-        *reinterpret_cast<uint32_t *>(q) = pack2(y0, y1);
-      } else {
-        q[0] = __float2bfloat16_rn(y0);
-        if (has1) q[1] = __float2bfloat16_rn(y1);
-      }
+// A warp's box of results in shared memory: 32 rows of 64 bf16, in the
+// 128-byte swizzle of the tensor maps (16-byte piece j of row r at piece j ^
+// (r & 7)), so that a lane per row writes it without bank conflicts.
+__device__ __forceinline__ uint4 *box_piece(uint8_t *box, int r, int j) {
+  return reinterpret_cast<uint4 *>(box + r * ROW_BYTES + ((j ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void box_store_tma(const CUtensorMap *map, uint32_t box, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(box)
+      : "memory");
+}
+
+// Where TMA cannot go (rows not on 16-byte boundaries): a row at a time, two
+// columns a lane, eight rows in flight.
+__device__ __forceinline__ void box_store_rows(uint8_t *box, __nv_bfloat16 *p, int64_t ld, int rows,
+                                               int cols, int lane) {
+  const int c = 2 * lane;
+  const bool pair = ((reinterpret_cast<uintptr_t>(p) | (2 * ld)) & 3) == 0 && c + 1 < cols;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r) {
+    const uint32_t w = *(reinterpret_cast<const uint32_t *>(box_piece(box, r, lane >> 2)) +
+                         (lane & 3));
+    if (r >= rows) continue;
+    unsigned short *q = reinterpret_cast<unsigned short *>(p + r * ld + c);
+    if (pair) {
+      *reinterpret_cast<uint32_t *>(q) = w;
+    } else {
+      if (c < cols) q[0] = static_cast<unsigned short>(w);
+      if (c + 1 < cols) q[1] = static_cast<unsigned short>(w >> 16);
     }
   }
 }
 
+__device__ __forceinline__ void box_load_rows(uint8_t *box, const __nv_bfloat16 *p, int64_t ld,
+                                              int rows, int cols, int lane) {
+  const int c = 2 * lane;
+  const bool pair = ((reinterpret_cast<uintptr_t>(p) | (2 * ld)) & 3) == 0 && c + 1 < cols;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + i;
+      const unsigned short *q = reinterpret_cast<const unsigned short *>(p + r * ld + c);
+      w[i] = 0;
+      if (r < rows) {
+        if (pair) {
+          w[i] = *reinterpret_cast<const uint32_t *>(q);
+        } else {
+          if (c < cols) w[i] = q[0];
+          if (c + 1 < cols) w[i] |= static_cast<uint32_t>(q[1]) << 16;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *(reinterpret_cast<uint32_t *>(box_piece(box, r0 + i, lane >> 2)) + (lane & 3)) = w[i];
+  }
+}
+
+// Accumulators -> box: columns taddr .. + 63 of this warp's 32 TMEM lanes (a
+// lane per row), plus bias, through the activation, plus what the box holds
+// when `add` (the residual).  32 columns at a time: unrolled further, the
+// longer activations outgrow the instruction cache.
+template <int kAct>
+__device__ __forceinline__ void box_fill_act(uint8_t *box, uint32_t taddr, const float *bias,
+                                             bool add, int lane) {
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r[32];
+    tmem_ld32(taddr + h * 32, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 *q = box_piece(box, lane, h * 4 + j);
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        const float4 b = *reinterpret_cast<const float4 *>(bias + h * 32 + j * 8 + i);
+        y[i] = activate(__uint_as_float(r[j * 8 + i]) + b.x, kAct);
+        y[i + 1] = activate(__uint_as_float(r[j * 8 + i + 1]) + b.y, kAct);
+        y[i + 2] = activate(__uint_as_float(r[j * 8 + i + 2]) + b.z, kAct);
+        y[i + 3] = activate(__uint_as_float(r[j * 8 + i + 3]) + b.w, kAct);
+      }
+      if (add) {
+        const uint4 w = *q;
+        y[0] += bf16_lo(w.x);
+        y[1] += bf16_hi(w.x);
+        y[2] += bf16_lo(w.y);
+        y[3] += bf16_hi(w.y);
+        y[4] += bf16_lo(w.z);
+        y[5] += bf16_hi(w.z);
+        y[6] += bf16_lo(w.w);
+        y[7] += bf16_hi(w.w);
+      }
+      *q = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+    }
+  }
+}
+
+__device__ __forceinline__ void box_fill(uint8_t *box, uint32_t taddr, const float *bias, int act,
+                                         bool add, int lane) {
+  switch (act) {
+    case SGA_ACT_RELU: return box_fill_act<SGA_ACT_RELU>(box, taddr, bias, add, lane);
+    case SGA_ACT_SILU: return box_fill_act<SGA_ACT_SILU>(box, taddr, bias, add, lane);
+    case SGA_ACT_GELU: return box_fill_act<SGA_ACT_GELU>(box, taddr, bias, add, lane);
+    case SGA_ACT_GELU_TANH: return box_fill_act<SGA_ACT_GELU_TANH>(box, taddr, bias, add, lane);
+    default: return box_fill_act<SGA_ACT_NONE>(box, taddr, bias, add, lane);
+  }
+}
+
 template <int kBN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Products prods,
                 uint32_t *err) {
   constexpr int kStages = gemm_stages<kBN>;
@@ -262,13 +369,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float *epi = reinterpret_cast<float *>(base + kStages * kStageB);
+  uint8_t *boxes = base + kStages * kStageB;
   SharedGemm<kBN> *sh =
       reinterpret_cast<SharedGemm<kBN> *>(base + kStages * kStageB + kEpiBytes);
   const volatile int *abort_flag = &sh->abort;
-  const int warp = threadIdx.x >> 5;
+  const int warp = uniform(threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = uniform(cluster_rank());
   const bool leader = rank == 0;
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int num_pairs = static_cast<int>(gridDim.x >> 1);
@@ -281,8 +388,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sh->tmem_full[b]), 1);
-      mbar_init(smem_u32(&sh->tmem_empty[b]), 8);
+      mbar_init(smem_u32(&sh->tmem_empty[b]), 2 * kEpiWarps);
     }
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(smem_u32(&sh->res_full[w]), 1);
     mbar_init(smem_u32(&sh->drain), 1);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -298,44 +406,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   tc_fence_before();
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   tc_fence_after();
-  const uint32_t tmem_base = sh->tmem_base;
+  const uint32_t tmem_base = uniform(sh->tmem_base);
   pdl_wait();
 
   int prod_stage = 0;
   uint32_t prod_phase = 0;
   long long issued = 0;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // -------------------------------------------------- producer (both CTAs)
     int pi = 0;
-    for (int t = pair; t < total && !*abort_flag; t += num_pairs) {
+    for (int t = pair; t < total && !aborted(abort_flag); t += num_pairs) {
       while (t >= prods.tile0[pi + 1]) ++pi;
       const Product &p = prods.p[pi];
       int tr, tc;
       tile_at(p, t - prods.tile0[pi], tr, tc);
       const int row = tr * 256 + static_cast<int>(rank) * 128;
       const int col = tc * kBN + static_cast<int>(rank) * (kBN / 2);
-      for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!mbar_wait(smem_u32(&sh->empty[prod_stage]), prod_phase ^ 1, abort_flag)) {
-          raise_abort(&sh->abort, err);
+      // held in registers: inside the loop the asm statements would make the
+      // compiler read the table again for every K block
+      const int num_kb = p.num_kb;
+      const bool a_strided = p.a_strided != 0, b_strided = p.b_strided != 0;
+      const CUtensorMap *map_a = &maps.a[pi], *map_b = &maps.b[pi];
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!__all_sync(0xffffffffu, pipe_wait(smem_u32(&sh->empty[prod_stage]), prod_phase ^ 1,
+                                               abort_flag))) {
+          if (lane == 0) raise_abort(&sh->abort, err);
           break;
         }
         const uint32_t full = map_to_rank(smem_u32(&sh->full[prod_stage]), 0);
-        if (leader) mbar_expect_tx(smem_u32(&sh->full[prod_stage]), 2 * kStageB);
-        const uint32_t a = smem_u32(base + prod_stage * kStageB);
-        if (p.a_strided) {
-          tma_load_2d_pair(a, &maps.a[pi], row, kb * 64, full);
-          tma_load_2d_pair(a + 8192, &maps.a[pi], row + 64, kb * 64, full);
-        } else {
-          tma_load_2d_pair(a, &maps.a[pi], kb * 64, row, full);
-        }
-        if (p.b_strided) {
+        if (elect_one()) {
+          if (leader) mbar_expect_tx(smem_u32(&sh->full[prod_stage]), 2 * kStageB);
+          const uint32_t a = smem_u32(base + prod_stage * kStageB);
+          if (a_strided) {
+            tma_load_2d_pair(a, map_a, row, kb * 64, full);
+            tma_load_2d_pair(a + 8192, map_a, row + 64, kb * 64, full);
+          } else {
+            tma_load_2d_pair(a, map_a, kb * 64, row, full);
+          }
+          if (b_strided) {
 #pragma unroll
-          for (int i = 0; i < kBN / 128; ++i)
-            tma_load_2d_pair(a + kTileA + i * 8192, &maps.b[pi], col + i * 64, kb * 64, full);
-        } else {
-          tma_load_2d_pair(a + kTileA, &maps.b[pi], kb * 64, col, full);
+            for (int i = 0; i < kBN / 128; ++i)
+              tma_load_2d_pair(a + kTileA + i * 8192, map_b, col + i * 64, kb * 64, full);
+          } else {
+            tma_load_2d_pair(a + kTileA, map_b, kb * 64, col, full);
+          }
         }
+        __syncwarp();
         ++issued;
         if (++prod_stage == kStages) {
           prod_stage = 0;
@@ -343,98 +460,183 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     }
-  } else if (warp == 1 && lane == 0 && leader) {
+  } else if (warp == 1 && leader) {
     // --------------------------------------------------- MMA issuer (leader)
     int stage = 0, acc = 0, pi = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    for (int t = pair; t < total && ok && !*abort_flag; t += num_pairs) {
+    for (int t = pair; t < total && ok && !aborted(abort_flag); t += num_pairs) {
       while (t >= prods.tile0[pi + 1]) ++pi;
       const Product &p = prods.p[pi];
-      const uint32_t idesc = operand_idesc(256, kBN, p.a_strided, p.b_strided);
-      const uint32_t step_a = k_step(p.a_strided), step_b = k_step(p.b_strided);
-      if (!mbar_wait(smem_u32(&sh->tmem_empty[acc]), acc_phase ^ 1, abort_flag)) {
-        raise_abort(&sh->abort, err);
+      const int num_kb = p.num_kb;
+      const bool a_strided = p.a_strided != 0, b_strided = p.b_strided != 0;
+      const uint32_t idesc = operand_idesc(256, kBN, a_strided, b_strided);
+      const uint32_t step_a = k_step(a_strided), step_b = k_step(b_strided);
+      if (!__all_sync(0xffffffffu, pipe_wait(smem_u32(&sh->tmem_empty[acc]), acc_phase ^ 1,
+                                             abort_flag))) {
+        if (lane == 0) raise_abort(&sh->abort, err);
         break;
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * kBN;
-      for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!mbar_wait(smem_u32(&sh->full[stage]), phase, abort_flag)) {
-          raise_abort(&sh->abort, err);
+      for (int kb = 0; kb < num_kb; ++kb) {
+        if (!__all_sync(0xffffffffu, pipe_wait(smem_u32(&sh->full[stage]), phase, abort_flag))) {
+          if (lane == 0) raise_abort(&sh->abort, err);
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t a = smem_u32(base + stage * kStageB);
-        const uint64_t a_desc = operand_desc(a, p.a_strided);
-        const uint64_t b_desc = operand_desc(a + kTileA, p.b_strided);
+        const uint64_t a_desc = operand_desc(a, a_strided);
+        const uint64_t b_desc = operand_desc(a + kTileA, b_strided);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_pair_rt(d_tmem, a_desc + step_a * kk, b_desc + step_b * kk, idesc, (kb | kk) != 0);
-        mma_commit_pair(smem_u32(&sh->empty[stage]));
+          for (int kk = 0; kk < 4; ++kk)
+            mma_pair_rt(d_tmem, a_desc + step_a * kk, b_desc + step_b * kk, idesc, (kb | kk) != 0);
+          mma_commit_pair(smem_u32(&sh->empty[stage]));
+        }
+        __syncwarp();
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
-      mma_commit_pair(smem_u32(&sh->tmem_full[acc]));
+      if (elect_one()) mma_commit_pair(smem_u32(&sh->tmem_full[acc]));
+      __syncwarp();
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
   } else if (warp >= 2) {
     // -------------------------------------------------- epilogue (both CTAs)
+    // Warps 2..5 and 6..9 each cover the four TMEM lane quarters and take the
+    // tile's 64-column pieces alternately.
     const int quarter = warp & 3;
-    float *sq = epi + quarter * 32 * kEpiPitch;
+    const int half = warp >= 6;
+    uint8_t *box = boxes + (warp - 2) * kBox;
+    const uint32_t box_u32 = smem_u32(box);
+    const uint32_t res_bar = smem_u32(&sh->res_full[warp - 2]);
     const uint32_t empty_leader[2] = {map_to_rank(smem_u32(&sh->tmem_empty[0]), 0),
                                       map_to_rank(smem_u32(&sh->tmem_empty[1]), 0)};
     int acc = 0, pi = 0;
-    uint32_t acc_phase = 0;
-    for (int t = pair; t < total; t += num_pairs) {
+    uint32_t acc_phase = 0, res_phase = 0;
+    bool ok = true, res_inflight = false;
+    for (int t = pair; t < total && ok; t += num_pairs) {
       while (t >= prods.tile0[pi + 1]) ++pi;
       const Product &p = prods.p[pi];
       int tr, tc;
       tile_at(p, t - prods.tile0[pi], tr, tc);
-      const bool ok = __all_sync(
-          0xffffffffu, mbar_wait(smem_u32(&sh->tmem_full[acc]), acc_phase, abort_flag));
-      if (!ok) {
-        if (lane == 0) raise_abort(&sh->abort, err);
-        break;
-      }
-      tc_fence_after();
-      const int64_t row0 = tr * 256 + static_cast<int>(rank) * 128 + quarter * 32;
-      const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.rows - row0));
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN;
-#pragma unroll 1
-      for (int q = 0; q < kBN / 32; ++q) {
-        uint32_t r[32];
-        tmem_ld32(taddr + q * 32, r);
-        tmem_ld_wait();
-        if (q == kBN / 32 - 1) {
-          // the accumulator is in registers: the MMA may overwrite it
-          tc_fence_before();
+      const Epilogue ep = p.ep;
+      const int cols = p.cols;
+      const int row0 = tr * 256 + static_cast<int>(rank) * 128 + quarter * 32;
+      const int rows = min(32, p.rows - row0);
+      const CUtensorMap *map_out = &maps.out[pi], *map_pre = &maps.pre[pi],
+                        *map_res = &maps.res[pi];
+      // the tile's bias, once every warp is done with the last tile's
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      for (int c = threadIdx.x - 64; c < kBN; c += 32 * kEpiWarps)
+        sh->bias[c] = tc * kBN + c < cols
+                          ? ld_bias(ep.bias, ep.bias_f32, static_cast<int64_t>(tc) * kBN + c)
+                          : 0.0f;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      // fills the box with the residual; true when TMA does (wait on res_bar)
+      auto load_res = [&](int col0) {
+        if (ep.tma_res) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) {
-            if (leader)
-              mbar_arrive(smem_u32(&sh->tmem_empty[acc]));
-            else
-              mbar_arrive_remote(empty_leader[acc]);
+          if (elect_one()) {
+            mbar_expect_tx(res_bar, kBox);
+            tma_load_2d(box_u32, map_res, col0, row0, res_bar);
           }
+          res_inflight = true;
+        } else {
+          box_load_rows(box, ep.res + row0 * ep.ldr + col0, ep.ldr, rows, cols - col0, lane);
         }
-        const int64_t col0 = static_cast<int64_t>(tc) * kBN + q * 32;
-        if (rows > 0 && col0 < p.cols) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sq[lane * kEpiPitch + i] = __uint_as_float(r[i]);
+        __syncwarp();
+      };
+      // waits until the last store from the box has been read out of it
+      auto box_free = [&]() {
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+      };
+      auto store = [&](bool tma, const CUtensorMap *map, __nv_bfloat16 *q, int64_t ld, int col0) {
+        if (tma) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          square_epilogue(p.ep, sq, row0, rows, col0,
-                          static_cast<int>(min(static_cast<int64_t>(32), p.cols - col0)), lane);
+          if (elect_one()) box_store_tma(map, box_u32, col0, row0);
+        } else {
           __syncwarp();
+          box_store_rows(box, q + row0 * ld + col0, ld, rows, cols - col0, lane);
+        }
+        __syncwarp();
+      };
+      const int first = tc * kBN + half * 64;
+      const bool any = rows > 0 && half * 64 < kBN && first < cols;
+      bool res_ready = false;  // asked for ahead of the accumulators
+      if (any && ep.res != nullptr && ep.pre == nullptr) {
+        box_free();
+        load_res(first);
+        res_ready = true;
+      }
+      ok = __all_sync(0xffffffffu,
+                      pipe_wait(smem_u32(&sh->tmem_full[acc]), acc_phase, abort_flag));
+      if (!ok && lane == 0) raise_abort(&sh->abort, err);
+      if (ok) {
+        tc_fence_after();
+        const uint32_t tlane =
+            tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN;
+#pragma unroll 1
+        for (int q = half * 64; q < kBN; q += 128) {
+          const int col0 = tc * kBN + q;
+          if (rows <= 0 || col0 >= cols) break;
+          if (!res_ready) box_free();
+          if (ep.pre != nullptr) {
+            box_fill_act<SGA_ACT_NONE>(box, tlane + q, sh->bias + q, false, lane);
+            store(ep.tma_pre, map_pre, ep.pre, ep.ldp, col0);
+            box_free();
+          }
+          if (ep.res != nullptr) {
+            if (!res_ready) load_res(col0);
+            res_ready = false;
+            if (ep.tma_res) {
+              ok = __all_sync(0xffffffffu, pipe_wait(res_bar, res_phase, abort_flag));
+              if (!ok) {
+                if (lane == 0) raise_abort(&sh->abort, err);
+                break;
+              }
+              res_inflight = false;
+              res_phase ^= 1;
+            }
+          }
+          box_fill(box, tlane + q, sh->bias + q, ep.act, ep.res != nullptr, lane);
+          store(ep.tma_out, map_out, ep.out, ep.ldo, col0);
+        }
+        // the accumulators have been read: the MMA may overwrite them
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            mbar_arrive(smem_u32(&sh->tmem_empty[acc]));
+          else
+            mbar_arrive_remote(empty_leader[acc]);
         }
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
+      // (an epilogue warp that gives up keeps to the barriers of the others)
+      if (!ok) {
+        for (int u = t + num_pairs; u < total; u += num_pairs) {
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+      }
     }
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (res_inflight) {  // gave up with a copy under way
+      const int zero = 0;
+      mbar_wait(res_bar, res_phase, &zero);
+    }
+    __syncwarp();
   }
 
   pdl_launch_dependents();
@@ -462,7 +664,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
       }
     }
-    if (warp == 1 && lane == 0 && leader) {
+    if (warp == 1 && leader && elect_one()) {  // the lane that issued the MMAs
       mma_commit_pair(smem_u32(&sh->drain));
       mbar_wait(smem_u32(&sh->drain), 0, &zero);
     }
@@ -793,9 +995,16 @@ bool operand_map(CUtensorMap *map, const Operand &o, int64_t other, int64_t summ
                    : make_map_ld(map, o.ptr, other, summed, o.ld, box);
 }
 
+// Map of a result (or residual) matrix, where TMA can reach it: a 16-byte
+// aligned base and row stride.
+int result_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld) {
+  if (ptr == nullptr || reinterpret_cast<uintptr_t>(ptr) % 16 != 0 || ld % 8 != 0) return 0;
+  return make_map_ld(map, ptr, rows, cols, ld, 32) ? 1 : 0;
+}
+
 template <int kBN>
 cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cudaStream_t stream) {
-  Maps maps;
+  Maps maps = {};
   Products prods = {};
   prods.n = n;
   for (int i = 0; i < n; ++i) {
@@ -813,17 +1022,26 @@ cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cuda
     if (!operand_map(&maps.a[i], m.a, m.rows, m.summed, 128) ||
         !operand_map(&maps.b[i], m.b, m.cols, m.summed, kBN / 2))
       return cudaErrorNotSupported;
-  }
-  for (int i = n; i < kMaxProducts; ++i) {
-    maps.a[i] = maps.a[0];
-    maps.b[i] = maps.b[0];
+    p.ep.tma_out = result_map(&maps.out[i], m.ep.out, m.rows, m.cols, m.ep.ldo);
+    p.ep.tma_pre = result_map(&maps.pre[i], m.ep.pre, m.rows, m.cols, m.ep.ldp);
+    p.ep.tma_res = result_map(&maps.res[i], m.ep.res, m.rows, m.cols, m.ep.ldr);
   }
   auto kern = gemm_kernel<kBN>;
   const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), gemm_smem<kBN>,
                                       kBN == 256 ? 0 : (kBN == 128 ? 1 : 2));
   if (e != cudaSuccess) return e;
   const int pairs = num_sms / 2 < prods.tile0[n] ? num_sms / 2 : prods.tile0[n];
-  return launch_pdl(kern, 2 * pairs, gemm_smem<kBN>, stream, maps, prods, err);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = gemm_smem<kBN>;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, prods, err);
 }
 
 // Columns of a tile: the widest that does not leave SMs idle.  Cost of a
