@@ -125,7 +125,7 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t
                             int64_t shard_start, int64_t valid, const int32_t *tokens, int top_k,
                             float *logprob, float *entropy, float *lse, int32_t *top_ids,
                             float *top_logprobs, sga_logprob_part *part, sga_stat *top,
-                            int num_sms, cudaStream_t stream);
+                            int num_sms, uint32_t *err, cudaStream_t stream);
 cudaError_t launch_logprob_reduce(const sga_logprob_part *parts, const sga_stat *tops,
                                   int num_shards, int64_t rows, int top_k, const int32_t *tokens,
                                   float *logprob, float *entropy, float *lse, int32_t *top_ids,

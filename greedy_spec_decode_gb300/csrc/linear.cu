@@ -17,54 +17,12 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
-#include "tcgen05.cuh"
+#include "pipe.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace sga {
 namespace {
-
-// mbar_wait that sleeps in the barrier unit (try_wait with a time hint)
-// between looks at the clock and the abort flag.
-__device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity,
-                                          const volatile int *abort_flag) {
-  unsigned long long t0 = 0;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(100000u)
-        : "memory");
-    if (ok) return true;
-    if (*abort_flag) return false;
-    const unsigned long long t = global_timer_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitLimitNs) return false;
-  }
-}
-
-// True in one lane of a converged warp.  The producer and MMA warps run their
-// loops with all lanes and elect one around each issue: the operands of TMA
-// and MMA instructions then stay in uniform registers.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
-// The abort flag as the whole warp sees it.
-__device__ __forceinline__ bool aborted(const volatile int *abort_flag) {
-  return __any_sync(0xffffffffu, *abort_flag != 0) != 0;
-}
-
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // ------------------------------------------------------------- activations
 
@@ -228,11 +186,6 @@ struct SharedGemm {
   alignas(16) float bias[kBN];  // the tile's
 };
 static_assert(sizeof(SharedGemm<256>) <= 1536 && sizeof(SharedGemm<64>) <= 1536, "shared block");
-
-__device__ __forceinline__ void raise_abort(int *flag, uint32_t *err) {
-  *reinterpret_cast<volatile int *>(flag) = 1;
-  atomicOr(err, SGA_DEVERR_TIMEOUT);
-}
 
 // Tile t of a product: bands of 8 row tiles, row tiles fastest, so that the
 // pairs at work share a few A and B panels through L2.
@@ -429,8 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const bool a_strided = p.a_strided != 0, b_strided = p.b_strided != 0;
       const CUtensorMap *map_a = &maps.a[pi], *map_b = &maps.b[pi];
       for (int kb = 0; kb < num_kb; ++kb) {
-        if (!__all_sync(0xffffffffu, pipe_wait(smem_u32(&sh->empty[prod_stage]), prod_phase ^ 1,
-                                               abort_flag))) {
+        if (!warp_wait(smem_u32(&sh->empty[prod_stage]), prod_phase ^ 1, abort_flag)) {
           if (lane == 0) raise_abort(&sh->abort, err);
           break;
         }
@@ -472,15 +424,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const bool a_strided = p.a_strided != 0, b_strided = p.b_strided != 0;
       const uint32_t idesc = operand_idesc(256, kBN, a_strided, b_strided);
       const uint32_t step_a = k_step(a_strided), step_b = k_step(b_strided);
-      if (!__all_sync(0xffffffffu, pipe_wait(smem_u32(&sh->tmem_empty[acc]), acc_phase ^ 1,
-                                             abort_flag))) {
+      if (!warp_wait(smem_u32(&sh->tmem_empty[acc]), acc_phase ^ 1, abort_flag)) {
         if (lane == 0) raise_abort(&sh->abort, err);
         break;
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * kBN;
       for (int kb = 0; kb < num_kb; ++kb) {
-        if (!__all_sync(0xffffffffu, pipe_wait(smem_u32(&sh->full[stage]), phase, abort_flag))) {
+        if (!warp_wait(smem_u32(&sh->full[stage]), phase, abort_flag)) {
           if (lane == 0) raise_abort(&sh->abort, err);
           ok = false;
           break;
@@ -578,8 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         load_res(first);
         res_ready = true;
       }
-      ok = __all_sync(0xffffffffu,
-                      pipe_wait(smem_u32(&sh->tmem_full[acc]), acc_phase, abort_flag));
+      ok = warp_wait(smem_u32(&sh->tmem_full[acc]), acc_phase, abort_flag);
       if (!ok && lane == 0) raise_abort(&sh->abort, err);
       if (ok) {
         tc_fence_after();
@@ -599,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             if (!res_ready) load_res(col0);
             res_ready = false;
             if (ep.tma_res) {
-              ok = __all_sync(0xffffffffu, pipe_wait(res_bar, res_phase, abort_flag));
+              ok = warp_wait(res_bar, res_phase, abort_flag);
               if (!ok) {
                 if (lane == 0) raise_abort(&sh->abort, err);
                 break;

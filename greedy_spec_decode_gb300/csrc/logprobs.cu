@@ -15,7 +15,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "pipe.cuh"
 #include "scan.cuh"
 
 namespace cg = cooperative_groups;
@@ -27,7 +27,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Logits below kLow count as kLow in the fast pass (their terms are zero
 // there); a row whose maximum lies outside +-kFastMax takes the exact pass.
-constexpr float kLow = -1e38f;
+constexpr float kLow = -8.507059e37f;  // -2^126
 constexpr float kUnset = -1e6f;
 constexpr float kFastMax = 5e5f;
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -62,12 +62,68 @@ __device__ __forceinline__ void lse_merge(Lse &a, const Lse &b) {
   a.r = r;
 }
 
-// ------------------------------------------------------------ alternatives
+// ---------------------------------------------------------------- forward
+// One cluster of `chunks` CTAs per row; each CTA reads a contiguous piece of
+// the row and the first CTA joins the pieces through distributed shared
+// memory, so that a row needs one launch and no workspace.  The 16-byte
+// aligned body of a piece comes through a shared-memory ring (cp.async.bulk by
+// a copy warp); its unaligned ends are read element by element.
+//
+// Alternatives.  Keeping a sorted list while streaming costs a serial
+// insertion for every element that enters it.  Instead a threshold is taken
+// once from the piece's first ring stage: the top_k-th largest of the maxima
+// of 64 groups of threads, which at least top_k elements reach.  Elements that
+// reach it go to a candidate buffer (a few hundred of 200000), from which the
+// top_k are selected at the end.  -inf is never a candidate: where fewer than
+// top_k elements are above it, the lowest masked ids fill the list.  If the
+// buffer overflows (rows with very many equal values, or rising ones) the
+// piece is read again with per-warp sorted lists.
+constexpr int kGroups = 64;
+constexpr int kCandidates = 1024;
+constexpr int kVecPerThread = 4;  // 16-byte vectors of a ring stage per thread
+constexpr int kRing = 3;
+constexpr int kMaxChunks = 8;
+constexpr int kMaxWarps = 8;
+
+struct RowOut {
+  // final results (nullable each), or with part set the shard's statistics
+  float *logprob, *entropy, *lse, *top_logprobs;
+  int32_t *top_ids;
+  sga_logprob_part *part;
+  sga_stat *top;
+};
+
+template <int kT>
+struct PieceShared {
+  uint64_t full[kRing], empty[kRing];
+  int abort, count, count2;
+  float threshold;
+  float max;
+  Lse lse;
+  Lse warp_lse[kMaxWarps];
+  float warp_max[kMaxWarps];
+  float group[kGroups];
+  float best_v[SGA_MAX_TOP];
+  int32_t best_id[SGA_MAX_TOP];
+  sga_stat cand[kCandidates];
+};
+
+// Scratch of the selection, in the ring once the row has been read.
+struct SelectScratch {
+  sga_stat group[kGroups];
+  sga_stat cand[kCandidates];
+  float list_v[kMaxWarps * SGA_MAX_TOP];
+  int32_t list_id[kMaxWarps * SGA_MAX_TOP];
+};
+template <int kT>
+constexpr int ring_bytes = kRing * kT * kVecPerThread * 16;
+static_assert(sizeof(SelectScratch) <= ring_bytes<64>, "selection scratch fits the ring");
+
 // A warp's best entries so far, in the argmax order: lane i holds the i-th.
 struct WarpTop {
   float v;
   int32_t id;
-  float kth_v;     // entry k - 1: what a new element has to beat
+  float kth_v;  // entry k - 1: what a new element has to beat
   int32_t kth_id;
 };
 
@@ -97,53 +153,6 @@ __device__ __forceinline__ void top_offer(WarpTop &t, float x, int32_t id, int l
     const int32_t i = __shfl_sync(0xffffffffu, id, src);
     if (pair_beats(v, i, t.kth_v, t.kth_id)) top_insert(t, v, i, lane, k);
   }
-}
-
-// ---------------------------------------------------------------- forward
-// One cluster of `chunks` CTAs per row; each CTA reads a contiguous piece of
-// the row and the first CTA joins the pieces through distributed shared
-// memory, so that a row needs one launch and no workspace.
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;
-constexpr int kMaxChunks = 8;
-
-struct RowOut {
-  // final results (nullable each), or with part set the shard's statistics
-  float *logprob, *entropy, *lse, *top_logprobs;
-  int32_t *top_ids;
-  sga_logprob_part *part;
-  sga_stat *top;
-};
-
-// What one CTA knows of its piece.
-struct PieceShared {
-  Lse lse;
-  float max;
-  float cand_v[kWarps * SGA_MAX_TOP];  // the warps' sorted lists, then the CTA's
-  int32_t cand_id[kWarps * SGA_MAX_TOP];
-  float best_v[SGA_MAX_TOP];
-  int32_t best_id[SGA_MAX_TOP];
-  Lse warp_lse[kWarps];
-  float warp_max[kWarps];
-};
-
-// Element-wise absorption of one logit (row heads and tails).
-__device__ __forceinline__ void lse_absorb(Lse &a, float x) {
-  const float c = max_nan(x, kLow);
-  if (c > kUnset && (a.s == 0.0f || c * kLog2e > a.r + 12.0f)) {
-    const float r = c * kLog2e;
-    if (a.s != 0.0f) {
-      const float d = a.r - r, f = ex2(d);
-      a.w = f == 0.0f ? 0.0f : f * fmaf(d, a.s, a.w);
-      a.s *= f;
-    }
-    a.r = r;
-  }
-  const float t = fmaf(c, kLog2e, -a.r);
-  const float e = ex2(t);
-  a.s += e;
-  a.w = fmaf(e, t, a.w);
 }
 
 // The position of entry (v, id) of list `own` among n sorted lists of k
@@ -193,139 +202,368 @@ __device__ __forceinline__ void finish_row(float max, float s, float w, float &l
   }
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack_f32(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A thread's running statistics: two interleaved pairs of sums relative to r.
+struct ThreadSums {
+  float r;
+  uint64_t s, w;
+  bool set;
+};
+
+// Two more logits (none below kLow).
+__device__ __forceinline__ void sums_add(ThreadSums &a, float lo, float hi) {
+  const uint64_t t = fma2(pack_f32(lo, hi), pack_f32(kLog2e, kLog2e), pack_f32(-a.r, -a.r));
+  float t0, t1;
+  unpack_f32(t, t0, t1);
+  const uint64_t e = pack_f32(ex2(t0), ex2(t1));
+  a.s = add2(a.s, e);
+  a.w = fma2(e, t, a.w);
+}
+
+__device__ __forceinline__ Lse sums_total(const ThreadSums &a) {
+  float s0, s1, w0, w1;
+  unpack_f32(a.s, s0, s1);
+  unpack_f32(a.w, w0, w1);
+  return {a.r, s0 + s1, w0 + w1};
+}
+
+// Move the reference up to m where the sums would grow too large (rarely: it
+// only has to stay within 2^12 of the maximum).
+__device__ __forceinline__ void sums_rebase(ThreadSums &a, float m) {
+  if (m > kUnset && (!a.set || m * kLog2e > a.r + 12.0f)) {
+    const float r = m * kLog2e;
+    if (a.set) {
+      const Lse b = sums_total(a);
+      const float d = a.r - r, f = ex2(d);
+      a.w = pack_f32(f == 0.0f ? 0.0f : f * fmaf(d, b.s, b.w), 0.0f);
+      a.s = pack_f32(f * b.s, 0.0f);
+    }
+    a.r = r;
+    a.set = true;
+  }
+}
+
+// The logits of a 16-byte vector.
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ void vec_elems(const uint4 q, float (&x)[kBf16 ? 8 : 4]) {
+  const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kBf16) {
+      x[2 * i] = bf16_lo(wd[i]);
+      x[2 * i + 1] = bf16_hi(wd[i]);
+    } else {
+      x[i] = __uint_as_float(wd[i]);
+    }
+  }
+}
+
+constexpr uint32_t kLowBf16x2 = 0xfe80fe80u;  // -2^126, twice
+
+template <bool kBf16>
+__device__ __forceinline__ void sums_vector(ThreadSums &a, const uint4 q) {
+  if constexpr (kBf16) {
+    const uint32_t wd[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = max_nan_bf16x2(wd[i], kLowBf16x2);
+      sums_add(a, bf16_lo(w), bf16_hi(w));
+    }
+  } else {
+    sums_add(a, max_nan(__uint_as_float(q.x), kLow), max_nan(__uint_as_float(q.y), kLow));
+    sums_add(a, max_nan(__uint_as_float(q.z), kLow), max_nan(__uint_as_float(q.w), kLow));
+  }
+}
+
+// A candidate: reaches the threshold and is not masked.
+__device__ __forceinline__ bool reaches(float x, float threshold) {
+  return !(x < threshold) && x != neg_inf();
+}
+
+__device__ __forceinline__ void push(sga_stat *buf, int *count, float x, int32_t id) {
+  const int at = atomicAdd(count, 1);
+  if (at < kCandidates) buf[at] = {x, id};
+}
+
+// The top_k of the n <= kCandidates candidates into best (sorted), with the
+// same two steps as the row: a threshold from group maxima (pairs here, so
+// that it is exact about ties), then the few that reach it by counting.
+template <int kT>
+__device__ __forceinline__ void select_top(PieceShared<kT> &sh, SelectScratch &sc, int n, int k,
+                                           int tid) {
+  const sga_stat *from = sh.cand;
+  if (n > kGroups) {
+    sga_stat m = {neg_inf(), kNoId};
+    for (int i = tid; i < n; i += kT)
+      if (pair_beats(sh.cand[i].v, sh.cand[i].id, m.v, m.id)) m = sh.cand[i];
+#pragma unroll
+    for (int off = kT / kGroups / 2; off > 0; off >>= 1) {
+      const float ov = __shfl_xor_sync(0xffffffffu, m.v, off);
+      const int32_t oi = __shfl_xor_sync(0xffffffffu, m.id, off);
+      if (pair_beats(ov, oi, m.v, m.id)) m = {ov, oi};
+    }
+    if (tid % (kT / kGroups) == 0) sc.group[tid / (kT / kGroups)] = m;
+    if (tid == 0) sh.count2 = 0;
+    asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+    if (tid < kGroups) {
+      const sga_stat me = sc.group[tid];
+      int rank = 0;
+      for (int g = 0; g < kGroups; ++g)
+        rank += pair_beats(sc.group[g].v, sc.group[g].id, me.v, me.id) ||
+                (sc.group[g].id == me.id && g < tid);
+      if (rank == k - 1) {
+        sh.threshold = me.v;
+        sh.best_id[0] = me.id;
+      }
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+    const float tv = sh.threshold;
+    const int32_t ti = sh.best_id[0];
+    for (int i = tid; i < n; i += kT) {
+      const sga_stat c = sh.cand[i];
+      if (!pair_beats(tv, ti, c.v, c.id)) sc.cand[atomicAdd(&sh.count2, 1)] = c;
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+    n = sh.count2;
+    from = sc.cand;
+  }
+  for (int i = tid; i < n; i += kT) {
+    const sga_stat c = from[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += pair_beats(from[j].v, from[j].id, c.v, c.id);
+    if (rank < k) {
+      sh.best_v[rank] = c.v;
+      sh.best_id[rank] = c.id;
+    }
+  }
+}
+
+template <bool kBf16, int kT>
+__global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
     logprobs_kernel(const char *__restrict__ logits, int64_t ld_bytes, int valid, int32_t id0,
-                    const int32_t *__restrict__ tokens, int k, int chunks, RowOut out) {
+                    const int32_t *__restrict__ tokens, int k, int chunks, RowOut out,
+                    uint32_t *err) {
   constexpr int kElt = kBf16 ? 2 : 4;
   constexpr int kVec = 16 / kElt;
-  __shared__ PieceShared sh;
+  constexpr int kStageVec = kT * kVecPerThread;
+  constexpr int kWarps = kT / 32;
+  extern __shared__ __align__(128) uint4 ring[];
+  __shared__ PieceShared<kT> sh;
+  SelectScratch &sc = *reinterpret_cast<SelectScratch *>(ring);
   const int chunk = static_cast<int>(blockIdx.x % chunks);
   const int64_t row = blockIdx.x / chunks;
   const char *p = logits + row * ld_bytes;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
 
   int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / kElt);
   if (head > valid) head = valid;
   const int nvec = (valid - head) / kVec;
-  const int tail = valid - head - nvec * kVec;
   const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * chunk / chunks);
   const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (chunk + 1) / chunks);
-  const uint4 *vp = reinterpret_cast<const uint4 *>(p + head * kElt);
+  const int nbody = v1 - v0;
+  const int nst = (nbody + kStageVec - 1) / kStageVec;
+  // the piece's columns, and its two unaligned ends [c0, b0) and [b1, c1)
+  const int b0 = head + v0 * kVec, b1 = head + v1 * kVec;
+  const int c0 = chunk == 0 ? 0 : b0, c1 = chunk == chunks - 1 ? valid : b1;
+  const char *body = p + static_cast<int64_t>(b0) * kElt;
+  const volatile int *abort_flag = &sh.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), kWarps);
+    }
+    sh.abort = 0;
+    sh.count = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
   pdl_wait();
 
-  Lse a = {0.0f, 0.0f, 0.0f};
-  float mx = neg_inf();
-  WarpTop top = {neg_inf(), kNoId, neg_inf(), kNoId};
-
-  // head (first piece) and tail (last piece): one element per thread
-  {
-    const bool h = chunk == 0 && tid < head;
-    const bool t = chunk == chunks - 1 && tid >= 32 && tid - 32 < tail;
-    if (warp < 2) {
-      const int j = h ? tid : head + nvec * kVec + tid - 32;
-      const float x = h || t ? load_elem<kBf16>(p, j) : neg_inf();
-      if (h || t) {
-        lse_absorb(a, x);
-        mx = x;
+  if (warp == kWarps) {
+    // ------------------------------------------------------------- copy warp
+    int issued = 0;
+    for (int j = 0; j < nst; ++j) {
+      const int slot = j % kRing;
+      if (j >= kRing && !warp_wait(smem_u32(&sh.empty[slot]), (j / kRing - 1) & 1, abort_flag)) {
+        if (lane == 0) raise_abort(&sh.abort, err);
+        break;
       }
-      if (k > 0) top_offer(top, x, h || t ? id0 + j : kNoId, lane, k);
+      if (elect_one()) {
+        const uint32_t bytes = static_cast<uint32_t>(min(kStageVec, nbody - j * kStageVec)) * 16;
+        mbar_expect_tx(smem_u32(&sh.full[slot]), bytes);
+        bulk_load(smem_u32(ring + slot * kStageVec),
+                  body + static_cast<int64_t>(j) * kStageVec * 16, bytes,
+                  smem_u32(&sh.full[slot]));
+      }
+      __syncwarp();
+      issued = j + 1;
     }
-  }
-
-  for (int base = v0 + warp * 32; base < v1; base += kThreads * kUnroll) {
-    uint4 q[kUnroll];
+    // every copy has landed before the ring is used for anything else
+    const int zero = 0;
+    for (int j = max(0, issued - kRing); j < issued; ++j)
+      pipe_wait(smem_u32(&sh.full[j % kRing]), (j / kRing) & 1, &zero);
+  } else {
+    // -------------------------------------------------------------- consumers
+    ThreadSums a = {0.0f, 0u, 0u, false};
+    float mx = neg_inf();
+    float threshold = __int_as_float(0x7f800000);
+    for (int j = 0; j < nst; ++j) {
+      const int slot = j % kRing;
+      const bool ok = warp_wait(smem_u32(&sh.full[slot]), (j / kRing) & 1, abort_flag);
+      if (!ok && lane == 0) raise_abort(&sh.abort, err);
+      const int n = min(kStageVec, nbody - j * kStageVec);
+      const uint4 *st = ring + slot * kStageVec;
+      if (j == 0 && k > 0) {
+        float m = neg_inf();
+        for (int i = tid; i < n; i += kT) m = max_nan(m, vec_max<kBf16>(st[i]));
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int v = base + u * kThreads + lane;
-      q[u] = v < v1 ? ld_stream_v4(vp + v)
-                    : (kBf16 ? make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u)
-                             : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u));
-    }
+        for (int off = kT / kGroups / 2; off > 0; off >>= 1)
+          m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (tid % (kT / kGroups) == 0) sh.group[tid / (kT / kGroups)] = m;
+        asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+        if (tid < kGroups) {
+          const float me = sh.group[tid];
+          int rank = 0;
+#pragma unroll 8
+          for (int g = 0; g < kGroups; ++g)
+            rank += pair_beats(sh.group[g], g, me, tid);
+          if (rank == k - 1) sh.threshold = me;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+        threshold = sh.threshold;
+      }
+      if (!ok) break;  // (after the first stage's barriers, which every warp keeps to)
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const float vm = vec_max<kBf16>(q[u]);
-      mx = max_nan(mx, vm);
-      const uint32_t wd[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-      float x[kVec];
+      for (int u = 0; u < kVecPerThread; ++u) {
+        const int i = u * kT + tid;
+        if (i < n) {
+          const uint4 q = st[i];
+          const float vm = vec_max<kBf16>(q);
+          mx = max_nan(mx, vm);
+          sums_rebase(a, vm);
+          sums_vector<kBf16>(a, q);
+          if (!(vm < threshold) && k > 0) {
+            float x[kVec];
+            vec_elems<kBf16>(q, x);
+            const int32_t id = id0 + b0 + (j * kStageVec + i) * kVec;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (kBf16) {
-          x[2 * i] = bf16_lo(wd[i]);
-          x[2 * i + 1] = bf16_hi(wd[i]);
-        } else {
-          x[i] = __uint_as_float(wd[i]);
+            for (int e = 0; e < kVec; ++e)
+              if (reaches(x[e], threshold)) push(sh.cand, &sh.count, x[e], id + e);
+          }
         }
       }
-      if (vm > kUnset && (a.s == 0.0f || vm * kLog2e > a.r + 12.0f)) {
-        const float r = vm * kLog2e;
-        if (a.s != 0.0f) {
-          const float d = a.r - r, f = ex2(d);
-          a.w = f == 0.0f ? 0.0f : f * fmaf(d, a.s, a.w);
-          a.s *= f;
-        }
-        a.r = r;
-      }
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const float t = fmaf(max_nan(x[i], kLow), kLog2e, -a.r);
-        const float e = ex2(t);
-        a.s += e;
-        a.w = fmaf(e, t, a.w);
-      }
-      if (k > 0 && __any_sync(0xffffffffu, !(vm < top.kth_v))) {
-        const int v = base + u * kThreads + lane;
-        const int32_t id = id0 + head + v * kVec;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-          top_offer(top, x[i], v < v1 ? id + i : kNoId, lane, k);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
+    }
+    // the unaligned ends: at most one element per thread on either side
+    if (nst == 0) threshold = neg_inf();
+    for (int side = 0; side < 2; ++side) {
+      const int j = (side == 0 ? c0 : b1) + tid;
+      if (j < (side == 0 ? b0 : c1)) {
+        const float x = load_elem<kBf16>(p, j);
+        mx = max_nan(mx, x);
+        sums_rebase(a, x);
+        sums_add(a, max_nan(x, kLow), kLow);
+        if (k > 0 && reaches(x, threshold)) push(sh.cand, &sh.count, x, id0 + j);
       }
     }
-  }
-
-  // ---- the CTA's pieces
-  auto block_max = [&](float m) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane == 0) sh.warp_max[warp] = m;
-  };
-  auto block_lse = [&](Lse b) {
+    Lse b = sums_total(a);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const Lse o = {__shfl_xor_sync(0xffffffffu, b.r, off), __shfl_xor_sync(0xffffffffu, b.s, off),
                      __shfl_xor_sync(0xffffffffu, b.w, off)};
       lse_merge(b, o);
     }
-    if (lane == 0) sh.warp_lse[warp] = b;
-  };
-  block_max(mx);
-  block_lse(a);
-  if (lane < k) {
-    sh.cand_v[warp * k + lane] = top.v;
-    sh.cand_id[warp * k + lane] = top.id;
-  }
-  __syncthreads();
-  for (int c = tid; c < kWarps * k; c += kThreads) {
-    const int rank = rank_in_lists(sh.cand_v, sh.cand_id, kWarps, k, c / k, c % k);
-    if (rank < k) {
-      sh.best_v[rank] = sh.cand_v[c];
-      sh.best_id[rank] = sh.cand_id[c];
+    if (lane == 0) {
+      sh.warp_max[warp] = mx;
+      sh.warp_lse[warp] = b;
     }
   }
-  if (tid == 0) {
-    float m = sh.warp_max[0];
-    Lse t = sh.warp_lse[0];
-    for (int w = 1; w < kWarps; ++w) {
-      m = max_nan(m, sh.warp_max[w]);
-      lse_merge(t, sh.warp_lse[w]);
+  __syncthreads();  // the copies have landed and every candidate is in the buffer
+  if (warp < kWarps) {
+    if (k > 0) {
+      const int n = sh.count;
+      if (n <= kCandidates) {
+        select_top(sh, sc, n, k, tid);
+        if (n < k) {
+          // masked elements fill the list, lowest ids first
+          asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+          if (warp == 0) {
+            int have = n;
+            for (int base = c0; base < c1 && have < k; base += 32) {
+              const int j = base + lane;
+              const bool masked = j < c1 && load_elem<kBf16>(p, j) == neg_inf();
+              const unsigned m = __ballot_sync(0xffffffffu, masked);
+              const int at = have + __popc(m & ((1u << lane) - 1));
+              if (masked && at < k) {
+                sh.best_v[at] = neg_inf();
+                sh.best_id[at] = id0 + j;
+              }
+              have += __popc(m);
+            }
+            if (lane >= have && lane < k) {
+              sh.best_v[lane] = neg_inf();
+              sh.best_id[lane] = kNoId;
+            }
+          }
+        }
+      } else {
+        WarpTop top = {neg_inf(), kNoId, neg_inf(), kNoId};
+        for (int base = c0 + warp * 32; base < c1; base += kT) {
+          const int j = base + lane;
+          top_offer(top, j < c1 ? load_elem<kBf16>(p, j) : neg_inf(), j < c1 ? id0 + j : kNoId,
+                    lane, k);
+        }
+        if (lane < k) {
+          sc.list_v[warp * k + lane] = top.v;
+          sc.list_id[warp * k + lane] = top.id;
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+        for (int c = tid; c < kWarps * k; c += kT) {
+          const int rank = rank_in_lists(sc.list_v, sc.list_id, kWarps, k, c / k, c % k);
+          if (rank < k) {
+            sh.best_v[rank] = sc.list_v[c];
+            sh.best_id[rank] = sc.list_id[c];
+          }
+        }
+      }
     }
-    sh.max = m;
-    sh.lse = t;
+    if (tid == 0) {
+      float m = sh.warp_max[0];
+      Lse t = sh.warp_lse[0];
+      for (int w = 1; w < kWarps; ++w) {
+        m = max_nan(m, sh.warp_max[w]);
+        lse_merge(t, sh.warp_lse[w]);
+      }
+      sh.max = m;
+      sh.lse = t;
+    }
   }
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
 
-  // ---- the row: every CTA joins the maxima (the exact pass needs it)
+  // ---- the row: every CTA joins the maxima and restates its sums
   float row_max = sh.max;
   for (int c = 0; c < chunks; ++c) row_max = max_nan(row_max, *cluster.map_shared_rank(&sh.max, c));
   // An extreme finite maximum: sums relative to the maximum itself, in
@@ -334,22 +572,20 @@ __global__ void __launch_bounds__(kThreads)
                      (row_max < -kFastMax && row_max > neg_inf());
   if (exact) {
     float es = 0.0f, ew = 0.0f;
-    auto term = [&](float x) {
-      const float t = max_nan((x - row_max) * kLog2e, -1e30f);
-      const float e = ex2(t);
-      es += e;
-      ew = fmaf(e, t, ew);
-    };
-    if (chunk == 0 && tid < head) term(load_elem<kBf16>(p, tid));
-    for (int j = head + v0 * kVec + tid; j < head + v1 * kVec; j += kThreads)
-      term(load_elem<kBf16>(p, j));
-    if (chunk == chunks - 1 && tid < tail) term(load_elem<kBf16>(p, head + nvec * kVec + tid));
+    if (warp < kWarps) {
+      for (int j = c0 + tid; j < c1; j += kT) {
+        const float t = max_nan((load_elem<kBf16>(p, j) - row_max) * kLog2e, -1e30f);
+        const float e = ex2(t);
+        es += e;
+        ew = fmaf(e, t, ew);
+      }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      es += __shfl_xor_sync(0xffffffffu, es, off);
-      ew += __shfl_xor_sync(0xffffffffu, ew, off);
+      for (int off = 16; off > 0; off >>= 1) {
+        es += __shfl_xor_sync(0xffffffffu, es, off);
+        ew += __shfl_xor_sync(0xffffffffu, ew, off);
+      }
+      if (lane == 0) sh.warp_lse[warp] = {0.0f, es, ew};
     }
-    if (lane == 0) sh.warp_lse[warp] = {0.0f, es, ew};
     __syncthreads();
     if (tid == 0) {
       for (int w = 1; w < kWarps; ++w) {
@@ -359,7 +595,6 @@ __global__ void __launch_bounds__(kThreads)
       sh.lse = {0.0f, es, ew};
     }
   } else if (tid == 0) {
-    // restate the piece relative to the row's maximum
     const Lse t = sh.lse;
     const float d = fmaf(-row_max, kLog2e, t.r);
     const float f = t.s == 0.0f ? 0.0f : ex2(d);
@@ -369,10 +604,9 @@ __global__ void __launch_bounds__(kThreads)
   pdl_launch_dependents();
 
   if (chunk == 0) {
-    // gather the pieces' lists (the warps' lists are no longer needed)
-    for (int c = tid; c < chunks * k; c += kThreads) {
-      sh.cand_v[c] = *cluster.map_shared_rank(&sh.best_v[c % k], c / k);
-      sh.cand_id[c] = *cluster.map_shared_rank(&sh.best_id[c % k], c / k);
+    for (int c = tid; c < chunks * k; c += kT + 32) {
+      sc.list_v[c] = *cluster.map_shared_rank(&sh.best_v[c % k], c / k);
+      sc.list_id[c] = *cluster.map_shared_rank(&sh.best_id[c % k], c / k);
     }
     float s = sh.lse.s, w = sh.lse.w;
     for (int c = 1; c < chunks; ++c) {
@@ -396,11 +630,11 @@ __global__ void __launch_bounds__(kThreads)
         if (out.lse != nullptr) out.lse[row] = lse;
       }
     }
-    for (int c = tid; c < chunks * k; c += kThreads) {
-      const int rank = rank_in_lists(sh.cand_v, sh.cand_id, chunks, k, c / k, c % k);
+    for (int c = tid; c < chunks * k; c += kT + 32) {
+      const int rank = rank_in_lists(sc.list_v, sc.list_id, chunks, k, c / k, c % k);
       if (rank >= k) continue;
-      const float v = sh.cand_v[c];
-      const int32_t id = sh.cand_id[c];
+      const float v = sc.list_v[c];
+      const int32_t id = sc.list_id[c];
       if (out.part != nullptr) {
         out.top[row * k + rank] = {v, id};
       } else {
@@ -484,6 +718,8 @@ __global__ void logprob_reduce_kernel(const sga_logprob_part *__restrict__ parts
 }
 
 // ---------------------------------------------------------------- gradient
+constexpr int kThreads = 256;
+
 // dx_j = p_j (A + B (log p_j + H)) plus, at the token and at the alternatives,
 // their upstream gradients; A = -(sum of those), B = -(gradient of the
 // entropy).  One pass, each logit read and each gradient written once; the few
@@ -617,29 +853,29 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Pieces per row: a row is split (in powers of two) while the grid stays
-// within the resident CTAs and a piece keeps a few vectors per thread.
-int pick_row_chunks(int64_t rows, int64_t width, int elt, int num_sms, int most) {
-  const int64_t nvec = width * elt / 16;
+// within the resident CTAs and a piece keeps a ring stage.
+int pick_row_chunks(int64_t rows, int64_t nvec, int num_sms) {
   int chunks = 1;
-  while (chunks < most && rows * chunks * 2 <= num_sms * 4 && nvec / (2 * chunks) >= kThreads)
+  while (chunks < kMaxChunks && rows * chunks * 2 <= num_sms * 3 && nvec / (2 * chunks) >= 1024)
     chunks *= 2;
   return chunks;
 }
 
-}  // namespace
-
-cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld,
-                            int64_t shard_start, int64_t valid, const int32_t *tokens, int top_k,
-                            float *logprob, float *entropy, float *lse, int32_t *top_ids,
-                            float *top_logprobs, sga_logprob_part *part, sga_stat *top,
-                            int num_sms, cudaStream_t stream) {
-  const int elt = dtype == SGA_BF16 ? 2 : 4;
-  const int chunks = pick_row_chunks(rows, valid, elt, num_sms, kMaxChunks);
-  const RowOut out = {logprob, entropy, lse, top_logprobs, top_ids, part, top};
+template <bool kBf16, int kT>
+cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t shard_start,
+                        int64_t valid, const int32_t *tokens, int top_k, int chunks,
+                        const RowOut &out, uint32_t *err, cudaStream_t stream) {
+  auto kern = logprobs_kernel<kBf16, kT>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * chunks));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kT + 32);
+  cfg.dynamicSmemBytes = ring_bytes<kT>;
   cfg.stream = stream;
+  if (ring_bytes<kT> > 40 * 1024) {
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), ring_bytes<kT>,
+                                        kBf16 ? 0 : 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = chunks;
@@ -649,10 +885,32 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  auto kern = dtype == SGA_BF16 ? logprobs_kernel<true> : logprobs_kernel<false>;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits), ld * elt,
-                            static_cast<int>(valid), static_cast<int32_t>(shard_start), tokens,
-                            top_k, chunks, out);
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits),
+                            ld * (kBf16 ? 2 : 4), static_cast<int>(valid),
+                            static_cast<int32_t>(shard_start), tokens, top_k, chunks, out, err);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld,
+                            int64_t shard_start, int64_t valid, const int32_t *tokens, int top_k,
+                            float *logprob, float *entropy, float *lse, int32_t *top_ids,
+                            float *top_logprobs, sga_logprob_part *part, sga_stat *top,
+                            int num_sms, uint32_t *err, cudaStream_t stream) {
+  const RowOut out = {logprob, entropy, lse, top_logprobs, top_ids, part, top};
+  const int64_t nvec = valid * (dtype == SGA_BF16 ? 2 : 4) / 16;
+  const int chunks = pick_row_chunks(rows, nvec, num_sms);
+  // many short rows: small CTAs, ten per SM
+  const bool small = chunks == 1 && nvec <= 2048 && rows > num_sms;
+  if (dtype == SGA_BF16)
+    return small ? launch_rows<true, 64>(logits, rows, ld, shard_start, valid, tokens, top_k,
+                                         chunks, out, err, stream)
+                 : launch_rows<true, 256>(logits, rows, ld, shard_start, valid, tokens, top_k,
+                                          chunks, out, err, stream);
+  return small ? launch_rows<false, 64>(logits, rows, ld, shard_start, valid, tokens, top_k,
+                                        chunks, out, err, stream)
+               : launch_rows<false, 256>(logits, rows, ld, shard_start, valid, tokens, top_k,
+                                         chunks, out, err, stream);
 }
 
 cudaError_t launch_logprob_reduce(const sga_logprob_part *parts, const sga_stat *tops,

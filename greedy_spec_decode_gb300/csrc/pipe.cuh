@@ -1,0 +1,78 @@
+// pipe.cuh -- waiting and issuing inside the pipelined kernels of linear.cu and
+// logprobs.cu: bounded mbarrier waits that sleep in the barrier unit, and
+// single-lane issue from a converged warp.
+#pragma once
+
+#include "tcgen05.cuh"
+
+namespace sga {
+namespace {
+
+// Bounded wait (as mbar_wait) that sleeps in the barrier unit (try_wait with a
+// time hint) between looks at the clock and the abort flag.
+__device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity,
+                                          const volatile int *abort_flag) {
+  unsigned long long t0 = 0;
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    const unsigned long long t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) return false;
+  }
+}
+
+// The same, agreed on by the whole (converged) warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
+                                          const volatile int *abort_flag) {
+  return __all_sync(0xffffffffu, pipe_wait(bar, parity, abort_flag)) != 0;
+}
+
+// True in one lane of a converged warp.  Producer and MMA warps run their
+// loops with all lanes and elect one around each issue, so that the operands
+// of TMA and MMA instructions stay in uniform registers: issued from a branch
+// on the lane number, the two copies and four MMAs of a K block took about 650
+// cycles of their warps, more than the tensor core needs for them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// The abort flag as the whole warp sees it.
+__device__ __forceinline__ bool aborted(const volatile int *abort_flag) {
+  return __any_sync(0xffffffffu, *abort_flag != 0) != 0;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ void raise_abort(int *flag, uint32_t *err) {
+  *reinterpret_cast<volatile int *>(flag) = 1;
+  atomicOr(err, SGA_DEVERR_TIMEOUT);
+}
+
+// Untiled copy of global memory into shared memory (16-byte aligned, size a
+// multiple of 16), counted on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+}  // namespace
+}  // namespace sga

@@ -567,7 +567,7 @@ int sga_token_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld, 
   if ((st = current_device(&d)) != SGA_OK) return st;
   return launch_status(sga::launch_logprobs(
       logits, dtype, rows, ld, 0, valid_ids(0, vocab, org_vocab), tokens, top_k, out_logprob,
-      out_entropy, out_lse, out_top_ids, out_top_logprobs, nullptr, nullptr, d.num_sms,
+      out_entropy, out_lse, out_top_ids, out_top_logprobs, nullptr, nullptr, d.num_sms, d.err,
       static_cast<cudaStream_t>(stream)));
 }
 
@@ -591,7 +591,7 @@ int sga_local_logprobs(const void *logits, int dtype, int64_t rows, int64_t ld,
   if ((st = current_device(&d)) != SGA_OK) return st;
   return launch_status(sga::launch_logprobs(
       logits, dtype, rows, ld, shard_start, valid_ids(shard_start, shard_width, org_vocab), tokens,
-      top_k, nullptr, nullptr, nullptr, nullptr, nullptr, out_parts, out_top, d.num_sms,
+      top_k, nullptr, nullptr, nullptr, nullptr, nullptr, out_parts, out_top, d.num_sms, d.err,
       static_cast<cudaStream_t>(stream)));
 }
 

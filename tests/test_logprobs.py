@@ -135,6 +135,7 @@ CASES = [  # rows, vocab, org, dtype, k, pad, offset
     (30, 4099, 4099, "bf16", 32, 0, 7), (4, 20000, 19990, "bf16", 20, 8, 0),
     (2, 50257, 50257, "f32", 1, 0, 0), (1, 152064, 151936, "bf16", 20, 0, 0),
     (700, 600, 600, "bf16", 0, 0, 0), (30, 8192, 8192, "f32", 3, 0, 1),
+    (300, 3001, 3000, "bf16", 20, 0, 3), (300, 2000, 1999, "f32", 32, 1, 0),
 ]
 
 
@@ -212,6 +213,44 @@ def test_sharded_parts_reduce_to_the_same(sga_lib, case, shards):
     sga_lib.sga_logprob_reduce(parts, tops, shards, tok, *out)
     check_outputs(x64, org, tokens, k, out)
     assert torch.equal(out[3], whole[3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [1, 5, 32])
+@pytest.mark.parametrize("vocab", [20000, 70001])
+def test_rows_that_are_hard_to_select_from(sga_lib, vocab, k, dtype):
+    """Rising and falling rows, equal values, masks that leave fewer ids than
+    top_k or none in the first thousands, NaNs among them."""
+    rng = np.random.default_rng(vocab + k)
+    x = rng.standard_normal((14, vocab)).astype(np.float32)
+    x[0] = np.linspace(-5, 5, vocab)
+    x[1] = np.linspace(5, -5, vocab)
+    x[2] = 1.5
+    x[3] = LOWEST[dtype]
+    x[3, [7, vocab - 3]] = 2.0
+    x[4] = NEG
+    x[4, [vocab // 2, vocab - 1]] = [1.0, 3.0]
+    x[5, :15000] = NEG
+    x[6] = NEG
+    x[6, 15000:15030] = 0.5
+    x[7, 9000:] = NEG
+    x[8] = np.round(x[8])
+    x[9, ::1000] = math.nan
+    x[10, -5:] = 40.0
+    x[11] = NEG
+    x[12, :] = np.where(rng.random(vocab) < 1e-3, x[12], NEG)
+    x[13] = -0.0
+    x[13, 5::11] = 0.0
+    dev, x64 = to_cuda(x, dtype, vocab, 1)
+    tokens = make_tokens(14, vocab, vocab, 1)
+    out = run_forward(sga_lib, dev, vocab, torch.from_numpy(tokens).cuda(), k)
+    check_outputs(x64, vocab, tokens, k, out)
+    # many rows at once: other CTA shapes
+    many = dev.repeat(60, 1)
+    big = run_forward(sga_lib, many, vocab, torch.from_numpy(np.tile(tokens, 60)).cuda(), k)
+    check_outputs(x64, vocab, tokens, k, [o[-14:] for o in big])
+    assert sga_lib.sga_device_error() == 0
 
 
 @pytest.mark.gpu
