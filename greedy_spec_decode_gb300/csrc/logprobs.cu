@@ -63,23 +63,24 @@ __device__ __forceinline__ void lse_merge(Lse &a, const Lse &b) {
 }
 
 // ---------------------------------------------------------------- forward
-// One cluster of `chunks` CTAs per row; each CTA reads a contiguous piece of
-// the row and the first CTA joins the pieces through distributed shared
-// memory, so that a row needs one launch and no workspace.  The 16-byte
-// aligned body of a piece comes through a shared-memory ring (cp.async.bulk by
-// a copy warp); its unaligned ends are read element by element.
+// A row is read once through a shared-memory ring (cp.async.bulk by a copy
+// warp; the row's unaligned ends element by element).  CTAs are persistent and
+// the copy warp runs on into the next row while a row is being finished.  Few
+// rows: a cluster of `chunks` CTAs shares a row and its first CTA joins the
+// pieces through distributed shared memory (one launch, no workspace).
 //
-// Alternatives.  Keeping a sorted list while streaming costs a serial
-// insertion for every element that enters it.  Instead a threshold is taken
-// once from the piece's first ring stage: the top_k-th largest of the maxima
-// of 64 groups of threads, which at least top_k elements reach.  Elements that
-// reach it go to a candidate buffer (a few hundred of 200000), from which the
-// top_k are selected at the end.  -inf is never a candidate: where fewer than
+// Alternatives.  A sorted list kept while streaming costs a serial insertion
+// for every element that enters it (measured: 4096 x 202048 bf16, 5
+// alternatives 809 us against 278 without).  Instead a threshold is taken
+// from what the ring holds at first (24576 bf16 ids): the top_k-th largest of
+// the maxima of 64 groups of threads, which at least top_k elements reach.
+// Vectors that reach it go to a candidate buffer (about a hundred of 25000),
+// from which the top_k are selected at the end by counting, on 64-bit keys
+// that order (value, id) pairs.  -inf is never a candidate: where fewer than
 // top_k elements are above it, the lowest masked ids fill the list.  If the
-// buffer overflows (rows with very many equal values, or rising ones) the
+// buffer overflows (very many equal values, or rows that keep rising) the
 // piece is read again with per-warp sorted lists.
 constexpr int kGroups = 64;
-constexpr int kCandidates = 1024;
 constexpr int kVecPerThread = 4;  // 16-byte vectors of a ring stage per thread
 constexpr int kRing = 3;
 constexpr int kMaxChunks = 8;
@@ -93,91 +94,79 @@ struct RowOut {
   sga_stat *top;
 };
 
+using Key = unsigned long long;
+
+// Unsigned order of the values of the argmax order (NaN above +inf, +0 == -0).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 becomes +0
+  if (is_nan(v)) return 0xffffffffu;
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float order_value(uint32_t o) {
+  if (o == 0xffffffffu) return __uint_as_float(0x7fc00000u);
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+
+// Key of a (value, id) pair: the argmax order, larger is better; 0 is no pair.
+__device__ __forceinline__ Key pair_key(float v, int32_t id) {
+  return (static_cast<Key>(order_key(v)) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+}
+__device__ __forceinline__ float key_value(Key k) {
+  return k == 0 ? neg_inf() : order_value(static_cast<uint32_t>(k >> 32));
+}
+__device__ __forceinline__ int32_t key_id(Key k) {
+  return k == 0 ? kNoId : static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k));
+}
+
 template <int kT>
 struct PieceShared {
+  static constexpr int kVecs = 2 * kT;  // candidate vectors
+  static constexpr int kKeys = 4 * kT;  // candidate elements
   uint64_t full[kRing], empty[kRing];
-  int abort, count, count2;
-  float threshold;
-  float max;
-  Lse lse;
+  int abort, num_vecs, num_keys;
+  uint32_t threshold;
+  float max, sum, wsum;
   Lse warp_lse[kMaxWarps];
   float warp_max[kMaxWarps];
-  float group[kGroups];
-  float best_v[SGA_MAX_TOP];
-  int32_t best_id[SGA_MAX_TOP];
-  sga_stat cand[kCandidates];
-};
-
-// Scratch of the selection, in the ring once the row has been read.
-struct SelectScratch {
-  sga_stat group[kGroups];
-  sga_stat cand[kCandidates];
-  float list_v[kMaxWarps * SGA_MAX_TOP];
-  int32_t list_id[kMaxWarps * SGA_MAX_TOP];
+  alignas(16) uint32_t group[kGroups];
+  alignas(16) uint4 vec[kVecs];
+  int32_t vec_id[kVecs];
+  alignas(16) Key key[kKeys];
+  alignas(16) Key list[kMaxWarps * SGA_MAX_TOP];  // lists of warps, or of the row's pieces
+  Key best[SGA_MAX_TOP];
 };
 template <int kT>
 constexpr int ring_bytes = kRing * kT * kVecPerThread * 16;
-static_assert(sizeof(SelectScratch) <= ring_bytes<64>, "selection scratch fits the ring");
 
-// A warp's best entries so far, in the argmax order: lane i holds the i-th.
-struct WarpTop {
-  float v;
-  int32_t id;
-  float kth_v;  // entry k - 1: what a new element has to beat
-  int32_t kth_id;
-};
-
-__device__ __forceinline__ void top_insert(WarpTop &t, float v, int32_t id, int lane, int k) {
-  const unsigned before = __ballot_sync(0xffffffffu, pair_beats(t.v, t.id, v, id));
-  const int pos = __popc(before);  // the list is sorted: the entries that stay ahead are a prefix
-  const float up_v = __shfl_up_sync(0xffffffffu, t.v, 1);
-  const int32_t up_id = __shfl_up_sync(0xffffffffu, t.id, 1);
-  if (lane > pos) {
-    t.v = up_v;
-    t.id = up_id;
-  } else if (lane == pos) {
-    t.v = v;
-    t.id = id;
-  }
-  t.kth_v = __shfl_sync(0xffffffffu, t.v, k - 1);
-  t.kth_id = __shfl_sync(0xffffffffu, t.id, k - 1);
-}
-
-// Offer one element per lane (id kNoId: none) to the warp's list.
-__device__ __forceinline__ void top_offer(WarpTop &t, float x, int32_t id, int lane, int k) {
-  unsigned m = __ballot_sync(0xffffffffu, pair_beats(x, id, t.kth_v, t.kth_id));
+// A warp's best keys so far: lane i holds the i-th.
+__device__ __forceinline__ void top_offer(Key &t, Key x, int lane, int k) {
+  Key kth = __shfl_sync(0xffffffffu, t, k - 1);
+  unsigned m = __ballot_sync(0xffffffffu, x > kth);
   while (m != 0) {
     const int src = __ffs(m) - 1;
     m &= m - 1;
-    const float v = __shfl_sync(0xffffffffu, x, src);
-    const int32_t i = __shfl_sync(0xffffffffu, id, src);
-    if (pair_beats(v, i, t.kth_v, t.kth_id)) top_insert(t, v, i, lane, k);
+    const Key v = __shfl_sync(0xffffffffu, x, src);
+    if (v <= kth) continue;
+    const int pos = __popc(__ballot_sync(0xffffffffu, t > v));
+    const Key up = __shfl_up_sync(0xffffffffu, t, 1);
+    if (lane > pos)
+      t = up;
+    else if (lane == pos)
+      t = v;
+    kth = __shfl_sync(0xffffffffu, t, k - 1);
   }
 }
 
-// The position of entry (v, id) of list `own` among n sorted lists of k
-// entries each: its index in its own list plus the entries of the others that
-// come before it (a binary search per list).  Empty entries (kNoId) compare
-// equal and go by list.
-__device__ __forceinline__ int rank_in_lists(const float *vs, const int32_t *ids, int n, int k,
-                                             int own, int idx) {
-  const float v = vs[own * k + idx];
-  const int32_t id = ids[own * k + idx];
-  int rank = idx;
-  for (int l = 0; l < n; ++l) {
-    if (l == own) continue;
-    int lo = 0, hi = k;  // entries [0, lo) of list l come before (v, id)
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      const float ov = vs[l * k + mid];
-      const int32_t oi = ids[l * k + mid];
-      const bool before = oi == id ? l < own : pair_beats(ov, oi, v, id);
-      if (before)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    rank += lo;
+// The number of keys[0 .. n) above `mine`; n is rounded up to even, the entry
+// past an odd end has to be 0.
+__device__ __forceinline__ int keys_above(const Key *keys, int n, Key mine) {
+  int rank = 0;
+#pragma unroll 4
+  for (int j = 0; j < n; j += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(keys + j);
+    rank += o.x > mine;
+    rank += o.y > mine;
   }
   return rank;
 }
@@ -225,8 +214,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // A thread's running statistics: two interleaved pairs of sums relative to r.
 struct ThreadSums {
   float r;
+  float limit;  // a logit above it moves the reference (kUnset: there is none yet)
   uint64_t s, w;
-  bool set;
 };
 
 // Two more logits (none below kLow).
@@ -249,17 +238,16 @@ __device__ __forceinline__ Lse sums_total(const ThreadSums &a) {
 // Move the reference up to m where the sums would grow too large (rarely: it
 // only has to stay within 2^12 of the maximum).
 __device__ __forceinline__ void sums_rebase(ThreadSums &a, float m) {
-  if (m > kUnset && (!a.set || m * kLog2e > a.r + 12.0f)) {
-    const float r = m * kLog2e;
-    if (a.set) {
-      const Lse b = sums_total(a);
-      const float d = a.r - r, f = ex2(d);
-      a.w = pack_f32(f == 0.0f ? 0.0f : f * fmaf(d, b.s, b.w), 0.0f);
-      a.s = pack_f32(f * b.s, 0.0f);
-    }
-    a.r = r;
-    a.set = true;
+  if (!(m > a.limit)) return;
+  const float r = m * kLog2e;
+  if (a.limit > kUnset) {
+    const Lse b = sums_total(a);
+    const float d = a.r - r, f = ex2(d);
+    a.w = pack_f32(f == 0.0f ? 0.0f : f * fmaf(d, b.s, b.w), 0.0f);
+    a.s = pack_f32(f * b.s, 0.0f);
   }
+  a.r = r;
+  a.limit = m + 8.0f;
 }
 
 // The logits of a 16-byte vector.
@@ -299,93 +287,87 @@ __device__ __forceinline__ bool reaches(float x, float threshold) {
   return !(x < threshold) && x != neg_inf();
 }
 
-__device__ __forceinline__ void push(sga_stat *buf, int *count, float x, int32_t id) {
-  const int at = atomicAdd(count, 1);
-  if (at < kCandidates) buf[at] = {x, id};
+// Whether a vector holds a logit that reaches `lo` (or a NaN), on the way to
+// which its maximum joins the thread's.  lo: two copies for bf16.
+template <bool kBf16>
+__device__ __forceinline__ bool vec_reaches(const uint4 q, uint32_t &mx, uint32_t lo) {
+  if constexpr (kBf16) {
+    const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(q.x, q.y), max_nan_bf16x2(q.z, q.w));
+    mx = max_nan_bf16x2(mx, m);
+    uint32_t hit;
+    asm("{\n\t.reg .pred p, q;\n\t"
+        "setp.geu.bf16x2 p|q, %1, %2;\n\t"
+        "or.pred p, p, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(hit)
+        : "r"(m), "r"(lo));
+    return hit != 0;
+  } else {
+    const float m = vec_max<false>(q);
+    mx = __float_as_uint(max_nan(__uint_as_float(mx), m));
+    return !(m < __uint_as_float(lo));
+  }
 }
 
-// The top_k of the n <= kCandidates candidates into best (sorted), with the
-// same two steps as the row: a threshold from group maxima (pairs here, so
-// that it is exact about ties), then the few that reach it by counting.
+// The larger of the reference limit and the candidates' threshold may be
+// ignored by vec_reaches; what it compares with is the smaller.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack_lo(float limit, float threshold) {
+  const float lo = threshold < limit ? threshold : limit;  // threshold is exact in the logits' type
+  if (!kBf16) return __float_as_uint(lo);
+  const uint32_t b = __float_as_uint(lo) >> 16;
+  return b | (b << 16);
+}
+
 template <int kT>
-__device__ __forceinline__ void select_top(PieceShared<kT> &sh, SelectScratch &sc, int n, int k,
-                                           int tid) {
-  const sga_stat *from = sh.cand;
-  if (n > kGroups) {
-    sga_stat m = {neg_inf(), kNoId};
-    for (int i = tid; i < n; i += kT)
-      if (pair_beats(sh.cand[i].v, sh.cand[i].id, m.v, m.id)) m = sh.cand[i];
-#pragma unroll
-    for (int off = kT / kGroups / 2; off > 0; off >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, m.v, off);
-      const int32_t oi = __shfl_xor_sync(0xffffffffu, m.id, off);
-      if (pair_beats(ov, oi, m.v, m.id)) m = {ov, oi};
-    }
-    if (tid % (kT / kGroups) == 0) sc.group[tid / (kT / kGroups)] = m;
-    if (tid == 0) sh.count2 = 0;
-    asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
-    if (tid < kGroups) {
-      const sga_stat me = sc.group[tid];
-      int rank = 0;
-      for (int g = 0; g < kGroups; ++g)
-        rank += pair_beats(sc.group[g].v, sc.group[g].id, me.v, me.id) ||
-                (sc.group[g].id == me.id && g < tid);
-      if (rank == k - 1) {
-        sh.threshold = me.v;
-        sh.best_id[0] = me.id;
-      }
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
-    const float tv = sh.threshold;
-    const int32_t ti = sh.best_id[0];
-    for (int i = tid; i < n; i += kT) {
-      const sga_stat c = sh.cand[i];
-      if (!pair_beats(tv, ti, c.v, c.id)) sc.cand[atomicAdd(&sh.count2, 1)] = c;
-    }
-    asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
-    n = sh.count2;
-    from = sc.cand;
-  }
-  for (int i = tid; i < n; i += kT) {
-    const sga_stat c = from[i];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += pair_beats(from[j].v, from[j].id, c.v, c.id);
-    if (rank < k) {
-      sh.best_v[rank] = c.v;
-      sh.best_id[rank] = c.id;
-    }
-  }
+__device__ __forceinline__ void push_key(PieceShared<kT> &sh, float x, int32_t id) {
+  const int at = atomicAdd(&sh.num_keys, 1);
+  if (at < sh.kKeys) sh.key[at] = pair_key(x, id);
+}
+
+template <int kT>
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
 }
 
 template <bool kBf16, int kT>
 __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
-    logprobs_kernel(const char *__restrict__ logits, int64_t ld_bytes, int valid, int32_t id0,
-                    const int32_t *__restrict__ tokens, int k, int chunks, RowOut out,
+    logprobs_kernel(const char *__restrict__ logits, int64_t ld_bytes, int64_t num_rows, int valid,
+                    int32_t id0, const int32_t *__restrict__ tokens, int k, int chunks, RowOut out,
                     uint32_t *err) {
   constexpr int kElt = kBf16 ? 2 : 4;
   constexpr int kVec = 16 / kElt;
   constexpr int kStageVec = kT * kVecPerThread;
   constexpr int kWarps = kT / 32;
+  constexpr int kPerGroup = kT / kGroups;
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ PieceShared<kT> sh;
-  SelectScratch &sc = *reinterpret_cast<SelectScratch *>(ring);
   const int chunk = static_cast<int>(blockIdx.x % chunks);
-  const int64_t row = blockIdx.x / chunks;
-  const char *p = logits + row * ld_bytes;
+  const int64_t row0 = blockIdx.x / chunks, row_step = gridDim.x / chunks;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
-
-  int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / kElt);
-  if (head > valid) head = valid;
-  const int nvec = (valid - head) / kVec;
-  const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * chunk / chunks);
-  const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (chunk + 1) / chunks);
-  const int nbody = v1 - v0;
-  const int nst = (nbody + kStageVec - 1) / kStageVec;
-  // the piece's columns, and its two unaligned ends [c0, b0) and [b1, c1)
-  const int b0 = head + v0 * kVec, b1 = head + v1 * kVec;
-  const int c0 = chunk == 0 ? 0 : b0, c1 = chunk == chunks - 1 ? valid : b1;
-  const char *body = p + static_cast<int64_t>(b0) * kElt;
   const volatile int *abort_flag = &sh.abort;
+
+  // This CTA's piece of a row: columns [c0, c1), of which [b0, b1) are whole
+  // 16-byte vectors.
+  struct Piece {
+    const char *p;
+    int c0, b0, b1, c1, stages;
+  };
+  auto piece_of = [&](int64_t row) {
+    Piece q;
+    q.p = logits + row * ld_bytes;
+    int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(q.p) & 15u)) & 15u) / kElt);
+    if (head > valid) head = valid;
+    const int nvec = (valid - head) / kVec;
+    const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * chunk / chunks);
+    const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (chunk + 1) / chunks);
+    q.b0 = head + v0 * kVec;
+    q.b1 = head + v1 * kVec;
+    q.c0 = chunk == 0 ? 0 : q.b0;
+    q.c1 = chunk == chunks - 1 ? valid : q.b1;
+    q.stages = (v1 - v0 + kStageVec - 1) / kStageVec;
+    return q;
+  };
 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
@@ -393,187 +375,234 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       mbar_init(smem_u32(&sh.empty[i]), kWarps);
     }
     sh.abort = 0;
-    sh.count = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   pdl_wait();
+  cg::cluster_group cluster = cg::this_cluster();
 
   if (warp == kWarps) {
     // ------------------------------------------------------------- copy warp
-    int issued = 0;
-    for (int j = 0; j < nst; ++j) {
-      const int slot = j % kRing;
-      if (j >= kRing && !warp_wait(smem_u32(&sh.empty[slot]), (j / kRing - 1) & 1, abort_flag)) {
-        if (lane == 0) raise_abort(&sh.abort, err);
-        break;
-      }
-      if (elect_one()) {
-        const uint32_t bytes = static_cast<uint32_t>(min(kStageVec, nbody - j * kStageVec)) * 16;
-        mbar_expect_tx(smem_u32(&sh.full[slot]), bytes);
-        bulk_load(smem_u32(ring + slot * kStageVec),
-                  body + static_cast<int64_t>(j) * kStageVec * 16, bytes,
-                  smem_u32(&sh.full[slot]));
-      }
-      __syncwarp();
-      issued = j + 1;
-    }
-    // every copy has landed before the ring is used for anything else
-    const int zero = 0;
-    for (int j = max(0, issued - kRing); j < issued; ++j)
-      pipe_wait(smem_u32(&sh.full[j % kRing]), (j / kRing) & 1, &zero);
-  } else {
-    // -------------------------------------------------------------- consumers
-    ThreadSums a = {0.0f, 0u, 0u, false};
-    float mx = neg_inf();
-    float threshold = __int_as_float(0x7f800000);
-    for (int j = 0; j < nst; ++j) {
-      const int slot = j % kRing;
-      const bool ok = warp_wait(smem_u32(&sh.full[slot]), (j / kRing) & 1, abort_flag);
-      if (!ok && lane == 0) raise_abort(&sh.abort, err);
-      const int n = min(kStageVec, nbody - j * kStageVec);
-      const uint4 *st = ring + slot * kStageVec;
-      if (j == 0 && k > 0) {
-        float m = neg_inf();
-        for (int i = tid; i < n; i += kT) m = max_nan(m, vec_max<kBf16>(st[i]));
-#pragma unroll
-        for (int off = kT / kGroups / 2; off > 0; off >>= 1)
-          m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
-        if (tid % (kT / kGroups) == 0) sh.group[tid / (kT / kGroups)] = m;
-        asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
-        if (tid < kGroups) {
-          const float me = sh.group[tid];
-          int rank = 0;
-#pragma unroll 8
-          for (int g = 0; g < kGroups; ++g)
-            rank += pair_beats(sh.group[g], g, me, tid);
-          if (rank == k - 1) sh.threshold = me;
+    int g = 0;  // stages issued
+    bool ok = true;
+    for (int64_t row = row0; row < num_rows && ok; row += row_step) {
+      const Piece q = piece_of(row);
+      for (int j = 0; j < q.stages; ++j, ++g) {
+        const int slot = g % kRing;
+        if (g >= kRing && !warp_wait(smem_u32(&sh.empty[slot]), (g / kRing - 1) & 1, abort_flag)) {
+          if (lane == 0) raise_abort(&sh.abort, err);
+          ok = false;
+          break;
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
-        threshold = sh.threshold;
+        if (elect_one()) {
+          const int at = q.b0 + j * kStageVec * kVec;
+          const uint32_t bytes = static_cast<uint32_t>(min(kStageVec * kVec, q.b1 - at)) * kElt;
+          mbar_expect_tx(smem_u32(&sh.full[slot]), bytes);
+          bulk_load(smem_u32(ring + slot * kStageVec), q.p + static_cast<int64_t>(at) * kElt,
+                    bytes, smem_u32(&sh.full[slot]));
+        }
+        __syncwarp();
       }
-      if (!ok) break;  // (after the first stage's barriers, which every warp keeps to)
+    }
+    // every copy has landed before the CTA ends
+    const int zero = 0;
+    for (int j = max(0, g - kRing); j < g; ++j)
+      pipe_wait(smem_u32(&sh.full[j % kRing]), (j / kRing) & 1, &zero);
+    pdl_launch_dependents();
+    if (chunks > 1) {  // the consumers' cluster barriers count every thread
+      cluster.sync();
+      cluster.sync();
+      cluster.sync();
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- consumers
+  int g = 0;  // stages consumed
+  int32_t tok_next = tid == 0 && tokens != nullptr && row0 < num_rows ? tokens[row0] : -1;
+  bool ok = true;
+  for (int64_t row = row0; row < num_rows; row += row_step) {
+    const Piece pc = piece_of(row);
+    const char *p = pc.p;
+    if (tid == 0) {
+      sh.num_vecs = sh.num_keys = 0;
+      sh.threshold = 0xffffffffu;
+    }
+    const int32_t tok = tok_next;
+    float xt = neg_inf();  // the token's logit (thread 0)
+    if (tid == 0) {
+      if (tokens != nullptr && row + row_step < num_rows) tok_next = tokens[row + row_step];
+      const int64_t at = static_cast<int64_t>(tok) - id0;
+      if (tok >= 0 && at >= 0 && at < valid) xt = load_elem<kBf16>(p, static_cast<int>(at));
+    }
+    consumers_sync<kT>();
+
+    float threshold = __int_as_float(0x7f800000);
+    if (k > 0) {
+      threshold = neg_inf();
+      const int held = min(kRing, pc.stages);
+      if (held > 0) {
+        float m = neg_inf();
+        for (int j = 0; j < held; ++j) {
+          const int slot = (g + j) % kRing;
+          ok = ok && warp_wait(smem_u32(&sh.full[slot]), ((g + j) / kRing) & 1, abort_flag);
+          const int n = min(kStageVec, (pc.b1 - pc.b0) / kVec - j * kStageVec);
+          for (int i = tid; i < n; i += kT) m = max_nan(m, vec_max<kBf16>(ring[slot * kStageVec + i]));
+        }
+#pragma unroll
+        for (int off = kPerGroup / 2; off > 0; off >>= 1)
+          m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (tid % kPerGroup == 0) sh.group[tid / kPerGroup] = order_key(m);
+        consumers_sync<kT>();
+        if (tid < kGroups) {
+          const uint32_t me = sh.group[tid];
+          int above = 0;
+#pragma unroll 4
+          for (int i = 0; i < kGroups; i += 4) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(sh.group + i);
+            above += (o.x > me) + (o.y > me) + (o.z > me) + (o.w > me);
+          }
+          // the k-th largest: the smallest with fewer than k above it
+          if (above < k) atomicMin(&sh.threshold, me);
+        }
+        consumers_sync<kT>();
+        threshold = order_value(sh.threshold);
+      }
+    }
+
+    ThreadSums a = {0.0f, kUnset, 0u, 0u};
+    uint32_t mxb = kBf16 ? 0xff80ff80u : 0xff800000u;
+    uint32_t lo = pack_lo<kBf16>(a.limit, threshold);
+    for (int j = 0; j < pc.stages; ++j, ++g) {
+      const int slot = g % kRing;
+      ok = ok && warp_wait(smem_u32(&sh.full[slot]), (g / kRing) & 1, abort_flag);
+      if (!ok) continue;  // (every warp keeps to the rows' barriers)
+      const int at = pc.b0 + j * kStageVec * kVec;
+      const int n = min(kStageVec, (pc.b1 - at) / kVec);
+      const uint4 *st = ring + slot * kStageVec;
 #pragma unroll
       for (int u = 0; u < kVecPerThread; ++u) {
         const int i = u * kT + tid;
         if (i < n) {
           const uint4 q = st[i];
-          const float vm = vec_max<kBf16>(q);
-          mx = max_nan(mx, vm);
-          sums_rebase(a, vm);
-          sums_vector<kBf16>(a, q);
-          if (!(vm < threshold) && k > 0) {
-            float x[kVec];
-            vec_elems<kBf16>(q, x);
-            const int32_t id = id0 + b0 + (j * kStageVec + i) * kVec;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-              if (reaches(x[e], threshold)) push(sh.cand, &sh.count, x[e], id + e);
+          if (vec_reaches<kBf16>(q, mxb, lo)) {
+            const float vm = vec_max<kBf16>(q);
+            sums_rebase(a, vm);
+            lo = pack_lo<kBf16>(a.limit, threshold);
+            if (!(vm < threshold) && k > 0) {
+              const int c = atomicAdd(&sh.num_vecs, 1);
+              if (c < sh.kVecs) {
+                sh.vec[c] = q;
+                sh.vec_id[c] = id0 + at + i * kVec;
+              }
+            }
           }
+          sums_vector<kBf16>(a, q);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
     }
+    if (!ok && lane == 0) raise_abort(&sh.abort, err);
+    float mx = kBf16 ? max_nan(bf16_lo(mxb), bf16_hi(mxb)) : __uint_as_float(mxb);
     // the unaligned ends: at most one element per thread on either side
-    if (nst == 0) threshold = neg_inf();
     for (int side = 0; side < 2; ++side) {
-      const int j = (side == 0 ? c0 : b1) + tid;
-      if (j < (side == 0 ? b0 : c1)) {
+      const int j = (side == 0 ? pc.c0 : pc.b1) + tid;
+      if (j < (side == 0 ? pc.b0 : pc.c1)) {
         const float x = load_elem<kBf16>(p, j);
         mx = max_nan(mx, x);
         sums_rebase(a, x);
         sums_add(a, max_nan(x, kLow), kLow);
-        if (k > 0 && reaches(x, threshold)) push(sh.cand, &sh.count, x, id0 + j);
+        if (k > 0 && reaches(x, threshold)) push_key(sh, x, id0 + j);
       }
     }
-    Lse b = sums_total(a);
+    {
+      Lse b = sums_total(a);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      const Lse o = {__shfl_xor_sync(0xffffffffu, b.r, off), __shfl_xor_sync(0xffffffffu, b.s, off),
-                     __shfl_xor_sync(0xffffffffu, b.w, off)};
-      lse_merge(b, o);
+      for (int off = 16; off > 0; off >>= 1) {
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const Lse o = {__shfl_xor_sync(0xffffffffu, b.r, off),
+                       __shfl_xor_sync(0xffffffffu, b.s, off),
+                       __shfl_xor_sync(0xffffffffu, b.w, off)};
+        lse_merge(b, o);
+      }
+      if (lane == 0) {
+        sh.warp_max[warp] = mx;
+        sh.warp_lse[warp] = b;
+      }
     }
-    if (lane == 0) {
-      sh.warp_max[warp] = mx;
-      sh.warp_lse[warp] = b;
-    }
-  }
-  __syncthreads();  // the copies have landed and every candidate is in the buffer
-  if (warp < kWarps) {
+    consumers_sync<kT>();  // every candidate vector is in the buffer
+
+    // ---- the piece's alternatives into best[]
     if (k > 0) {
-      const int n = sh.count;
-      if (n <= kCandidates) {
-        select_top(sh, sc, n, k, tid);
-        if (n < k) {
+      const int nv = min(sh.num_vecs, sh.kVecs);
+      for (int i = tid; i < nv; i += kT) {
+        float x[kVec];
+        vec_elems<kBf16>(sh.vec[i], x);
+        const int32_t id = sh.vec_id[i];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+          if (reaches(x[e], threshold)) push_key(sh, x[e], id + e);
+      }
+      if (tid < k) sh.best[tid] = 0;
+      consumers_sync<kT>();
+      const int n = sh.num_keys;
+      if (sh.num_vecs <= sh.kVecs && n <= sh.kKeys) {
+        if (tid == 0 && (n & 1)) sh.key[n] = 0;  // (kKeys is even)
+        consumers_sync<kT>();
+        for (int i = tid; i < n; i += kT) {
+          const Key mine = sh.key[i];
+          const int rank = keys_above(sh.key, n, mine);
+          if (rank < k) sh.best[rank] = mine;
+        }
+        if (n < k && warp == 0) {
           // masked elements fill the list, lowest ids first
-          asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
-          if (warp == 0) {
-            int have = n;
-            for (int base = c0; base < c1 && have < k; base += 32) {
-              const int j = base + lane;
-              const bool masked = j < c1 && load_elem<kBf16>(p, j) == neg_inf();
-              const unsigned m = __ballot_sync(0xffffffffu, masked);
-              const int at = have + __popc(m & ((1u << lane) - 1));
-              if (masked && at < k) {
-                sh.best_v[at] = neg_inf();
-                sh.best_id[at] = id0 + j;
-              }
-              have += __popc(m);
-            }
-            if (lane >= have && lane < k) {
-              sh.best_v[lane] = neg_inf();
-              sh.best_id[lane] = kNoId;
-            }
+          int have = n;
+          for (int base = pc.c0; base < pc.c1 && have < k; base += 32) {
+            const int j = base + lane;
+            const bool masked = j < pc.c1 && load_elem<kBf16>(p, j) == neg_inf();
+            const unsigned m = __ballot_sync(0xffffffffu, masked);
+            const int at = have + __popc(m & ((1u << lane) - 1));
+            if (masked && at < k) sh.best[at] = pair_key(neg_inf(), id0 + j);
+            have += __popc(m);
           }
         }
       } else {
-        WarpTop top = {neg_inf(), kNoId, neg_inf(), kNoId};
-        for (int base = c0 + warp * 32; base < c1; base += kT) {
+        Key top = 0;
+        for (int base = pc.c0 + warp * 32; base < pc.c1; base += kT) {
           const int j = base + lane;
-          top_offer(top, j < c1 ? load_elem<kBf16>(p, j) : neg_inf(), j < c1 ? id0 + j : kNoId,
-                    lane, k);
+          top_offer(top, j < pc.c1 ? pair_key(load_elem<kBf16>(p, j), id0 + j) : 0, lane, k);
         }
-        if (lane < k) {
-          sc.list_v[warp * k + lane] = top.v;
-          sc.list_id[warp * k + lane] = top.id;
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+        if (lane < k) sh.list[warp * k + lane] = top;
+        consumers_sync<kT>();
         for (int c = tid; c < kWarps * k; c += kT) {
-          const int rank = rank_in_lists(sc.list_v, sc.list_id, kWarps, k, c / k, c % k);
-          if (rank < k) {
-            sh.best_v[rank] = sc.list_v[c];
-            sh.best_id[rank] = sc.list_id[c];
-          }
+          const Key mine = sh.list[c];
+          const int rank = keys_above(sh.list, kWarps * k, mine);
+          if (mine != 0 && rank < k) sh.best[rank] = mine;
         }
       }
     }
     if (tid == 0) {
       float m = sh.warp_max[0];
-      Lse t = sh.warp_lse[0];
-      for (int w = 1; w < kWarps; ++w) {
-        m = max_nan(m, sh.warp_max[w]);
-        lse_merge(t, sh.warp_lse[w]);
-      }
+      for (int w = 1; w < kWarps; ++w) m = max_nan(m, sh.warp_max[w]);
       sh.max = m;
-      sh.lse = t;
     }
-  }
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
+    if (chunks > 1)
+      cluster.sync();
+    else
+      consumers_sync<kT>();
 
-  // ---- the row: every CTA joins the maxima and restates its sums
-  float row_max = sh.max;
-  for (int c = 0; c < chunks; ++c) row_max = max_nan(row_max, *cluster.map_shared_rank(&sh.max, c));
-  // An extreme finite maximum: sums relative to the maximum itself, in
-  // differences from it, over the piece once more.
-  const bool exact = (row_max > kFastMax && row_max < __int_as_float(0x7f800000)) ||
-                     (row_max < -kFastMax && row_max > neg_inf());
-  if (exact) {
-    float es = 0.0f, ew = 0.0f;
-    if (warp < kWarps) {
-      for (int j = c0 + tid; j < c1; j += kT) {
+    // ---- the row: every CTA joins the maxima and restates its sums
+    float row_max = sh.max;
+    for (int c = 0; c < chunks && chunks > 1; ++c)
+      row_max = max_nan(row_max, *cluster.map_shared_rank(&sh.max, c));
+    // An extreme finite maximum: sums relative to the maximum itself, in
+    // differences from it, over the piece once more.
+    const bool exact = (row_max > kFastMax && row_max < __int_as_float(0x7f800000)) ||
+                       (row_max < -kFastMax && row_max > neg_inf());
+    if (exact) {
+      float es = 0.0f, ew = 0.0f;
+      for (int j = pc.c0 + tid; j < pc.c1; j += kT) {
         const float t = max_nan((load_elem<kBf16>(p, j) - row_max) * kLog2e, -1e30f);
         const float e = ex2(t);
         es += e;
@@ -585,65 +614,72 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
         ew += __shfl_xor_sync(0xffffffffu, ew, off);
       }
       if (lane == 0) sh.warp_lse[warp] = {0.0f, es, ew};
+      consumers_sync<kT>();
     }
-    __syncthreads();
     if (tid == 0) {
-      for (int w = 1; w < kWarps; ++w) {
-        es += sh.warp_lse[w].s;
-        ew += sh.warp_lse[w].w;
+      float s = 0.0f, w = 0.0f;
+      for (int i = 0; i < kWarps; ++i) {
+        const Lse t = sh.warp_lse[i];
+        const float d = exact ? 0.0f : fmaf(-row_max, kLog2e, t.r);
+        const float f = t.s == 0.0f ? 0.0f : ex2(d);
+        s = fmaf(f, t.s, s);
+        if (f != 0.0f) w = fmaf(f, fmaf(d, t.s, t.w), w);
       }
-      sh.lse = {0.0f, es, ew};
+      sh.sum = s;
+      sh.wsum = w;
     }
-  } else if (tid == 0) {
-    const Lse t = sh.lse;
-    const float d = fmaf(-row_max, kLog2e, t.r);
-    const float f = t.s == 0.0f ? 0.0f : ex2(d);
-    sh.lse = {0.0f, f * t.s, f == 0.0f ? 0.0f : f * fmaf(d, t.s, t.w)};
+    const Key *list = sh.best;
+    if (chunks > 1) {
+      cluster.sync();
+      if (chunk == 0)
+        for (int c = tid; c < chunks * k; c += kT)
+          sh.list[c] = *cluster.map_shared_rank(&sh.best[c % k], c / k);
+      list = sh.list;
+    }
+    consumers_sync<kT>();
+    if (chunk == 0) {
+      float s = sh.sum, w = sh.wsum;
+      for (int c = 1; c < chunks; ++c) {
+        s += *cluster.map_shared_rank(&sh.sum, c);
+        w += *cluster.map_shared_rank(&sh.wsum, c);
+      }
+      float lse, entropy;
+      finish_row(row_max, s, w, lse, entropy);
+      if (tid == 0) {
+        if (out.part != nullptr) {
+          out.part[row] = {row_max, s, w, xt};
+        } else {
+          if (out.logprob != nullptr) out.logprob[row] = tok < 0 ? 0.0f : to_logprob(xt, lse);
+          if (out.entropy != nullptr) out.entropy[row] = entropy;
+          if (out.lse != nullptr) out.lse[row] = lse;
+        }
+      }
+      for (int c = tid; c < chunks * k; c += kT) {
+        const Key mine = list[c];
+        int rank = c;
+        if (chunks > 1) {
+          // empty entries (0) come last, in the order they stand
+          rank = 0;
+          for (int i = 0; i < chunks * k; ++i)
+            rank += list[i] > mine || (list[i] == mine && i < c);
+          if (rank >= k) continue;
+        }
+        const float v = key_value(mine);
+        const int32_t id = key_id(mine);
+        if (out.part != nullptr) {
+          out.top[row * k + rank] = {v, id};
+        } else {
+          if (out.top_ids != nullptr) out.top_ids[row * k + rank] = id == kNoId ? -1 : id;
+          if (out.top_logprobs != nullptr) out.top_logprobs[row * k + rank] = to_logprob(v, lse);
+        }
+      }
+    }
+    // what this row kept in shared memory has been read
+    if (chunks > 1)
+      cluster.sync();
+    else
+      consumers_sync<kT>();
   }
-  cluster.sync();
-  pdl_launch_dependents();
-
-  if (chunk == 0) {
-    for (int c = tid; c < chunks * k; c += kT + 32) {
-      sc.list_v[c] = *cluster.map_shared_rank(&sh.best_v[c % k], c / k);
-      sc.list_id[c] = *cluster.map_shared_rank(&sh.best_id[c % k], c / k);
-    }
-    float s = sh.lse.s, w = sh.lse.w;
-    for (int c = 1; c < chunks; ++c) {
-      const Lse o = *cluster.map_shared_rank(&sh.lse, c);
-      s += o.s;
-      w += o.w;
-    }
-    __syncthreads();
-    const int32_t tok = tokens != nullptr ? tokens[row] : -1;
-    const int64_t at = static_cast<int64_t>(tok) - id0;
-    const float xt = tok >= 0 && at >= 0 && at < valid ? load_elem<kBf16>(p, static_cast<int>(at))
-                                                       : neg_inf();
-    float lse, entropy;
-    finish_row(row_max, s, w, lse, entropy);
-    if (tid == 0) {
-      if (out.part != nullptr) {
-        out.part[row] = {row_max, s, w, xt};
-      } else {
-        if (out.logprob != nullptr) out.logprob[row] = tok < 0 ? 0.0f : to_logprob(xt, lse);
-        if (out.entropy != nullptr) out.entropy[row] = entropy;
-        if (out.lse != nullptr) out.lse[row] = lse;
-      }
-    }
-    for (int c = tid; c < chunks * k; c += kT + 32) {
-      const int rank = rank_in_lists(sc.list_v, sc.list_id, chunks, k, c / k, c % k);
-      if (rank >= k) continue;
-      const float v = sc.list_v[c];
-      const int32_t id = sc.list_id[c];
-      if (out.part != nullptr) {
-        out.top[row * k + rank] = {v, id};
-      } else {
-        if (out.top_ids != nullptr) out.top_ids[row * k + rank] = id == kNoId ? -1 : id;
-        if (out.top_logprobs != nullptr) out.top_logprobs[row * k + rank] = to_logprob(v, lse);
-      }
-    }
-  }
-  cluster.sync();  // the pieces' shared memory stays alive until it has been read
 }
 
 // ------------------------------------------------------------------ reduce
@@ -853,7 +889,8 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // Pieces per row: a row is split (in powers of two) while the grid stays
-// within the resident CTAs and a piece keeps a ring stage.
+// within the resident CTAs and a piece keeps a ring stage.  Whole rows go to
+// persistent CTAs.
 int pick_row_chunks(int64_t rows, int64_t nvec, int num_sms) {
   int chunks = 1;
   while (chunks < kMaxChunks && rows * chunks * 2 <= num_sms * 3 && nvec / (2 * chunks) >= 1024)
@@ -863,15 +900,17 @@ int pick_row_chunks(int64_t rows, int64_t nvec, int num_sms) {
 
 template <bool kBf16, int kT>
 cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t shard_start,
-                        int64_t valid, const int32_t *tokens, int top_k, int chunks,
+                        int64_t valid, const int32_t *tokens, int top_k, int chunks, int num_sms,
                         const RowOut &out, uint32_t *err, cudaStream_t stream) {
   auto kern = logprobs_kernel<kBf16, kT>;
+  const int64_t resident = static_cast<int64_t>(num_sms) * (kT == 256 ? 3 : 10);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * chunks));
+  cfg.gridDim = dim3(static_cast<unsigned>(chunks > 1 || rows < resident ? rows * chunks
+                                                                         : resident));
   cfg.blockDim = dim3(kT + 32);
   cfg.dynamicSmemBytes = ring_bytes<kT>;
   cfg.stream = stream;
-  if (ring_bytes<kT> > 40 * 1024) {
+  if (kT == 256) {
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), ring_bytes<kT>,
                                         kBf16 ? 0 : 1);
     if (e != cudaSuccess) return e;
@@ -886,7 +925,7 @@ cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t sh
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits),
-                            ld * (kBf16 ? 2 : 4), static_cast<int>(valid),
+                            ld * (kBf16 ? 2 : 4), rows, static_cast<int>(valid),
                             static_cast<int32_t>(shard_start), tokens, top_k, chunks, out, err);
 }
 
@@ -904,13 +943,13 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t
   const bool small = chunks == 1 && nvec <= 2048 && rows > num_sms;
   if (dtype == SGA_BF16)
     return small ? launch_rows<true, 64>(logits, rows, ld, shard_start, valid, tokens, top_k,
-                                         chunks, out, err, stream)
+                                         chunks, num_sms, out, err, stream)
                  : launch_rows<true, 256>(logits, rows, ld, shard_start, valid, tokens, top_k,
-                                          chunks, out, err, stream);
+                                          chunks, num_sms, out, err, stream);
   return small ? launch_rows<false, 64>(logits, rows, ld, shard_start, valid, tokens, top_k,
-                                        chunks, out, err, stream)
+                                        chunks, num_sms, out, err, stream)
                : launch_rows<false, 256>(logits, rows, ld, shard_start, valid, tokens, top_k,
-                                         chunks, out, err, stream);
+                                         chunks, num_sms, out, err, stream);
 }
 
 cudaError_t launch_logprob_reduce(const sga_logprob_part *parts, const sga_stat *tops,
