@@ -357,19 +357,25 @@ def sga_lmhead_argmax_shards_fp8(hidden_q, hidden_scale, weight_q, weight_scale,
 
 
 def _bf16_rows(t, rows, cols, name):
-    """Row stride of a bf16 [rows, cols] tensor with unit column stride."""
-    if t.dtype != torch.bfloat16 or t.shape != (rows, cols) or (
-            cols > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be bf16 [{rows}, {cols}] with unit column stride")
-    return t.stride(0) if rows > 1 else cols  # the stride of a single row is never used
-
-
-def _bias_code(t, n, name):
+    """(address, row stride) of a bf16 [rows, cols] tensor with unit column
+    stride; (None, 0) for None."""
     if t is None:
-        return SGA_F32
+        return None, 0
+    if t.dtype is not torch.bfloat16 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must be bf16 [{rows}, {cols}]")
+    row, col = t.stride()
+    if col != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), row if rows > 1 else cols  # a single row's stride is never used
+
+
+def _bias(t, n, name):
+    """(address, dtype code) of a float32 or bf16 vector of n, or (None, SGA_F32)."""
+    if t is None:
+        return None, SGA_F32
     if t.dtype not in (torch.float32, torch.bfloat16) or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 or bf16 tensor of {n} elements")
-    return SGA_F32 if t.dtype == torch.float32 else SGA_BF16
+    return t.data_ptr(), SGA_F32 if t.dtype is torch.float32 else SGA_BF16
 
 
 def sga_linear(x, weight, out, bias=None, act=SGA_ACT_NONE, residual=None, out_preact=None,
@@ -381,14 +387,15 @@ def sga_linear(x, weight, out, bias=None, act=SGA_ACT_NONE, residual=None, out_p
     sga_linear_grad needs when there is an activation (see include/sga.h)."""
     M, K = x.shape
     N = weight.size(0)
-    ldx, ldw = _bf16_rows(x, M, K, "x"), _bf16_rows(weight, N, K, "weight")
-    ldo = _bf16_rows(out, M, N, "out")
-    ldr = 0 if residual is None else _bf16_rows(residual, M, N, "residual")
-    ldp = 0 if out_preact is None else _bf16_rows(out_preact, M, N, "out_preact")
-    code = _bias_code(bias, N, "bias")
+    px, ldx = _bf16_rows(x, M, K, "x")
+    pw, ldw = _bf16_rows(weight, N, K, "weight")
+    po, ldo = _bf16_rows(out, M, N, "out")
+    pr, ldr = _bf16_rows(residual, M, N, "residual")
+    pp, ldp = _bf16_rows(out_preact, M, N, "out_preact")
+    pb, code = _bias(bias, N, "bias")
     _check("sga_linear", lib().sga_linear(
-        _ptr(x), M, K, ldx, _ptr(weight), N, ldw, _ptr(bias), code, int(act), _ptr(residual), ldr,
-        _ptr(out_preact), ldp, _ptr(out), ldo, _stream(stream)))
+        px, M, K, ldx, pw, N, ldw, pb, code, int(act), pr, ldr, pp, ldp, po, ldo,
+        _raw_stream(stream)))
     return out
 
 
@@ -404,42 +411,59 @@ def sga_linear_grad(grad_out, x, weight, workspace, act=SGA_ACT_NONE, preact=Non
     CUDA tensor of at least sga_linear_grad_workspace(M, N, K) bytes."""
     M, K = x.shape
     N = weight.size(0)
-    ldx, ldw = _bf16_rows(x, M, K, "x"), _bf16_rows(weight, N, K, "weight")
-    ldg = _bf16_rows(grad_out, M, N, "grad_out")
-    ldp = 0 if preact is None else _bf16_rows(preact, M, N, "preact")
-    ldgx = 0 if grad_x is None else _bf16_rows(grad_x, M, K, "grad_x")
-    ldgw = 0 if grad_weight is None else _bf16_rows(grad_weight, N, K, "grad_weight")
-    code = _bias_code(grad_bias, N, "grad_bias")
+    px, ldx = _bf16_rows(x, M, K, "x")
+    pw, ldw = _bf16_rows(weight, N, K, "weight")
+    pg, ldg = _bf16_rows(grad_out, M, N, "grad_out")
+    pp, ldp = _bf16_rows(preact, M, N, "preact")
+    pgx, ldgx = _bf16_rows(grad_x, M, K, "grad_x")
+    pgw, ldgw = _bf16_rows(grad_weight, N, K, "grad_weight")
+    pb, code = _bias(grad_bias, N, "grad_bias")
     _check("sga_linear_grad", lib().sga_linear_grad(
-        _ptr(grad_out), M, N, ldg, _ptr(preact), ldp, int(act), _ptr(x), K, ldx, _ptr(weight),
-        ldw, _ptr(grad_x), ldgx, _ptr(grad_weight), ldgw, _ptr(grad_bias), code, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+        pg, M, N, ldg, pp, ldp, int(act), px, K, ldx, pw, ldw, pgx, ldgx, pgw, ldgw, pb, code,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
+
+
+# The calls below run beside single-token steps of a few microseconds, so their
+# marshalling is kept short: plain integers for pointers (ctypes takes them for
+# c_void_p) and the raw handle of the current stream.
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check_out(t, dtype, numel, name):
-    """A contiguous CUDA tensor of `dtype` with `numel` elements, or None."""
-    if t is not None and not (t.dtype == dtype and t.numel() == numel and t.is_contiguous()):
+    """Address of a contiguous tensor of `dtype` with `numel` elements, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements")
+    return t.data_ptr()
 
 
 def _logits_2d(logits):
-    if logits.dim() != 2 or (logits.size(1) > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be 2-D with unit stride along the vocab")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D")
     rows, width = logits.shape
-    return rows, width, logits.stride(0) if rows > 1 else max(logits.stride(0), width)
+    ld, col = logits.stride()
+    if col != 1 and width > 1:
+        raise ValueError("logits must have unit stride along the vocab")
+    return rows, width, ld if rows > 1 else max(ld, width)
 
 
 def _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids, out_top_logprobs):
-    """Checks the per-row tensors of the log-probability calls; returns top_k."""
-    _check_out(tokens, torch.int32, rows, "tokens")
-    _check_out(out_logprob, torch.float32, rows, "out_logprob")
-    _check_out(out_entropy, torch.float32, rows, "out_entropy")
-    _check_out(out_lse, torch.float32, rows, "out_lse")
+    """top_k and the addresses of the per-row tensors of the log-probability calls."""
     top = out_top_ids if out_top_ids is not None else out_top_logprobs
     k = 0 if top is None else top.size(-1)
-    _check_out(out_top_ids, torch.int32, rows * k, "out_top_ids")
-    _check_out(out_top_logprobs, torch.float32, rows * k, "out_top_logprobs")
-    return k
+    f32, i32 = torch.float32, torch.int32
+    return k, (_check_out(tokens, i32, rows, "tokens"),
+               _check_out(out_logprob, f32, rows, "out_logprob"),
+               _check_out(out_entropy, f32, rows, "out_entropy"),
+               _check_out(out_lse, f32, rows, "out_lse"),
+               _check_out(out_top_ids, i32, rows * k, "out_top_ids"),
+               _check_out(out_top_logprobs, f32, rows * k, "out_top_logprobs"))
 
 
 def sga_token_logprobs(logits, org_vocab, tokens=None, out_logprob=None, out_entropy=None,
@@ -450,12 +474,11 @@ def sga_token_logprobs(logits, org_vocab, tokens=None, out_logprob=None, out_ent
     are contiguous CUDA tensors or None: float32 [rows], and int32 / float32
     [rows, top_k], whose last size is top_k (see include/sga.h)."""
     rows, width, ld = _logits_2d(logits)
-    k = _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
-                     out_top_logprobs)
+    k, (tok, *outs) = _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
+                                   out_top_logprobs)
     _check("sga_token_logprobs", lib().sga_token_logprobs(
-        _ptr(logits), _dtype_code(logits), rows, ld, width, int(org_vocab), _ptr(tokens), k,
-        _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse), _ptr(out_top_ids),
-        _ptr(out_top_logprobs), _stream(stream)))
+        logits.data_ptr(), _dtype_code(logits), rows, ld, width, int(org_vocab), tok, k, *outs,
+        _raw_stream(stream)))
 
 
 def sga_local_logprobs(logits, shard_start, shard_width, org_vocab, tokens, out_parts,
@@ -468,12 +491,11 @@ def sga_local_logprobs(logits, shard_start, shard_width, org_vocab, tokens, out_
     if width < shard_width:
         raise ValueError("logits has fewer columns than the shard")
     k = 0 if out_top is None else out_top.size(-2)
-    _check_out(tokens, torch.int32, rows, "tokens")
-    _check_out(out_parts, torch.float32, 4 * rows, "out_parts")
-    _check_out(out_top, torch.int32, 2 * k * rows, "out_top")
     _check("sga_local_logprobs", lib().sga_local_logprobs(
-        _ptr(logits), _dtype_code(logits), rows, ld, int(shard_start), int(shard_width),
-        int(org_vocab), _ptr(tokens), k, _ptr(out_parts), _ptr(out_top), _stream(stream)))
+        logits.data_ptr(), _dtype_code(logits), rows, ld, int(shard_start), int(shard_width),
+        int(org_vocab), _check_out(tokens, torch.int32, rows, "tokens"), k,
+        _check_out(out_parts, torch.float32, 4 * rows, "out_parts"),
+        _check_out(out_top, torch.int32, 2 * k * rows, "out_top"), _raw_stream(stream)))
     return out_parts
 
 
@@ -482,18 +504,16 @@ def sga_logprob_reduce(parts, tops, num_shards, tokens=None, out_logprob=None, o
     """Results of sga_token_logprobs from the gathered parts (float32
     [num_shards, rows, 4]) and lists (int32 [num_shards, rows, top_k, 2] or
     None)."""
-    rows = parts.numel() // (4 * int(num_shards))
-    k = _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
-                     out_top_logprobs)
-    _check_out(parts, torch.float32, 4 * rows * num_shards, "parts")
+    num_shards = int(num_shards)
+    rows = parts.numel() // (4 * num_shards)
+    k, (tok, *outs) = _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
+                                   out_top_logprobs)
     if k and tops is None:
         raise ValueError("alternatives are asked for without tops")
-    if k:
-        _check_out(tops, torch.int32, 2 * k * rows * num_shards, "tops")
     _check("sga_logprob_reduce", lib().sga_logprob_reduce(
-        _ptr(parts), _ptr(tops) if k else None, int(num_shards), rows, k, _ptr(tokens),
-        _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse), _ptr(out_top_ids),
-        _ptr(out_top_logprobs), _stream(stream)))
+        _check_out(parts, torch.float32, 4 * rows * num_shards, "parts"),
+        _check_out(tops, torch.int32, 2 * k * rows * num_shards, "tops") if k else None,
+        num_shards, rows, k, tok, *outs, _raw_stream(stream)))
 
 
 def sga_token_logprobs_grad(logits, shard_start, org_vocab, tokens, lse, entropy, grad_logprob,
@@ -509,16 +529,16 @@ def sga_token_logprobs_grad(logits, shard_start, org_vocab, tokens, lse, entropy
         raise ValueError("out_grad must match logits, unit stride along the vocab")
     ldg = out_grad.stride(0) if rows > 1 else max(out_grad.stride(0), width)
     k = 0 if top_ids is None else top_ids.size(-1)
-    _check_out(tokens, torch.int32, rows, "tokens")
-    for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob"),
-                    (grad_entropy, "grad_entropy")):
-        _check_out(t, torch.float32, rows, name)
-    _check_out(top_ids, torch.int32, rows * k, "top_ids")
-    _check_out(grad_top, torch.float32, rows * k, "grad_top")
+    f32, i32 = torch.float32, torch.int32
     _check("sga_token_logprobs_grad", lib().sga_token_logprobs_grad(
-        _ptr(logits), _dtype_code(logits), rows, ld, int(shard_start), width, int(org_vocab),
-        _ptr(tokens), _ptr(lse), _ptr(entropy), _ptr(grad_logprob), _ptr(grad_entropy), k,
-        _ptr(top_ids), _ptr(grad_top), _ptr(out_grad), ldg, _stream(stream)))
+        logits.data_ptr(), _dtype_code(logits), rows, ld, int(shard_start), width, int(org_vocab),
+        _check_out(tokens, i32, rows, "tokens"), _check_out(lse, f32, rows, "lse"),
+        _check_out(entropy, f32, rows, "entropy"),
+        _check_out(grad_logprob, f32, rows, "grad_logprob"),
+        _check_out(grad_entropy, f32, rows, "grad_entropy"), k,
+        _check_out(top_ids, i32, rows * k, "top_ids"),
+        _check_out(grad_top, f32, rows * k, "grad_top"), out_grad.data_ptr(), ldg,
+        _raw_stream(stream)))
     return out_grad
 
 
