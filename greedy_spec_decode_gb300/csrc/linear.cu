@@ -26,8 +26,13 @@ namespace {
 
 // ------------------------------------------------------------- activations
 
-__device__ __forceinline__ float sigmoid_times(float z, float u) {  // z / (1 + e^-u)
-  return __fdividef(z, 1.0f + __expf(-u));
+// z / (1 + e^-u) with the hardware's 2^x and 1/x (2 ulp each; e^-u past the
+// range of fp32 gives 0, as it should).
+__device__ __forceinline__ float sigmoid_times(float z, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(u * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return z * r;
 }
 
 constexpr float kGeluA = 0.7978845608028654f;  // sqrt(2 / pi)
@@ -55,8 +60,11 @@ __device__ __forceinline__ float activate_grad(float z, int act) {
       return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z),
                   0.5f * (1.0f + erff(z * 0.7071067811865476f)));
     case SGA_ACT_GELU_TANH: {
-      const float q = sigmoid_times(1.0f, 2.0f * kGeluA * fmaf(kGeluB * z * z, z, z));
-      const float du = 2.0f * kGeluA * fmaf(3.0f * kGeluB * z, z, 1.0f);
+      // beyond +-16 the derivative is 0 or 1 (and z^3 stays finite below)
+      z = z < -16.0f ? -16.0f : (z > 16.0f ? 16.0f : z);
+      const float z2 = z * z;
+      const float q = sigmoid_times(1.0f, z * fmaf(2.0f * kGeluA * kGeluB, z2, 2.0f * kGeluA));
+      const float du = fmaf(6.0f * kGeluA * kGeluB, z2, 2.0f * kGeluA);
       return fmaf(z * q * (1.0f - q), du, q);
     }
     default: return 1.0f;
@@ -148,11 +156,30 @@ struct Product {
   Epilogue ep;
 };
 
+// Pair i of CTAs takes tiles i, i + pairs, ... of product 0 and a contiguous
+// run of product 1's: `lead` pairs (those with one tile more of product 0)
+// take runs of run[0], the others of run[1], so that all end together although
+// the two products' tiles differ in length.
 struct Products {
-  int n;
-  int tile0[kMaxProducts + 1];  // first tile number of each product
+  int tiles[kMaxProducts];  // (0: no such product)
+  int lead, run[2];
   Product p[kMaxProducts];
 };
+
+// The i-th tile of a pair: product and tile number; false past its last.
+__device__ __forceinline__ bool pair_tile(const Products &prods, int pair, int num_pairs, int i,
+                                          int &pi, int &t) {
+  pi = 0;
+  t = pair + i * num_pairs;
+  if (t < prods.tiles[0]) return true;
+  const int own = prods.tiles[0] / num_pairs + (pair < prods.lead ? 1 : 0);
+  const int run = prods.run[pair < prods.lead ? 0 : 1];
+  const int first = pair < prods.lead ? pair * prods.run[0]
+                                      : prods.lead * prods.run[0] + (pair - prods.lead) * prods.run[1];
+  pi = 1;
+  t = first + i - own;
+  return i - own < run && t < prods.tiles[1];
+}
 
 struct Maps {
   CUtensorMap a[kMaxProducts], b[kMaxProducts];
@@ -261,54 +288,76 @@ __device__ __forceinline__ void box_load_rows(uint8_t *box, const __nv_bfloat16 
   }
 }
 
-// Accumulators -> box: columns taddr .. + 63 of this warp's 32 TMEM lanes (a
-// lane per row), plus bias, through the activation, plus what the box holds
-// when `add` (the residual).  32 columns at a time: unrolled further, the
-// longer activations outgrow the instruction cache.
+// Eight accumulators (columns 8 j .. + 7 of the box) -> box: plus bias, through
+// the activation, plus what the box holds there when `add` (the residual).
 template <int kAct>
+__device__ __forceinline__ void box_fill_piece(uint8_t *box, const uint32_t *r, const float *bias,
+                                               int j, bool add, int lane) {
+  uint4 *q = box_piece(box, lane, j);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 b = *reinterpret_cast<const float4 *>(bias + j * 8 + i);
+    y[i] = activate(__uint_as_float(r[i]) + b.x, kAct);
+    y[i + 1] = activate(__uint_as_float(r[i + 1]) + b.y, kAct);
+    y[i + 2] = activate(__uint_as_float(r[i + 2]) + b.z, kAct);
+    y[i + 3] = activate(__uint_as_float(r[i + 3]) + b.w, kAct);
+  }
+  if (add) {
+    const uint4 w = *q;
+    y[0] += bf16_lo(w.x);
+    y[1] += bf16_hi(w.x);
+    y[2] += bf16_lo(w.y);
+    y[3] += bf16_hi(w.y);
+    y[4] += bf16_lo(w.z);
+    y[5] += bf16_hi(w.z);
+    y[6] += bf16_lo(w.w);
+    y[7] += bf16_hi(w.w);
+  }
+  *q = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+}
+
+// Columns taddr .. + 63 of this warp's 32 TMEM lanes (a lane per row) -> box.
+// `done` runs once the accumulators are in registers.  All 64 columns are
+// asked for at once (a tcgen05.ld and its wait take some 300 cycles), but for
+// the erf activation, whose code, unrolled 64 times, would outgrow the
+// instruction cache.
+template <int kAct, typename Done>
 __device__ __forceinline__ void box_fill_act(uint8_t *box, uint32_t taddr, const float *bias,
-                                             bool add, int lane) {
+                                             bool add, int lane, Done done) {
+  if constexpr (kAct == SGA_ACT_GELU) {
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    uint32_t r[32];
-    tmem_ld32(taddr + h * 32, r);
-    tmem_ld_wait();
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[32];
+      tmem_ld32(taddr + h * 32, r);
+      tmem_ld_wait();
+      if (h == 1) done();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint4 *q = box_piece(box, lane, h * 4 + j);
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 b = *reinterpret_cast<const float4 *>(bias + h * 32 + j * 8 + i);
-        y[i] = activate(__uint_as_float(r[j * 8 + i]) + b.x, kAct);
-        y[i + 1] = activate(__uint_as_float(r[j * 8 + i + 1]) + b.y, kAct);
-        y[i + 2] = activate(__uint_as_float(r[j * 8 + i + 2]) + b.z, kAct);
-        y[i + 3] = activate(__uint_as_float(r[j * 8 + i + 3]) + b.w, kAct);
-      }
-      if (add) {
-        const uint4 w = *q;
-        y[0] += bf16_lo(w.x);
-        y[1] += bf16_hi(w.x);
-        y[2] += bf16_lo(w.y);
-        y[3] += bf16_hi(w.y);
-        y[4] += bf16_lo(w.z);
-        y[5] += bf16_hi(w.z);
-        y[6] += bf16_lo(w.w);
-        y[7] += bf16_hi(w.w);
-      }
-      *q = make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+      for (int j = 0; j < 4; ++j)
+        box_fill_piece<kAct>(box, r + j * 8, bias, h * 4 + j, add, lane);
     }
+  } else {
+    uint32_t r[2][32];
+    tmem_ld32(taddr, r[0]);
+    tmem_ld32(taddr + 32, r[1]);
+    tmem_ld_wait();
+    done();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      box_fill_piece<kAct>(box, r[j / 4] + j % 4 * 8, bias, j, add, lane);
   }
 }
 
+template <typename Done>
 __device__ __forceinline__ void box_fill(uint8_t *box, uint32_t taddr, const float *bias, int act,
-                                         bool add, int lane) {
+                                         bool add, int lane, Done done) {
   switch (act) {
-    case SGA_ACT_RELU: return box_fill_act<SGA_ACT_RELU>(box, taddr, bias, add, lane);
-    case SGA_ACT_SILU: return box_fill_act<SGA_ACT_SILU>(box, taddr, bias, add, lane);
-    case SGA_ACT_GELU: return box_fill_act<SGA_ACT_GELU>(box, taddr, bias, add, lane);
-    case SGA_ACT_GELU_TANH: return box_fill_act<SGA_ACT_GELU_TANH>(box, taddr, bias, add, lane);
-    default: return box_fill_act<SGA_ACT_NONE>(box, taddr, bias, add, lane);
+    case SGA_ACT_RELU: return box_fill_act<SGA_ACT_RELU>(box, taddr, bias, add, lane, done);
+    case SGA_ACT_SILU: return box_fill_act<SGA_ACT_SILU>(box, taddr, bias, add, lane, done);
+    case SGA_ACT_GELU: return box_fill_act<SGA_ACT_GELU>(box, taddr, bias, add, lane, done);
+    case SGA_ACT_GELU_TANH:
+      return box_fill_act<SGA_ACT_GELU_TANH>(box, taddr, bias, add, lane, done);
+    default: return box_fill_act<SGA_ACT_NONE>(box, taddr, bias, add, lane, done);
   }
 }
 
@@ -332,7 +381,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const bool leader = rank == 0;
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int num_pairs = static_cast<int>(gridDim.x >> 1);
-  const int total = prods.tile0[prods.n];
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -368,12 +416,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   if (warp == 0) {
     // -------------------------------------------------- producer (both CTAs)
-    int pi = 0;
-    for (int t = pair; t < total && !aborted(abort_flag); t += num_pairs) {
-      while (t >= prods.tile0[pi + 1]) ++pi;
+    int pi, t;
+    for (int n = 0; pair_tile(prods, pair, num_pairs, n, pi, t) && !aborted(abort_flag); ++n) {
       const Product &p = prods.p[pi];
       int tr, tc;
-      tile_at(p, t - prods.tile0[pi], tr, tc);
+      tile_at(p, t, tr, tc);
       const int row = tr * 256 + static_cast<int>(rank) * 128;
       const int col = tc * kBN + static_cast<int>(rank) * (kBN / 2);
       // held in registers: inside the loop the asm statements would make the
@@ -414,11 +461,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   } else if (warp == 1 && leader) {
     // --------------------------------------------------- MMA issuer (leader)
-    int stage = 0, acc = 0, pi = 0;
+    int stage = 0, acc = 0, pi, t;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    for (int t = pair; t < total && ok && !aborted(abort_flag); t += num_pairs) {
-      while (t >= prods.tile0[pi + 1]) ++pi;
+    for (int n = 0;
+         pair_tile(prods, pair, num_pairs, n, pi, t) && ok && !aborted(abort_flag); ++n) {
       const Product &p = prods.p[pi];
       const int num_kb = p.num_kb;
       const bool a_strided = p.a_strided != 0, b_strided = p.b_strided != 0;
@@ -469,14 +516,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const uint32_t res_bar = smem_u32(&sh->res_full[warp - 2]);
     const uint32_t empty_leader[2] = {map_to_rank(smem_u32(&sh->tmem_empty[0]), 0),
                                       map_to_rank(smem_u32(&sh->tmem_empty[1]), 0)};
-    int acc = 0, pi = 0;
+    int acc = 0, pi, t;
     uint32_t acc_phase = 0, res_phase = 0;
     bool ok = true, res_inflight = false;
-    for (int t = pair; t < total && ok; t += num_pairs) {
-      while (t >= prods.tile0[pi + 1]) ++pi;
+    for (int n = 0; ok && pair_tile(prods, pair, num_pairs, n, pi, t); ++n) {
       const Product &p = prods.p[pi];
       int tr, tc;
-      tile_at(p, t - prods.tile0[pi], tr, tc);
+      tile_at(p, t, tr, tc);
       const Epilogue ep = p.ep;
       const int cols = p.cols;
       const int row0 = tr * 256 + static_cast<int>(rank) * 128 + quarter * 32;
@@ -535,13 +581,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         tc_fence_after();
         const uint32_t tlane =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN;
+        // the accumulators have been read: the MMA may overwrite them.  (Early:
+        // an arrival at the peer waits for the writes before it.)
+        bool released = false;
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              mbar_arrive(smem_u32(&sh->tmem_empty[acc]));
+            else
+              mbar_arrive_remote(empty_leader[acc]);
+          }
+          released = true;
+        };
 #pragma unroll 1
         for (int q = half * 64; q < kBN; q += 128) {
           const int col0 = tc * kBN + q;
           if (rows <= 0 || col0 >= cols) break;
+          const bool last = q + 128 >= kBN || col0 + 128 >= cols;
           if (!res_ready) box_free();
           if (ep.pre != nullptr) {
-            box_fill_act<SGA_ACT_NONE>(box, tlane + q, sh->bias + q, false, lane);
+            box_fill_act<SGA_ACT_NONE>(box, tlane + q, sh->bias + q, false, lane, [] {});
             store(ep.tma_pre, map_pre, ep.pre, ep.ldp, col0);
             box_free();
           }
@@ -558,24 +619,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
               res_phase ^= 1;
             }
           }
-          box_fill(box, tlane + q, sh->bias + q, ep.act, ep.res != nullptr, lane);
+          box_fill(box, tlane + q, sh->bias + q, ep.act, ep.res != nullptr, lane, [&] {
+            if (last) release();
+          });
           store(ep.tma_out, map_out, ep.out, ep.ldo, col0);
         }
-        // the accumulators have been read: the MMA may overwrite them
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader)
-            mbar_arrive(smem_u32(&sh->tmem_empty[acc]));
-          else
-            mbar_arrive_remote(empty_leader[acc]);
-        }
+        if (!released) release();
       }
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
       // (an epilogue warp that gives up keeps to the barriers of the others)
       if (!ok) {
-        for (int u = t + num_pairs; u < total; u += num_pairs) {
+        for (int u = n + 1; pair_tile(prods, pair, num_pairs, u, pi, t); ++u) {
           asm volatile("bar.sync 1, 256;" ::: "memory");
           asm volatile("bar.sync 1, 256;" ::: "memory");
         }
@@ -850,63 +905,127 @@ __global__ void __launch_bounds__(THREADS, 2)
 }
 
 // ---------------------------------------------------------------------------
-// dz = g * act'(z) in bf16 and the partial column sums of dz (fp32, before the
-// rounding).  A CTA covers 64 columns x kDzRows rows: a warp per row, two
-// columns a lane.
+// dz = g * act'(z) in bf16 (dz nullable) and db = the column sums of dz in
+// fp32, before the rounding (db nullable).  HBM-bound: g and z are read once
+// and dz written once.  A cluster covers a strip of 64 columns, its CTAs
+// contiguous ranges of rows; their column sums meet in the first CTA through
+// distributed shared memory, in a fixed order, so db needs no second launch.
+// Wide: eight lanes of 16 bytes per row, 32 rows at a time; narrow (rows not on
+// 16-byte boundaries): a warp per row, two columns a lane.
 // ---------------------------------------------------------------------------
-constexpr int kDzRows = 128;
 constexpr int kDzThreads = 256;
+constexpr int kDzCols = 64;
+constexpr int kDzMaxSplits = 8;
 
-__global__ void __launch_bounds__(kDzThreads)
-    dz_kernel(const __nv_bfloat16 *__restrict__ g, int64_t ldg,
-              const __nv_bfloat16 *__restrict__ z, int64_t ldz, int act, int M, int N,
-              __nv_bfloat16 *__restrict__ dz, int64_t lddz, float *__restrict__ partial) {
-  __shared__ float2 sums[kDzThreads / 32][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 64 + 2 * lane;
-  const int m0 = blockIdx.y * kDzRows, m1 = min(M, m0 + kDzRows);
-  pdl_wait();
-  float2 s = {0.0f, 0.0f};
-  for (int m = m0 + warp; m < m1; m += kDzThreads / 32) {
-    float d[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (c + i < N) {
-        d[i] = ld_bf16(g + m * ldg + c + i);
-        if (act != SGA_ACT_NONE) d[i] *= activate_grad(ld_bf16(z + m * ldz + c + i), act);
-        if (dz != nullptr) dz[m * lddz + c + i] = __float2bfloat16_rn(d[i]);
-      }
-    }
-    s.x += d[0];
-    s.y += d[1];
-  }
-  pdl_launch_dependents();
-  if (partial == nullptr) return;
-  sums[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < kDzThreads / 32; ++w) {
-      s.x += sums[w][lane].x;
-      s.y += sums[w][lane].y;
-    }
-    float *q = partial + static_cast<int64_t>(blockIdx.y) * N + c;
-    if (c < N) q[0] = s.x;
-    if (c + 1 < N) q[1] = s.y;
-  }
+// (A product of its own, not contracted into the column sum: db is the same
+// whether dz is asked for or not.)
+template <int kAct>
+__device__ __forceinline__ float dz_term(float g, float z) {
+  return kAct == SGA_ACT_NONE ? g : __fmul_rn(g, activate_grad(z, kAct));
 }
 
-__global__ void bias_grad_kernel(const float *__restrict__ partial, int n, int N,
-                                 void *__restrict__ db, int f32) {
+template <int kAct, bool kWide>
+__global__ void __launch_bounds__(kDzThreads)
+    dz_kernel(const __nv_bfloat16 *__restrict__ g, int64_t ldg,
+              const __nv_bfloat16 *__restrict__ z, int64_t ldz, int M, int N, int splits,
+              __nv_bfloat16 *__restrict__ dz, int64_t lddz, void *__restrict__ db, int f32) {
+  constexpr int kRowsAtOnce = kWide ? 32 : 8;
+  constexpr int kOwn = kWide ? 8 : 2;  // columns per thread
+  constexpr int kBatch = 4;  // rows in flight per thread
+  __shared__ float sums[kRowsAtOnce][kDzCols];
+  __shared__ float total[kDzCols];
+  const int tid = threadIdx.x;
+  const int split = static_cast<int>(blockIdx.x) % splits;
+  const int strip = static_cast<int>(blockIdx.x) / splits;
+  const int m0 = static_cast<int>(static_cast<int64_t>(M) * split / splits);
+  const int m1 = static_cast<int>(static_cast<int64_t>(M) * (split + 1) / splits);
+  const int r0 = kWide ? tid >> 3 : tid >> 5;
+  const int c0 = kWide ? (tid & 7) * 8 : tid & 31;  // wide: c0 .. + 7; narrow: c0, c0 + 32
+  const int64_t col = static_cast<int64_t>(strip) * kDzCols + c0;
   pdl_wait();
+  float s[kOwn] = {};
+  if (kWide && col + 8 <= N) {
+    for (int m = m0 + r0; m < m1; m += kBatch * kRowsAtOnce) {
+      uint4 vg[kBatch], vz[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t r = m + u * kRowsAtOnce;
+        if (r < m1) {
+          vg[u] = ld_stream_v4(g + r * ldg + col);
+          if (kAct != SGA_ACT_NONE) vz[u] = ld_stream_v4(z + r * ldz + col);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int64_t r = m + u * kRowsAtOnce;
+        if (r >= m1) continue;
+        const uint32_t wg[4] = {vg[u].x, vg[u].y, vg[u].z, vg[u].w};
+        const uint32_t wz[4] = {vz[u].x, vz[u].y, vz[u].z, vz[u].w};
+        uint32_t wo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float d0 = dz_term<kAct>(bf16_lo(wg[i]), bf16_lo(wz[i]));
+          const float d1 = dz_term<kAct>(bf16_hi(wg[i]), bf16_hi(wz[i]));
+          s[2 * i % kOwn] += d0;
+          s[(2 * i + 1) % kOwn] += d1;
+          wo[i] = pack2(d0, d1);
+        }
+        if (dz != nullptr)
+          *reinterpret_cast<uint4 *>(dz + r * lddz + col) = make_uint4(wo[0], wo[1], wo[2], wo[3]);
+      }
+    }
+  } else {
+    constexpr int kStep = kWide ? 1 : 32;  // (wide: the strip's ragged end)
+    for (int m = m0 + r0; m < m1; m += kBatch * kRowsAtOnce) {
+      float vg[kBatch][kOwn], vz[kBatch][kOwn];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          const int64_t r = m + u * kRowsAtOnce, c = col + i * kStep;
+          vg[u][i] = vz[u][i] = 0.0f;
+          if (r < m1 && c < N) {
+            vg[u][i] = ld_bf16(g + r * ldg + c);
+            if (kAct != SGA_ACT_NONE) vz[u][i] = ld_bf16(z + r * ldz + c);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          const int64_t r = m + u * kRowsAtOnce, c = col + i * kStep;
+          if (r < m1 && c < N) {
+            const float d = dz_term<kAct>(vg[u][i], vz[u][i]);
+            s[i] += d;
+            if (dz != nullptr) dz[r * lddz + c] = __float2bfloat16_rn(d);
+          }
+        }
+      }
+    }
+  }
   pdl_launch_dependents();
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= N) return;
-  float s = 0.0f;
-  for (int i = 0; i < n; ++i) s += partial[static_cast<int64_t>(i) * N + c];
-  if (f32)
-    static_cast<float *>(db)[c] = s;
-  else
-    static_cast<__nv_bfloat16 *>(db)[c] = __float2bfloat16_rn(s);
+  if (db == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) sums[r0][kWide ? c0 + i : c0 + 32 * i] = s[i];
+  __syncthreads();
+  if (tid < kDzCols) {
+    float t = 0.0f;
+    for (int r = 0; r < kRowsAtOnce; ++r) t += sums[r][tid];
+    total[tid] = t;
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  if (split == 0 && tid < kDzCols && strip * kDzCols + tid < N) {
+    float t = 0.0f;
+    for (int i = 0; i < splits; ++i) t += cluster.map_shared_rank(total, i)[tid];
+    const int c = strip * kDzCols + tid;
+    if (f32)
+      static_cast<float *>(db)[c] = t;
+    else
+      static_cast<__nv_bfloat16 *>(db)[c] = __float2bfloat16_rn(t);
+  }
+  cluster.sync();  // the totals stay alive until they have been read
 }
 
 // ------------------------------------------------------------------ host
@@ -945,6 +1064,10 @@ bool operand_map(CUtensorMap *map, const Operand &o, int64_t other, int64_t summ
                    : make_map_ld(map, o.ptr, other, summed, o.ld, box);
 }
 
+// Length of a tile in K blocks: its own, at least what its epilogue takes, and
+// the turn of the pipeline between tiles.
+int64_t tile_cost(int num_kb) { return (num_kb > 12 ? num_kb : 12) + 2; }
+
 // Map of a result (or residual) matrix, where TMA can reach it: a 16-byte
 // aligned base and row stride.
 int result_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld) {
@@ -956,7 +1079,6 @@ template <int kBN>
 cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cudaStream_t stream) {
   Maps maps = {};
   Products prods = {};
-  prods.n = n;
   for (int i = 0; i < n; ++i) {
     const Mat &m = mats[i];
     Product &p = prods.p[i];
@@ -968,7 +1090,7 @@ cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cuda
     p.a_strided = m.a.strided;
     p.b_strided = m.b.strided;
     p.ep = m.ep;
-    prods.tile0[i + 1] = prods.tile0[i] + p.tiles_r * p.tiles_c;
+    prods.tiles[i] = p.tiles_r * p.tiles_c;
     if (!operand_map(&maps.a[i], m.a, m.rows, m.summed, 128) ||
         !operand_map(&maps.b[i], m.b, m.cols, m.summed, kBN / 2))
       return cudaErrorNotSupported;
@@ -980,7 +1102,29 @@ cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cuda
   const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), gemm_smem<kBN>,
                                       kBN == 256 ? 0 : (kBN == 128 ? 1 : 2));
   if (e != cudaSuccess) return e;
-  const int pairs = num_sms / 2 < prods.tile0[n] ? num_sms / 2 : prods.tile0[n];
+  const int all = prods.tiles[0] + prods.tiles[1];
+  const int pairs = num_sms / 2 < all ? num_sms / 2 : all;
+  prods.lead = prods.tiles[0] % pairs;
+  if (n > 1) {
+    // the shortest end time for which the runs of product 1 fit
+    const int64_t c0 = tile_cost(prods.p[0].num_kb), c1 = tile_cost(prods.p[1].num_kb);
+    const int64_t q = prods.tiles[0] / pairs;
+    int64_t best = -1;
+    for (int64_t a = 0; a <= prods.tiles[1]; ++a) {
+      // lead pairs take a, the others what is left
+      const int64_t rest = prods.tiles[1] - a * prods.lead;
+      const int64_t b = rest <= 0 ? 0 : (rest + pairs - prods.lead - 1) / (pairs - prods.lead);
+      const int64_t end_lead = prods.lead > 0 ? (q + 1) * c0 + a * c1 : 0;
+      const int64_t end_rest = q * c0 + b * c1;
+      const int64_t end = end_lead > end_rest ? end_lead : end_rest;
+      if (best < 0 || end < best) {
+        best = end;
+        prods.run[0] = static_cast<int>(a);
+        prods.run[1] = static_cast<int>(b);
+      }
+      if (end_lead >= end_rest) break;  // more for the lead pairs only lengthens theirs
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(kGemmThreads);
@@ -994,24 +1138,30 @@ cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cuda
   return cudaLaunchKernelEx(&cfg, kern, maps, prods, err);
 }
 
-// Columns of a tile: the widest that does not leave SMs idle.  Cost of a
-// width: the waves of pairs times the time of a tile, kBN columns plus about
-// 32 columns' worth of filling and draining the pipeline.
+// Columns of a tile: the widest that does not leave SMs idle.  A K block of a
+// 256-column tile takes 280 ns, of a 128-column one 215 ns and of a 64-column
+// one 200 ns (the copies and issues that a block needs whatever its width);
+// the cost of a width is the waves of pairs times the length of a tile.
 cudaError_t launch_products(const Mat *mats, int n, int num_sms, uint32_t *err,
                             cudaStream_t stream) {
-  bool strided = false;
-  int64_t tiles[3] = {0, 0, 0};
   constexpr int widths[3] = {256, 128, 64};
-  for (int i = 0; i < n; ++i) {
-    strided = strided || mats[i].b.strided;
-    for (int w = 0; w < 3; ++w)
-      tiles[w] += (mats[i].rows + 255) / 256 * ((mats[i].cols + widths[w] - 1) / widths[w]);
-  }
+  constexpr int64_t kb_ns[3] = {280, 215, 200};
+  const int64_t pairs = num_sms / 2;
+  bool strided = false;
+  for (int i = 0; i < n; ++i) strided = strided || mats[i].b.strided;
   int best = 0;
   int64_t cost = 0;
   for (int w = 0; w < (strided ? 2 : 3); ++w) {
-    const int64_t pairs = num_sms / 2;
-    const int64_t c = (tiles[w] + pairs - 1) / pairs * (widths[w] + 32);
+    int64_t work = 0, longest = 0;
+    for (int i = 0; i < n; ++i) {
+      const int64_t tiles =
+          (mats[i].rows + 255) / 256 * ((mats[i].cols + widths[w] - 1) / widths[w]);
+      const int64_t tile = tile_cost(static_cast<int>((mats[i].summed + 63) / 64)) * kb_ns[w];
+      // one product alone: whole waves; two fill each other's last wave
+      work += n == 1 ? (tiles + pairs - 1) / pairs * pairs * tile : tiles * tile;
+      if (tile > longest) longest = tile;
+    }
+    const int64_t c = work / pairs > longest ? work / pairs : longest;
     if (w == 0 || c < cost) {
       best = w;
       cost = c;
@@ -1070,6 +1220,33 @@ cudaError_t launch_product(const Mat &m, int num_sms, uint32_t *err, cudaStream_
 
 int64_t dz_ld(int64_t N) { return (N + 7) / 8 * 8; }
 
+template <int kAct>
+cudaError_t launch_dz(const __nv_bfloat16 *g, int64_t ldg, const __nv_bfloat16 *z, int64_t ldz,
+                      int64_t M, int64_t N, __nv_bfloat16 *dz, void *db, bool f32,
+                      cudaStream_t stream) {
+  uintptr_t bits = reinterpret_cast<uintptr_t>(g) | (2 * ldg);
+  if (kAct != SGA_ACT_NONE) bits |= reinterpret_cast<uintptr_t>(z) | (2 * ldz);
+  const bool wide = bits % 16 == 0;
+  int splits = 1;  // 32 rows or more per CTA
+  while (splits < kDzMaxSplits && M >= 64 * splits) splits *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((N + kDzCols - 1) / kDzCols * splits));
+  cfg.blockDim = dim3(kDzThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  auto kern = wide ? dz_kernel<kAct, true> : dz_kernel<kAct, false>;
+  return cudaLaunchKernelEx(&cfg, kern, g, ldg, z, ldz, static_cast<int>(M), static_cast<int>(N),
+                            splits, dz, dz_ld(N), db, static_cast<int>(f32));
+}
+
 }  // namespace
 
 cudaError_t launch_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const void *weight,
@@ -1089,8 +1266,7 @@ cudaError_t launch_linear(const void *x, int64_t M, int64_t K, int64_t ldx, cons
 }
 
 size_t linear_grad_workspace_bytes(int64_t M, int64_t N) {
-  const int64_t blocks = (M + kDzRows - 1) / kDzRows;
-  return static_cast<size_t>((M * dz_ld(N) * 2 + 15) / 16 * 16 + blocks * N * 4);
+  return static_cast<size_t>((M * dz_ld(N) * 2 + 15) / 16 * 16);
 }
 
 cudaError_t launch_linear_grad(const void *grad_out, int64_t M, int64_t N, int64_t ldg,
@@ -1102,34 +1278,16 @@ cudaError_t launch_linear_grad(const void *grad_out, int64_t M, int64_t N, int64
   // dz lies where g lies when there is nothing to multiply and TMA can read it
   const bool direct =
       act == SGA_ACT_NONE && ldg % 8 == 0 && reinterpret_cast<uintptr_t>(grad_out) % 16 == 0;
-  const int64_t blocks = (M + kDzRows - 1) / kDzRows;
+  const bool products = grad_x != nullptr || grad_weight != nullptr;
   auto *dz = static_cast<__nv_bfloat16 *>(workspace);
-  float *partial = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                             (M * dz_ld(N) * 2 + 15) / 16 * 16);
   cudaError_t e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (!direct || grad_bias != nullptr) {
-    cfg.gridDim = dim3(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(kDzThreads);
-    e = cudaLaunchKernelEx(&cfg, dz_kernel, static_cast<const __nv_bfloat16 *>(grad_out), ldg,
-                           static_cast<const __nv_bfloat16 *>(preact), ldp, act,
-                           static_cast<int>(M), static_cast<int>(N),
-                           direct ? static_cast<__nv_bfloat16 *>(nullptr) : dz, dz_ld(N),
-                           grad_bias != nullptr ? partial : static_cast<float *>(nullptr));
-    if (e != cudaSuccess) return e;
-  }
-  if (grad_bias != nullptr) {
-    cfg.gridDim = dim3(static_cast<unsigned>((N + 127) / 128));
-    cfg.blockDim = dim3(128);
-    e = cudaLaunchKernelEx(&cfg, bias_grad_kernel, static_cast<const float *>(partial),
-                           static_cast<int>(blocks), static_cast<int>(N), grad_bias,
-                           static_cast<int>(bias_dtype == SGA_F32));
+  if ((products && !direct) || grad_bias != nullptr) {
+    decltype(&launch_dz<SGA_ACT_NONE>) const launch[] = {
+        launch_dz<SGA_ACT_NONE>, launch_dz<SGA_ACT_RELU>, launch_dz<SGA_ACT_SILU>,
+        launch_dz<SGA_ACT_GELU>, launch_dz<SGA_ACT_GELU_TANH>};
+    e = launch[act](static_cast<const __nv_bfloat16 *>(grad_out), ldg,
+                    static_cast<const __nv_bfloat16 *>(preact), ldp, M, N,
+                    products && !direct ? dz : nullptr, grad_bias, bias_dtype == SGA_F32, stream);
     if (e != cudaSuccess) return e;
   }
   const Operand d = direct ? Operand{grad_out, ldg, false} : Operand{dz, dz_ld(N), false};

@@ -755,6 +755,9 @@ __global__ void logprob_reduce_kernel(const sga_logprob_part *__restrict__ parts
 
 // ---------------------------------------------------------------- gradient
 constexpr int kThreads = 256;
+#ifndef SGA_GRAD_PIECE
+#define SGA_GRAD_PIECE 65536  // bytes of a row per CTA
+#endif
 
 // dx_j = p_j (A + B (log p_j + H)) plus, at the token and at the alternatives,
 // their upstream gradients; A = -(sum of those), B = -(gradient of the
@@ -865,21 +868,31 @@ __global__ void __launch_bounds__(kThreads)
     const int ve = v1 < full ? v1 : full;
     const char *xv = x + head * kElt;
     char *gv = g + head * kElt;
-    for (int v = v0 + tid; v < ve; v += kThreads) {
-      uint4 q = __ldcs(reinterpret_cast<const uint4 *>(xv) + v);
-      uint32_t wd[4] = {q.x, q.y, q.z, q.w};
+    constexpr int kBatch = 4;  // loads in flight per thread
+    for (int v = v0 + tid; v < ve; v += kBatch * kThreads) {
+      uint4 q[kBatch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!live) {
-          wd[i] = 0u;
-        } else if (kBf16) {
-          wd[i] = pack_bf16(grad_term(bf16_lo(wd[i]), lse, a, bh, b),
-                            grad_term(bf16_hi(wd[i]), lse, a, bh, b));
-        } else {
-          wd[i] = __float_as_uint(grad_term(__uint_as_float(wd[i]), lse, a, bh, b));
+      for (int u = 0; u < kBatch; ++u)
+        if (v + u * kThreads < ve)
+          q[u] = __ldcs(reinterpret_cast<const uint4 *>(xv) + v + u * kThreads);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (v + u * kThreads >= ve) continue;
+        uint32_t wd[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!live) {
+            wd[i] = 0u;
+          } else if (kBf16) {
+            wd[i] = pack_bf16(grad_term(bf16_lo(wd[i]), lse, a, bh, b),
+                              grad_term(bf16_hi(wd[i]), lse, a, bh, b));
+          } else {
+            wd[i] = __float_as_uint(grad_term(__uint_as_float(wd[i]), lse, a, bh, b));
+          }
         }
+        __stcs(reinterpret_cast<uint4 *>(gv) + v + u * kThreads,
+               make_uint4(wd[0], wd[1], wd[2], wd[3]));
       }
-      __stcs(reinterpret_cast<uint4 *>(gv) + v, make_uint4(wd[0], wd[1], wd[2], wd[3]));
     }
     for (int j = head + (ve > v0 ? ve : v0) * kVec + tid; j < c1; j += kThreads) one(j);
   }
@@ -977,7 +990,7 @@ cudaError_t launch_logprobs_grad(const void *logits, int dtype, int64_t rows, in
                                  const int32_t *top_ids, const float *g_top, void *grad,
                                  int64_t ldg, int num_sms, cudaStream_t stream) {
   const int elt = dtype == SGA_BF16 ? 2 : 4;
-  int64_t chunks = (width * elt + 32767) / 32768;  // 32 KB of a row per CTA
+  int64_t chunks = (width * elt + SGA_GRAD_PIECE - 1) / SGA_GRAD_PIECE;
   if (rows * chunks > (int64_t(1) << 30)) chunks = (int64_t(1) << 30) / rows;
   const GradIn in = {tokens, lse, entropy, g_logprob, g_entropy, g_top, top_ids};
   cudaLaunchConfig_t cfg = {};
