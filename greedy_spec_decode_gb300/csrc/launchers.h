@@ -135,7 +135,7 @@ cudaError_t launch_logprobs_grad(const void *logits, int dtype, int64_t rows, in
                                  const int32_t *tokens, const float *lse, const float *entropy,
                                  const float *g_logprob, const float *g_entropy, int top_k,
                                  const int32_t *top_ids, const float *g_top, void *grad,
-                                 int64_t ldg, int num_sms, cudaStream_t stream);
+                                 int64_t ldg, cudaStream_t stream);
 
 // Bounded-wait self-test (lmhead.cu).
 cudaError_t launch_selftest_timeout(unsigned long long limit_ns, uint32_t *err,

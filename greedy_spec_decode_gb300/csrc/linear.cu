@@ -240,51 +240,112 @@ __device__ __forceinline__ void box_store_tma(const CUtensorMap *map, uint32_t b
       : "memory");
 }
 
-// Where TMA cannot go (rows not on 16-byte boundaries): a row at a time, two
-// columns a lane, eight rows in flight.
+// Bytes s .. s + 15 (s even, 0 .. 16) of two 16-byte pieces in a row.
+__device__ __forceinline__ uint4 bytes_of(const uint4 a, const uint4 b, int s) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = (s & 8) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = (s & 4) ? w[i + 1] : w[i];
+  uint4 r;
+  r.x = __funnelshift_r(w[0], w[1], (s & 2) * 8);
+  r.y = __funnelshift_r(w[1], w[2], (s & 2) * 8);
+  r.z = __funnelshift_r(w[2], w[3], (s & 2) * 8);
+  r.w = __funnelshift_r(w[3], w[4], (s & 2) * 8);
+  return (s & 16) ? b : r;
+}
+
+__device__ __forceinline__ unsigned short *box_elem(uint8_t *box, int r, int c) {
+  return reinterpret_cast<unsigned short *>(box_piece(box, r, c >> 3)) + (c & 7);
+}
+
+// Where TMA cannot go (rows not on 16-byte boundaries).  Whole boxes: eight
+// lanes per row; with the row `off` bytes past a boundary, its aligned 16-byte
+// pieces (seven, or eight where off is 0) go as such, put together from two
+// pieces of the box, and the eight columns at its ends one by one.  (Two-byte
+// accesses throughout: 3660 x 14645 x 144 took 81 us.)  Boxes at the right
+// edge: two columns a lane.
 __device__ __forceinline__ void box_store_rows(uint8_t *box, __nv_bfloat16 *p, int64_t ld, int rows,
                                                int cols, int lane) {
-  const int c = 2 * lane;
-  const bool pair = ((reinterpret_cast<uintptr_t>(p) | (2 * ld)) & 3) == 0 && c + 1 < cols;
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r) {
-    const uint32_t w = *(reinterpret_cast<const uint32_t *>(box_piece(box, r, lane >> 2)) +
-                         (lane & 3));
-    if (r >= rows) continue;
-    unsigned short *q = reinterpret_cast<unsigned short *>(p + r * ld + c);
-    if (pair) {
-      *reinterpret_cast<uint32_t *>(q) = w;
-    } else {
-      if (c < cols) q[0] = static_cast<unsigned short>(w);
-      if (c + 1 < cols) q[1] = static_cast<unsigned short>(w >> 16);
+  if (cols >= 64) {
+    const int j = lane & 7;
+#pragma unroll 2
+    for (int r = lane >> 3; r < 32; r += 4) {
+      unsigned short *q = reinterpret_cast<unsigned short *>(p + r * ld);
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
+      const uint4 w = bytes_of(*box_piece(box, r, max(j - 1, 0)), *box_piece(box, r, j), 16 - off);
+      const int e = 2 * j < 16 - off ? j : 56 + j;
+      const unsigned short edge = *box_elem(box, r, e);
+      if (r < rows && (j > 0 || off == 0))
+        *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(q) - off + 16 * j) = w;
+      if (r < rows && off != 0) q[e] = edge;
     }
+    return;
+  }
+  const int c = 2 * lane;
+  unsigned short *q = reinterpret_cast<unsigned short *>(p) + c;
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(box_elem(box, r, c));
+    if (c < cols) q[0] = static_cast<unsigned short>(w);
+    if (c + 1 < cols) q[1] = static_cast<unsigned short>(w >> 16);
+    q += ld;
   }
 }
 
 __device__ __forceinline__ void box_load_rows(uint8_t *box, const __nv_bfloat16 *p, int64_t ld,
                                               int rows, int cols, int lane) {
-  const int c = 2 * lane;
-  const bool pair = ((reinterpret_cast<uintptr_t>(p) | (2 * ld)) & 3) == 0 && c + 1 < cols;
+  if (cols >= 64) {
+    const int j = lane & 7;
+    constexpr int kBatch = 4;
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += 8) {
-    uint32_t w[8];
+    for (int r0 = lane >> 3; r0 < 32; r0 += 4 * kBatch) {
+      uint4 w[kBatch];
+      unsigned short edge[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const unsigned short *q = reinterpret_cast<const unsigned short *>(
+            p + min(r0 + 4 * u, rows - 1) * ld);
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
+        // (piece 0 of an unaligned row starts before it: piece 1 is read again)
+        const int at = j > 0 || off == 0 ? j : 1;
+        w[u] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(q) - off + 16 * at);
+        edge[u] = q[2 * j < 16 - off ? j : 56 + j];
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int r = r0 + 4 * u;
+        const int off = static_cast<int>(
+            reinterpret_cast<uintptr_t>(p + min(r, rows - 1) * ld) & 15);
+        uint4 next;
+        next.x = __shfl_down_sync(0xffffffffu, w[u].x, 1);
+        next.y = __shfl_down_sync(0xffffffffu, w[u].y, 1);
+        next.z = __shfl_down_sync(0xffffffffu, w[u].z, 1);
+        next.w = __shfl_down_sync(0xffffffffu, w[u].w, 1);
+        *box_piece(box, r, j) = bytes_of(w[u], next, off);
+        __syncwarp();
+        if (off != 0) *box_elem(box, r, 2 * j < 16 - off ? j : 56 + j) = edge[u];
+      }
+    }
+    return;
+  }
+  const int c = 2 * lane;
+  const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+  // (loads at clamped addresses, not behind branches: eight rows in flight)
+  const int lo = c < cols ? c : cols - 1, hi = c + 1 < cols ? c + 1 : cols - 1;
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    unsigned short a[8], b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = r0 + i;
-      const unsigned short *q = reinterpret_cast<const unsigned short *>(p + r * ld + c);
-      w[i] = 0;
-      if (r < rows) {
-        if (pair) {
-          w[i] = *reinterpret_cast<const uint32_t *>(q);
-        } else {
-          if (c < cols) w[i] = q[0];
-          if (c + 1 < cols) w[i] |= static_cast<uint32_t>(q[1]) << 16;
-        }
-      }
+      const int r = min(r0 + i, rows - 1);
+      a[i] = q[r * ld + lo];
+      b[i] = q[r * ld + hi];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      *(reinterpret_cast<uint32_t *>(box_piece(box, r0 + i, lane >> 2)) + (lane & 3)) = w[i];
+      *reinterpret_cast<uint32_t *>(box_elem(box, r0 + i, c)) =
+          a[i] | (static_cast<uint32_t>(b[i]) << 16);
   }
 }
 
@@ -686,13 +747,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// few_rows_kernel, M <= 128: out[m, r] = act(sum_k A[r, k] x[m, k] + bias[r])
-// + res[m, r] with A the weight (128 rows r per CTA, its TMEM lanes) and the M
-// rows of x the MMA's kN columns.  The weight is read once and sets the pace.
-// A cluster of `splits` CTAs shares a tile: each sums its range of K blocks,
-// stores its fp32 partial tile in its own shared memory, and adds up
-// 128 / splits of the rows from every CTA's, in rank order (a fixed order:
-// results do not vary from run to run).
+// few_rows_kernel: out[m, r] = act(sum_k A[r, k] x[m, k] + bias[r]) + res[m, r]
+// with A the weight (128 rows r per CTA, its TMEM lanes) and up to kN rows of x
+// the MMA's columns (kN <= 128; more rows: blocks of 128).  For M <= 128 the
+// weight is read once and sets the pace; for more rows this form pays where the
+// product has too few 256-row tiles to fill the SMs.
+// A cluster of `splits` CTAs shares a tile: each sums its range of K blocks
+// (maybe none), stores its fp32 partial tile in its own shared memory, and
+// finishes 128 / splits of the rows from every CTA's part, in rank order (a
+// fixed order: results do not vary from run to run).
 // ---------------------------------------------------------------------------
 template <int kN>
 constexpr int few_stage = kTileA + kN * ROW_BYTES;
@@ -717,8 +780,8 @@ static_assert(few_stages<128> * few_stage<128> >= 128 * 128 * 4, "a partial tile
 template <int kN>
 __global__ void __launch_bounds__(THREADS, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                    const __grid_constant__ CUtensorMap tmap_x, int M, int rows, int num_kb,
-                    int splits, int strided, const Epilogue ep, uint32_t *err) {
+                    const __grid_constant__ CUtensorMap tmap_x, int all_m, int rows, int num_kb,
+                    int blocks, int splits, int strided, const Epilogue ep, uint32_t *err) {
   constexpr int kStages = few_stages<kN>;
   constexpr int kStageB = few_stage<kN>;
   extern __shared__ uint8_t smem_raw[];
@@ -728,10 +791,13 @@ __global__ void __launch_bounds__(THREADS, 2)
   const volatile int *abort_flag = &sh->abort;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int tile = static_cast<int>(blockIdx.x) / splits;
-  const int split = static_cast<int>(blockIdx.x) - tile * splits;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * split / splits);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (split + 1) / splits);
+  const int unit = static_cast<int>(blockIdx.x) / splits;
+  const int split = static_cast<int>(blockIdx.x) - unit * splits;
+  const int tile = unit / blocks;
+  const int first_m = (unit - tile * blocks) * kN;  // this CTA's rows of x
+  const int M = min(kN, all_m - first_m);
+  const int kb0 = num_kb * split / splits;  // (num_kb <= 2^18)
+  const int kb1 = num_kb * (split + 1) / splits;
   const int row0 = tile * 128;
 
   if (threadIdx.x == 64) {
@@ -790,7 +856,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       } else {
         tma_load_2d(a, &tmap_w, kb * 64, row0, full);
       }
-      tma_load_2d(a + kTileA, &tmap_x, kb * 64, 0, full);
+      tma_load_2d(a + kTileA, &tmap_x, kb * 64, first_m, full);
       ++issued;
       if (++prod_stage == kStages) {
         prod_stage = 0;
@@ -823,8 +889,8 @@ __global__ void __launch_bounds__(THREADS, 2)
         phase ^= 1;
       }
     }
-    if (ok) mma_commit(smem_u32(&sh->done));
-  } else if (warp >= 2) {
+    if (ok && kb1 > kb0) mma_commit(smem_u32(&sh->done));
+  } else if (warp >= 2 && kb1 > kb0) {
     good = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sh->done), 0, abort_flag));
     if (!good && lane == 0) raise_abort(&sh->abort, err);
     if (good) {
@@ -873,27 +939,53 @@ __global__ void __launch_bounds__(THREADS, 2)
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   pdl_launch_dependents();
-  // this CTA's share of the tile's rows, for every m; rows fastest
+  // this CTA's share of the tile's rows, for every m: a row per thread, so many
+  // m at once as there are threads for, four of those in flight
   const int share = 128 / splits;
-  const int mine = split * share;
-  const float *src[8];
+  const int at_once = splits == 1 ? 1 : THREADS / share;
+  const int r = split * share + static_cast<int>(threadIdx.x) % share;
+  const int64_t col = row0 + r;
+  if (static_cast<int>(threadIdx.x) < at_once * share && col < rows) {
+    const float bias = ld_bias(ep.bias, ep.bias_f32, col);
+    const uint32_t mine = smem_u32(part) + r * 4;
+    unsigned parts = 0;
+    for (int i = 0; i < splits; ++i)
+      parts |= static_cast<unsigned>(num_kb * i / splits != num_kb * (i + 1) / splits) << i;
+    __nv_bfloat16 *out = ep.out + first_m * ep.ldo + col;
+    __nv_bfloat16 *pre = ep.pre + first_m * ep.ldp + col;
+    const __nv_bfloat16 *residual = ep.res + first_m * ep.ldr + col;
+    for (int m0 = static_cast<int>(threadIdx.x) / share; m0 < M; m0 += 4 * at_once) {
+      float z[4];
+      unsigned short res[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    src[i] = i < splits ? cluster.map_shared_rank(part, i) : nullptr;
-  for (int e = threadIdx.x; e < share * M; e += THREADS) {
-    const int m = e / share;
-    const int r = mine + e - m * share;
-    if (row0 + r >= rows) continue;
-    float z = 0.0f;
+      for (int u = 0; u < 4; ++u) {
+        const int m = min(m0 + u * at_once, M - 1);
+        if (ep.res != nullptr)
+          res[u] = *reinterpret_cast<const unsigned short *>(residual + m * ep.ldr);
+        z[u] = 0.0f;
+      }
+      for (int i = 0; i < splits; ++i) {
+        if ((parts >> i & 1) == 0) continue;  // a CTA without K blocks has no part
+        const uint32_t src = map_to_rank(mine, i);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < splits) z += src[i][m * 128 + r];
-    const int64_t col = row0 + r;
-    z += ld_bias(ep.bias, ep.bias_f32, col);
-    if (ep.pre != nullptr) ep.pre[m * ep.ldp + col] = __float2bfloat16_rn(z);
-    float y = activate(z, ep.act);
-    if (ep.res != nullptr) y += ld_bf16(ep.res + m * ep.ldr + col);
-    ep.out[m * ep.ldo + col] = __float2bfloat16_rn(y);
+        for (int u = 0; u < 4; ++u) {
+          const int m = min(m0 + u * at_once, M - 1);
+          float v;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(src + m * 512));
+          z[u] += v;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int m = m0 + u * at_once;
+        if (m >= M) break;
+        const float zz = z[u] + bias;
+        if (ep.pre != nullptr) pre[m * ep.ldp] = __float2bfloat16_rn(zz);
+        float y = activate(zz, ep.act);
+        if (ep.res != nullptr) y += __uint_as_float(static_cast<uint32_t>(res[u]) << 16);
+        out[m * ep.ldo] = __float2bfloat16_rn(y);
+      }
+    }
   }
   cluster.sync();  // partial tiles stay alive until every CTA has read them
   if (warp == 1) {
@@ -1141,16 +1233,19 @@ cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cuda
 // Columns of a tile: the widest that does not leave SMs idle.  A K block of a
 // 256-column tile takes 280 ns, of a 128-column one 215 ns and of a 64-column
 // one 200 ns (the copies and issues that a block needs whatever its width);
-// the cost of a width is the waves of pairs times the length of a tile.
-cudaError_t launch_products(const Mat *mats, int n, int num_sms, uint32_t *err,
-                            cudaStream_t stream) {
+// the time of a width is the waves of pairs times the length of a tile.
+struct Width {
+  int index;
+  int64_t ns;
+};
+
+Width pick_width(const Mat *mats, int n, int num_sms) {
   constexpr int widths[3] = {256, 128, 64};
   constexpr int64_t kb_ns[3] = {280, 215, 200};
   const int64_t pairs = num_sms / 2;
   bool strided = false;
   for (int i = 0; i < n; ++i) strided = strided || mats[i].b.strided;
-  int best = 0;
-  int64_t cost = 0;
+  Width best = {0, 0};
   for (int w = 0; w < (strided ? 2 : 3); ++w) {
     int64_t work = 0, longest = 0;
     for (int i = 0; i < n; ++i) {
@@ -1161,15 +1256,28 @@ cudaError_t launch_products(const Mat *mats, int n, int num_sms, uint32_t *err,
       work += n == 1 ? (tiles + pairs - 1) / pairs * pairs * tile : tiles * tile;
       if (tile > longest) longest = tile;
     }
-    const int64_t c = work / pairs > longest ? work / pairs : longest;
-    if (w == 0 || c < cost) {
-      best = w;
-      cost = c;
-    }
+    const int64_t ns = work / pairs > longest ? work / pairs : longest;
+    if (w == 0 || ns < best.ns) best = {w, ns};
   }
-  if (best == 0) return launch_gemm<256>(mats, n, num_sms, err, stream);
-  if (best == 1) return launch_gemm<128>(mats, n, num_sms, err, stream);
-  return launch_gemm<64>(mats, n, num_sms, err, stream);
+  return best;
+}
+
+cudaError_t launch_products(const Mat *mats, int n, int num_sms, uint32_t *err,
+                            cudaStream_t stream) {
+  switch (pick_width(mats, n, num_sms).index) {
+    case 0: return launch_gemm<256>(mats, n, num_sms, err, stream);
+    case 1: return launch_gemm<128>(mats, n, num_sms, err, stream);
+    default: return launch_gemm<64>(mats, n, num_sms, err, stream);
+  }
+}
+
+// CTAs per tile of few_rows_kernel: while all of them are resident (two per SM).
+// A CTA's share of K blocks may be one or none; it still takes its share of
+// the results.
+int few_splits(int64_t units, int num_kb, int num_sms) {
+  int splits = 1;
+  while (splits < 8 && units * splits * 2 <= 2 * num_sms && num_kb >= splits) splits *= 2;
+  return splits;
 }
 
 template <int kN>
@@ -1179,18 +1287,17 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   if (!operand_map(&map_w, m.a, m.rows, m.summed, 128) ||
       !operand_map(&map_x, m.b, m.cols, m.summed, kN))
     return cudaErrorNotSupported;
-  const int64_t tiles = (m.rows + 127) / 128;
   const int num_kb = static_cast<int>((m.summed + 63) / 64);
-  // splits: while every CTA is resident (two per SM) and keeps a few K blocks
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= 2 * num_sms && num_kb >= 4 * splits) splits *= 2;
+  const int blocks = static_cast<int>((m.cols + kN - 1) / kN);
+  const int64_t units = (m.rows + 127) / 128 * blocks;
+  const int splits = few_splits(units, num_kb, num_sms);
   auto kern = few_rows_kernel<kN>;
   const cudaError_t e =
       set_smem_once(reinterpret_cast<const void *>(kern), few_smem<kN>,
                     kN == 16 ? 3 : (kN == 32 ? 4 : (kN == 64 ? 5 : 6)));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = few_smem<kN>;
   cfg.stream = stream;
@@ -1204,13 +1311,29 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, static_cast<int>(m.cols),
-                            static_cast<int>(m.rows), num_kb, splits,
+                            static_cast<int>(m.rows), num_kb, blocks, splits,
                             static_cast<int>(m.a.strided), m.ep, err);
 }
 
-// out[M, cols] of few rows: the weight becomes the row operand.
+// Whether a product runs as few_rows_kernel: always up to 128 rows; above where
+// its tiles, split over K, end sooner than the pairs' (estimated as 350 ns a K
+// block for each CTA of an SM, which its 32 KB take from L2, and 25 ns for each
+// 64 results of a CTA's share).
+bool few_rows_form(const Mat &m, int num_sms) {
+  if (m.a.strided) return false;  // (few_rows_kernel reads x with K contiguous)
+  if (m.rows <= 128) return true;
+  if (m.rows > 2048) return false;
+  const int num_kb = static_cast<int>((m.summed + 63) / 64);
+  const int64_t units = (m.cols + 127) / 128 * ((m.rows + 127) / 128);
+  const int splits = few_splits(units, num_kb, num_sms);
+  const int64_t per_sm = (units * splits + num_sms - 1) / num_sms;
+  const int64_t ns = per_sm * ((num_kb + splits - 1) / splits * 350 + 128 * 128 / splits * 25 / 64);
+  return ns < pick_width(&m, 1, num_sms).ns;
+}
+
+// One product; of few rows with the weight as the row operand.
 cudaError_t launch_product(const Mat &m, int num_sms, uint32_t *err, cudaStream_t stream) {
-  if (m.rows > 128 || m.a.strided) return launch_products(&m, 1, num_sms, err, stream);
+  if (!few_rows_form(m, num_sms)) return launch_products(&m, 1, num_sms, err, stream);
   const Mat t = {m.b, m.a, m.cols, m.rows, m.summed, m.ep};
   if (m.rows <= 16) return launch_few_rows<16>(t, num_sms, err, stream);
   if (m.rows <= 32) return launch_few_rows<32>(t, num_sms, err, stream);
@@ -1302,7 +1425,7 @@ cudaError_t launch_linear_grad(const void *grad_out, int64_t M, int64_t N, int64
     m.summed = N;
     m.ep.out = static_cast<__nv_bfloat16 *>(grad_x);
     m.ep.ldo = ldgx;
-    if (M <= 128) {
+    if (few_rows_form(m, num_sms)) {
       e = launch_product(m, num_sms, err, stream);
       if (e != cudaSuccess) return e;
       n = 0;

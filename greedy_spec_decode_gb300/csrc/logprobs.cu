@@ -78,8 +78,9 @@ __device__ __forceinline__ void lse_merge(Lse &a, const Lse &b) {
 // from which the top_k are selected at the end by counting, on 64-bit keys
 // that order (value, id) pairs.  -inf is never a candidate: where fewer than
 // top_k elements are above it, the lowest masked ids fill the list.  If the
-// buffer overflows (very many equal values, or rows that keep rising) the
-// piece is read again with per-warp sorted lists.
+// buffer overflows the piece is read again: for what lies above the threshold,
+// the lowest ids that equal it filling up (rows with very many equal values),
+// and if that overflows too with per-warp sorted lists (rows that keep rising).
 constexpr int kGroups = 64;
 constexpr int kVecPerThread = 4;  // 16-byte vectors of a ring stage per thread
 constexpr int kRing = 3;
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
             const float vm = vec_max<kBf16>(q);
             sums_rebase(a, vm);
             lo = pack_lo<kBf16>(a.limit, threshold);
-            if (!(vm < threshold) && k > 0) {
+            if (!(vm < threshold) && vm != neg_inf() && k > 0) {
               const int c = atomicAdd(&sh.num_vecs, 1);
               if (c < sh.kVecs) {
                 sh.vec[c] = q;
@@ -568,17 +569,68 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
           }
         }
       } else {
-        Key top = 0;
-        for (int base = pc.c0 + warp * 32; base < pc.c1; base += kT) {
-          const int j = base + lane;
-          top_offer(top, j < pc.c1 ? pair_key(load_elem<kBf16>(p, j), id0 + j) : 0, lane, k);
-        }
-        if (lane < k) sh.list[warp * k + lane] = top;
+        // Too many reach the threshold.  Usually they equal it (a mask of the
+        // type's lowest value, constant rows): take those above it, and of
+        // the equal ones the lowest ids.
         consumers_sync<kT>();
-        for (int c = tid; c < kWarps * k; c += kT) {
-          const Key mine = sh.list[c];
-          const int rank = keys_above(sh.list, kWarps * k, mine);
-          if (mine != 0 && rank < k) sh.best[rank] = mine;
+        if (tid == 0) sh.num_keys = 0;
+        consumers_sync<kT>();
+        auto above = [&](float x, int j) {
+          if (!(x <= threshold)) push_key(sh, x, id0 + j);
+        };
+        const uint4 *body = reinterpret_cast<const uint4 *>(p + static_cast<int64_t>(pc.b0) * kElt);
+        const int nvec = (pc.b1 - pc.b0) / kVec;
+        constexpr int kBatch = 4;
+        for (int v = tid; v < nvec; v += kBatch * kT) {
+          uint4 q[kBatch];
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            if (v + u * kT < nvec) q[u] = ld_stream_v4(body + v + u * kT);
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            if (v + u * kT >= nvec || vec_max<kBf16>(q[u]) <= threshold) continue;
+            float x[kVec];
+            vec_elems<kBf16>(q[u], x);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) above(x[e], pc.b0 + (v + u * kT) * kVec + e);
+          }
+        }
+        for (int side = 0; side < 2; ++side) {
+          const int j = (side == 0 ? pc.c0 : pc.b1) + tid;
+          if (j < (side == 0 ? pc.b0 : pc.c1)) above(load_elem<kBf16>(p, j), j);
+        }
+        consumers_sync<kT>();
+        int n = sh.num_keys;
+        for (int base = pc.c0; base < pc.c1 && n < k; base += kT) {
+          consumers_sync<kT>();  // everyone has read the count
+          const int j = base + tid;
+          const float x = j < pc.c1 ? load_elem<kBf16>(p, j) : __int_as_float(0x7fc00000);
+          if (x == threshold) push_key(sh, x, id0 + j);
+          consumers_sync<kT>();
+          n = sh.num_keys;
+        }
+        if (n <= sh.kKeys) {
+          if (tid == 0 && (n & 1)) sh.key[n] = 0;
+          consumers_sync<kT>();
+          for (int i = tid; i < n; i += kT) {
+            const Key mine = sh.key[i];
+            const int rank = keys_above(sh.key, n, mine);
+            if (rank < k) sh.best[rank] = mine;
+          }
+        } else {
+          // rows that keep rising: a sorted list per warp
+          Key top = 0;
+          for (int base = pc.c0 + warp * 32; base < pc.c1; base += kT) {
+            const int j = base + lane;
+            top_offer(top, j < pc.c1 ? pair_key(load_elem<kBf16>(p, j), id0 + j) : 0, lane, k);
+          }
+          if (lane < k) sh.list[warp * k + lane] = top;
+          consumers_sync<kT>();
+          for (int c = tid; c < kWarps * k; c += kT) {
+            const Key mine = sh.list[c];
+            const int rank = keys_above(sh.list, kWarps * k, mine);
+            if (mine != 0 && rank < k) sh.best[rank] = mine;
+          }
         }
       }
     }
@@ -798,7 +850,9 @@ __device__ __forceinline__ float read_elem(const char *p, int j) {  // the buffe
   return reinterpret_cast<const volatile float *>(p)[j];
 }
 
-template <bool kBf16>
+// kShift: some rows of the logits and of the gradient lie at different 16-byte
+// offsets (apart from the other case, whose registers it would double).
+template <bool kBf16, bool kShift>
 __global__ void __launch_bounds__(kThreads)
     logprobs_grad_kernel(const char *logits, int64_t ld_bytes, int valid, int width, int32_t id0,
                          GradIn in, int k, int chunks, char *grad, int64_t ldg_bytes) {
@@ -859,43 +913,68 @@ __global__ void __launch_bounds__(kThreads)
     if (live && j < valid) v = grad_term(read_elem<kBf16>(x, j), lse, a, bh, b);
     store_elem<kBf16>(g, j, v);
   };
-  const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(g)) & 15u) == 0;
-  if (!same) {
-    for (int j = c0 + tid; j < c1; j += kThreads) one(j);
-  } else {
-    if (chunk == 0 && tid < head) one(tid);
-    const int full = valid > head ? (valid - head) / kVec : 0;  // vectors without padding ids
-    const int ve = v1 < full ? v1 : full;
-    const char *xv = x + head * kElt;
-    char *gv = g + head * kElt;
-    constexpr int kBatch = 4;  // loads in flight per thread
-    for (int v = v0 + tid; v < ve; v += kBatch * kThreads) {
-      uint4 q[kBatch];
+  if (chunk == 0 && tid < head) one(tid);
+  // whole vectors of the output without padding ids.  Where the logits' row
+  // lies at another 16-byte offset, a vector is put together from the two
+  // aligned ones that hold it; the row's first and last vectors are left to
+  // the single columns, so that no load leaves the row.
+  const int offset = kShift ? static_cast<int>((reinterpret_cast<uintptr_t>(x) -
+                                                reinterpret_cast<uintptr_t>(g)) & 15u)
+                            : 0;
+  const int full = valid > head ? (valid - head) / kVec : 0;
+  const int vs = offset != 0 && v0 == 0 ? min(1, v1) : v0;
+  const int ve = max(vs, min(v1, offset != 0 ? full - 1 : full));
+  const char *xv = x + head * kElt - offset;  // 16-byte aligned
+  char *gv = g + head * kElt;
+  constexpr int kBatch = 4;  // loads in flight per thread
+  for (int v = vs + tid; v < ve; v += kBatch * kThreads) {
+    uint4 q[kBatch], q1[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        if (v + u * kThreads < ve)
-          q[u] = __ldcs(reinterpret_cast<const uint4 *>(xv) + v + u * kThreads);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (v + u * kThreads >= ve) continue;
-        uint32_t wd[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!live) {
-            wd[i] = 0u;
-          } else if (kBf16) {
-            wd[i] = pack_bf16(grad_term(bf16_lo(wd[i]), lse, a, bh, b),
-                              grad_term(bf16_hi(wd[i]), lse, a, bh, b));
-          } else {
-            wd[i] = __float_as_uint(grad_term(__uint_as_float(wd[i]), lse, a, bh, b));
-          }
-        }
-        __stcs(reinterpret_cast<uint4 *>(gv) + v + u * kThreads,
-               make_uint4(wd[0], wd[1], wd[2], wd[3]));
+    for (int u = 0; u < kBatch; ++u) {
+      if (v + u * kThreads >= ve) continue;
+      const uint4 *src = reinterpret_cast<const uint4 *>(xv) + v + u * kThreads;
+      if (!kShift || offset == 0) {
+        q[u] = __ldcs(src);
+      } else {
+        q[u] = src[0];
+        q1[u] = src[1];
       }
     }
-    for (int j = head + (ve > v0 ? ve : v0) * kVec + tid; j < c1; j += kThreads) one(j);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (v + u * kThreads >= ve) continue;
+      uint32_t wd[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+      if (kShift && offset != 0) {
+        uint32_t w[8] = {q[u].x, q[u].y, q[u].z, q[u].w, q1[u].x, q1[u].y, q1[u].z, q1[u].w};
+        if (offset & 8) {
+#pragma unroll
+          for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (offset & 4) {
+#pragma unroll
+          for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wd[i] = __funnelshift_r(w[i], w[i + 1], (offset & 2) * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!live) {
+          wd[i] = 0u;
+        } else if (kBf16) {
+          wd[i] = pack_bf16(grad_term(bf16_lo(wd[i]), lse, a, bh, b),
+                            grad_term(bf16_hi(wd[i]), lse, a, bh, b));
+        } else {
+          wd[i] = __float_as_uint(grad_term(__uint_as_float(wd[i]), lse, a, bh, b));
+        }
+      }
+      __stcs(reinterpret_cast<uint4 *>(gv) + v + u * kThreads,
+             make_uint4(wd[0], wd[1], wd[2], wd[3]));
+    }
   }
+  if (vs > v0)
+    for (int j = head + v0 * kVec + tid; j < head + vs * kVec; j += kThreads) one(j);
+  for (int j = head + ve * kVec + tid; j < c1; j += kThreads) one(j);
   pdl_launch_dependents();
   __syncthreads();
   if (fix_col >= 0 && live) store_elem<kBf16>(g, fix_col, fix);
@@ -988,7 +1067,7 @@ cudaError_t launch_logprobs_grad(const void *logits, int dtype, int64_t rows, in
                                  const int32_t *tokens, const float *lse, const float *entropy,
                                  const float *g_logprob, const float *g_entropy, int top_k,
                                  const int32_t *top_ids, const float *g_top, void *grad,
-                                 int64_t ldg, int num_sms, cudaStream_t stream) {
+                                 int64_t ldg, cudaStream_t stream) {
   const int elt = dtype == SGA_BF16 ? 2 : 4;
   int64_t chunks = (width * elt + SGA_GRAD_PIECE - 1) / SGA_GRAD_PIECE;
   if (rows * chunks > (int64_t(1) << 30)) chunks = (int64_t(1) << 30) / rows;
@@ -1002,8 +1081,11 @@ cudaError_t launch_logprobs_grad(const void *logits, int dtype, int64_t rows, in
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto kern = dtype == SGA_BF16 ? logprobs_grad_kernel<true> : logprobs_grad_kernel<false>;
-  (void)num_sms;
+  const bool shift = ((reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(grad)) |
+                      ((ld - ldg) * elt)) % 16 != 0;
+  auto kern = dtype == SGA_BF16
+                  ? (shift ? logprobs_grad_kernel<true, true> : logprobs_grad_kernel<true, false>)
+                  : (shift ? logprobs_grad_kernel<false, true> : logprobs_grad_kernel<false, false>);
   return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits), ld * elt,
                             static_cast<int>(valid), static_cast<int>(width),
                             static_cast<int32_t>(shard_start), in, top_k,

@@ -644,8 +644,7 @@ int sga_token_logprobs_grad(const void *logits, int dtype, int64_t rows, int64_t
   return launch_status(sga::launch_logprobs_grad(
       logits, dtype, rows, ld, shard_start, shard_width,
       valid_ids(shard_start, shard_width, org_vocab), tokens, lse, entropy, grad_logprob,
-      grad_entropy, top_k, top_ids, grad_top, out_grad, ldg, d.num_sms,
-      static_cast<cudaStream_t>(stream)));
+      grad_entropy, top_k, top_ids, grad_top, out_grad, ldg, static_cast<cudaStream_t>(stream)));
 }
 
 int sga_selftest_wait_timeout(uint64_t limit_ns, uint64_t *waited_ns, sga_stream stream) {
