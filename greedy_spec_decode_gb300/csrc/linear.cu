@@ -999,14 +999,17 @@ __global__ void __launch_bounds__(THREADS, 2)
 // ---------------------------------------------------------------------------
 // dz = g * act'(z) in bf16 (dz nullable) and db = the column sums of dz in
 // fp32, before the rounding (db nullable).  HBM-bound: g and z are read once
-// and dz written once.  A cluster covers a strip of 64 columns, its CTAs
+// and dz written once.  A cluster covers a strip of columns, its CTAs
 // contiguous ranges of rows; their column sums meet in the first CTA through
 // distributed shared memory, in a fixed order, so db needs no second launch.
-// Wide: eight lanes of 16 bytes per row, 32 rows at a time; narrow (rows not on
-// 16-byte boundaries): a warp per row, two columns a lane.
+// A strip has 64 columns, or 32 or 16 where that leaves SMs idle; a thread takes
+// eight columns of a row.  Rows of g and z that
+// do not start on 16-byte boundaries (kAligned false) are put together from the
+// aligned pieces that hold them (with two-byte loads 3899 x 3205 took 50 us); a
+// strip's columns at a row's ends, where such pieces would leave the row, go
+// one by one.
 // ---------------------------------------------------------------------------
 constexpr int kDzThreads = 256;
-constexpr int kDzCols = 64;
 constexpr int kDzMaxSplits = 8;
 
 // (A product of its own, not contracted into the column sum: db is the same
@@ -1016,82 +1019,93 @@ __device__ __forceinline__ float dz_term(float g, float z) {
   return kAct == SGA_ACT_NONE ? g : __fmul_rn(g, activate_grad(z, kAct));
 }
 
-template <int kAct, bool kWide>
+// Eight bf16 at p, and with kAligned false what surrounds them (see above).
+template <bool kAligned>
+struct Eight {
+  uint4 a, b;
+  int off;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    if (kAligned) {
+      a = ld_stream_v4(p);
+    } else {
+      off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+      const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(p) - off);
+      a = __ldg(q);
+      b = __ldg(q + (off != 0 ? 1 : 0));
+    }
+  }
+  __device__ __forceinline__ uint4 get() const { return kAligned ? a : bytes_of(a, b, off); }
+};
+
+template <int kAct, bool kAligned>
 __global__ void __launch_bounds__(kDzThreads)
     dz_kernel(const __nv_bfloat16 *__restrict__ g, int64_t ldg,
-              const __nv_bfloat16 *__restrict__ z, int64_t ldz, int M, int N, int splits,
+              const __nv_bfloat16 *__restrict__ z, int64_t ldz, int M, int N, int cols, int splits,
               __nv_bfloat16 *__restrict__ dz, int64_t lddz, void *__restrict__ db, int f32) {
-  constexpr int kRowsAtOnce = kWide ? 32 : 8;
-  constexpr int kOwn = kWide ? 8 : 2;  // columns per thread
-  constexpr int kBatch = 4;  // rows in flight per thread
-  __shared__ float sums[kRowsAtOnce][kDzCols];
-  __shared__ float total[kDzCols];
+  constexpr int kBatch = kAligned ? 4 : 2;  // rows in flight per thread
+  __shared__ float sums[kDzThreads * 8];  // [rows at once][cols]
+  __shared__ float total[64];
   const int tid = threadIdx.x;
+  const int lanes = cols / 8;  // threads per row: 8, 4 or 2
+  const int rows_at_once = kDzThreads / lanes;
   const int split = static_cast<int>(blockIdx.x) % splits;
   const int strip = static_cast<int>(blockIdx.x) / splits;
   const int m0 = static_cast<int>(static_cast<int64_t>(M) * split / splits);
   const int m1 = static_cast<int>(static_cast<int64_t>(M) * (split + 1) / splits);
-  const int r0 = kWide ? tid >> 3 : tid >> 5;
-  const int c0 = kWide ? (tid & 7) * 8 : tid & 31;  // wide: c0 .. + 7; narrow: c0, c0 + 32
-  const int64_t col = static_cast<int64_t>(strip) * kDzCols + c0;
+  const int r0 = tid / lanes;
+  const int c0 = tid % lanes * 8;
+  const int64_t col = static_cast<int64_t>(strip) * cols + c0;
   pdl_wait();
-  float s[kOwn] = {};
-  if (kWide && col + 8 <= N) {
-    for (int m = m0 + r0; m < m1; m += kBatch * kRowsAtOnce) {
-      uint4 vg[kBatch], vz[kBatch];
+  float s[8] = {};
+  if (kAligned ? col + 8 <= N : col >= 8 && col + 16 <= N) {
+    for (int m = m0 + r0; m < m1; m += kBatch * rows_at_once) {
+      Eight<kAligned> vg[kBatch], vz[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t r = m + u * kRowsAtOnce;
-        if (r < m1) {
-          vg[u] = ld_stream_v4(g + r * ldg + col);
-          if (kAct != SGA_ACT_NONE) vz[u] = ld_stream_v4(z + r * ldz + col);
-        }
+        // (a row past the end reads the last one again)
+        const int64_t r = min(m + u * rows_at_once, m1 - 1);
+        vg[u].load(g + r * ldg + col);
+        if (kAct != SGA_ACT_NONE) vz[u].load(z + r * ldz + col);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int64_t r = m + u * kRowsAtOnce;
+        const int64_t r = m + u * rows_at_once;
         if (r >= m1) continue;
-        const uint32_t wg[4] = {vg[u].x, vg[u].y, vg[u].z, vg[u].w};
-        const uint32_t wz[4] = {vz[u].x, vz[u].y, vz[u].z, vz[u].w};
+        const uint4 qg = vg[u].get();
+        uint4 qz = qg;
+        if (kAct != SGA_ACT_NONE) qz = vz[u].get();
+        const uint32_t wg[4] = {qg.x, qg.y, qg.z, qg.w};
+        const uint32_t wz[4] = {qz.x, qz.y, qz.z, qz.w};
         uint32_t wo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float d0 = dz_term<kAct>(bf16_lo(wg[i]), bf16_lo(wz[i]));
           const float d1 = dz_term<kAct>(bf16_hi(wg[i]), bf16_hi(wz[i]));
-          s[2 * i % kOwn] += d0;
-          s[(2 * i + 1) % kOwn] += d1;
+          s[2 * i] += d0;
+          s[2 * i + 1] += d1;
           wo[i] = pack2(d0, d1);
         }
         if (dz != nullptr)
           *reinterpret_cast<uint4 *>(dz + r * lddz + col) = make_uint4(wo[0], wo[1], wo[2], wo[3]);
       }
     }
-  } else {
-    constexpr int kStep = kWide ? 1 : 32;  // (wide: the strip's ragged end)
-    for (int m = m0 + r0; m < m1; m += kBatch * kRowsAtOnce) {
-      float vg[kBatch][kOwn], vz[kBatch][kOwn];
+  } else if (col < N) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(8), N - col));
+    for (int m = m0 + r0; m < m1; m += rows_at_once) {
+      const __nv_bfloat16 *pg = g + m * ldg + col;
+      const __nv_bfloat16 *pz = kAct != SGA_ACT_NONE ? z + m * ldz + col : pg;
+      float vg[8], vz[8];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-          const int64_t r = m + u * kRowsAtOnce, c = col + i * kStep;
-          vg[u][i] = vz[u][i] = 0.0f;
-          if (r < m1 && c < N) {
-            vg[u][i] = ld_bf16(g + r * ldg + c);
-            if (kAct != SGA_ACT_NONE) vz[u][i] = ld_bf16(z + r * ldz + c);
-          }
-        }
+      for (int i = 0; i < 8; ++i) {  // (columns past the end read the last one again)
+        vg[i] = ld_bf16(pg + min(i, n - 1));
+        vz[i] = ld_bf16(pz + min(i, n - 1));
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-          const int64_t r = m + u * kRowsAtOnce, c = col + i * kStep;
-          if (r < m1 && c < N) {
-            const float d = dz_term<kAct>(vg[u][i], vz[u][i]);
-            s[i] += d;
-            if (dz != nullptr) dz[r * lddz + c] = __float2bfloat16_rn(d);
-          }
+      for (int i = 0; i < 8; ++i) {
+        const float d = dz_term<kAct>(vg[i], vz[i]);
+        if (i < n) {
+          s[i] += d;
+          if (dz != nullptr) dz[m * lddz + col + i] = __float2bfloat16_rn(d);
         }
       }
     }
@@ -1099,19 +1113,20 @@ __global__ void __launch_bounds__(kDzThreads)
   pdl_launch_dependents();
   if (db == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < kOwn; ++i) sums[r0][kWide ? c0 + i : c0 + 32 * i] = s[i];
+  for (int i = 0; i < 8; ++i) sums[r0 * cols + c0 + i] = s[i];
   __syncthreads();
-  if (tid < kDzCols) {
+  if (tid < cols) {
     float t = 0.0f;
-    for (int r = 0; r < kRowsAtOnce; ++r) t += sums[r][tid];
+#pragma unroll 8
+    for (int r = 0; r < min(rows_at_once, m1 - m0); ++r) t += sums[r * cols + tid];
     total[tid] = t;
   }
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
-  if (split == 0 && tid < kDzCols && strip * kDzCols + tid < N) {
+  if (split == 0 && tid < cols && strip * cols + tid < N) {
     float t = 0.0f;
     for (int i = 0; i < splits; ++i) t += cluster.map_shared_rank(total, i)[tid];
-    const int c = strip * kDzCols + tid;
+    const int c = strip * cols + tid;
     if (f32)
       static_cast<float *>(db)[c] = t;
     else
@@ -1315,25 +1330,28 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
                             static_cast<int>(m.a.strided), m.ep, err);
 }
 
-// Whether a product runs as few_rows_kernel: always up to 128 rows; above where
-// its tiles, split over K, end sooner than the pairs' (estimated as 350 ns a K
-// block for each CTA of an SM, which its 32 KB take from L2, and 25 ns for each
-// 64 results of a CTA's share).
-bool few_rows_form(const Mat &m, int num_sms) {
-  if (m.a.strided) return false;  // (few_rows_kernel reads x with K contiguous)
-  if (m.rows <= 128) return true;
-  if (m.rows > 2048) return false;
+// Estimated time of a product as few_rows_kernel: 350 ns a K block for each CTA
+// of an SM, which its 32 KB take from L2, and 25 ns for each 64 results of a
+// CTA's share.
+int64_t few_rows_ns(const Mat &m, int num_sms) {
   const int num_kb = static_cast<int>((m.summed + 63) / 64);
   const int64_t units = (m.cols + 127) / 128 * ((m.rows + 127) / 128);
   const int splits = few_splits(units, num_kb, num_sms);
   const int64_t per_sm = (units * splits + num_sms - 1) / num_sms;
-  const int64_t ns = per_sm * ((num_kb + splits - 1) / splits * 350 + 128 * 128 / splits * 25 / 64);
-  return ns < pick_width(&m, 1, num_sms).ns;
+  const int64_t rows = m.rows < 128 ? m.rows : 128;
+  return per_sm * ((num_kb + splits - 1) / splits * 350 + 128 * rows / splits * 25 / 64);
 }
 
-// One product; of few rows with the weight as the row operand.
-cudaError_t launch_product(const Mat &m, int num_sms, uint32_t *err, cudaStream_t stream) {
-  if (!few_rows_form(m, num_sms)) return launch_products(&m, 1, num_sms, err, stream);
+// Whether a product runs as few_rows_kernel: always up to 128 rows; above where
+// its tiles, split over K, end sooner than the pairs'.
+bool few_rows_form(const Mat &m, int num_sms) {
+  if (m.a.strided) return false;  // (few_rows_kernel reads x with K contiguous)
+  if (m.rows <= 128) return true;
+  return m.rows <= 2048 && few_rows_ns(m, num_sms) < pick_width(&m, 1, num_sms).ns;
+}
+
+// As few_rows_kernel: the weight becomes the row operand.
+cudaError_t launch_few(const Mat &m, int num_sms, uint32_t *err, cudaStream_t stream) {
   const Mat t = {m.b, m.a, m.cols, m.rows, m.summed, m.ep};
   if (m.rows <= 16) return launch_few_rows<16>(t, num_sms, err, stream);
   if (m.rows <= 32) return launch_few_rows<32>(t, num_sms, err, stream);
@@ -1345,15 +1363,17 @@ int64_t dz_ld(int64_t N) { return (N + 7) / 8 * 8; }
 
 template <int kAct>
 cudaError_t launch_dz(const __nv_bfloat16 *g, int64_t ldg, const __nv_bfloat16 *z, int64_t ldz,
-                      int64_t M, int64_t N, __nv_bfloat16 *dz, void *db, bool f32,
+                      int64_t M, int64_t N, __nv_bfloat16 *dz, void *db, bool f32, int num_sms,
                       cudaStream_t stream) {
   uintptr_t bits = reinterpret_cast<uintptr_t>(g) | (2 * ldg);
   if (kAct != SGA_ACT_NONE) bits |= reinterpret_cast<uintptr_t>(z) | (2 * ldz);
-  const bool wide = bits % 16 == 0;
+  const bool aligned = bits % 16 == 0;
   int splits = 1;  // 32 rows or more per CTA
   while (splits < kDzMaxSplits && M >= 64 * splits) splits *= 2;
+  int cols = 64;
+  while (cols > 16 && M > 256 && (N + cols - 1) / cols * splits < 3 * num_sms) cols /= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((N + kDzCols - 1) / kDzCols * splits));
+  cfg.gridDim = dim3(static_cast<unsigned>((N + cols - 1) / cols * splits));
   cfg.blockDim = dim3(kDzThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -1365,9 +1385,9 @@ cudaError_t launch_dz(const __nv_bfloat16 *g, int64_t ldg, const __nv_bfloat16 *
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  auto kern = wide ? dz_kernel<kAct, true> : dz_kernel<kAct, false>;
+  auto kern = aligned ? dz_kernel<kAct, true> : dz_kernel<kAct, false>;
   return cudaLaunchKernelEx(&cfg, kern, g, ldg, z, ldz, static_cast<int>(M), static_cast<int>(N),
-                            splits, dz, dz_ld(N), db, static_cast<int>(f32));
+                            cols, splits, dz, dz_ld(N), db, static_cast<int>(f32));
 }
 
 }  // namespace
@@ -1385,7 +1405,8 @@ cudaError_t launch_linear(const void *x, int64_t M, int64_t K, int64_t ldx, cons
   m.ep = {static_cast<__nv_bfloat16 *>(out), static_cast<__nv_bfloat16 *>(preact),
           static_cast<const __nv_bfloat16 *>(residual), bias, ldo, ldp, ldr,
           bias_dtype == SGA_F32, act};
-  return launch_product(m, num_sms, err, stream);
+  return few_rows_form(m, num_sms) ? launch_few(m, num_sms, err, stream)
+                                   : launch_products(&m, 1, num_sms, err, stream);
 }
 
 size_t linear_grad_workspace_bytes(int64_t M, int64_t N) {
@@ -1410,39 +1431,41 @@ cudaError_t launch_linear_grad(const void *grad_out, int64_t M, int64_t N, int64
         launch_dz<SGA_ACT_GELU>, launch_dz<SGA_ACT_GELU_TANH>};
     e = launch[act](static_cast<const __nv_bfloat16 *>(grad_out), ldg,
                     static_cast<const __nv_bfloat16 *>(preact), ldp, M, N,
-                    products && !direct ? dz : nullptr, grad_bias, bias_dtype == SGA_F32, stream);
+                    products && !direct ? dz : nullptr, grad_bias, bias_dtype == SGA_F32, num_sms,
+                    stream);
     if (e != cudaSuccess) return e;
   }
   const Operand d = direct ? Operand{grad_out, ldg, false} : Operand{dz, dz_ld(N), false};
-  Mat mats[2] = {};
-  int n = 0;
-  if (grad_x != nullptr) {
-    Mat &m = mats[n++];
-    m.a = d;
-    m.b = {weight, ldw, true};
-    m.rows = M;
-    m.cols = K;
-    m.summed = N;
-    m.ep.out = static_cast<__nv_bfloat16 *>(grad_x);
-    m.ep.ldo = ldgx;
-    if (few_rows_form(m, num_sms)) {
-      e = launch_product(m, num_sms, err, stream);
-      if (e != cudaSuccess) return e;
-      n = 0;
-    }
+  Mat dx = {}, dw = {};
+  dx.a = d;
+  dx.b = {weight, ldw, true};
+  dx.rows = M;
+  dx.cols = K;
+  dx.summed = N;
+  dx.ep.out = static_cast<__nv_bfloat16 *>(grad_x);
+  dx.ep.ldo = ldgx;
+  dw.a = {d.ptr, d.ld, true};
+  dw.b = {x, ldx, true};
+  dw.rows = N;
+  dw.cols = K;
+  dw.summed = M;
+  dw.ep.out = static_cast<__nv_bfloat16 *>(grad_weight);
+  dw.ep.ldo = ldgw;
+  const Mat both[2] = {dx, dw};
+  // grad_x and grad_weight share a launch unless grad_x as few_rows_kernel, a
+  // launch of its own (5 us more), ends sooner.  (Decided as if both were asked
+  // for: the forms add up in different orders.)
+  const bool few =
+      M <= 2048 && few_rows_ns(dx, num_sms) + pick_width(&dw, 1, num_sms).ns + 5000 <
+                       pick_width(both, 2, num_sms).ns;
+  if (grad_x != nullptr && few) {
+    e = launch_few(dx, num_sms, err, stream);
+    if (e != cudaSuccess) return e;
   }
-  if (grad_weight != nullptr) {
-    Mat &m = mats[n++];
-    m = Mat{};
-    m.a = {d.ptr, d.ld, true};
-    m.b = {x, ldx, true};
-    m.rows = N;
-    m.cols = K;
-    m.summed = M;
-    m.ep.out = static_cast<__nv_bfloat16 *>(grad_weight);
-    m.ep.ldo = ldgw;
-  }
-  return n > 0 ? launch_products(mats, n, num_sms, err, stream) : cudaSuccess;
+  const bool with_x = grad_x != nullptr && !few;
+  if (with_x && grad_weight != nullptr) return launch_products(both, 2, num_sms, err, stream);
+  if (with_x) return launch_products(&dx, 1, num_sms, err, stream);
+  return grad_weight != nullptr ? launch_products(&dw, 1, num_sms, err, stream) : cudaSuccess;
 }
 
 }  // namespace sga
