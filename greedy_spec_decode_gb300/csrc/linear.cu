@@ -96,7 +96,7 @@ struct Epilogue {
   const void *bias;
   int64_t ldo, ldp, ldr;
   int bias_f32, act;
-  int tma_out, tma_pre, tma_res;  // gemm_kernel: TMA can reach the matrix
+  int aligned;  // gemm_kernel: rows of out, pre and res start on 16-byte boundaries
 };
 
 // ------------------------------------------------------------- descriptors
@@ -183,7 +183,6 @@ __device__ __forceinline__ bool pair_tile(const Products &prods, int pair, int n
 
 struct Maps {
   CUtensorMap a[kMaxProducts], b[kMaxProducts];
-  CUtensorMap out[kMaxProducts], pre[kMaxProducts], res[kMaxProducts];  // 32 x 64 boxes
 };
 
 constexpr int kGemmThreads = 320;        // producer, MMA, eight epilogue warps
@@ -206,7 +205,6 @@ struct SharedGemm {
   uint64_t empty[gemm_stages<kBN>];
   uint64_t tmem_full[2];
   uint64_t tmem_empty[2];
-  uint64_t res_full[kEpiWarps];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -225,19 +223,13 @@ __device__ __forceinline__ void tile_at(const Product &p, int t, int &tr, int &t
   tr = band * kBand + in - tc * height;
 }
 
-// A warp's box of results in shared memory: 32 rows of 64 bf16, in the
-// 128-byte swizzle of the tensor maps (16-byte piece j of row r at piece j ^
-// (r & 7)), so that a lane per row writes it without bank conflicts.
+// A warp's box of results in shared memory: 32 rows of 64 bf16, 16-byte piece j
+// of row r at piece j ^ (r & 7), so that a lane per row (from the accumulators)
+// and eight lanes per row (to global memory) access it without bank conflicts.
+// (TMA stores from the box were slower: their reads of it hold up the next box
+// by 350 to 750 cycles, the eight 16-byte stores a lane by about 250.)
 __device__ __forceinline__ uint4 *box_piece(uint8_t *box, int r, int j) {
   return reinterpret_cast<uint4 *>(box + r * ROW_BYTES + ((j ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ void box_store_tma(const CUtensorMap *map, uint32_t box, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
-      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
-      "r"(x), "r"(y), "r"(box)
-      : "memory");
 }
 
 // Bytes s .. s + 15 (s even, 0 .. 16) of two 16-byte pieces in a row.
@@ -259,18 +251,29 @@ __device__ __forceinline__ unsigned short *box_elem(uint8_t *box, int r, int c) 
   return reinterpret_cast<unsigned short *>(box_piece(box, r, c >> 3)) + (c & 7);
 }
 
-// Where TMA cannot go (rows not on 16-byte boundaries).  Whole boxes: eight
-// lanes per row; with the row `off` bytes past a boundary, its aligned 16-byte
-// pieces (seven, or eight where off is 0) go as such, put together from two
-// pieces of the box, and the eight columns at its ends one by one.  (Two-byte
-// accesses throughout: 3660 x 14645 x 144 took 81 us.)  Boxes at the right
-// edge: two columns a lane.
+// Box <-> global memory, whole boxes: eight lanes per row.  Rows on 16-byte
+// boundaries (kAligned) as they are; else, with the row `off` bytes past a
+// boundary, its aligned 16-byte pieces go as such, put together from two pieces
+// of the box, and the eight columns at its ends one by one.  (Two-byte accesses
+// throughout: 3660 x 14645 x 144 took 81 us.)  Boxes at the right edge: two
+// columns a lane.
+template <bool kAligned>
 __device__ __forceinline__ void box_store_rows(uint8_t *box, __nv_bfloat16 *p, int64_t ld, int rows,
                                                int cols, int lane) {
   if (cols >= 64) {
     const int j = lane & 7;
+    if constexpr (kAligned) {
+      uint4 *q = reinterpret_cast<uint4 *>(p + (lane >> 3) * ld) + j;
+#pragma unroll
+      for (int r = lane >> 3; r < 32; r += 4) {
+        const uint4 w = *box_piece(box, r, j);
+        if (r < rows) *q = w;
+        q += ld / 2;  // four rows on
+      }
+      return;
+    }
 #pragma unroll 2
-    for (int r = lane >> 3; r < 32; r += 4) {
+    for (int r = lane >> 3; !kAligned && r < 32; r += 4) {
       unsigned short *q = reinterpret_cast<unsigned short *>(p + r * ld);
       const int off = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
       const uint4 w = bytes_of(*box_piece(box, r, max(j - 1, 0)), *box_piece(box, r, j), 16 - off);
@@ -293,10 +296,20 @@ __device__ __forceinline__ void box_store_rows(uint8_t *box, __nv_bfloat16 *p, i
   }
 }
 
+template <bool kAligned>
 __device__ __forceinline__ void box_load_rows(uint8_t *box, const __nv_bfloat16 *p, int64_t ld,
                                               int rows, int cols, int lane) {
   if (cols >= 64) {
     const int j = lane & 7;
+    if (kAligned) {
+      uint4 w[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        w[u] = *(reinterpret_cast<const uint4 *>(p + min((lane >> 3) + 4 * u, rows - 1) * ld) + j);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) *box_piece(box, (lane >> 3) + 4 * u, j) = w[u];
+      return;
+    }
     constexpr int kBatch = 4;
 #pragma unroll 1
     for (int r0 = lane >> 3; r0 < 32; r0 += 4 * kBatch) {
@@ -358,7 +371,8 @@ __device__ __forceinline__ void box_fill_piece(uint8_t *box, const uint32_t *r, 
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; i += 4) {
-    const float4 b = *reinterpret_cast<const float4 *>(bias + j * 8 + i);
+    float4 b = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (bias != nullptr) b = *reinterpret_cast<const float4 *>(bias + j * 8 + i);
     y[i] = activate(__uint_as_float(r[i]) + b.x, kAct);
     y[i + 1] = activate(__uint_as_float(r[i + 1]) + b.y, kAct);
     y[i + 2] = activate(__uint_as_float(r[i + 2]) + b.z, kAct);
@@ -450,9 +464,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sh->tmem_full[b]), 1);
-      mbar_init(smem_u32(&sh->tmem_empty[b]), 2 * kEpiWarps);
+      // this CTA's epilogue warps, and in the leader the follower's word
+      mbar_init(smem_u32(&sh->tmem_empty[b]), kEpiWarps + (leader ? 1 : 0));
     }
-    for (int w = 0; w < kEpiWarps; ++w) mbar_init(smem_u32(&sh->res_full[w]), 1);
     mbar_init(smem_u32(&sh->drain), 1);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -566,6 +580,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
     }
+  } else if (warp == 1) {
+    // ----------------------------------------------------- word to the leader
+    // The follower's epilogue warps release an accumulator on a barrier of
+    // their own; this otherwise idle warp passes that on.  (An arrival at the
+    // peer waits for the writes before it: 1400 cycles of an epilogue warp.)
+    int acc = 0, pi, t;
+    uint32_t acc_phase = 0;
+    const uint32_t at_leader[2] = {map_to_rank(smem_u32(&sh->tmem_empty[0]), 0),
+                                   map_to_rank(smem_u32(&sh->tmem_empty[1]), 0)};
+    for (int n = 0; pair_tile(prods, pair, num_pairs, n, pi, t); ++n) {
+      if (!warp_wait(smem_u32(&sh->tmem_empty[acc]), acc_phase, abort_flag)) {
+        if (lane == 0) raise_abort(&sh->abort, err);
+        break;
+      }
+      tc_fence_after();
+      tc_fence_before();
+      if (lane == 0) mbar_arrive_remote(at_leader[acc]);
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
   } else if (warp >= 2) {
     // -------------------------------------------------- epilogue (both CTAs)
     // Warps 2..5 and 6..9 each cover the four TMEM lane quarters and take the
@@ -573,13 +608,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int quarter = warp & 3;
     const int half = warp >= 6;
     uint8_t *box = boxes + (warp - 2) * kBox;
-    const uint32_t box_u32 = smem_u32(box);
-    const uint32_t res_bar = smem_u32(&sh->res_full[warp - 2]);
-    const uint32_t empty_leader[2] = {map_to_rank(smem_u32(&sh->tmem_empty[0]), 0),
-                                      map_to_rank(smem_u32(&sh->tmem_empty[1]), 0)};
     int acc = 0, pi, t;
-    uint32_t acc_phase = 0, res_phase = 0;
-    bool ok = true, res_inflight = false;
+    uint32_t acc_phase = 0;
+    bool ok = true;
     for (int n = 0; ok && pair_tile(prods, pair, num_pairs, n, pi, t); ++n) {
       const Product &p = prods.p[pi];
       int tr, tc;
@@ -588,72 +619,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const int cols = p.cols;
       const int row0 = tr * 256 + static_cast<int>(rank) * 128 + quarter * 32;
       const int rows = min(32, p.rows - row0);
-      const CUtensorMap *map_out = &maps.out[pi], *map_pre = &maps.pre[pi],
-                        *map_res = &maps.res[pi];
-      // the tile's bias, once every warp is done with the last tile's
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      for (int c = threadIdx.x - 64; c < kBN; c += 32 * kEpiWarps)
-        sh->bias[c] = tc * kBN + c < cols
-                          ? ld_bias(ep.bias, ep.bias_f32, static_cast<int64_t>(tc) * kBN + c)
-                          : 0.0f;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      // fills the box with the residual; true when TMA does (wait on res_bar)
-      auto load_res = [&](int col0) {
-        if (ep.tma_res) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (elect_one()) {
-            mbar_expect_tx(res_bar, kBox);
-            tma_load_2d(box_u32, map_res, col0, row0, res_bar);
-          }
-          res_inflight = true;
-        } else {
-          box_load_rows(box, ep.res + row0 * ep.ldr + col0, ep.ldr, rows, cols - col0, lane);
-        }
+      if (ep.bias != nullptr) {
+        // the tile's bias, once every warp is done with the last tile's
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        for (int c = threadIdx.x - 64; c < kBN; c += 32 * kEpiWarps)
+          sh->bias[c] = tc * kBN + c < cols
+                            ? ld_bias(ep.bias, ep.bias_f32, static_cast<int64_t>(tc) * kBN + c)
+                            : 0.0f;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+      }
+      auto load = [&](const __nv_bfloat16 *q, int64_t ld, int col0) {
+        if (ep.aligned)
+          box_load_rows<true>(box, q + row0 * ld + col0, ld, rows, cols - col0, lane);
+        else
+          box_load_rows<false>(box, q + row0 * ld + col0, ld, rows, cols - col0, lane);
         __syncwarp();
       };
-      // waits until the last store from the box has been read out of it
-      auto box_free = [&]() {
-        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      auto store = [&](__nv_bfloat16 *q, int64_t ld, int col0) {
         __syncwarp();
-      };
-      auto store = [&](bool tma, const CUtensorMap *map, __nv_bfloat16 *q, int64_t ld, int col0) {
-        if (tma) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (elect_one()) box_store_tma(map, box_u32, col0, row0);
-        } else {
-          __syncwarp();
-          box_store_rows(box, q + row0 * ld + col0, ld, rows, cols - col0, lane);
-        }
+        if (ep.aligned)
+          box_store_rows<true>(box, q + row0 * ld + col0, ld, rows, cols - col0, lane);
+        else
+          box_store_rows<false>(box, q + row0 * ld + col0, ld, rows, cols - col0, lane);
         __syncwarp();
       };
       const int first = tc * kBN + half * 64;
-      const bool any = rows > 0 && half * 64 < kBN && first < cols;
-      bool res_ready = false;  // asked for ahead of the accumulators
-      if (any && ep.res != nullptr && ep.pre == nullptr) {
-        box_free();
-        load_res(first);
-        res_ready = true;
-      }
+      // the first piece's residual, ahead of the accumulators
+      const bool early = rows > 0 && half * 64 < kBN && first < cols && ep.res != nullptr &&
+                         ep.pre == nullptr;
+      if (early) load(ep.res, ep.ldr, first);
       ok = warp_wait(smem_u32(&sh->tmem_full[acc]), acc_phase, abort_flag);
       if (!ok && lane == 0) raise_abort(&sh->abort, err);
       if (ok) {
         tc_fence_after();
         const uint32_t tlane =
             tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN;
-        // the accumulators have been read: the MMA may overwrite them.  (Early:
-        // an arrival at the peer waits for the writes before it.)
+        // the accumulators have been read: the MMA may overwrite them
         bool released = false;
         auto release = [&]() {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            if (leader)
-              mbar_arrive(smem_u32(&sh->tmem_empty[acc]));
-            else
-              mbar_arrive_remote(empty_leader[acc]);
-          }
+          if (lane == 0) mbar_arrive(smem_u32(&sh->tmem_empty[acc]));
           released = true;
         };
 #pragma unroll 1
@@ -661,29 +667,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           const int col0 = tc * kBN + q;
           if (rows <= 0 || col0 >= cols) break;
           const bool last = q + 128 >= kBN || col0 + 128 >= cols;
-          if (!res_ready) box_free();
+          const float *bias = ep.bias != nullptr ? sh->bias + q : nullptr;
           if (ep.pre != nullptr) {
-            box_fill_act<SGA_ACT_NONE>(box, tlane + q, sh->bias + q, false, lane, [] {});
-            store(ep.tma_pre, map_pre, ep.pre, ep.ldp, col0);
-            box_free();
+            box_fill_act<SGA_ACT_NONE>(box, tlane + q, bias, false, lane, [] {});
+            store(ep.pre, ep.ldp, col0);
           }
-          if (ep.res != nullptr) {
-            if (!res_ready) load_res(col0);
-            res_ready = false;
-            if (ep.tma_res) {
-              ok = warp_wait(res_bar, res_phase, abort_flag);
-              if (!ok) {
-                if (lane == 0) raise_abort(&sh->abort, err);
-                break;
-              }
-              res_inflight = false;
-              res_phase ^= 1;
-            }
-          }
-          box_fill(box, tlane + q, sh->bias + q, ep.act, ep.res != nullptr, lane, [&] {
+          if (ep.res != nullptr && !(early && q < 128)) load(ep.res, ep.ldr, col0);
+          box_fill(box, tlane + q, bias, ep.act, ep.res != nullptr, lane, [&] {
             if (last) release();
           });
-          store(ep.tma_out, map_out, ep.out, ep.ldo, col0);
+          store(ep.out, ep.ldo, col0);
         }
         if (!released) release();
       }
@@ -692,17 +685,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       // (an epilogue warp that gives up keeps to the barriers of the others)
       if (!ok) {
         for (int u = n + 1; pair_tile(prods, pair, num_pairs, u, pi, t); ++u) {
+          if (prods.p[pi].ep.bias == nullptr) continue;
           asm volatile("bar.sync 1, 256;" ::: "memory");
           asm volatile("bar.sync 1, 256;" ::: "memory");
         }
       }
     }
-    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    if (res_inflight) {  // gave up with a copy under way
-      const int zero = 0;
-      mbar_wait(res_bar, res_phase, &zero);
-    }
-    __syncwarp();
   }
 
   pdl_launch_dependents();
@@ -1175,11 +1163,8 @@ bool operand_map(CUtensorMap *map, const Operand &o, int64_t other, int64_t summ
 // the turn of the pipeline between tiles.
 int64_t tile_cost(int num_kb) { return (num_kb > 12 ? num_kb : 12) + 2; }
 
-// Map of a result (or residual) matrix, where TMA can reach it: a 16-byte
-// aligned base and row stride.
-int result_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t cols, int64_t ld) {
-  if (ptr == nullptr || reinterpret_cast<uintptr_t>(ptr) % 16 != 0 || ld % 8 != 0) return 0;
-  return make_map_ld(map, ptr, rows, cols, ld, 32) ? 1 : 0;
+bool aligned_rows(const void *p, int64_t ld) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) | (2 * ld)) % 16 == 0;
 }
 
 template <int kBN>
@@ -1201,9 +1186,8 @@ cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cuda
     if (!operand_map(&maps.a[i], m.a, m.rows, m.summed, 128) ||
         !operand_map(&maps.b[i], m.b, m.cols, m.summed, kBN / 2))
       return cudaErrorNotSupported;
-    p.ep.tma_out = result_map(&maps.out[i], m.ep.out, m.rows, m.cols, m.ep.ldo);
-    p.ep.tma_pre = result_map(&maps.pre[i], m.ep.pre, m.rows, m.cols, m.ep.ldp);
-    p.ep.tma_res = result_map(&maps.res[i], m.ep.res, m.rows, m.cols, m.ep.ldr);
+    p.ep.aligned = aligned_rows(m.ep.out, m.ep.ldo) && aligned_rows(m.ep.pre, m.ep.ldp) &&
+                   aligned_rows(m.ep.res, m.ep.ldr);
   }
   auto kern = gemm_kernel<kBN>;
   const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), gemm_smem<kBN>,

@@ -12,6 +12,7 @@ namespace {
 // time hint) between looks at the clock and the abort flag.
 __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity,
                                           const volatile int *abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
   unsigned long long t0 = 0;
   while (true) {
     uint32_t ok;
