@@ -43,22 +43,13 @@ struct Lse {
   float r, s, w;
 };
 
-// a += b.  An empty side (s == 0) leaves the other's reference; otherwise the
-// larger reference stays and the other side is scaled down to it.
-__device__ __forceinline__ void lse_merge(Lse &a, const Lse &b) {
-  if (b.s == 0.0f) return;
-  if (a.s == 0.0f) {
-    a = b;
-    return;
-  }
-  const float r = max_nan(a.r, b.r);
-  const float da = a.r - r, db = b.r - r;  // <= 0, one of them 0
-  const float fa = ex2(da), fb = ex2(db);
-  // sum (t + d) 2^(t + d) = 2^d (w + d s); a vanished side contributes 0
-  const float wa = fa == 0.0f ? 0.0f : fa * fmaf(da, a.s, a.w);
-  const float wb = fb == 0.0f ? 0.0f : fb * fmaf(db, b.s, b.w);
-  a.s = fa * a.s + fb * b.s;
-  a.w = wa + wb;
+// The same sums relative to r >= a.r (or with a empty, s == 0):
+// sum (t + d) 2^(t + d) = 2^d (w + d s); what vanishes contributes 0.
+__device__ __forceinline__ void lse_restate(Lse &a, float r) {
+  const float d = a.r - r;
+  const float f = a.s == 0.0f ? 0.0f : ex2(d);
+  a.w = f == 0.0f ? 0.0f : f * fmaf(d, a.s, a.w);
+  a.s = f * a.s;
   a.r = r;
 }
 
@@ -320,6 +311,15 @@ __device__ __forceinline__ uint32_t pack_lo(float limit, float threshold) {
   return b | (b << 16);
 }
 
+// Element i of an array of vectors in shared memory.
+template <bool kBf16>
+__device__ __forceinline__ float load_shared_elem(const uint4 *v, int i) {
+  if (kBf16)
+    return __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const unsigned short *>(v)[i])
+                           << 16);
+  return reinterpret_cast<const float *>(v)[i];
+}
+
 template <int kT>
 __device__ __forceinline__ void push_key(PieceShared<kT> &sh, float x, int32_t id) {
   const int at = atomicAdd(&sh.num_keys, 1);
@@ -360,8 +360,10 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
     int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(q.p) & 15u)) & 15u) / kElt);
     if (head > valid) head = valid;
     const int nvec = (valid - head) / kVec;
-    const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * chunk / chunks);
-    const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (chunk + 1) / chunks);
+    // (nvec < 2^22, chunks <= 8)
+    const int v0 = chunks == 1 ? 0 : static_cast<int>(static_cast<uint32_t>(nvec * chunk) / chunks);
+    const int v1 = chunks == 1 ? nvec
+                               : static_cast<int>(static_cast<uint32_t>(nvec * (chunk + 1)) / chunks);
     q.b0 = head + v0 * kVec;
     q.b1 = head + v1 * kVec;
     q.c0 = chunk == 0 ? 0 : q.b0;
@@ -518,18 +520,20 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       }
     }
     {
-      Lse b = sums_total(a);
+      // the warp's sums, relative to its largest reference
+      Lse t = sums_total(a);
+      mx = order_value(__reduce_max_sync(0xffffffffu, order_key(mx)));
+      const float r = order_value(
+          __reduce_max_sync(0xffffffffu, order_key(t.s == 0.0f ? neg_inf() : t.r)));
+      lse_restate(t, r);
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) {
-        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const Lse o = {__shfl_xor_sync(0xffffffffu, b.r, off),
-                       __shfl_xor_sync(0xffffffffu, b.s, off),
-                       __shfl_xor_sync(0xffffffffu, b.w, off)};
-        lse_merge(b, o);
+        t.s += __shfl_xor_sync(0xffffffffu, t.s, off);
+        t.w += __shfl_xor_sync(0xffffffffu, t.w, off);
       }
       if (lane == 0) {
         sh.warp_max[warp] = mx;
-        sh.warp_lse[warp] = b;
+        sh.warp_lse[warp] = t;
       }
     }
     consumers_sync<kT>();  // every candidate vector is in the buffer
@@ -537,13 +541,10 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
     // ---- the piece's alternatives into best[]
     if (k > 0) {
       const int nv = min(sh.num_vecs, sh.kVecs);
-      for (int i = tid; i < nv; i += kT) {
-        float x[kVec];
-        vec_elems<kBf16>(sh.vec[i], x);
-        const int32_t id = sh.vec_id[i];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-          if (reaches(x[e], threshold)) push_key(sh, x[e], id + e);
+      for (int i = tid; i < nv * kVec; i += kT) {
+        const int e = i % kVec;
+        const float x = load_shared_elem<kBf16>(sh.vec, i);
+        if (reaches(x, threshold)) push_key(sh, x, sh.vec_id[i / kVec] + e);
       }
       if (tid < k) sh.best[tid] = 0;
       consumers_sync<kT>();
@@ -634,20 +635,16 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
         }
       }
     }
-    if (tid == 0) {
-      float m = sh.warp_max[0];
-      for (int w = 1; w < kWarps; ++w) m = max_nan(m, sh.warp_max[w]);
-      sh.max = m;
-    }
-    if (chunks > 1)
-      cluster.sync();
-    else
-      consumers_sync<kT>();
-
     // ---- the row: every CTA joins the maxima and restates its sums
-    float row_max = sh.max;
-    for (int c = 0; c < chunks && chunks > 1; ++c)
-      row_max = max_nan(row_max, *cluster.map_shared_rank(&sh.max, c));
+    float row_max = neg_inf();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) row_max = max_nan(row_max, sh.warp_max[w]);
+    if (chunks > 1) {
+      if (tid == 0) sh.max = row_max;
+      cluster.sync();
+      for (int c = 0; c < chunks; ++c)
+        row_max = max_nan(row_max, *cluster.map_shared_rank(&sh.max, c));
+    }
     // An extreme finite maximum: sums relative to the maximum itself, in
     // differences from it, over the piece once more.
     const bool exact = (row_max > kFastMax && row_max < __int_as_float(0x7f800000)) ||
@@ -665,39 +662,70 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
         es += __shfl_xor_sync(0xffffffffu, es, off);
         ew += __shfl_xor_sync(0xffffffffu, ew, off);
       }
+      consumers_sync<kT>();  // the others have read the sums of the first pass
       if (lane == 0) sh.warp_lse[warp] = {0.0f, es, ew};
-      consumers_sync<kT>();
     }
-    if (tid == 0) {
-      float s = 0.0f, w = 0.0f;
-      for (int i = 0; i < kWarps; ++i) {
-        const Lse t = sh.warp_lse[i];
-        const float d = exact ? 0.0f : fmaf(-row_max, kLog2e, t.r);
-        const float f = t.s == 0.0f ? 0.0f : ex2(d);
-        s = fmaf(f, t.s, s);
-        if (f != 0.0f) w = fmaf(f, fmaf(d, t.s, t.w), w);
+    // (best[] and, after an exact pass, the sums)
+    consumers_sync<kT>();
+    float s = 0.0f, w = 0.0f;
+    if (warp == 0) {
+      Lse t = {0.0f, 0.0f, 0.0f};
+      if (lane < kWarps) t = sh.warp_lse[lane];
+      // (the difference to the maximum in one rounding)
+      const float d = exact ? 0.0f : fmaf(-row_max, kLog2e, t.r);
+      const float f = t.s == 0.0f ? 0.0f : ex2(d);
+      s = f * t.s;
+      w = f == 0.0f ? 0.0f : f * fmaf(d, t.s, t.w);
+#pragma unroll
+      for (int off = kMaxWarps / 2; off > 0; off >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, off);
+        w += __shfl_xor_sync(0xffffffffu, w, off);
       }
-      sh.sum = s;
-      sh.wsum = w;
+      if (lane == 0) {
+        sh.sum = s;
+        sh.wsum = w;
+      }
     }
-    const Key *list = sh.best;
     if (chunks > 1) {
       cluster.sync();
-      if (chunk == 0)
+      if (chunk == 0) {
         for (int c = tid; c < chunks * k; c += kT)
           sh.list[c] = *cluster.map_shared_rank(&sh.best[c % k], c / k);
-      list = sh.list;
-    }
-    consumers_sync<kT>();
-    if (chunk == 0) {
-      float s = sh.sum, w = sh.wsum;
-      for (int c = 1; c < chunks; ++c) {
-        s += *cluster.map_shared_rank(&sh.sum, c);
-        w += *cluster.map_shared_rank(&sh.wsum, c);
+        consumers_sync<kT>();  // this piece's list has been gathered too
+        if (tid < k) sh.best[tid] = 0;
+        consumers_sync<kT>();
       }
+      if (chunk == 0 && warp == 0 && lane < chunks) {
+        s = *cluster.map_shared_rank(&sh.sum, lane);
+        w = *cluster.map_shared_rank(&sh.wsum, lane);
+      } else {
+        s = w = 0.0f;
+      }
+      if (chunk == 0 && warp == 0) {
+#pragma unroll
+        for (int off = kMaxChunks / 2; off > 0; off >>= 1) {
+          s += __shfl_xor_sync(0xffffffffu, s, off);
+          w += __shfl_xor_sync(0xffffffffu, w, off);
+        }
+        if (lane == 0) {
+          sh.sum = s;
+          sh.wsum = w;
+        }
+      }
+    }
+    if (chunk == 0) {
+      if (chunks > 1)
+        for (int c = tid; c < chunks * k; c += kT) {
+          const Key mine = sh.list[c];
+          const int rank = keys_above(sh.list, chunks * k, mine);
+          if (mine != 0 && rank < k) sh.best[rank] = mine;
+        }
+      consumers_sync<kT>();
       float lse, entropy;
-      finish_row(row_max, s, w, lse, entropy);
+      finish_row(row_max, sh.sum, sh.wsum, lse, entropy);
       if (tid == 0) {
+        s = sh.sum;
+        w = sh.wsum;
         if (out.part != nullptr) {
           out.part[row] = {row_max, s, w, xt};
         } else {
@@ -706,23 +734,14 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
           if (out.lse != nullptr) out.lse[row] = lse;
         }
       }
-      for (int c = tid; c < chunks * k; c += kT) {
-        const Key mine = list[c];
-        int rank = c;
-        if (chunks > 1) {
-          // empty entries (0) come last, in the order they stand
-          rank = 0;
-          for (int i = 0; i < chunks * k; ++i)
-            rank += list[i] > mine || (list[i] == mine && i < c);
-          if (rank >= k) continue;
-        }
-        const float v = key_value(mine);
-        const int32_t id = key_id(mine);
+      if (tid < k) {
+        const float v = key_value(sh.best[tid]);
+        const int32_t id = key_id(sh.best[tid]);
         if (out.part != nullptr) {
-          out.top[row * k + rank] = {v, id};
+          out.top[row * k + tid] = {v, id};
         } else {
-          if (out.top_ids != nullptr) out.top_ids[row * k + rank] = id == kNoId ? -1 : id;
-          if (out.top_logprobs != nullptr) out.top_logprobs[row * k + rank] = to_logprob(v, lse);
+          if (out.top_ids != nullptr) out.top_ids[row * k + tid] = id == kNoId ? -1 : id;
+          if (out.top_logprobs != nullptr) out.top_logprobs[row * k + tid] = to_logprob(v, lse);
         }
       }
     }
