@@ -65,9 +65,9 @@ __device__ __forceinline__ void lse_restate(Lse &a, float r) {
 // alternatives 809 us against 278 without).  Instead a threshold is taken
 // from what the ring holds at first (24576 bf16 ids): the top_k-th largest of
 // the maxima of 64 groups of threads, which at least top_k elements reach.
-// Vectors that reach it go to a candidate buffer (about a hundred of 25000),
-// from which the top_k are selected at the end by counting, on 64-bit keys
-// that order (value, id) pairs.  -inf is never a candidate: where fewer than
+// Vectors that reach it go to a candidate buffer (some tens to hundreds of
+// 25000), from which the top_k are selected at the end by counting, on 64-bit
+// keys that order (value, id) pairs.  -inf is never a candidate: where fewer than
 // top_k elements are above it, the lowest masked ids fill the list.  If the
 // buffer overflows the piece is read again: for what lies above the threshold,
 // the lowest ids that equal it filling up (rows with very many equal values),
@@ -321,14 +321,54 @@ __device__ __forceinline__ float load_shared_elem(const uint4 *v, int i) {
 }
 
 template <int kT>
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+}
+
+template <int kT>
 __device__ __forceinline__ void push_key(PieceShared<kT> &sh, float x, int32_t id) {
   const int at = atomicAdd(&sh.num_keys, 1);
   if (at < sh.kKeys) sh.key[at] = pair_key(x, id);
 }
 
+// The top_k of the n <= kKeys candidates into best (sorted), by counting.  Many
+// candidates are first cut by a threshold, as the row was: the top_k-th largest
+// of the maxima of 64 groups.
 template <int kT>
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+__device__ __forceinline__ void select_top(PieceShared<kT> &sh, int n, int k, int tid) {
+  const Key *from = sh.key;
+  if (n > kGroups) {
+    if (tid < kGroups) {
+      Key m = 0;
+      for (int i = tid; i < n; i += kGroups) m = max(m, sh.key[i]);
+      sh.list[tid] = m;
+    }
+    if (tid == 0) sh.num_vecs = 0;
+    consumers_sync<kT>();
+    if (tid < kGroups) {
+      const Key mine = sh.list[tid];
+      if (keys_above(sh.list, kGroups, mine) == k - 1) sh.best[0] = mine;
+    }
+    consumers_sync<kT>();
+    const Key threshold = sh.best[0];
+    Key *kept = reinterpret_cast<Key *>(sh.vec);  // (the candidate vectors have been read)
+    for (int i = tid; i < n; i += kT) {
+      const Key mine = sh.key[i];
+      if (mine >= threshold) kept[atomicAdd(&sh.num_vecs, 1)] = mine;
+    }
+    consumers_sync<kT>();
+    n = sh.num_vecs;
+    if (tid == 0 && (n & 1)) kept[n] = 0;
+    from = kept;
+  } else if (tid == 0 && (n & 1)) {
+    sh.key[n] = 0;
+  }
+  consumers_sync<kT>();
+  for (int i = tid; i < n; i += kT) {
+    const Key mine = from[i];
+    const int rank = keys_above(from, n, mine);
+    if (rank < k) sh.best[rank] = mine;
+  }
 }
 
 template <bool kBf16, int kT>
@@ -550,13 +590,7 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       consumers_sync<kT>();
       const int n = sh.num_keys;
       if (sh.num_vecs <= sh.kVecs && n <= sh.kKeys) {
-        if (tid == 0 && (n & 1)) sh.key[n] = 0;  // (kKeys is even)
-        consumers_sync<kT>();
-        for (int i = tid; i < n; i += kT) {
-          const Key mine = sh.key[i];
-          const int rank = keys_above(sh.key, n, mine);
-          if (rank < k) sh.best[rank] = mine;
-        }
+        select_top(sh, n, k, tid);
         if (n < k && warp == 0) {
           // masked elements fill the list, lowest ids first
           int have = n;
@@ -611,13 +645,7 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
           n = sh.num_keys;
         }
         if (n <= sh.kKeys) {
-          if (tid == 0 && (n & 1)) sh.key[n] = 0;
-          consumers_sync<kT>();
-          for (int i = tid; i < n; i += kT) {
-            const Key mine = sh.key[i];
-            const int rank = keys_above(sh.key, n, mine);
-            if (rank < k) sh.best[rank] = mine;
-          }
+          select_top(sh, n, k, tid);
         } else {
           // rows that keep rising: a sorted list per warp
           Key top = 0;
@@ -1050,8 +1078,12 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t
   const RowOut out = {logprob, entropy, lse, top_logprobs, top_ids, part, top};
   const int64_t nvec = valid * (dtype == SGA_BF16 ? 2 : 4) / 16;
   const int chunks = pick_row_chunks(rows, nvec, num_sms);
-  // many short rows: small CTAs, ten per SM
-  const bool small = chunks == 1 && nvec <= 2048 && rows > num_sms;
+  // Many short rows: small CTAs, ten per SM (bf16, 5 alternatives, wide / small:
+  // 1000 rows of 6000 ids 13.7 / 8.9 us, 4000 of 20000 64 / 58; 300 of 6000
+  // 5.4 / 6.5, 4096 of 32000 77 / 84), while their shorter ring still leaves few
+  // candidates.
+  const bool small = chunks == 1 && rows > 3 * num_sms && nvec <= 3072 &&
+                     nvec * (top_k > 0 ? top_k : 1) <= 768 * 80;
   if (dtype == SGA_BF16)
     return small ? launch_rows<true, 64>(logits, rows, ld, shard_start, valid, tokens, top_k,
                                          chunks, num_sms, out, err, stream)
