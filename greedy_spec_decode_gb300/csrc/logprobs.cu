@@ -179,7 +179,7 @@ __device__ __forceinline__ void finish_row(float max, float s, float w, float &l
   } else {
     const float l = logf(s);
     lse = max + l;
-    entropy = fmaf(-kLn2, w / s, l);
+    entropy = max_nan(fmaf(-kLn2, w / s, l), 0.0f);  // (rounding can leave it just below)
   }
 }
 
