@@ -765,6 +765,30 @@ template <int kN>
 constexpr int few_smem = 1024 + few_stages<kN> * few_stage<kN> + static_cast<int>(sizeof(SharedFew<kN>));
 static_assert(few_stages<128> * few_stage<128> >= 128 * 128 * 4, "a partial tile fits the ring");
 
+// n <= 4 consecutive bf16, as one access where they are four and aligned.
+__device__ __forceinline__ void load_four(const __nv_bfloat16 *p, int n, float (&x)[4]) {
+  if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    x[0] = bf16_lo(w.x);
+    x[1] = bf16_hi(w.x);
+    x[2] = bf16_lo(w.y);
+    x[3] = bf16_hi(w.y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = ld_bf16(p + (i < n ? i : n - 1));
+  }
+}
+
+__device__ __forceinline__ void store_four(__nv_bfloat16 *p, int n, const float (&x)[4]) {
+  if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = __float2bfloat16_rn(x[i]);
+  }
+}
+
 template <int kN>
 __global__ void __launch_bounds__(THREADS, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
@@ -927,51 +951,59 @@ __global__ void __launch_bounds__(THREADS, 2)
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   pdl_launch_dependents();
-  // this CTA's share of the tile's rows, for every m: a row per thread, so many
-  // m at once as there are threads for, four of those in flight
-  const int share = 128 / splits;
-  const int at_once = splits == 1 ? 1 : THREADS / share;
-  const int r = split * share + static_cast<int>(threadIdx.x) % share;
+  // This CTA's share of the tile's rows, for every m: a thread takes four rows
+  // of two m at a time and asks for every CTA's part at once (one after the
+  // other, the reads of the peers' memory took 500 cycles each).
+  const int quads = 32 / splits;
+  const int at_once = THREADS / quads;  // (quads divides THREADS)
+  const int r = (split * quads + static_cast<int>(threadIdx.x) % quads) * 4;
   const int64_t col = row0 + r;
-  if (static_cast<int>(threadIdx.x) < at_once * share && col < rows) {
-    const float bias = ld_bias(ep.bias, ep.bias_f32, col);
-    const uint32_t mine = smem_u32(part) + r * 4;
-    unsigned parts = 0;
-    for (int i = 0; i < splits; ++i)
-      parts |= static_cast<unsigned>(num_kb * i / splits != num_kb * (i + 1) / splits) << i;
-    __nv_bfloat16 *out = ep.out + first_m * ep.ldo + col;
-    __nv_bfloat16 *pre = ep.pre + first_m * ep.ldp + col;
-    const __nv_bfloat16 *residual = ep.res + first_m * ep.ldr + col;
-    for (int m0 = static_cast<int>(threadIdx.x) / share; m0 < M; m0 += 4 * at_once) {
-      float z[4];
-      unsigned short res[4];
+  const int n = static_cast<int>(min(static_cast<int64_t>(4), rows - col));
+  if (n > 0) {
+    float bias[4] = {};
+    for (int i = 0; i < n; ++i) bias[i] = ld_bias(ep.bias, ep.bias_f32, col + i);
+    uint32_t src[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+    for (int i = 0; i < 8; ++i)
+      src[i] = i < splits && num_kb * i / splits != num_kb * (i + 1) / splits
+                   ? map_to_rank(smem_u32(part) + r * 4, i)
+                   : 0u;  // (a CTA without K blocks has no part)
+    for (int m0 = static_cast<int>(threadIdx.x) / quads; m0 < M; m0 += 2 * at_once) {
+      float4 v[2][8];
+      float res[2][4] = {};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
         const int m = min(m0 + u * at_once, M - 1);
-        if (ep.res != nullptr)
-          res[u] = *reinterpret_cast<const unsigned short *>(residual + m * ep.ldr);
-        z[u] = 0.0f;
-      }
-      for (int i = 0; i < splits; ++i) {
-        if ((parts >> i & 1) == 0) continue;  // a CTA without K blocks has no part
-        const uint32_t src = map_to_rank(mine, i);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int m = min(m0 + u * at_once, M - 1);
-          float v;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(src + m * 512));
-          z[u] += v;
+        for (int i = 0; i < 8; ++i) {
+          v[u][i] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (src[i] != 0 && (u == 0 || M > at_once))
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[u][i].x), "=f"(v[u][i].y), "=f"(v[u][i].z), "=f"(v[u][i].w)
+                         : "r"(src[i] + m * 512));
         }
+        if (ep.res != nullptr)
+          load_four(ep.res + (first_m + m) * ep.ldr + col, n, res[u]);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int m = m0 + u * at_once;
-        if (m >= M) break;
-        const float zz = z[u] + bias;
-        if (ep.pre != nullptr) pre[m * ep.ldp] = __float2bfloat16_rn(zz);
-        float y = activate(zz, ep.act);
-        if (ep.res != nullptr) y += __uint_as_float(static_cast<uint32_t>(res[u]) << 16);
-        out[m * ep.ldo] = __float2bfloat16_rn(y);
+      for (int u = 0; u < 2; ++u) {
+        const int64_t m = first_m + m0 + u * at_once;
+        if (m0 + u * at_once >= M) break;
+        float z[4] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          z[0] += v[u][i].x;
+          z[1] += v[u][i].y;
+          z[2] += v[u][i].z;
+          z[3] += v[u][i].w;
+        }
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] += bias[i];
+        if (ep.pre != nullptr) store_four(ep.pre + m * ep.ldp + col, n, z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = activate(z[i], ep.act) + res[u][i];
+        store_four(ep.out + m * ep.ldo + col, n, y);
       }
     }
   }
@@ -1272,10 +1304,13 @@ cudaError_t launch_products(const Mat *mats, int n, int num_sms, uint32_t *err,
 
 // CTAs per tile of few_rows_kernel: while all of them are resident (two per SM).
 // A CTA's share of K blocks may be one or none; it still takes its share of
-// the results.
-int few_splits(int64_t units, int num_kb, int num_sms) {
+// the results.  Eight only for a long sum, or the least rows (M x N x K, 4 / 8
+// CTAs: 64 x 4096 x 4096 11.8 / 12.6 us, 64 x 1024 x 8192 14.8 / 11.0, 1 x 1024
+// x 8192 12.7 / 9.1, 1 x 4096 x 4096 10.0 / 9.7).
+int few_splits(int64_t units, int num_kb, int64_t m, int num_sms) {
+  const int most = num_kb >= 80 || (m <= 16 && num_kb >= 32) ? 8 : 4;
   int splits = 1;
-  while (splits < 8 && units * splits * 2 <= 2 * num_sms && num_kb >= splits) splits *= 2;
+  while (splits < most && units * splits * 2 <= 2 * num_sms && num_kb >= splits) splits *= 2;
   return splits;
 }
 
@@ -1289,7 +1324,7 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   const int num_kb = static_cast<int>((m.summed + 63) / 64);
   const int blocks = static_cast<int>((m.cols + kN - 1) / kN);
   const int64_t units = (m.rows + 127) / 128 * blocks;
-  const int splits = few_splits(units, num_kb, num_sms);
+  const int splits = few_splits(units, num_kb, m.cols, num_sms);
   auto kern = few_rows_kernel<kN>;
   const cudaError_t e =
       set_smem_once(reinterpret_cast<const void *>(kern), few_smem<kN>,
@@ -1314,24 +1349,25 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
                             static_cast<int>(m.a.strided), m.ep, err);
 }
 
-// Estimated time of a product as few_rows_kernel: 350 ns a K block for each CTA
-// of an SM, which its 32 KB take from L2, and 25 ns for each 64 results of a
-// CTA's share.
+// Estimated time of a product as few_rows_kernel, over what gemm_kernel takes
+// besides its K blocks: 330 ns a K block for each CTA of an SM (its copies), and
+// 0.5 to 3 us, growing with the rows, to join the parts.
 int64_t few_rows_ns(const Mat &m, int num_sms) {
   const int num_kb = static_cast<int>((m.summed + 63) / 64);
   const int64_t units = (m.cols + 127) / 128 * ((m.rows + 127) / 128);
-  const int splits = few_splits(units, num_kb, num_sms);
-  const int64_t per_sm = (units * splits + num_sms - 1) / num_sms;
+  const int splits = few_splits(units, num_kb, m.rows, num_sms);
+  const int64_t ctas = units * splits > num_sms ? units * splits : num_sms;
   const int64_t rows = m.rows < 128 ? m.rows : 128;
-  return per_sm * ((num_kb + splits - 1) / splits * 350 + 128 * rows / splits * 25 / 64);
+  return ctas * ((num_kb + splits - 1) / splits) * 330 / num_sms + 500 + rows * 20;
 }
 
-// Whether a product runs as few_rows_kernel: always up to 128 rows; above where
-// its tiles, split over K, end sooner than the pairs'.
+// Whether a product runs as few_rows_kernel: where its tiles, split over K, end
+// sooner than the pairs' (measured, few rows / pairs: 16 x 4096 x 4096 8.9 /
+// 16.3 us, 512 x 512 x 4096 11.1 / 15.7, 100 x 512 x 512 6.7 / 5.2, 512 x 4096 x
+// 1024 12.5 / 7.8).
 bool few_rows_form(const Mat &m, int num_sms) {
-  if (m.a.strided) return false;  // (few_rows_kernel reads x with K contiguous)
-  if (m.rows <= 128) return true;
-  return m.rows <= 2048 && few_rows_ns(m, num_sms) < pick_width(&m, 1, num_sms).ns;
+  return !m.a.strided && m.rows <= 2048 &&
+         few_rows_ns(m, num_sms) < pick_width(&m, 1, num_sms).ns;
 }
 
 // As few_rows_kernel: the weight becomes the row operand.
