@@ -149,9 +149,12 @@ __device__ __forceinline__ void mma_one_rt(uint32_t d_tmem, uint64_t a_desc, uin
 // ---------------------------------------------------------------------------
 constexpr int kMaxProducts = 2;
 
+constexpr int kBand = 8;  // row tiles of a band (see tile_at)
+
 struct Product {
   int rows, cols, num_kb;       // D's size; 64-deep blocks of the summed dimension
   int tiles_r, tiles_c;         // 256 x kBN tiles
+  uint32_t inv_band, inv_last;  // reciprocals of a band's tiles, of the last band's height
   int a_strided, b_strided;
   Epilogue ep;
 };
@@ -166,20 +169,28 @@ struct Products {
   Product p[kMaxProducts];
 };
 
-// The i-th tile of a pair: product and tile number; false past its last.
-__device__ __forceinline__ bool pair_tile(const Products &prods, int pair, int num_pairs, int i,
-                                          int &pi, int &t) {
-  pi = 0;
-  t = pair + i * num_pairs;
-  if (t < prods.tiles[0]) return true;
-  const int own = prods.tiles[0] / num_pairs + (pair < prods.lead ? 1 : 0);
-  const int run = prods.run[pair < prods.lead ? 0 : 1];
-  const int first = pair < prods.lead ? pair * prods.run[0]
-                                      : prods.lead * prods.run[0] + (pair - prods.lead) * prods.run[1];
-  pi = 1;
-  t = first + i - own;
-  return i - own < run && t < prods.tiles[1];
-}
+// A pair's tiles in order, without divisions on the way.
+struct PairTiles {
+  int t0, step, own0;   // product 0: t0, t0 + step, ... (own0 of them)
+  int first1, own1;     // product 1: first1, first1 + 1, ...
+
+  __device__ __forceinline__ PairTiles(const Products &prods, int pair, int num_pairs) {
+    const bool lead = pair < prods.lead;
+    t0 = pair;
+    step = num_pairs;
+    own0 = prods.tiles[0] / num_pairs + (lead ? 1 : 0);
+    first1 = lead ? pair * prods.run[0]
+                  : prods.lead * prods.run[0] + (pair - prods.lead) * prods.run[1];
+    own1 = max(0, min(prods.run[lead ? 0 : 1], prods.tiles[1] - first1));
+  }
+
+  // The i-th: product and tile number; false past the last.
+  __device__ __forceinline__ bool at(int i, int &pi, int &t) const {
+    pi = i < own0 ? 0 : 1;
+    t = pi == 0 ? t0 + i * step : first1 + i - own0;
+    return i < own0 + own1;
+  }
+};
 
 struct Maps {
   CUtensorMap a[kMaxProducts], b[kMaxProducts];
@@ -212,14 +223,20 @@ struct SharedGemm {
 };
 static_assert(sizeof(SharedGemm<256>) <= 1536 && sizeof(SharedGemm<64>) <= 1536, "shared block");
 
-// Tile t of a product: bands of 8 row tiles, row tiles fastest, so that the
+// t / d from the reciprocal m = 2^32 / d (rounded down): the estimate is short
+// by at most one.
+__device__ __forceinline__ int quotient(int t, int d, uint32_t m) {
+  const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(t), m));
+  return t - q * d >= d ? q + 1 : q;
+}
+
+// Tile t of a product: bands of kBand row tiles, row tiles fastest, so that the
 // pairs at work share a few A and B panels through L2.
 __device__ __forceinline__ void tile_at(const Product &p, int t, int &tr, int &tc) {
-  constexpr int kBand = 8;
-  const int band = t / (kBand * p.tiles_c);
-  const int height = min(kBand, p.tiles_r - band * kBand);
+  const int band = quotient(t, kBand * p.tiles_c, p.inv_band);
   const int in = t - band * kBand * p.tiles_c;
-  tc = in / height;
+  const int height = min(kBand, p.tiles_r - band * kBand);
+  tc = height == kBand ? in / kBand : quotient(in, height, p.inv_last);
   tr = band * kBand + in - tc * height;
 }
 
@@ -456,6 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const bool leader = rank == 0;
   const int pair = static_cast<int>(blockIdx.x >> 1);
   const int num_pairs = static_cast<int>(gridDim.x >> 1);
+  const PairTiles tiles(prods, pair, num_pairs);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -492,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   if (warp == 0) {
     // -------------------------------------------------- producer (both CTAs)
     int pi, t;
-    for (int n = 0; pair_tile(prods, pair, num_pairs, n, pi, t) && !aborted(abort_flag); ++n) {
+    for (int n = 0; tiles.at(n, pi, t) && !aborted(abort_flag); ++n) {
       const Product &p = prods.p[pi];
       int tr, tc;
       tile_at(p, t, tr, tc);
@@ -540,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     for (int n = 0;
-         pair_tile(prods, pair, num_pairs, n, pi, t) && ok && !aborted(abort_flag); ++n) {
+         tiles.at(n, pi, t) && ok && !aborted(abort_flag); ++n) {
       const Product &p = prods.p[pi];
       const int num_kb = p.num_kb;
       const bool a_strided = p.a_strided != 0, b_strided = p.b_strided != 0;
@@ -589,7 +607,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     uint32_t acc_phase = 0;
     const uint32_t at_leader[2] = {map_to_rank(smem_u32(&sh->tmem_empty[0]), 0),
                                    map_to_rank(smem_u32(&sh->tmem_empty[1]), 0)};
-    for (int n = 0; pair_tile(prods, pair, num_pairs, n, pi, t); ++n) {
+    for (int n = 0; tiles.at(n, pi, t); ++n) {
       if (!warp_wait(smem_u32(&sh->tmem_empty[acc]), acc_phase, abort_flag)) {
         if (lane == 0) raise_abort(&sh->abort, err);
         break;
@@ -611,7 +629,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     int acc = 0, pi, t;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int n = 0; ok && pair_tile(prods, pair, num_pairs, n, pi, t); ++n) {
+    for (int n = 0; ok && tiles.at(n, pi, t); ++n) {
       const Product &p = prods.p[pi];
       int tr, tc;
       tile_at(p, t, tr, tc);
@@ -684,7 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (acc == 0) acc_phase ^= 1;
       // (an epilogue warp that gives up keeps to the barriers of the others)
       if (!ok) {
-        for (int u = n + 1; pair_tile(prods, pair, num_pairs, u, pi, t); ++u) {
+        for (int u = n + 1; tiles.at(u, pi, t); ++u) {
           if (prods.p[pi].ep.bias == nullptr) continue;
           asm volatile("bar.sync 1, 256;" ::: "memory");
           asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1195,6 +1213,10 @@ bool operand_map(CUtensorMap *map, const Operand &o, int64_t other, int64_t summ
 // the turn of the pipeline between tiles.
 int64_t tile_cost(int num_kb) { return (num_kb > 12 ? num_kb : 12) + 2; }
 
+uint32_t reciprocal(int d) {  // for quotient(); 2^32 / 1 does not fit, and is short by one too
+  return static_cast<uint32_t>(d == 1 ? 0xffffffffu : (uint64_t(1) << 32) / d);
+}
+
 bool aligned_rows(const void *p, int64_t ld) {
   return p == nullptr || (reinterpret_cast<uintptr_t>(p) | (2 * ld)) % 16 == 0;
 }
@@ -1211,6 +1233,8 @@ cudaError_t launch_gemm(const Mat *mats, int n, int num_sms, uint32_t *err, cuda
     p.num_kb = static_cast<int>((m.summed + 63) / 64);
     p.tiles_r = static_cast<int>((m.rows + 255) / 256);
     p.tiles_c = static_cast<int>((m.cols + kBN - 1) / kBN);
+    p.inv_band = reciprocal(kBand * p.tiles_c);
+    p.inv_last = reciprocal(p.tiles_r % kBand != 0 ? p.tiles_r % kBand : kBand);
     p.a_strided = m.a.strided;
     p.b_strided = m.b.strided;
     p.ep = m.ep;
