@@ -1035,6 +1035,105 @@ __global__ void __launch_bounds__(THREADS, 2)
 }
 
 // ---------------------------------------------------------------------------
+// dot_kernel, M <= 4 (single tokens): CUDA cores, since the weight's stream is
+// all there is and the tensor-core kernels' barriers, tensor memory and joins
+// are latency.  A CTA takes kDotRows weight rows; its threads share their
+// columns, so that every 16-byte load of a pass over up to 4096 columns is in
+// flight at once and nothing is staged.  x comes from L2.
+// ---------------------------------------------------------------------------
+constexpr int kDotRows = 8;
+constexpr int kDotMaxM = 4;
+
+template <int kM, int kThreads>
+__global__ void __launch_bounds__(kThreads)
+    dot_kernel(const __nv_bfloat16 *__restrict__ x, int64_t ldx, const __nv_bfloat16 *__restrict__ w,
+               int64_t ldw, int M, int N, int K, const Epilogue ep) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kSteps = kM > 2 ? 1 : 2;  // 16-byte loads of a row per thread and pass
+  __shared__ float parts[kWarps][kDotRows * kM];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = blockIdx.x * kDotRows;
+  const int nvec = K / 8;
+  pdl_wait();
+  uint64_t acc[kDotRows][kM] = {};  // sums over even and odd columns
+  for (int v0 = threadIdx.x; v0 < nvec; v0 += kSteps * kThreads) {
+    uint4 a[kSteps][kDotRows], b[kSteps][kM];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int v = v0 + s * kThreads;
+      const bool in = v < nvec;
+#pragma unroll
+      for (int r = 0; r < kDotRows; ++r)  // (rows past the last read it again)
+        a[s][r] = in ? ld_stream_v4(w + min(row0 + r, N - 1) * ldw + v * 8)
+                     : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+        b[s][m] = in ? __ldg(reinterpret_cast<const uint4 *>(x + min(m, M - 1) * ldx) + v)
+                     : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      uint64_t xf[kM][4];
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        const uint32_t xb[4] = {b[s][m].x, b[s][m].y, b[s][m].z, b[s][m].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xf[m][i] = pack_f32(bf16_lo(xb[i]), bf16_hi(xb[i]));
+      }
+#pragma unroll
+      for (int r = 0; r < kDotRows; ++r) {
+        const uint32_t wb[4] = {a[s][r].x, a[s][r].y, a[s][r].z, a[s][r].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t wf = pack_f32(bf16_lo(wb[i]), bf16_hi(wb[i]));
+#pragma unroll
+          for (int m = 0; m < kM; ++m) acc[r][m] = fma2(wf, xf[m][i], acc[r][m]);
+        }
+      }
+    }
+  }
+  pdl_launch_dependents();
+#pragma unroll
+  for (int m = 0; m < kM; ++m) {
+    // eight sums over the warp's lanes in nine exchanges: each of the first
+    // three halves the sums a lane holds
+    float t[kDotRows];
+#pragma unroll
+    for (int r = 0; r < kDotRows; ++r) {
+      float lo, hi;
+      unpack_f32(acc[r][m], lo, hi);
+      t[r] = lo + hi;
+    }
+#pragma unroll
+    for (int n = kDotRows / 2, bit = 16; n > 0; n /= 2, bit /= 2) {
+      const bool upper = (lane & bit) != 0;
+#pragma unroll
+      for (int r = 0; r < n; ++r) {
+        const float send = upper ? t[r] : t[n + r];
+        t[r] = (upper ? t[n + r] : t[r]) + __shfl_xor_sync(0xffffffffu, send, bit);
+      }
+    }
+    t[0] += __shfl_xor_sync(0xffffffffu, t[0], 2);
+    t[0] += __shfl_xor_sync(0xffffffffu, t[0], 1);
+    if ((lane & 3) == 0) parts[warp][(lane >> 2) * kM + m] = t[0];
+  }
+  __syncthreads();
+  const int e = threadIdx.x;
+  if (e >= kDotRows * kM) return;
+  const int m = e / kDotRows, r = e % kDotRows;  // rows fastest: neighbouring results
+  const int64_t col = row0 + r;
+  if (m >= M || col >= N) return;
+  float z = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) z += parts[i][r * kM + m];
+  z += ld_bias(ep.bias, ep.bias_f32, col);
+  if (ep.pre != nullptr) ep.pre[m * ep.ldp + col] = __float2bfloat16_rn(z);
+  float y = activate(z, ep.act);
+  if (ep.res != nullptr) y += ld_bf16(ep.res + m * ep.ldr + col);
+  ep.out[m * ep.ldo + col] = __float2bfloat16_rn(y);
+}
+
+// ---------------------------------------------------------------------------
 // dz = g * act'(z) in bf16 (dz nullable) and db = the column sums of dz in
 // fp32, before the rounding (db nullable).  HBM-bound: g and z are read once
 // and dz written once.  A cluster covers a strip of columns, its CTAs
@@ -1403,6 +1502,51 @@ cudaError_t launch_few(const Mat &m, int num_sms, uint32_t *err, cudaStream_t st
   return launch_few_rows<128>(t, num_sms, err, stream);
 }
 
+template <int kThreads>
+cudaError_t launch_dot_threads(const Mat &m, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((m.cols + kDotRows - 1) / kDotRows));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto kern = m.rows == 1 ? dot_kernel<1, kThreads>
+                          : (m.rows == 2 ? dot_kernel<2, kThreads> : dot_kernel<4, kThreads>);
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const __nv_bfloat16 *>(m.a.ptr), m.a.ld,
+                            static_cast<const __nv_bfloat16 *>(m.b.ptr), m.b.ld,
+                            static_cast<int>(m.rows), static_cast<int>(m.cols),
+                            static_cast<int>(m.summed), m.ep);
+}
+
+// Threads of a dot_kernel CTA: a quarter of a row's 16-byte vectors, 32 to 128
+// (more idle in short rows, fewer wait longer in long ones), twice that where
+// the CTAs are few.  Measured, 32 / 64 / 128 / 256 threads: 1 x 4096 x 4096 10.2
+// / 7.9 / 7.0 / 8.3 us, 1 x 1024 x 8192 15.8 / 9.4 / 6.4 / 5.6, 1 x 16384 x 512
+// 4.8 / 5.9 / 8.0 / 12.5, 1 x 152064 x 2048 85 / 85 / 87 / 130.
+cudaError_t launch_dot(const Mat &m, cudaStream_t stream, int num_sms) {
+  int threads = 32;
+  while (threads < 128 && threads * 4 < m.summed / 8) threads *= 2;
+  if ((m.cols + kDotRows - 1) / kDotRows < 2 * num_sms) threads *= 2;
+  switch (threads) {
+    case 32: return launch_dot_threads<32>(m, stream);
+    case 64: return launch_dot_threads<64>(m, stream);
+    case 128: return launch_dot_threads<128>(m, stream);
+    default: return launch_dot_threads<256>(m, stream);
+  }
+}
+
+// Whether a product of at most four rows runs as dot_kernel.  With more than one
+// row its reads of x from L2 weigh on a large weight of long rows (few_rows_kernel
+// / dot_kernel: 4 x 8192 x 8192 24.4 / 30.6 us, 4 x 2048 x 2048 6.5 / 4.6, 4 x
+// 152064 x 2048 149 / 118).
+bool dot_form(const Mat &m) {
+  return m.rows == 1 || (m.rows <= kDotMaxM &&
+                         (m.summed <= 2048 || m.cols * m.summed <= (int64_t(1) << 23)));
+}
+
 int64_t dz_ld(int64_t N) { return (N + 7) / 8 * 8; }
 
 template <int kAct>
@@ -1449,6 +1593,7 @@ cudaError_t launch_linear(const void *x, int64_t M, int64_t K, int64_t ldx, cons
   m.ep = {static_cast<__nv_bfloat16 *>(out), static_cast<__nv_bfloat16 *>(preact),
           static_cast<const __nv_bfloat16 *>(residual), bias, ldo, ldp, ldr,
           bias_dtype == SGA_F32, act};
+  if (dot_form(m)) return launch_dot(m, stream, num_sms);
   return few_rows_form(m, num_sms) ? launch_few(m, num_sms, err, stream)
                                    : launch_products(&m, 1, num_sms, err, stream);
 }

@@ -1,6 +1,6 @@
-// pipe.cuh -- waiting and issuing inside the pipelined kernels of linear.cu and
-// logprobs.cu: bounded mbarrier waits that sleep in the barrier unit, and
-// single-lane issue from a converged warp.
+// pipe.cuh -- pieces shared by linear.cu and logprobs.cu: bounded mbarrier waits
+// that sleep in the barrier unit, single-lane issue from a converged warp, and
+// paired fp32 arithmetic.
 #pragma once
 
 #include "tcgen05.cuh"
@@ -62,6 +62,26 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 __device__ __forceinline__ void raise_abort(int *flag, uint32_t *err) {
   *reinterpret_cast<volatile int *>(flag) = 1;
   atomicOr(err, SGA_DEVERR_TIMEOUT);
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack_f32(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Untiled copy of global memory into shared memory (16-byte aligned, size a

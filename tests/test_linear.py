@@ -65,7 +65,10 @@ def sum_tol(k, sizes):
 SHAPES = [(1, 1, 8), (1, 128, 64), (1, 4096, 4096), (3, 130, 72), (16, 257, 640), (17, 300, 136),
           (33, 1000, 520), (64, 127, 2048), (65, 513, 64), (100, 2100, 1032), (128, 129, 4096),
           (129, 64, 64), (129, 200, 72), (200, 1531, 1160), (256, 256, 128), (257, 257, 264),
-          (300, 5000, 256), (1000, 2050, 200), (2111, 3333, 104), (9, 40000, 16)]
+          (300, 5000, 256), (1000, 2050, 200), (2111, 3333, 104), (9, 40000, 16),
+          # single tokens: every CTA width, and the rows that go to the tensor cores
+          (1, 3000, 264), (1, 5000, 1032), (1, 77, 9000), (2, 301, 5000), (2, 2500, 4104),
+          (3, 4099, 2048), (3, 20, 8), (4, 1000, 640), (4, 3000, 4096), (4, 513, 64)]
 
 
 @pytest.mark.gpu
