@@ -811,7 +811,7 @@ template <int kN>
 __global__ void __launch_bounds__(THREADS, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
                     const __grid_constant__ CUtensorMap tmap_x, int all_m, int rows, int num_kb,
-                    int blocks, int splits, int strided, const Epilogue ep, uint32_t *err) {
+                    int blocks, int splits, int box, int strided, const Epilogue ep, uint32_t *err) {
   constexpr int kStages = few_stages<kN>;
   constexpr int kStageB = few_stage<kN>;
   extern __shared__ uint8_t smem_raw[];
@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
       const uint32_t full = smem_u32(&sh->full[prod_stage]);
       const uint32_t a = smem_u32(base + prod_stage * kStageB);
-      mbar_expect_tx(full, kStageB);
+      mbar_expect_tx(full, kTileA + box * ROW_BYTES);
       if (strided) {
         tma_load_2d(a, &tmap_w, row0, kb * 64, full);
         tma_load_2d(a + 8192, &tmap_w, row0 + 64, kb * 64, full);
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   } else if (warp == 1 && lane == 0) {
     int stage = 0;
     uint32_t phase = 0;
-    const uint32_t idesc = operand_idesc(128, kN, strided, false);
+    const uint32_t idesc = operand_idesc(128, box, strided, false);
     const uint32_t step_a = k_step(strided);
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
@@ -1441,8 +1441,10 @@ template <int kN>
 cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream_t stream) {
   // m: D^T, rows = weight rows, cols = M
   CUtensorMap map_w, map_x;
+  // rows of x that a K block brings: no more than there are, in steps of the MMA
+  const int box = m.cols < kN ? static_cast<int>((m.cols + 15) / 16 * 16) : kN;
   if (!operand_map(&map_w, m.a, m.rows, m.summed, 128) ||
-      !operand_map(&map_x, m.b, m.cols, m.summed, kN))
+      !operand_map(&map_x, m.b, m.cols, m.summed, box))
     return cudaErrorNotSupported;
   const int num_kb = static_cast<int>((m.summed + 63) / 64);
   const int blocks = static_cast<int>((m.cols + kN - 1) / kN);
@@ -1468,7 +1470,7 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, static_cast<int>(m.cols),
-                            static_cast<int>(m.rows), num_kb, blocks, splits,
+                            static_cast<int>(m.rows), num_kb, blocks, splits, box,
                             static_cast<int>(m.a.strided), m.ep, err);
 }
 
