@@ -59,7 +59,6 @@ __device__ __forceinline__ float activate(float z, int act) {
 
 __device__ __forceinline__ float activate_grad(float z, int act) {
   switch (act) {
-    case SGA_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
     case SGA_ACT_SILU: {
       const float q = sigmoid_times(1.0f, z);
       return q * fmaf(z, 1.0f - q, 1.0f);
@@ -1158,10 +1157,13 @@ constexpr int kDzThreads = 256;
 constexpr int kDzMaxSplits = 8;
 
 // (A product of its own, not contracted into the column sum: db is the same
-// whether dz is asked for or not.)
+// whether dz is asked for or not.  relu chooses: what it cut off has no gradient,
+// though g be infinite or NaN there; a NaN z stays one.)
 template <int kAct>
 __device__ __forceinline__ float dz_term(float g, float z) {
-  return kAct == SGA_ACT_NONE ? g : __fmul_rn(g, activate_grad(z, kAct));
+  if (kAct == SGA_ACT_NONE) return g;
+  if (kAct == SGA_ACT_RELU) return z > 0.0f ? g : (z != z ? z : 0.0f);
+  return __fmul_rn(g, activate_grad(z, kAct));
 }
 
 // Eight bf16 at p, and with kAligned false what surrounds them (see above).

@@ -497,7 +497,7 @@ int sga_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const void *wei
  * sga_linear_grad -- gradient of sga_linear: with g the gradient of out,
  *   dz = g act'(z),  grad_x = dz . weight,  grad_weight = dz^T . x,
  *   grad_bias = sum over rows of dz          (the residual's gradient is g).
- * relu's slope at 0 is 0.
+ * relu's dz is g where z > 0, 0 where z <= 0 (whatever g is there).
  *
  *   grad_out     device bf16 [M, N], row stride ldg >= N, 2-byte aligned.
  *   preact       device bf16 [M, N], row stride ldp >= N, 2-byte aligned: z

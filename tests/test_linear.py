@@ -267,6 +267,30 @@ def test_no_rows(sga_lib):
     assert (buf[:, :64] == 0).all() and (buf[:, 64:] == 1).all() and (gb == 0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [0, 3])
+def test_relu_cuts_off_infinities(sga_lib, pad):
+    """Where relu gave 0 nothing comes back, whatever the upstream gradient is."""
+    M, N, K = 40, 72, 64
+    x, x64 = mat(21, M, K, 1.0)
+    w, w64 = mat(22, N, K, 1.0)
+    z, z64 = mat(23, M, N, 1.0, pad)
+    g, g64 = mat(24, M, N, 1.0, pad)
+    z[3, 5] = 0.0
+    z64 = z.double().cpu()
+    bad = torch.tensor([float("inf"), float("-inf"), float("nan")], dtype=torch.bfloat16).cuda()
+    g.copy_(torch.where(z > 0, g, bad[torch.arange(M * N, device="cuda").reshape(M, N) % 3]))
+    dz64 = torch.where(z64 > 0, g64, 0.0)
+    gx, gw = torch.empty_like(x), torch.empty_like(w)
+    gb = torch.empty(N, device="cuda")
+    ws = torch.empty(sga_lib.sga_linear_grad_workspace(M, N, K), dtype=torch.uint8, device="cuda")
+    sga_lib.sga_linear_grad(g, x, w, ws, ACTS.index("relu"), z, gx, gw, gb)
+    check(gx, dz64 @ w64, sum_tol(N, dz64.abs() @ w64.abs()) + 2.0 ** -8 * (dz64 @ w64).abs(), "x")
+    check(gw, dz64.T @ x64, sum_tol(M, dz64.abs().T @ x64.abs()) + 2.0 ** -8 * (dz64.T @ x64).abs(),
+          "w")
+    check(gb, dz64.sum(0), sum_tol(M, dz64.abs().sum(0)), "b")
+
+
 # ----------------------------------------------------------------- refusals
 
 
@@ -341,3 +365,12 @@ def test_binding_refuses_wrong_tensors(sga_lib):
         sga_lib.sga_linear_grad(y, x, w, torch.zeros(1), grad_x=w)
     with pytest.raises(ValueError):
         sga_lib.sga_linear_grad(y, x, w, torch.zeros(1), preact=x)
+
+
+def test_binding_refuses_host_tensors(sga_lib):
+    b = torch.bfloat16
+    x, w, y = torch.zeros(3, 64, dtype=b), torch.zeros(5, 64, dtype=b), torch.zeros(3, 5, dtype=b)
+    with pytest.raises(ValueError, match="CUDA"):
+        sga_lib.sga_linear(x, w, y)
+    with pytest.raises(ValueError, match="CUDA"):
+        sga_lib.sga_linear_grad(y, x, w, torch.zeros(40), grad_x=torch.zeros(3, 64, dtype=b))
