@@ -393,6 +393,7 @@ def sga_linear(x, weight, out, bias=None, act=SGA_ACT_NONE, residual=None, out_p
     pr, ldr = _bf16_rows(residual, M, N, "residual")
     pp, ldp = _bf16_rows(out_preact, M, N, "out_preact")
     pb, code = _bias(bias, N, "bias")
+    _on_gpu(x, weight, out, bias, residual, out_preact)
     _check("sga_linear", lib().sga_linear(
         px, M, K, ldx, pw, N, ldw, pb, code, int(act), pr, ldr, pp, ldp, po, ldo,
         _raw_stream(stream)))
@@ -418,6 +419,7 @@ def sga_linear_grad(grad_out, x, weight, workspace, act=SGA_ACT_NONE, preact=Non
     pgx, ldgx = _bf16_rows(grad_x, M, K, "grad_x")
     pgw, ldgw = _bf16_rows(grad_weight, N, K, "grad_weight")
     pb, code = _bias(grad_bias, N, "grad_bias")
+    _on_gpu(grad_out, x, weight, workspace, preact, grad_x, grad_weight, grad_bias)
     _check("sga_linear_grad", lib().sga_linear_grad(
         pg, M, N, ldg, pp, ldp, int(act), px, K, ldx, pw, ldw, pgx, ldgx, pgw, ldgw, pb, code,
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
@@ -443,6 +445,12 @@ def _check_out(t, dtype, numel, name):
     return t.data_ptr()
 
 
+def _on_gpu(*tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("CUDA tensors are needed")
+
+
 def _logits_2d(logits):
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D")
@@ -450,7 +458,7 @@ def _logits_2d(logits):
     ld, col = logits.stride()
     if col != 1 and width > 1:
         raise ValueError("logits must have unit stride along the vocab")
-    return rows, width, ld if rows > 1 else max(ld, width)
+    return rows, width, ld if rows > 1 else max(ld, width), _dtype_code(logits)
 
 
 def _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids, out_top_logprobs):
@@ -473,11 +481,12 @@ def sga_token_logprobs(logits, org_vocab, tokens=None, out_logprob=None, out_ent
     their log probabilities.  logits: 2-D, unit stride along the vocab; outputs
     are contiguous CUDA tensors or None: float32 [rows], and int32 / float32
     [rows, top_k], whose last size is top_k (see include/sga.h)."""
-    rows, width, ld = _logits_2d(logits)
+    rows, width, ld, code = _logits_2d(logits)
     k, (tok, *outs) = _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
                                    out_top_logprobs)
+    _on_gpu(logits, tokens, out_logprob, out_entropy, out_lse, out_top_ids, out_top_logprobs)
     _check("sga_token_logprobs", lib().sga_token_logprobs(
-        logits.data_ptr(), _dtype_code(logits), rows, ld, width, int(org_vocab), tok, k, *outs,
+        logits.data_ptr(), code, rows, ld, width, int(org_vocab), tok, k, *outs,
         _raw_stream(stream)))
 
 
@@ -487,12 +496,13 @@ def sga_local_logprobs(logits, shard_start, shard_width, org_vocab, tokens, out_
     global id shard_start; out_parts: float32 [rows, 4]; out_top: int32 [rows,
     top_k, 2] stats, or None (pass slices of the gathered buffers to emulate
     all_gather on dim 0)."""
-    rows, width, ld = _logits_2d(logits)
+    rows, width, ld, code = _logits_2d(logits)
     if width < shard_width:
         raise ValueError("logits has fewer columns than the shard")
     k = 0 if out_top is None else out_top.size(-2)
+    _on_gpu(logits, tokens, out_parts, out_top)
     _check("sga_local_logprobs", lib().sga_local_logprobs(
-        logits.data_ptr(), _dtype_code(logits), rows, ld, int(shard_start), int(shard_width),
+        logits.data_ptr(), code, rows, ld, int(shard_start), int(shard_width),
         int(org_vocab), _check_out(tokens, torch.int32, rows, "tokens"), k,
         _check_out(out_parts, torch.float32, 4 * rows, "out_parts"),
         _check_out(out_top, torch.int32, 2 * k * rows, "out_top"), _raw_stream(stream)))
@@ -510,6 +520,8 @@ def sga_logprob_reduce(parts, tops, num_shards, tokens=None, out_logprob=None, o
                                    out_top_logprobs)
     if k and tops is None:
         raise ValueError("alternatives are asked for without tops")
+    _on_gpu(parts, tops, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
+            out_top_logprobs)
     _check("sga_logprob_reduce", lib().sga_logprob_reduce(
         _check_out(parts, torch.float32, 4 * rows * num_shards, "parts"),
         _check_out(tops, torch.int32, 2 * k * rows * num_shards, "tops") if k else None,
@@ -523,15 +535,17 @@ def sga_token_logprobs_grad(logits, shard_start, org_vocab, tokens, lse, entropy
     alternatives with respect to the logits (a whole vocabulary, shard_start 0,
     or one shard).  lse, entropy: the forward results; the upstream gradients
     are float32 or None; out_grad: like logits, or logits itself."""
-    rows, width, ld = _logits_2d(logits)
+    rows, width, ld, code = _logits_2d(logits)
     if out_grad.dtype != logits.dtype or out_grad.shape != logits.shape or (
             width > 1 and out_grad.stride(1) != 1):
         raise ValueError("out_grad must match logits, unit stride along the vocab")
     ldg = out_grad.stride(0) if rows > 1 else max(out_grad.stride(0), width)
     k = 0 if top_ids is None else top_ids.size(-1)
     f32, i32 = torch.float32, torch.int32
+    _on_gpu(logits, tokens, lse, entropy, grad_logprob, grad_entropy, top_ids, grad_top,
+            out_grad)
     _check("sga_token_logprobs_grad", lib().sga_token_logprobs_grad(
-        logits.data_ptr(), _dtype_code(logits), rows, ld, int(shard_start), width, int(org_vocab),
+        logits.data_ptr(), code, rows, ld, int(shard_start), width, int(org_vocab),
         _check_out(tokens, i32, rows, "tokens"), _check_out(lse, f32, rows, "lse"),
         _check_out(entropy, f32, rows, "entropy"),
         _check_out(grad_logprob, f32, rows, "grad_logprob"),

@@ -850,7 +850,7 @@ struct GradIn {
 };
 
 __device__ __forceinline__ float grad_term(float x, float lse, float a, float bh, float b) {
-  const float lp = max_nan(x - lse, -1e30f);  // a masked logit: p = 0 times a finite factor
+  const float lp = max_nan(x - lse, -256.0f);  // p is 0 from there on: times a finite factor
   return ex2(lp * kLog2e) * fmaf(b, lp, fmaf(b, bh, a));
 }
 

@@ -450,6 +450,31 @@ def test_gradient_against_differences(sga_lib):
         assert ((diff - grad[:, j].double()).abs() <= 6e-3 * size).all(), j
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad", [0, 1])
+def test_masked_ids_stay_zero_under_a_huge_entropy_gradient(sga_lib, pad):
+    """p = 0 times a finite factor, however large.  Error of the others: p and
+    the factor b (log p + H) are each off by a few 2^-23 of |b| times log p and
+    H, which are below 5: 2^-18 |b| bounds it."""
+    b = 1e12
+    x = torch.full((3, 64 + pad), -1e30)
+    x[0, :4] = torch.tensor([0.5, 1.0, float("-inf"), -2.0])
+    x[1, 5:30] = torch.linspace(-1, 1, 25)
+    x[1, 40:] = float("-inf")
+    x[2, 63] = 3.0
+    x = x.cuda()[:, :64]
+    tok = torch.tensor([1, 7, 63], dtype=torch.int32, device="cuda")
+    lse, ent = torch.empty(3, device="cuda"), torch.empty(3, device="cuda")
+    sga_lib.sga_token_logprobs(x, 64, tok, None, ent, lse)
+    grad = torch.empty((3, 64), device="cuda")
+    ge = torch.full((3,), b, device="cuda")
+    sga_lib.sga_token_logprobs_grad(x, 0, 64, tok, lse, ent, None, grad, ge)
+    lp = x.double() - lse.double()[:, None]
+    exp = torch.where(lp < -200, 0.0, -b * lp.exp() * (lp.clamp(min=-300) + ent.double()[:, None]))
+    assert (grad[lp < -200] == 0).all()
+    assert ((grad.double() - exp).abs() <= 2.0 ** -18 * b).all()
+
+
 # ----------------------------------------------------------------- refusals
 
 
@@ -540,3 +565,16 @@ def test_binding_refuses_wrong_tensors(sga_lib):
         sga_lib.sga_token_logprobs_grad(x, 0, 8, i32, f32, f32, f32, x[:, :4])
     with pytest.raises(ValueError):
         sga_lib.sga_token_logprobs_grad(x, 0, 8, i32, f32, f32, f32, x.bfloat16())
+
+
+def test_binding_refuses_host_tensors(sga_lib):
+    x = torch.zeros(3, 8)
+    f32, i32 = torch.zeros(3), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        sga_lib.sga_token_logprobs(x, 8, i32, f32)
+    with pytest.raises(ValueError, match="CUDA"):
+        sga_lib.sga_local_logprobs(x, 0, 8, 8, i32, torch.zeros(3, 4))
+    with pytest.raises(ValueError, match="CUDA"):
+        sga_lib.sga_logprob_reduce(torch.zeros(1, 3, 4), None, 1, i32, f32)
+    with pytest.raises(ValueError, match="CUDA"):
+        sga_lib.sga_token_logprobs_grad(x, 0, 8, i32, f32, f32, f32, torch.zeros(3, 8))
