@@ -762,27 +762,97 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
 }
 
 // ------------------------------------------------------------------ reduce
-// One warp per row: lanes share the row's parts, then its n sorted lists of k
-// entries (each entry finds its own place by binary searches in the others).
-__global__ void logprob_reduce_kernel(const sga_logprob_part *__restrict__ parts,
-                                      const sga_stat *__restrict__ tops, int n, int64_t rows,
-                                      int k, const int32_t *__restrict__ tokens, RowOut out) {
+// One warp per row: lanes share the row's n parts and its n sorted lists of k
+// entries.  At least k entries reach the largest of the lists' last entries, and
+// the smallest of their (k / n)-th; what reaches the larger of the two (some 2 k
+// entries) goes to shared memory and finds its place by counting.  Latency-bound:
+// 96 rows of 4 lists of 5 3.2 us, of 8 lists of 20 5.6 us (searching the other
+// lists in global memory for each entry's place took 4.2 and 31.7).
+constexpr int kReduceWarps = 4;
+constexpr int kReduceKeys = 256;  // a row's entries that reach the threshold
+
+__device__ __forceinline__ Key stat_key(const sga_stat &q) {
+  return q.id == kNoId ? 0 : pair_key(q.v, q.id);
+}
+
+// Of the m <= kReduceKeys keys, k of which reach lo, leaves at least k and at most
+// 32 in keys[] and returns how many: the threshold is raised by bisection (counting
+// 200 keys against each other instead took 10 us).
+__device__ __forceinline__ int raise_threshold(Key *keys, int m, int k, Key lo, int lane) {
+  constexpr int kMine = kReduceKeys / 32;
+  Key mine[kMine];
+  uint32_t most = 0;
+#pragma unroll
+  for (int r = 0; r < kMine; ++r) {
+    const int c = r * 32 + lane;
+    mine[r] = c < m ? keys[c] : 0;
+    most = max(most, static_cast<uint32_t>(mine[r] >> 32));
+  }
+  const int held = m;
+  Key hi = (static_cast<Key>(__reduce_max_sync(0xffffffffu, most)) << 32) | 0xffffffffu;
+  while (m > 32 && lo < hi) {
+    const Key mid = hi - (hi - lo) / 2;
+    int n = 0;
+#pragma unroll
+    for (int r = 0; r < kMine; ++r)
+      if (r * 32 < held) n += __popc(__ballot_sync(0xffffffffu, mine[r] >= mid));
+    if (n >= k) {
+      lo = mid;
+      m = n;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  __syncwarp();  // every lane has read its keys
+  m = 0;
+#pragma unroll
+  for (int r = 0; r < kMine; ++r) {
+    const bool take = mine[r] >= lo && mine[r] != 0;
+    const unsigned votes = __ballot_sync(0xffffffffu, take);
+    const int at = m + __popc(votes & ((1u << lane) - 1));
+    if (take && at < 32) keys[at] = mine[r];
+    m += __popc(votes);
+  }
+  return min(m, 32);
+}
+
+__global__ void __launch_bounds__(32 * kReduceWarps)
+    logprob_reduce_kernel(const sga_logprob_part *__restrict__ parts,
+                          const sga_stat *__restrict__ tops, int n, int64_t rows, int k,
+                          const int32_t *__restrict__ tokens, RowOut out) {
+  __shared__ alignas(16) Key held[kReduceWarps][kReduceKeys + 2];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kReduceWarps + warp;
   if (row >= rows) return;
+  const int32_t tok = tokens != nullptr ? tokens[row] : -1;
   float max = neg_inf(), xt = neg_inf();
   for (int i = lane; i < n; i += 32) {
     const sga_logprob_part q = parts[i * rows + row];
     max = max_nan(max, q.max);
     xt = max_nan(xt, q.token);
   }
+  // (reads every entry, so that the second pass finds them in L1)
+  Key threshold = 0, least = ~Key(0);
+  const int share = (k + n - 1) / n - 1;
+#pragma unroll 4
+  for (int c = lane; c < n * k; c += 32) {
+    const int own = c / k, idx = c - own * k;
+    const Key q = stat_key(tops[(own * rows + row) * k + idx]);
+    if (idx == k - 1 && q > threshold) threshold = q;
+    if (idx == share && q < least) least = q;
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     max = max_nan(max, __shfl_xor_sync(0xffffffffu, max, off));
     xt = max_nan(xt, __shfl_xor_sync(0xffffffffu, xt, off));
+    const Key o = __shfl_xor_sync(0xffffffffu, threshold, off);
+    threshold = o > threshold ? o : threshold;
+    const Key l = __shfl_xor_sync(0xffffffffu, least, off);
+    least = l < least ? l : least;
   }
+  if (least > threshold) threshold = least;
   float s = 0.0f, w = 0.0f;
   for (int i = lane; i < n; i += 32) {
     const sga_logprob_part q = parts[i * rows + row];
@@ -801,35 +871,52 @@ __global__ void logprob_reduce_kernel(const sga_logprob_part *__restrict__ parts
   float lse, entropy;
   finish_row(max, s, w, lse, entropy);
   if (lane == 0) {
-    const int32_t tok = tokens != nullptr ? tokens[row] : -1;
     if (out.logprob != nullptr) out.logprob[row] = tok < 0 ? 0.0f : to_logprob(xt, lse);
     if (out.entropy != nullptr) out.entropy[row] = entropy;
     if (out.lse != nullptr) out.lse[row] = lse;
   }
-  for (int c = lane; c < n * k; c += 32) {
-    const int own = c / k, idx = c % k;
-    const sga_stat q = tops[(own * rows + row) * k + idx];
-    int rank = idx;
-    for (int l = 0; l < n && rank < k; ++l) {
-      if (l == own) continue;
-      const sga_stat *list = tops + (l * rows + row) * k;
-      int lo = 0, hi = k;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        const sga_stat o = list[mid];
-        const bool before = o.id == q.id ? l < own : pair_beats(o.v, o.id, q.v, q.id);
-        if (before)
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      rank += lo;
+  auto put = [&](int rank, Key q) {
+    if (out.top_ids != nullptr) out.top_ids[row * k + rank] = q == 0 ? -1 : key_id(q);
+    if (out.top_logprobs != nullptr)
+      out.top_logprobs[row * k + rank] = to_logprob(key_value(q), lse);
+  };
+  int m = 0;
+#pragma unroll 4
+  for (int base = 0; base < n * k; base += 32) {
+    const int c = base + lane;
+    Key q = 0;
+    if (c < n * k) {
+      const int own = c / k;
+      q = stat_key(tops[(own * rows + row) * k + (c - own * k)]);
     }
-    if (rank < k) {
-      if (out.top_ids != nullptr) out.top_ids[row * k + rank] = q.id == kNoId ? -1 : q.id;
-      if (out.top_logprobs != nullptr) out.top_logprobs[row * k + rank] = to_logprob(q.v, lse);
-    }
+    const bool take = q != 0 && q >= threshold;
+    const unsigned votes = __ballot_sync(0xffffffffu, take);
+    const int at = m + __popc(votes & ((1u << lane) - 1));
+    if (take && at < kReduceKeys) held[warp][at] = q;
+    m += __popc(votes);
   }
+  if (m <= kReduceKeys) {
+    __syncwarp();
+    if (m > 32) m = raise_threshold(held[warp], m, k, threshold, lane);
+    if (lane == 0) held[warp][m] = 0;
+    __syncwarp();
+    if (lane < m) {
+      const Key mine = held[warp][lane];
+      const int rank = keys_above(held[warp], m, mine);
+      if (rank < k) put(rank, mine);
+    }
+  } else {
+    // (more lists than that: a sorted list in the warp's registers)
+    Key top = 0;
+    for (int base = 0; base < n * k; base += 32) {
+      const int c = base + lane, own = c / k;
+      top_offer(top, c < n * k ? stat_key(tops[(own * rows + row) * k + (c - own * k)]) : 0, lane,
+                k);
+    }
+    m = __popc(__ballot_sync(0xffffffffu, lane < k && top != 0));
+    if (lane < m) put(lane, top);
+  }
+  if (lane >= m && lane < k) put(lane, 0);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -1081,8 +1168,8 @@ cudaError_t launch_logprob_reduce(const sga_logprob_part *parts, const sga_stat 
                                   float *top_logprobs, cudaStream_t stream) {
   const RowOut out = {logprob, entropy, lse, top_logprobs, top_ids, nullptr, nullptr};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kReduceWarps - 1) / kReduceWarps));
+  cfg.blockDim = dim3(32 * kReduceWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -217,6 +217,31 @@ def test_sharded_parts_reduce_to_the_same(sga_lib, case, shards):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shards,k", [(70, 32), (8, 20), (40, 1), (33, 7), (300, 3)])
+def test_many_shards(sga_lib, shards, k, dtype):
+    """Lists shorter than k, all of whose entries may be among the best; many
+    entries that reach every list's last."""
+    rows, vocab, org = 19, 700, 689
+    x, _ = make_logits(shards, rows, vocab, dtype, 0, 0)
+    plant(x[:, :vocab], dtype)
+    x[15] = np.linspace(3, -3, vocab)        # the best ids all in the first shards
+    x[16] = np.linspace(-3, 3, vocab)
+    dev, x64 = to_cuda(x, dtype, vocab, 0)
+    tokens = make_tokens(rows, org, vocab, 3)
+    tok = torch.from_numpy(tokens).cuda()
+    parts = torch.full((shards, rows, 4), 9.0, device="cuda")
+    tops = torch.full((shards, rows, k, 2), -9, dtype=torch.int32, device="cuda")
+    for s, (o, w) in enumerate(wl.even_shards(vocab, shards)):
+        sga_lib.sga_local_logprobs(dev[:, o:o + w], o, w, org, tok, parts[s], tops[s])
+    whole = run_forward(sga_lib, dev, org, tok, k)
+    out = [torch.full_like(t, 5) for t in whole]
+    sga_lib.sga_logprob_reduce(parts, tops, shards, tok, *out)
+    check_outputs(x64, org, tokens, k, out)
+    assert torch.equal(out[3], whole[3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("k", [1, 5, 32])
 @pytest.mark.parametrize("vocab", [20000, 70001])
 def test_rows_that_are_hard_to_select_from(sga_lib, vocab, k, dtype):
