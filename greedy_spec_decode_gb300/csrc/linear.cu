@@ -818,7 +818,8 @@ template <int kN>
 __global__ void __launch_bounds__(THREADS, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
                     const __grid_constant__ CUtensorMap tmap_x, int all_m, int rows, int num_kb,
-                    int blocks, int splits, int box, int strided, const Epilogue ep, uint32_t *err) {
+                    int blocks, int log_splits, int box, int strided, const Epilogue ep,
+                    uint32_t *err) {
   constexpr int kStages = few_stages<kN>;
   constexpr int kStageB = few_stage<kN>;
   extern __shared__ uint8_t smem_raw[];
@@ -828,13 +829,14 @@ __global__ void __launch_bounds__(THREADS, 2)
   const volatile int *abort_flag = &sh->abort;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int unit = static_cast<int>(blockIdx.x) / splits;
-  const int split = static_cast<int>(blockIdx.x) - unit * splits;
+  const int splits = 1 << log_splits;
+  const int unit = static_cast<int>(blockIdx.x) >> log_splits;
+  const int split = static_cast<int>(blockIdx.x) & (splits - 1);
   const int tile = unit / blocks;
   const int first_m = (unit - tile * blocks) * kN;  // this CTA's rows of x
   const int M = min(kN, all_m - first_m);
-  const int kb0 = num_kb * split / splits;  // (num_kb <= 2^18)
-  const int kb1 = num_kb * (split + 1) / splits;
+  const int kb0 = num_kb * split >> log_splits;  // (num_kb <= 2^18)
+  const int kb1 = num_kb * (split + 1) >> log_splits;
   const int row0 = tile * 128;
 
   if (threadIdx.x == 64) {
@@ -979,9 +981,9 @@ __global__ void __launch_bounds__(THREADS, 2)
   // This CTA's share of the tile's rows, for every m: a thread takes four rows
   // of two m at a time and asks for every CTA's part at once (one after the
   // other, the reads of the peers' memory took 500 cycles each).
-  const int quads = 32 / splits;
-  const int at_once = THREADS / quads;  // (quads divides THREADS)
-  const int r = (split * quads + static_cast<int>(threadIdx.x) % quads) * 4;
+  const int quads = 32 >> log_splits;
+  const int at_once = THREADS / 32 << log_splits;
+  const int r = (split * quads + (static_cast<int>(threadIdx.x) & (quads - 1))) * 4;
   const int64_t col = row0 + r;
   const int n = static_cast<int>(min(static_cast<int64_t>(4), rows - col));
   if (n > 0) {
@@ -990,10 +992,10 @@ __global__ void __launch_bounds__(THREADS, 2)
     uint32_t src[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      src[i] = i < splits && num_kb * i / splits != num_kb * (i + 1) / splits
+      src[i] = i < splits && num_kb * i >> log_splits != num_kb * (i + 1) >> log_splits
                    ? map_to_rank(smem_u32(part) + r * 4, i)
                    : 0u;  // (a CTA without K blocks has no part)
-    for (int m0 = static_cast<int>(threadIdx.x) / quads; m0 < M; m0 += 2 * at_once) {
+    for (int m0 = static_cast<int>(threadIdx.x) >> (5 - log_splits); m0 < M; m0 += 2 * at_once) {
       float4 v[2][8];
       float res[2][4] = {};
 #pragma unroll
@@ -1461,6 +1463,8 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   const int blocks = static_cast<int>((m.cols + kN - 1) / kN);
   const int64_t units = (m.rows + 127) / 128 * blocks;
   const int splits = few_splits(units, num_kb, m.cols, num_sms);
+  int log_splits = 0;
+  while (1 << log_splits < splits) ++log_splits;
   auto kern = few_rows_kernel<kN>;
   const cudaError_t e =
       set_smem_once(reinterpret_cast<const void *>(kern), few_smem<kN>,
@@ -1481,7 +1485,7 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, static_cast<int>(m.cols),
-                            static_cast<int>(m.rows), num_kb, blocks, splits, box,
+                            static_cast<int>(m.rows), num_kb, blocks, log_splits, box,
                             static_cast<int>(m.a.strided), m.ep, err);
 }
 
