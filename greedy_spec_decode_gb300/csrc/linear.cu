@@ -18,7 +18,7 @@
 //   few_rows_kernel  few rows or tiles: the weight is the MMA's 128-row operand
 //                    and a cluster splits the summed dimension, joined through
 //                    distributed shared memory.  Bound by the weight's stream and
-//                    the join: 96 x 8192 x 4096 18.0 us, weight from HBM.
+//                    the join: 96 x 8192 x 4096 16.5 us, weight from HBM.
 //   dot_kernel       at most four rows, on CUDA cores.  HBM- and latency-bound:
 //                    1 x 4096 x 4096 7.0 us, 1 x 152064 x 2048 85.5 us = 7.3 TB/s.
 //   dz_kernel        dz and db, HBM-bound.
@@ -772,23 +772,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 // ---------------------------------------------------------------------------
 template <int kN>
 constexpr int few_stage = kTileA + kN * ROW_BYTES;
+// Ring stages with two CTAs per SM, and where the CTAs are no more than the SMs
+// and turn the smaller ring three times (96 x 4096 x 4096 12.7 -> 11.9 us, 24 x
+// 1024 x 8192 9.1 -> 8.8; at two and a half turns, 333 x 1531 x 2056 11.6 -> 12.0).
 template <int kN>
-constexpr int few_stages = (110 * 1024) / few_stage<kN>;  // two CTAs per SM
+constexpr int few_stages = (110 * 1024) / few_stage<kN>;
+template <int kN>
+constexpr int few_most_stages = (220 * 1024) / few_stage<kN>;
 template <int kN>
 constexpr int few_cols = kN < 32 ? 32 : kN;  // TMEM columns (a power of two, at least 32)
 
 template <int kN>
 struct SharedFew {
-  uint64_t full[few_stages<kN>];
-  uint64_t empty[few_stages<kN>];
+  uint64_t full[few_most_stages<kN>];
+  uint64_t empty[few_most_stages<kN>];
   uint64_t done;
   uint32_t tmem_base;
   int abort;
 };
 
 template <int kN>
-constexpr int few_smem = 1024 + few_stages<kN> * few_stage<kN> + static_cast<int>(sizeof(SharedFew<kN>));
+constexpr int few_smem(int stages) {
+  return 1024 + stages * few_stage<kN> + static_cast<int>(sizeof(SharedFew<kN>));
+}
 static_assert(few_stages<128> * few_stage<128> >= 128 * 128 * 4, "a partial tile fits the ring");
+static_assert(2 * (few_smem<16>(few_stages<16>) + 1024) <= 228 * 1024 &&
+                  few_smem<16>(few_most_stages<16>) <= 227 * 1024,
+              "ring sizes");
 
 // n <= 4 consecutive bf16, as one access where they are four and aligned.
 __device__ __forceinline__ void load_four(const __nv_bfloat16 *p, int n, float (&x)[4]) {
@@ -814,18 +824,74 @@ __device__ __forceinline__ void store_four(__nv_bfloat16 *p, int n, const float 
   }
 }
 
+// A CTA's share of the tile's rows, for every m: a thread takes rows r .. r + 3 of
+// two m at a time and asks for all of their parts at once (one after the other,
+// the reads of the peers' memory took 500 cycles each; four m at a time: no gain).
+__device__ __forceinline__ void join_parts(const float *part, int M, int first_m, int row0, int rows,
+                                           int num_kb, int log_splits, int r,
+                                           const float (&bias)[4], const Epilogue &ep) {
+  const int at_once = THREADS / 32 << log_splits;
+  const int64_t col = row0 + r;
+  const int n = min(4, rows - row0 - r);
+  if (n > 0) {
+    uint32_t src[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      src[i] = i < 1 << log_splits && num_kb * i >> log_splits != num_kb * (i + 1) >> log_splits
+                   ? map_to_rank(smem_u32(part) + r * 4, i)
+                   : 0u;  // (a CTA without K blocks has no part)
+    for (int m0 = static_cast<int>(threadIdx.x) >> (5 - log_splits); m0 < M; m0 += 2 * at_once) {
+      float4 v[2][8];
+      float res[2][4] = {};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int m = min(m0 + u * at_once, M - 1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[u][i] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (src[i] != 0 && (u == 0 || M > u * at_once))
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[u][i].x), "=f"(v[u][i].y), "=f"(v[u][i].z), "=f"(v[u][i].w)
+                         : "r"(src[i] + m * 512));
+        }
+        if (ep.res != nullptr)
+          load_four(ep.res + (first_m + m) * ep.ldr + col, n, res[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t m = first_m + m0 + u * at_once;
+        if (m0 + u * at_once >= M) break;
+        float z[4] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          z[0] += v[u][i].x;
+          z[1] += v[u][i].y;
+          z[2] += v[u][i].z;
+          z[3] += v[u][i].w;
+        }
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] += bias[i];
+        if (ep.pre != nullptr) store_four(ep.pre + m * ep.ldp + col, n, z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = activate(z[i], ep.act) + res[u][i];
+        store_four(ep.out + m * ep.ldo + col, n, y);
+      }
+    }
+  }
+}
+
 template <int kN>
 __global__ void __launch_bounds__(THREADS, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmap_w,
                     const __grid_constant__ CUtensorMap tmap_x, int all_m, int rows, int num_kb,
-                    int blocks, int log_splits, int box, int strided, const Epilogue ep,
+                    int blocks, int stages, int log_splits, int box, int strided, const Epilogue ep,
                     uint32_t *err) {
-  constexpr int kStages = few_stages<kN>;
   constexpr int kStageB = few_stage<kN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  SharedFew<kN> *sh = reinterpret_cast<SharedFew<kN> *>(base + kStages * kStageB);
+  SharedFew<kN> *sh = reinterpret_cast<SharedFew<kN> *>(base + stages * kStageB);
   const volatile int *abort_flag = &sh->abort;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -843,7 +909,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     // Warm L2 with the first ring of the weight while the previous kernel
     // drains: a prefetch only fills L2, which stays coherent with any later
     // write, so it may precede the dependency wait.
-    for (int kb = kb0; kb < kb1 && kb < kb0 + kStages; ++kb) {
+    for (int kb = kb0; kb < kb1 && kb < kb0 + stages; ++kb) {
       if (strided) {
         tma_prefetch_2d(&tmap_w, row0, kb * 64);
         tma_prefetch_2d(&tmap_w, row0 + 64, kb * 64);
@@ -853,7 +919,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     }
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(smem_u32(&sh->full[s]), 1);
       mbar_init(smem_u32(&sh->empty[s]), 1);
     }
@@ -874,6 +940,18 @@ __global__ void __launch_bounds__(THREADS, 2)
   tc_fence_after();
   const uint32_t tmem_base = sh->tmem_base;
   pdl_wait();
+
+  // The rows r .. r + 3 of the tile that this thread finishes; their bias is asked
+  // for now, and L2 for the residual.
+  const int quads = 32 >> log_splits;
+  const int r = (split * quads + (static_cast<int>(threadIdx.x) & (quads - 1))) * 4;
+  float bias[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    bias[i] = row0 + r + i < rows ? ld_bias(ep.bias, ep.bias_f32, row0 + r + i) : 0.0f;
+  if (ep.res != nullptr && static_cast<int>(threadIdx.x) < M && row0 + split * quads * 4 < rows)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(ep.res + (first_m + threadIdx.x) * ep.ldr + row0 +
+                                                  split * quads * 4));
 
   int prod_stage = 0;
   uint32_t prod_phase = 0;
@@ -897,7 +975,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       }
       tma_load_2d(a + kTileA, &tmap_x, kb * 64, first_m, full);
       ++issued;
-      if (++prod_stage == kStages) {
+      if (++prod_stage == stages) {
         prod_stage = 0;
         prod_phase ^= 1;
       }
@@ -923,7 +1001,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         mma_one_rt(tmem_base, a_desc + step_a * kk, b_desc + 2 * kk, idesc,
                    (kb != kb0) || kk != 0);
       mma_commit(smem_u32(&sh->empty[stage]));
-      if (++stage == kStages) {
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1;
       }
@@ -959,12 +1037,12 @@ __global__ void __launch_bounds__(THREADS, 2)
     // let this CTA's own copies and MMAs land before its memory is released
     const int zero = 0;
     if (warp == 0 && lane == 0) {
-      const int outstanding = issued < kStages ? issued : kStages;
+      const int outstanding = issued < stages ? issued : stages;
       for (int i = 1; i <= outstanding; ++i) {
         int s = prod_stage - i;
         uint32_t ph = prod_phase;
         if (s < 0) {
-          s += kStages;
+          s += stages;
           ph ^= 1;
         }
         mbar_wait(smem_u32(&sh->full[s]), ph, &zero);
@@ -978,62 +1056,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   pdl_launch_dependents();
-  // This CTA's share of the tile's rows, for every m: a thread takes four rows
-  // of two m at a time and asks for every CTA's part at once (one after the
-  // other, the reads of the peers' memory took 500 cycles each).
-  const int quads = 32 >> log_splits;
-  const int at_once = THREADS / 32 << log_splits;
-  const int r = (split * quads + (static_cast<int>(threadIdx.x) & (quads - 1))) * 4;
-  const int64_t col = row0 + r;
-  const int n = static_cast<int>(min(static_cast<int64_t>(4), rows - col));
-  if (n > 0) {
-    float bias[4] = {};
-    for (int i = 0; i < n; ++i) bias[i] = ld_bias(ep.bias, ep.bias_f32, col + i);
-    uint32_t src[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      src[i] = i < splits && num_kb * i >> log_splits != num_kb * (i + 1) >> log_splits
-                   ? map_to_rank(smem_u32(part) + r * 4, i)
-                   : 0u;  // (a CTA without K blocks has no part)
-    for (int m0 = static_cast<int>(threadIdx.x) >> (5 - log_splits); m0 < M; m0 += 2 * at_once) {
-      float4 v[2][8];
-      float res[2][4] = {};
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int m = min(m0 + u * at_once, M - 1);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[u][i] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (src[i] != 0 && (u == 0 || M > at_once))
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(v[u][i].x), "=f"(v[u][i].y), "=f"(v[u][i].z), "=f"(v[u][i].w)
-                         : "r"(src[i] + m * 512));
-        }
-        if (ep.res != nullptr)
-          load_four(ep.res + (first_m + m) * ep.ldr + col, n, res[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int64_t m = first_m + m0 + u * at_once;
-        if (m0 + u * at_once >= M) break;
-        float z[4] = {};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          z[0] += v[u][i].x;
-          z[1] += v[u][i].y;
-          z[2] += v[u][i].z;
-          z[3] += v[u][i].w;
-        }
-        float y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] += bias[i];
-        if (ep.pre != nullptr) store_four(ep.pre + m * ep.ldp + col, n, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = activate(z[i], ep.act) + res[u][i];
-        store_four(ep.out + m * ep.ldo + col, n, y);
-      }
-    }
-  }
+  join_parts(part, M, first_m, row0, rows, num_kb, log_splits, r, bias, ep);
   cluster.sync();  // partial tiles stay alive until every CTA has read them
   if (warp == 1) {
     tc_fence_after();
@@ -1465,15 +1488,17 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   const int splits = few_splits(units, num_kb, m.cols, num_sms);
   int log_splits = 0;
   while (1 << log_splits < splits) ++log_splits;
+  const bool wide = units * splits <= num_sms && num_kb >= 3 * few_stages<kN> * splits;
+  const int stages = wide ? few_most_stages<kN> : few_stages<kN>;
   auto kern = few_rows_kernel<kN>;
   const cudaError_t e =
-      set_smem_once(reinterpret_cast<const void *>(kern), few_smem<kN>,
+      set_smem_once(reinterpret_cast<const void *>(kern), few_smem<kN>(few_most_stages<kN>),
                     kN == 16 ? 3 : (kN == 32 ? 4 : (kN == 64 ? 5 : 6)));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = few_smem<kN>;
+  cfg.dynamicSmemBytes = few_smem<kN>(stages);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1485,7 +1510,7 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, map_w, map_x, static_cast<int>(m.cols),
-                            static_cast<int>(m.rows), num_kb, blocks, log_splits, box,
+                            static_cast<int>(m.rows), num_kb, blocks, stages, log_splits, box,
                             static_cast<int>(m.a.strided), m.ep, err);
 }
 
