@@ -118,6 +118,11 @@ __device__ __forceinline__ int32_t key_id(Key k) {
   return k == 0 ? kNoId : static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(k));
 }
 
+// Sums of a piece relative to its maximum (sga_logprob_part).
+struct Stats {
+  float max, s, w;
+};
+
 template <int kT>
 struct PieceShared {
   static constexpr int kVecs = 2 * kT;  // candidate vectors
@@ -126,13 +131,15 @@ struct PieceShared {
   int abort, num_vecs, num_keys;
   uint32_t threshold;
   float max, sum, wsum;
+  Stats piece[kMaxChunks];  // the row's pieces, in its first CTA
   Lse warp_lse[kMaxWarps];
   float warp_max[kMaxWarps];
   alignas(16) uint32_t group[kGroups];
   alignas(16) uint4 vec[kVecs];
   int32_t vec_id[kVecs];
   alignas(16) Key key[kKeys];
-  alignas(16) Key list[kMaxWarps * SGA_MAX_TOP];  // lists of warps, or of the row's pieces
+  alignas(16) Key list[kMaxWarps * SGA_MAX_TOP];     // lists of warps
+  alignas(16) Key pieces[kMaxChunks * SGA_MAX_TOP];  // lists of the row's pieces, in its first CTA
   Key best[SGA_MAX_TOP];
 };
 template <int kT>
@@ -358,6 +365,36 @@ __device__ __forceinline__ void select_top(PieceShared<kT> &sh, int n, int k, in
   }
 }
 
+// The best k of the n pieces' sorted lists into best.  At least k entries reach
+// the largest of the lists' last entries, and the smallest of their (k / n)-th: what
+// does not reach the larger of the two is left out of the counting.
+template <int kT>
+__device__ __forceinline__ void join_lists(PieceShared<kT> &sh, int n, int k, int tid) {
+  Key threshold = 0, least = ~Key(0);
+  const int share = (k + n - 1) / n - 1;
+  for (int l = 0; l < n; ++l) {
+    threshold = max(threshold, sh.pieces[l * k + k - 1]);
+    least = min(least, sh.pieces[l * k + share]);
+  }
+  threshold = max(threshold, least);
+  if (tid == 0) sh.num_keys = 0;
+  if (tid < k) sh.best[tid] = 0;
+  consumers_sync<kT>();
+  for (int c = tid; c < n * k; c += kT) {
+    const Key mine = sh.pieces[c];
+    if (mine != 0 && mine >= threshold) sh.key[atomicAdd(&sh.num_keys, 1)] = mine;
+  }
+  consumers_sync<kT>();
+  const int m = sh.num_keys;
+  if (tid == 0 && (m & 1)) sh.key[m] = 0;
+  consumers_sync<kT>();
+  for (int c = tid; c < m; c += kT) {
+    const Key mine = sh.key[c];
+    const int rank = keys_above(sh.key, m, mine);
+    if (rank < k) sh.best[rank] = mine;
+  }
+}
+
 template <bool kBf16, int kT>
 __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
     logprobs_kernel(const char *__restrict__ logits, int64_t ld_bytes, int64_t num_rows, int valid,
@@ -408,8 +445,11 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  pdl_wait();
   cg::cluster_group cluster = cg::this_cluster();
+  // Two cluster barriers: every CTA has begun (its memory may be written), every
+  // piece has reached the row's first CTA.
+  if (chunks > 1) cluster.barrier_arrive();
+  pdl_wait();
 
   if (warp == kWarps) {
     // ------------------------------------------------------------- copy warp
@@ -439,10 +479,10 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
     for (int j = max(0, g - kRing); j < g; ++j)
       pipe_wait(smem_u32(&sh.full[j % kRing]), (j / kRing) & 1, &zero);
     pdl_launch_dependents();
-    if (chunks > 1) {  // the consumers' cluster barriers count every thread
-      cluster.sync();
-      cluster.sync();
-      cluster.sync();
+    if (chunks > 1) {  // (the barriers count every thread that has not ended)
+      __syncwarp();
+      cluster.barrier_wait();
+      cluster.barrier_arrive();
     }
     return;
   }
@@ -459,12 +499,6 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       sh.threshold = 0xffffffffu;
     }
     const int32_t tok = tok_next;
-    float xt = neg_inf();  // the token's logit (thread 0)
-    if (tid == 0) {
-      if (tokens != nullptr && row + row_step < num_rows) tok_next = tokens[row + row_step];
-      const int64_t at = static_cast<int64_t>(tok) - id0;
-      if (tok >= 0 && at >= 0 && at < valid) xt = load_elem<kBf16>(p, static_cast<int>(at));
-    }
     consumers_sync<kT>();
 
     float threshold = __int_as_float(0x7f800000);
@@ -500,6 +534,12 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       }
     }
 
+    float xt = neg_inf();  // the token's logit (thread 0; asked for here, used at the row's end)
+    if (tid == 0) {
+      if (tokens != nullptr && row + row_step < num_rows) tok_next = tokens[row + row_step];
+      const int64_t at = static_cast<int64_t>(tok) - id0;
+      if (tok >= 0 && at >= 0 && at < valid) xt = load_elem<kBf16>(p, static_cast<int>(at));
+    }
     ThreadSums a = {0.0f, kUnset, 0u, 0u};
     uint32_t mxb = kBf16 ? 0xff80ff80u : 0xff800000u;
     uint32_t lo = pack_lo<kBf16>(a.limit, threshold);
@@ -650,24 +690,18 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
         }
       }
     }
-    // ---- the row: every CTA joins the maxima and restates its sums
-    float row_max = neg_inf();
+    // ---- the piece's sums, restated relative to its maximum
+    float max = neg_inf();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) row_max = max_nan(row_max, sh.warp_max[w]);
-    if (chunks > 1) {
-      if (tid == 0) sh.max = row_max;
-      cluster.sync();
-      for (int c = 0; c < chunks; ++c)
-        row_max = max_nan(row_max, *cluster.map_shared_rank(&sh.max, c));
-    }
+    for (int w = 0; w < kWarps; ++w) max = max_nan(max, sh.warp_max[w]);
     // An extreme finite maximum: sums relative to the maximum itself, in
     // differences from it, over the piece once more.
-    const bool exact = (row_max > kFastMax && row_max < __int_as_float(0x7f800000)) ||
-                       (row_max < -kFastMax && row_max > neg_inf());
+    const bool exact = (max > kFastMax && max < __int_as_float(0x7f800000)) ||
+                       (max < -kFastMax && max > neg_inf());
     if (exact) {
       float es = 0.0f, ew = 0.0f;
       for (int j = pc.c0 + tid; j < pc.c1; j += kT) {
-        const float t = max_nan((load_elem<kBf16>(p, j) - row_max) * kLog2e, -1e30f);
+        const float t = max_nan((load_elem<kBf16>(p, j) - max) * kLog2e, -1e30f);
         const float e = ex2(t);
         es += e;
         ew = fmaf(e, t, ew);
@@ -687,7 +721,7 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       Lse t = {0.0f, 0.0f, 0.0f};
       if (lane < kWarps) t = sh.warp_lse[lane];
       // (the difference to the maximum in one rounding)
-      const float d = exact ? 0.0f : fmaf(-row_max, kLog2e, t.r);
+      const float d = exact ? 0.0f : fmaf(-max, kLog2e, t.r);
       const float f = t.s == 0.0f ? 0.0f : ex2(d);
       s = f * t.s;
       w = f == 0.0f ? 0.0f : f * fmaf(d, t.s, t.w);
@@ -696,27 +730,30 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
         s += __shfl_xor_sync(0xffffffffu, s, off);
         w += __shfl_xor_sync(0xffffffffu, w, off);
       }
-      if (lane == 0) {
+      if (lane == 0 && chunks == 1) {
         sh.sum = s;
         sh.wsum = w;
       }
     }
     if (chunks > 1) {
-      cluster.sync();
-      if (chunk == 0) {
-        for (int c = tid; c < chunks * k; c += kT)
-          sh.list[c] = *cluster.map_shared_rank(&sh.best[c % k], c / k);
-        consumers_sync<kT>();  // this piece's list has been gathered too
-        if (tid < k) sh.best[tid] = 0;
-        consumers_sync<kT>();
-      }
-      if (chunk == 0 && warp == 0 && lane < chunks) {
-        s = *cluster.map_shared_rank(&sh.sum, lane);
-        w = *cluster.map_shared_rank(&sh.wsum, lane);
-      } else {
+      // every piece to the row's first CTA
+      cluster.barrier_wait();
+      if (tid < k) cluster.map_shared_rank(sh.pieces, 0)[chunk * k + tid] = sh.best[tid];
+      if (tid == 0) cluster.map_shared_rank(sh.piece, 0)[chunk] = {max, s, w};
+      __syncwarp();
+      cluster.barrier_arrive();
+      if (chunk > 0) return;  // (such a launch has a row per cluster)
+      cluster.barrier_wait();
+      for (int c = 0; c < chunks; ++c) max = max_nan(max, sh.piece[c].max);
+      if (warp == 0) {
         s = w = 0.0f;
-      }
-      if (chunk == 0 && warp == 0) {
+        if (lane < chunks) {
+          const Stats q = sh.piece[lane];
+          const float d = (q.max - max) * kLog2e;  // <= 0
+          const float f = q.max == neg_inf() ? 0.0f : ex2(d);
+          s = f * q.s;
+          w = f == 0.0f ? 0.0f : f * fmaf(d, q.s, q.w);
+        }
 #pragma unroll
         for (int off = kMaxChunks / 2; off > 0; off >>= 1) {
           s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -727,44 +764,33 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
           sh.wsum = w;
         }
       }
+      if (k > 0) join_lists(sh, chunks, k, tid);
     }
-    if (chunk == 0) {
-      if (chunks > 1)
-        for (int c = tid; c < chunks * k; c += kT) {
-          const Key mine = sh.list[c];
-          const int rank = keys_above(sh.list, chunks * k, mine);
-          if (mine != 0 && rank < k) sh.best[rank] = mine;
-        }
-      consumers_sync<kT>();
-      float lse, entropy;
-      finish_row(row_max, sh.sum, sh.wsum, lse, entropy);
-      if (tid == 0) {
-        s = sh.sum;
-        w = sh.wsum;
-        if (out.part != nullptr) {
-          out.part[row] = {row_max, s, w, xt};
-        } else {
-          if (out.logprob != nullptr) out.logprob[row] = tok < 0 ? 0.0f : to_logprob(xt, lse);
-          if (out.entropy != nullptr) out.entropy[row] = entropy;
-          if (out.lse != nullptr) out.lse[row] = lse;
-        }
-      }
-      if (tid < k) {
-        const float v = key_value(sh.best[tid]);
-        const int32_t id = key_id(sh.best[tid]);
-        if (out.part != nullptr) {
-          out.top[row * k + tid] = {v, id};
-        } else {
-          if (out.top_ids != nullptr) out.top_ids[row * k + tid] = id == kNoId ? -1 : id;
-          if (out.top_logprobs != nullptr) out.top_logprobs[row * k + tid] = to_logprob(v, lse);
-        }
+    consumers_sync<kT>();
+    float lse, entropy;
+    finish_row(max, sh.sum, sh.wsum, lse, entropy);
+    if (tid == 0) {
+      s = sh.sum;
+      w = sh.wsum;
+      if (out.part != nullptr) {
+        out.part[row] = {max, s, w, xt};
+      } else {
+        if (out.logprob != nullptr) out.logprob[row] = tok < 0 ? 0.0f : to_logprob(xt, lse);
+        if (out.entropy != nullptr) out.entropy[row] = entropy;
+        if (out.lse != nullptr) out.lse[row] = lse;
       }
     }
-    // what this row kept in shared memory has been read
-    if (chunks > 1)
-      cluster.sync();
-    else
-      consumers_sync<kT>();
+    if (tid < k) {
+      const float v = key_value(sh.best[tid]);
+      const int32_t id = key_id(sh.best[tid]);
+      if (out.part != nullptr) {
+        out.top[row * k + tid] = {v, id};
+      } else {
+        if (out.top_ids != nullptr) out.top_ids[row * k + tid] = id == kNoId ? -1 : id;
+        if (out.top_logprobs != nullptr) out.top_logprobs[row * k + tid] = to_logprob(v, lse);
+      }
+    }
+    consumers_sync<kT>();  // what this row kept in shared memory has been read
   }
 }
 
