@@ -54,9 +54,9 @@ __device__ __forceinline__ void lse_restate(Lse &a, float r) {
 }
 
 // ---------------------------------------------------------------- forward
-// HBM-bound, with little issue to spare: 4096 x 202048 bf16 244 us without
-// alternatives (6.8 TB/s, the copy rate), 275 with 5, 312 with 20; one row of
-// 152064 5.6 us without and 9.3 with 20, latency.  The 2^x of every logit and the
+// HBM-bound, with little issue to spare: 4096 x 202048 bf16 231 us without
+// alternatives (7.15 TB/s), 265 with 5, 310 with 20; one row of
+// 152064 3.8 us without and 7.7 with 20, latency.  The 2^x of every logit and the
 // packed fp32 sums take 65 % of the issue slots, which is why the reference is
 // only moved when it has to be and candidates are tested a vector at a time.
 //
@@ -268,6 +268,16 @@ __device__ __forceinline__ void sums_vector(ThreadSums &a, const uint4 q) {
   }
 }
 
+// The larger of each pair of logits of two vectors (NaN wins).
+template <bool kBf16>
+__device__ __forceinline__ uint4 vec_larger(const uint4 a, const uint4 b) {
+  auto larger = [](uint32_t x, uint32_t y) {
+    return kBf16 ? max_nan_bf16x2(x, y)
+                 : __float_as_uint(max_nan(__uint_as_float(x), __uint_as_float(y)));
+  };
+  return make_uint4(larger(a.x, b.x), larger(a.y, b.y), larger(a.z, b.z), larger(a.w, b.w));
+}
+
 // A candidate: reaches the threshold and is not masked.
 __device__ __forceinline__ bool reaches(float x, float threshold) {
   return !(x < threshold) && x != neg_inf();
@@ -405,6 +415,7 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
   constexpr int kStageVec = kT * kVecPerThread;
   constexpr int kWarps = kT / 32;
   constexpr int kPerGroup = kT / kGroups;
+  constexpr uint32_t kMasked = kBf16 ? 0xff80ff80u : 0xff800000u;  // -inf
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ PieceShared<kT> sh;
   const int chunk = static_cast<int>(blockIdx.x % chunks);
@@ -446,9 +457,9 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
   }
   __syncthreads();
   cg::cluster_group cluster = cg::this_cluster();
-  // Two cluster barriers: every CTA has begun (its memory may be written), every
-  // piece has reached the row's first CTA.
-  if (chunks > 1) cluster.barrier_arrive();
+  // Two cluster barriers: every CTA has begun (its memory may be written; nothing
+  // else is handed over), every piece has reached the row's first CTA.
+  if (chunks > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   pdl_wait();
 
   if (warp == kWarps) {
@@ -501,6 +512,7 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
     const int32_t tok = tok_next;
     consumers_sync<kT>();
 
+    ThreadSums a = {0.0f, kUnset, 0u, 0u};
     float threshold = __int_as_float(0x7f800000);
     if (k > 0) {
       threshold = neg_inf();
@@ -513,6 +525,7 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
           const int n = min(kStageVec, (pc.b1 - pc.b0) / kVec - j * kStageVec);
           for (int i = tid; i < n; i += kT) m = max_nan(m, vec_max<kBf16>(ring[slot * kStageVec + i]));
         }
+        sums_rebase(a, m);  // a reference to begin with
 #pragma unroll
         for (int off = kPerGroup / 2; off > 0; off >>= 1)
           m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -540,8 +553,7 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       const int64_t at = static_cast<int64_t>(tok) - id0;
       if (tok >= 0 && at >= 0 && at < valid) xt = load_elem<kBf16>(p, static_cast<int>(at));
     }
-    ThreadSums a = {0.0f, kUnset, 0u, 0u};
-    uint32_t mxb = kBf16 ? 0xff80ff80u : 0xff800000u;
+    uint32_t mxb = kMasked;
     uint32_t lo = pack_lo<kBf16>(a.limit, threshold);
     for (int j = 0; j < pc.stages; ++j, ++g) {
       const int slot = g % kRing;
@@ -550,26 +562,37 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       const int at = pc.b0 + j * kStageVec * kVec;
       const int n = min(kStageVec, (pc.b1 - at) / kVec);
       const uint4 *st = ring + slot * kStageVec;
+      // All of the thread's vectors at once, with one test for all: with a test and a
+      // branch for each their latencies follow one another (4096 x 202048 242 us, so
+      // 231; vectors past a piece's end count as masked).
+      uint4 q[kVecPerThread];
 #pragma unroll
       for (int u = 0; u < kVecPerThread; ++u) {
         const int i = u * kT + tid;
-        if (i < n) {
-          const uint4 q = st[i];
-          if (vec_reaches<kBf16>(q, mxb, lo)) {
-            const float vm = vec_max<kBf16>(q);
-            sums_rebase(a, vm);
-            lo = pack_lo<kBf16>(a.limit, threshold);
-            if (!(vm < threshold) && vm != neg_inf() && k > 0) {
-              const int c = atomicAdd(&sh.num_vecs, 1);
-              if (c < sh.kVecs) {
-                sh.vec[c] = q;
-                sh.vec_id[c] = id0 + at + i * kVec;
-              }
+        q[u] = i < n ? st[i] : make_uint4(kMasked, kMasked, kMasked, kMasked);
+      }
+      uint4 most = q[0];
+#pragma unroll
+      for (int u = 1; u < kVecPerThread; ++u) most = vec_larger<kBf16>(most, q[u]);
+      if (vec_reaches<kBf16>(most, mxb, lo)) {
+        const float m = vec_max<kBf16>(most);
+        sums_rebase(a, m);
+        lo = pack_lo<kBf16>(a.limit, threshold);
+        if (k > 0 && !(m < threshold)) {
+#pragma unroll
+          for (int u = 0; u < kVecPerThread; ++u) {
+            const float vm = vec_max<kBf16>(q[u]);
+            if (vm < threshold || vm == neg_inf()) continue;
+            const int c = atomicAdd(&sh.num_vecs, 1);
+            if (c < sh.kVecs) {
+              sh.vec[c] = q[u];
+              sh.vec_id[c] = id0 + at + (u * kT + tid) * kVec;
             }
           }
-          sums_vector<kBf16>(a, q);
         }
       }
+#pragma unroll
+      for (int u = 0; u < kVecPerThread; ++u) sums_vector<kBf16>(a, q[u]);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.empty[slot]));
     }
