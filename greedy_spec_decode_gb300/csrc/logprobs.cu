@@ -377,31 +377,34 @@ __device__ __forceinline__ void select_top(PieceShared<kT> &sh, int n, int k, in
 
 // The best k of the n pieces' sorted lists into best.  At least k entries reach
 // the largest of the lists' last entries, and the smallest of their (k / n)-th: what
-// does not reach the larger of the two is left out of the counting.
+// does not reach the larger of the two is left out of the counting where there is
+// much.  best[] and num_keys are 0 on entry.
 template <int kT>
 __device__ __forceinline__ void join_lists(PieceShared<kT> &sh, int n, int k, int tid) {
-  Key threshold = 0, least = ~Key(0);
-  const int share = (k + n - 1) / n - 1;
-  for (int l = 0; l < n; ++l) {
-    threshold = max(threshold, sh.pieces[l * k + k - 1]);
-    least = min(least, sh.pieces[l * k + share]);
+  int m = n * k;  // (even: n is)
+  const Key *from = sh.pieces;
+  if (m > 64) {
+    Key threshold = 0, least = ~Key(0);
+    const int share = (k + n - 1) / n - 1;
+    for (int l = 0; l < n; ++l) {
+      threshold = max(threshold, sh.pieces[l * k + k - 1]);
+      least = min(least, sh.pieces[l * k + share]);
+    }
+    threshold = max(threshold, least);
+    for (int c = tid; c < m; c += kT) {
+      const Key mine = sh.pieces[c];
+      if (mine != 0 && mine >= threshold) sh.key[atomicAdd(&sh.num_keys, 1)] = mine;
+    }
+    consumers_sync<kT>();
+    m = sh.num_keys;
+    if (tid == 0 && (m & 1)) sh.key[m] = 0;
+    consumers_sync<kT>();
+    from = sh.key;
   }
-  threshold = max(threshold, least);
-  if (tid == 0) sh.num_keys = 0;
-  if (tid < k) sh.best[tid] = 0;
-  consumers_sync<kT>();
-  for (int c = tid; c < n * k; c += kT) {
-    const Key mine = sh.pieces[c];
-    if (mine != 0 && mine >= threshold) sh.key[atomicAdd(&sh.num_keys, 1)] = mine;
-  }
-  consumers_sync<kT>();
-  const int m = sh.num_keys;
-  if (tid == 0 && (m & 1)) sh.key[m] = 0;
-  consumers_sync<kT>();
   for (int c = tid; c < m; c += kT) {
-    const Key mine = sh.key[c];
-    const int rank = keys_above(sh.key, m, mine);
-    if (rank < k) sh.best[rank] = mine;
+    const Key mine = from[c];
+    const int rank = keys_above(from, m, mine);
+    if (mine != 0 && rank < k) sh.best[rank] = mine;
   }
 }
 
@@ -766,6 +769,8 @@ __global__ void __launch_bounds__(kT + 32, kT == 256 ? 3 : 10)
       __syncwarp();
       cluster.barrier_arrive();
       if (chunk > 0) return;  // (such a launch has a row per cluster)
+      if (tid < k) sh.best[tid] = 0;
+      if (tid == 0) sh.num_keys = 0;
       cluster.barrier_wait();
       for (int c = 0; c < chunks; ++c) max = max_nan(max, sh.piece[c].max);
       if (warp == 0) {
