@@ -772,8 +772,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 // ---------------------------------------------------------------------------
 template <int kN>
 constexpr int few_stage = kTileA + kN * ROW_BYTES;
-// Ring stages with two CTAs per SM, and where the CTAs are no more than the SMs
-// and turn the smaller ring three times (96 x 4096 x 4096 12.7 -> 11.9 us, 24 x
+// Ring stages with two CTAs per SM, and where one per SM holds all of them
+// and they turn the smaller ring three times (96 x 4096 x 4096 12.7 -> 11.9 us, 24 x
 // 1024 x 8192 9.1 -> 8.8; at two and a half turns, 333 x 1531 x 2056 11.6 -> 12.0).
 template <int kN>
 constexpr int few_stages = (110 * 1024) / few_stage<kN>;
@@ -1461,15 +1461,27 @@ cudaError_t launch_products(const Mat *mats, int n, int num_sms, uint32_t *err,
   }
 }
 
-// CTAs per tile of few_rows_kernel: while all of them are resident (two per SM).
-// A CTA's share of K blocks may be one or none; it still takes its share of
-// the results.  Eight only for a long sum, or the least rows (M x N x K, 4 / 8
-// CTAs: 64 x 4096 x 4096 11.8 / 12.6 us, 64 x 1024 x 8192 14.8 / 11.0, 1 x 1024
-// x 8192 12.7 / 9.1, 1 x 4096 x 4096 10.0 / 9.7).
+// Clusters of `splits` few_rows CTAs that run at once, at `per_sm` CTAs per SM: a
+// cluster lies in one GPC, whose SMs are not all a multiple of it (152 SMs hold 36
+// clusters of 4 or 15 of 8).
+int64_t resident_clusters(int splits, int per_sm, int num_sms) {
+  const int64_t ctas = static_cast<int64_t>(per_sm) * num_sms;
+  if (splits < 4) return ctas / splits;
+  return per_sm == 1 ? (splits == 4 ? ctas * 19 / 80 : ctas / 10)
+                     : (splits == 4 ? ctas * 39 / 160 : ctas * 19 / 160);
+}
+
+// CTAs per tile of few_rows_kernel: while all of them are resident (two per SM;
+// 128 x 4736 x 8192, 37 clusters of 8: 26.1 us, 36 of them 18.8; 96 x 9728 x 8192,
+// 76 of 4: 44.5, 74 of them 30.3).  A CTA's share of K blocks may be one or none; it
+// still takes its share of the results.  Eight only for a long sum, or the least rows
+// (M x N x K, 4 / 8 CTAs: 64 x 4096 x 4096 11.8 / 12.6 us, 64 x 1024 x 8192 14.8 /
+// 11.0, 1 x 1024 x 8192 12.7 / 9.1, 1 x 4096 x 4096 10.0 / 9.7).
 int few_splits(int64_t units, int num_kb, int64_t m, int num_sms) {
   const int most = num_kb >= 80 || (m <= 16 && num_kb >= 32) ? 8 : 4;
   int splits = 1;
-  while (splits < most && units * splits * 2 <= 2 * num_sms && num_kb >= splits) splits *= 2;
+  while (splits < most && units <= resident_clusters(2 * splits, 2, num_sms) && num_kb >= splits)
+    splits *= 2;
   return splits;
 }
 
@@ -1488,7 +1500,7 @@ cudaError_t launch_few_rows(const Mat &m, int num_sms, uint32_t *err, cudaStream
   const int splits = few_splits(units, num_kb, m.cols, num_sms);
   int log_splits = 0;
   while (1 << log_splits < splits) ++log_splits;
-  const bool wide = units * splits <= num_sms && num_kb >= 3 * few_stages<kN> * splits;
+  const bool wide = units <= resident_clusters(splits, 1, num_sms) && num_kb >= 3 * few_stages<kN> * splits;
   const int stages = wide ? few_most_stages<kN> : few_stages<kN>;
   auto kern = few_rows_kernel<kN>;
   const cudaError_t e =
