@@ -1476,9 +1476,12 @@ int64_t resident_clusters(int splits, int per_sm, int num_sms) {
 // 76 of 4: 44.5, 74 of them 30.3).  A CTA's share of K blocks may be one or none; it
 // still takes its share of the results.  Eight only for a long sum, or the least rows
 // (M x N x K, 4 / 8 CTAs: 64 x 4096 x 4096 11.8 / 12.6 us, 64 x 1024 x 8192 14.8 /
-// 11.0, 1 x 1024 x 8192 12.7 / 9.1, 1 x 4096 x 4096 10.0 / 9.7).
+// 11.0, 1 x 1024 x 8192 12.7 / 9.1, 1 x 4096 x 4096 10.0 / 9.7), and with many rows
+// only while there is one CTA per SM (128 x 2560 x 8192 16.3 / 18.1, 128 x 4096 x 8192
+// 17.7 / 19.9, 16 x 4096 x 8192 14.9 / 13.4).
 int few_splits(int64_t units, int num_kb, int64_t m, int num_sms) {
-  const int most = num_kb >= 80 || (m <= 16 && num_kb >= 32) ? 8 : 4;
+  const bool eight = m <= 16 ? num_kb >= 32 : num_kb >= 80 && (m <= 48 || units * 8 <= num_sms);
+  const int most = eight ? 8 : 4;
   int splits = 1;
   while (splits < most && units <= resident_clusters(2 * splits, 2, num_sms) && num_kb >= splits)
     splits *= 2;
