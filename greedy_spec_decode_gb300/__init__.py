@@ -356,14 +356,15 @@ def sga_lmhead_argmax_shards_fp8(hidden_q, hidden_scale, weight_q, weight_scale,
     return out_stats
 
 
-def _bf16_rows(t, rows, cols, name):
-    """(address, row stride) of a bf16 [rows, cols] tensor with unit column
+def _bf16_rows(t, shape, name):
+    """(address, row stride) of a bf16 tensor of that shape with unit column
     stride; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dtype is not torch.bfloat16 or tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name} must be bf16 [{rows}, {cols}]")
+    if t.dtype is not _BF16 or t.shape != shape:
+        raise ValueError(f"{name} must be bf16 {list(shape)}")
     row, col = t.stride()
+    rows, cols = shape
     if col != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     return t.data_ptr(), row if rows > 1 else cols  # a single row's stride is never used
@@ -373,9 +374,10 @@ def _bias(t, n, name):
     """(address, dtype code) of a float32 or bf16 vector of n, or (None, SGA_F32)."""
     if t is None:
         return None, SGA_F32
-    if t.dtype not in (torch.float32, torch.bfloat16) or t.numel() != n or not t.is_contiguous():
+    dtype = t.dtype
+    if (dtype is not _F32 and dtype is not _BF16) or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 or bf16 tensor of {n} elements")
-    return t.data_ptr(), SGA_F32 if t.dtype is torch.float32 else SGA_BF16
+    return t.data_ptr(), SGA_F32 if dtype is _F32 else SGA_BF16
 
 
 def sga_linear(x, weight, out, bias=None, act=SGA_ACT_NONE, residual=None, out_preact=None,
@@ -385,13 +387,14 @@ def sga_linear(x, weight, out, bias=None, act=SGA_ACT_NONE, residual=None, out_p
     row stride; x and weight rows 16-byte aligned), bias: float32 or bf16 [N].
     out may be residual itself; out_preact receives x . weight^T + bias, which
     sga_linear_grad needs when there is an activation (see include/sga.h)."""
-    M, K = x.shape
+    M, K = shape_x = x.shape
     N = weight.size(0)
-    px, ldx = _bf16_rows(x, M, K, "x")
-    pw, ldw = _bf16_rows(weight, N, K, "weight")
-    po, ldo = _bf16_rows(out, M, N, "out")
-    pr, ldr = _bf16_rows(residual, M, N, "residual")
-    pp, ldp = _bf16_rows(out_preact, M, N, "out_preact")
+    shape_y = (M, N)
+    px, ldx = _bf16_rows(x, shape_x, "x")
+    pw, ldw = _bf16_rows(weight, (N, K), "weight")
+    po, ldo = _bf16_rows(out, shape_y, "out")
+    pr, ldr = _bf16_rows(residual, shape_y, "residual")
+    pp, ldp = _bf16_rows(out_preact, shape_y, "out_preact")
     pb, code = _bias(bias, N, "bias")
     _on_gpu(x, weight, out, bias, residual, out_preact)
     _check("sga_linear", lib().sga_linear(
@@ -410,14 +413,15 @@ def sga_linear_grad(grad_out, x, weight, workspace, act=SGA_ACT_NONE, preact=Non
     bf16 like its operand, grad_bias float32 or bf16, or None); the residual's
     gradient is grad_out itself.  preact: sga_linear's out_preact; workspace: a
     CUDA tensor of at least sga_linear_grad_workspace(M, N, K) bytes."""
-    M, K = x.shape
+    M, K = shape_x = x.shape
     N = weight.size(0)
-    px, ldx = _bf16_rows(x, M, K, "x")
-    pw, ldw = _bf16_rows(weight, N, K, "weight")
-    pg, ldg = _bf16_rows(grad_out, M, N, "grad_out")
-    pp, ldp = _bf16_rows(preact, M, N, "preact")
-    pgx, ldgx = _bf16_rows(grad_x, M, K, "grad_x")
-    pgw, ldgw = _bf16_rows(grad_weight, N, K, "grad_weight")
+    shape_w, shape_y = (N, K), (M, N)
+    px, ldx = _bf16_rows(x, shape_x, "x")
+    pw, ldw = _bf16_rows(weight, shape_w, "weight")
+    pg, ldg = _bf16_rows(grad_out, shape_y, "grad_out")
+    pp, ldp = _bf16_rows(preact, shape_y, "preact")
+    pgx, ldgx = _bf16_rows(grad_x, shape_x, "grad_x")
+    pgw, ldgw = _bf16_rows(grad_weight, shape_w, "grad_weight")
     pb, code = _bias(grad_bias, N, "grad_bias")
     _on_gpu(grad_out, x, weight, workspace, preact, grad_x, grad_weight, grad_bias)
     _check("sga_linear_grad", lib().sga_linear_grad(
@@ -425,14 +429,20 @@ def sga_linear_grad(grad_out, x, weight, workspace, act=SGA_ACT_NONE, preact=Non
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
 
 
-# The calls below run beside single-token steps of a few microseconds, so their
+# The calls above and below run beside single-token steps of a few microseconds, so their
 # marshalling is kept short: plain integers for pointers (ctypes takes them for
 # c_void_p) and the raw handle of the current stream.
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+# (absent from builds of torch without CUDA; only reached with CUDA tensors)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _raw_stream(stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_raw_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -452,9 +462,10 @@ def _on_gpu(*tensors):
 
 
 def _logits_2d(logits):
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits must be 2-D")
-    rows, width = logits.shape
+    rows, width = shape
     ld, col = logits.stride()
     if col != 1 and width > 1:
         raise ValueError("logits must have unit stride along the vocab")
@@ -465,7 +476,7 @@ def _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids, o
     """top_k and the addresses of the per-row tensors of the log-probability calls."""
     top = out_top_ids if out_top_ids is not None else out_top_logprobs
     k = 0 if top is None else top.size(-1)
-    f32, i32 = torch.float32, torch.int32
+    f32, i32 = _F32, _I32
     return k, (_check_out(tokens, i32, rows, "tokens"),
                _check_out(out_logprob, f32, rows, "out_logprob"),
                _check_out(out_entropy, f32, rows, "out_entropy"),
@@ -503,9 +514,9 @@ def sga_local_logprobs(logits, shard_start, shard_width, org_vocab, tokens, out_
     _on_gpu(logits, tokens, out_parts, out_top)
     _check("sga_local_logprobs", lib().sga_local_logprobs(
         logits.data_ptr(), code, rows, ld, int(shard_start), int(shard_width),
-        int(org_vocab), _check_out(tokens, torch.int32, rows, "tokens"), k,
-        _check_out(out_parts, torch.float32, 4 * rows, "out_parts"),
-        _check_out(out_top, torch.int32, 2 * k * rows, "out_top"), _raw_stream(stream)))
+        int(org_vocab), _check_out(tokens, _I32, rows, "tokens"), k,
+        _check_out(out_parts, _F32, 4 * rows, "out_parts"),
+        _check_out(out_top, _I32, 2 * k * rows, "out_top"), _raw_stream(stream)))
     return out_parts
 
 
@@ -523,8 +534,8 @@ def sga_logprob_reduce(parts, tops, num_shards, tokens=None, out_logprob=None, o
     _on_gpu(parts, tops, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
             out_top_logprobs)
     _check("sga_logprob_reduce", lib().sga_logprob_reduce(
-        _check_out(parts, torch.float32, 4 * rows * num_shards, "parts"),
-        _check_out(tops, torch.int32, 2 * k * rows * num_shards, "tops") if k else None,
+        _check_out(parts, _F32, 4 * rows * num_shards, "parts"),
+        _check_out(tops, _I32, 2 * k * rows * num_shards, "tops") if k else None,
         num_shards, rows, k, tok, *outs, _raw_stream(stream)))
 
 
@@ -541,7 +552,7 @@ def sga_token_logprobs_grad(logits, shard_start, org_vocab, tokens, lse, entropy
         raise ValueError("out_grad must match logits, unit stride along the vocab")
     ldg = out_grad.stride(0) if rows > 1 else max(out_grad.stride(0), width)
     k = 0 if top_ids is None else top_ids.size(-1)
-    f32, i32 = torch.float32, torch.int32
+    f32, i32 = _F32, _I32
     _on_gpu(logits, tokens, lse, entropy, grad_logprob, grad_entropy, top_ids, grad_top,
             out_grad)
     _check("sga_token_logprobs_grad", lib().sga_token_logprobs_grad(
