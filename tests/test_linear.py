@@ -291,6 +291,65 @@ def test_relu_cuts_off_infinities(sga_lib, pad):
     check(gb, dz64.sum(0), sum_tol(M, dz64.abs().sum(0)), "b")
 
 
+# few rows: each number of parts of the sum, either ring, and around the numbers of
+# clusters that the GPU holds at once
+SPLIT_SHAPES = [(5, 1000, 8192), (20, 2000, 4104), (40, 1900, 5128), (40, 2100, 5128),
+                (96, 1920, 5128), (100, 2060, 5128), (96, 4608, 2056), (90, 4700, 2056),
+                (70, 9500, 1032), (70, 9700, 1032), (250, 1024, 5128)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SPLIT_SHAPES, ids=str)
+def test_split_sums_match_64_bits(sga_lib, shape):
+    M, N, K = shape
+    i = SPLIT_SHAPES.index(shape)
+    act = ACTS[i % 5]
+    x, x64 = mat(i + 401, M, K, 1.0)
+    w, w64 = mat(i + 501, N, K, K ** -0.5)
+    b, b64 = mat(i + 601, 1, N, 0.7, 0, torch.float32)
+    res, r64 = mat(i + 701, M, N, 1.0, i % 4)
+    out, pre = torch.empty_like(res), torch.empty_like(res)
+    sga_lib.sga_linear(x, w, out, b[0].contiguous(), ACTS.index(act), res, pre)
+    z64 = x64 @ w64.T + b64
+    y64 = act64(z64, act)[0] + r64
+    tol = 1.2 * sum_tol(K, x64.abs() @ w64.abs().T + b64.abs()) + 2.0 ** -19 * z64.abs()
+    check(out, y64, tol + 2.0 ** -8 * y64.abs() + 1e-30, "out")
+    check(pre, z64, tol + 2.0 ** -8 * z64.abs() + 1e-30, "preact")
+    assert sga_lib.sga_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_row_offsets_past_32_bits(sga_lib, M):
+    """Every matrix with rows so far apart that the last ones lie more than 2^32
+    elements on: the same results as from packed rows."""
+    N, K = 200, 136
+    ld = ((1 << 32) // (M - 1) // 8 + 33) * 8
+    buf = torch.empty((M - 1) * ld + 2048, dtype=torch.bfloat16, device="cuda")
+
+    def far(cols, at):
+        return torch.as_strided(buf, (M, cols), (ld, 1), at)
+
+    x, _ = mat(31, M, K, 1.0)
+    w, _ = mat(32, N, K, 1.0)
+    r, _ = mat(33, M, N, 1.0)
+    act = ACTS.index("silu")
+    out, z = torch.empty_like(r), torch.empty_like(r)
+    sga_lib.sga_linear(x, w, out, None, act, r, z)
+    fx, fr, fz, fout = far(K, 0), far(N, 256), far(N, 512), far(N, 768)
+    fx.copy_(x)
+    fr.copy_(r)
+    sga_lib.sga_linear(fx, w, fout, None, act, fr, fz)
+    assert torch.equal(fout, out) and torch.equal(fz, z)
+    ws = torch.empty(sga_lib.sga_linear_grad_workspace(M, N, K), dtype=torch.uint8, device="cuda")
+    gx, gw, gb = torch.empty_like(x), torch.empty_like(w), torch.empty(N, device="cuda")
+    sga_lib.sga_linear_grad(r, x, w, ws, act, z, gx, gw, gb)
+    fgx, fgw, fgb = far(K, 1024), torch.empty_like(w), torch.empty_like(gb)
+    sga_lib.sga_linear_grad(fr, fx, w, ws, act, fz, fgx, fgw, fgb)
+    assert torch.equal(fgx, gx) and torch.equal(fgw, gw) and torch.equal(fgb, gb)
+    assert sga_lib.sga_device_error() == 0
+
+
 # ----------------------------------------------------------------- refusals
 
 
