@@ -1176,7 +1176,7 @@ __global__ void __launch_bounds__(kThreads)
 // boundaries (kAligned false) are put together from the aligned pieces that hold
 // them (with two-byte loads the gradient of 3899 x 3205 x 536 took 109 us, so
 // 71); a strip's columns at a row's ends, where such pieces would leave the row,
-// go one by one.  4096 x 4096, tanh gelu: 23 us.
+// go one by one.  4096 x 4096, tanh gelu: 19 us.
 // ---------------------------------------------------------------------------
 constexpr int kDzThreads = 256;
 constexpr int kDzMaxSplits = 8;
@@ -1476,7 +1476,7 @@ int64_t resident_clusters(int splits, int per_sm, int num_sms) {
 // 76 of 4: 44.5, 74 of them 30.3).  A CTA's share of K blocks may be one or none; it
 // still takes its share of the results.  Eight only for a long sum, or the least rows
 // (M x N x K, 4 / 8 CTAs: 64 x 4096 x 4096 11.8 / 12.6 us, 64 x 1024 x 8192 14.8 /
-// 11.0, 1 x 1024 x 8192 12.7 / 9.1, 1 x 4096 x 4096 10.0 / 9.7), and with many rows
+// 11.0, 16 x 2560 x 4096 9.1 / 8.0, 48 x 2560 x 8192 13.7 / 12.8), and with many rows
 // only while there is one CTA per SM (128 x 2560 x 8192 16.3 / 18.1, 128 x 4096 x 8192
 // 17.7 / 19.9, 16 x 4096 x 8192 14.9 / 13.4).
 int few_splits(int64_t units, int num_kb, int64_t m, int num_sms) {
@@ -1542,9 +1542,9 @@ int64_t few_rows_ns(const Mat &m, int num_sms) {
 }
 
 // Whether a product runs as few_rows_kernel: where its tiles, split over K, end
-// sooner than the pairs' (measured, few rows / pairs: 16 x 4096 x 4096 8.9 /
-// 16.3 us, 512 x 512 x 4096 11.1 / 15.7, 100 x 512 x 512 6.7 / 5.2, 512 x 4096 x
-// 1024 12.5 / 7.8).
+// sooner than the pairs' (measured, few rows / pairs: 96 x 4096 x 4096 11.0 /
+// 16.6 us, 512 x 1024 x 8192 15.8 / 27.9, 96 x 512 x 512 6.5 / 5.4, 512 x 4096 x
+// 1024 14.0 / 8.4).
 bool few_rows_form(const Mat &m, int num_sms) {
   return !m.a.strided && m.rows <= 2048 &&
          few_rows_ns(m, num_sms) < pick_width(&m, 1, num_sms).ns;

@@ -1208,11 +1208,12 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t
   const int64_t nvec = valid * (dtype == SGA_BF16 ? 2 : 4) / 16;
   const int chunks = pick_row_chunks(rows, nvec, num_sms);
   // Many short rows: small CTAs, ten per SM (bf16, 5 alternatives, wide / small:
-  // 1000 rows of 6000 ids 13.7 / 8.9 us, 4000 of 20000 64 / 58; 300 of 6000
-  // 5.4 / 6.5, 4096 of 32000 77 / 84), while their shorter ring still leaves few
-  // candidates.
+  // 1000 rows of 6000 ids 14.2 / 8.7 us, 4000 of 20000 66 / 54; 300 of 6000 5.6 /
+  // 6.0, 4096 of 32000 75 / 77), while their shorter ring leaves few candidates: with
+  // many alternatives some rows would overflow the buffer (20: 4096 of 24000 73 / 106,
+  // 600 of 20000 15 / 31).
   const bool small = chunks == 1 && rows > 3 * num_sms && nvec <= 3072 &&
-                     nvec * (top_k > 0 ? top_k : 1) <= 768 * 80;
+                     nvec * (top_k > 0 ? top_k : 1) <= 768 * 48;
   if (dtype == SGA_BF16)
     return small ? launch_rows<true, 64>(logits, rows, ld, shard_start, valid, tokens, top_k,
                                          chunks, num_sms, out, err, stream)
