@@ -294,18 +294,19 @@ __device__ __forceinline__ void box_store_rows(uint8_t *box, __nv_bfloat16 *p, i
         if (r < rows) *q = w;
         q += ld / 2;  // four rows on
       }
-      return;
-    }
+    } else {
 #pragma unroll 2
-    for (int r = lane >> 3; !kAligned && r < 32; r += 4) {
-      unsigned short *q = reinterpret_cast<unsigned short *>(p + r * ld);
-      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
-      const uint4 w = bytes_of(*box_piece(box, r, max(j - 1, 0)), *box_piece(box, r, j), 16 - off);
-      const int e = 2 * j < 16 - off ? j : 56 + j;
-      const unsigned short edge = *box_elem(box, r, e);
-      if (r < rows && (j > 0 || off == 0))
-        *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(q) - off + 16 * j) = w;
-      if (r < rows && off != 0) q[e] = edge;
+      for (int r = lane >> 3; r < 32; r += 4) {
+        unsigned short *q = reinterpret_cast<unsigned short *>(p + r * ld);
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
+        const uint4 w =
+            bytes_of(*box_piece(box, r, max(j - 1, 0)), *box_piece(box, r, j), 16 - off);
+        const int e = 2 * j < 16 - off ? j : 56 + j;
+        const unsigned short edge = *box_elem(box, r, e);
+        if (r < rows && (j > 0 || off == 0))
+          *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(q) - off + 16 * j) = w;
+        if (r < rows && off != 0) q[e] = edge;
+      }
     }
     return;
   }
