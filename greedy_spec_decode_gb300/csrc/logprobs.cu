@@ -1212,8 +1212,9 @@ cudaError_t launch_logprobs(const void *logits, int dtype, int64_t rows, int64_t
   // 6.0, 4096 of 32000 75 / 77), while their shorter ring leaves few candidates: with
   // many alternatives some rows would overflow the buffer (20: 4096 of 24000 73 / 106,
   // 600 of 20000 15 / 31).
-  const bool small = chunks == 1 && rows > 3 * num_sms && nvec <= 3072 &&
-                     nvec * (top_k > 0 ? top_k : 1) <= 768 * 48;
+  constexpr int64_t held = ring_bytes<64> / 16;  // vectors that give the threshold
+  const bool small = chunks == 1 && rows > 3 * num_sms && nvec <= 4 * held &&
+                     nvec * (top_k > 0 ? top_k : 1) <= 48 * held;
   if (dtype == SGA_BF16)
     return small ? launch_rows<true, 64>(logits, rows, ld, shard_start, valid, tokens, top_k,
                                          chunks, num_sms, out, err, stream)
