@@ -128,6 +128,48 @@ def test_activations_over_their_range(sga_lib, M, act):
     check(acc, y64, 2.0 ** -19 * z64.abs().clamp(max=100) + 2.0 ** -8 * y64.abs() + 1e-30, act)
 
 
+def tail_exponent(z, act):
+    """u of the e^-u that an activation's left tail falls with."""
+    if act == "gelu":
+        return z * z / 2
+    if act == "gelu_tanh":
+        return 2 * math.sqrt(2 / math.pi) * (z.abs() + 0.044715 * z.abs() ** 3)
+    return z.abs()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [2, 40, 300, 3000])
+@pytest.mark.parametrize("act", ACTS)
+def test_activation_tails_relative_to_their_values(sga_lib, M, act):
+    """x . I from -12 to 12, where the values fall to 1e-32, and the derivatives
+    (dz . I of an upstream gradient of ones).  Relative to the value, or to the
+    sizes of a derivative's terms: the tails fall as e^-u, whose exponent takes at
+    most eight roundings (u 2^-21), 32 ulps for the rest (2^-19), and one rounding
+    to bf16; 1e-36 for what is flushed below the normal numbers of fp32."""
+    K = 64
+    x = torch.linspace(-12, 12, M * K).reshape(M, K).to(torch.bfloat16).cuda()
+    eye = torch.eye(K, dtype=torch.bfloat16, device="cuda")
+    z = x.double().cpu()
+    y64, d64 = act64(z, act)
+    if act == "gelu_tanh":       # (1 + tanh u) / 2 = 1 / (1 + e^-2u), which does not cancel
+        u = math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+        q = torch.sigmoid(2 * u)
+        y64 = z * q
+        d64 = q + 2 * y64 * torch.sigmoid(-2 * u) * math.sqrt(2 / math.pi) * (
+            1 + 3 * 0.044715 * z * z)
+    rel = 2.0 ** -19 + tail_exponent(z, act) * 2.0 ** -21
+    out = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    sga_lib.sga_linear(x, eye, out, act=ACTS.index(act))
+    check(out, y64, (2.0 ** -8 + rel) * y64.abs() + 1e-36, act)
+    ws = torch.empty(sga_lib.sga_linear_grad_workspace(M, K, K), dtype=torch.uint8, device="cuda")
+    sga_lib.sga_linear_grad(torch.ones_like(out), x, eye, ws, ACTS.index(act),
+                            None if act == "none" else x, grad_x=out)
+    # d = y / z + (d - y / z): the value's factor and z times that factor's slope
+    factor = torch.where(z == 0, 0.5, y64 / torch.where(z == 0, 1.0, z))
+    check(out, d64, 2.0 ** -8 * d64.abs() + rel * (factor.abs() + (d64 - factor).abs()) + 1e-36,
+          act + " derivative")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M", [4, 200])
 def test_runs_are_identical_on_any_stream_and_in_a_graph(sga_lib, M):
