@@ -456,9 +456,18 @@ def _check_out(t, dtype, numel, name):
 
 
 def _on_gpu(*tensors):
+    """Tensors of the current device, on whose stream the calls run."""
+    here = None
     for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("CUDA tensors are needed")
+        if t is None:
+            continue
+        at = t.get_device()      # -1: host memory
+        if at != here:
+            if at < 0:
+                raise ValueError("CUDA tensors are needed")
+            if here is not None or at != _current_device():
+                raise ValueError("CUDA tensors of the current device are needed")
+            here = at
 
 
 def _logits_2d(logits):

@@ -475,3 +475,39 @@ def test_binding_refuses_host_tensors(sga_lib):
         sga_lib.sga_linear(x, w, y)
     with pytest.raises(ValueError, match="CUDA"):
         sga_lib.sga_linear_grad(y, x, w, torch.zeros(40), grad_x=torch.zeros(3, 64, dtype=b))
+
+
+def test_binding_refuses_tensors_of_another_device(sga_lib, monkeypatch):
+    class Tensor:
+        is_cuda = True
+
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+    monkeypatch.setattr(sga_lib, "_current_device", lambda: 1)
+    sga_lib._on_gpu(None, Tensor(1), None, Tensor(1))
+    for other in (0, 2):
+        with pytest.raises(ValueError, match="current"):
+            sga_lib._on_gpu(Tensor(1), None, Tensor(other))
+
+
+@pytest.mark.gpu
+def test_calls_refuse_tensors_of_another_device(sga_lib, monkeypatch):
+    """Their kernels run on the current device's stream: nothing is launched."""
+    b = torch.bfloat16
+    x, w, y = (torch.zeros(s, dtype=b, device="cuda") for s in ((3, 64), (5, 64), (3, 5)))
+    f, t = torch.zeros(3, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    parts = torch.zeros(1, 3, 4, device="cuda")
+    ws = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    monkeypatch.setattr(sga_lib, "_current_device", lambda: 1)
+    for call in (lambda: sga_lib.sga_linear(x, w, y),
+                 lambda: sga_lib.sga_linear_grad(y, x, w, ws, grad_x=x.clone()),
+                 lambda: sga_lib.sga_token_logprobs(y, 5, t, f),
+                 lambda: sga_lib.sga_local_logprobs(y, 0, 5, 5, t, parts[0]),
+                 lambda: sga_lib.sga_logprob_reduce(parts, None, 1, t, f),
+                 lambda: sga_lib.sga_token_logprobs_grad(y, 0, 5, t, f, f, f, y.clone())):
+        with pytest.raises(ValueError, match="current"):
+            call()
