@@ -28,7 +28,7 @@
 // Every mbarrier wait is bounded in time; on expiry the CTA records
 // SGA_DEVERR_TIMEOUT, stops issuing work, waits (bounded) for its own copies
 // and MMAs in flight, frees its TMEM and exits.
-#include "tcgen05.cuh"
+#include "pipe.cuh"
 
 namespace sga {
 namespace {
@@ -435,20 +435,48 @@ __global__ void lmhead_finalize_kernel(const sga_stat *__restrict__ ws, int M, i
   }
 }
 
-// Self-test of the bounded wait: one thread waits on an mbarrier that nothing
-// ever arrives at; the wait gives up after limit_ns, the kernel records
-// SGA_DEVERR_TIMEOUT and returns, and the context stays usable.
+// Self-test of the bounded waits, on an mbarrier that nothing ever arrives at: a
+// thread in mbar_wait and a warp in warp_wait give up after limit_ns; the warp
+// then raises the abort flag, on which another, whose limit is kWaitLimitNs,
+// leaves.  The kernel records SGA_DEVERR_TIMEOUT if all three gave up and none
+// before limit_ns, and returns; the context stays usable.
 __global__ void selftest_timeout_kernel(unsigned long long limit_ns, uint32_t *err,
                                         unsigned long long *waited_ns) {
   __shared__ __align__(8) uint64_t bar;
-  __shared__ int no_abort;
-  if (threadIdx.x != 0) return;
-  no_abort = 0;
-  mbar_init(smem_u32(&bar), 1);
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __shared__ int no_abort, raised;
+  __shared__ uint32_t word;
+  __shared__ unsigned long long waited[3];  // 0: the wait did not give up
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    no_abort = raised = 0;
+    word = 0;
+    mbar_init(smem_u32(&bar), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
   const unsigned long long t0 = global_timer_ns();
-  if (!mbar_wait(smem_u32(&bar), 0, &no_abort, limit_ns)) atomicOr(err, SGA_DEVERR_TIMEOUT);
-  if (waited_ns) *waited_ns = global_timer_ns() - t0;
+  bool done = true;
+  if (warp == 0) {
+    if (lane == 0) done = mbar_wait(smem_u32(&bar), 0, &no_abort, limit_ns);
+  } else if (warp == 1) {
+    done = warp_wait(smem_u32(&bar), 0, &no_abort, limit_ns);
+  } else {
+    done = warp_wait(smem_u32(&bar), 0, &raised);
+  }
+  if (lane == 0) {
+    waited[warp] = done ? 0 : global_timer_ns() - t0;
+    if (warp == 1 && !done) raise_abort(&raised, &word);
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  unsigned long long most = 0;
+  bool all = true;
+  for (int i = 0; i < 3; ++i) {
+    most = waited[i] > most ? waited[i] : most;
+    all = all && waited[i] >= limit_ns;
+  }
+  if (all) atomicOr(err, word);
+  if (waited_ns) *waited_ns = most;
 }
 
 // Number of 2-CTA clusters of the 2-SM kernel that fit on the current device
@@ -513,7 +541,7 @@ cudaError_t launch_gemm_2sm(const void *hidden, int64_t M, int64_t H, const void
 
 cudaError_t launch_selftest_timeout(unsigned long long limit_ns, uint32_t *err,
                                     unsigned long long *waited_ns, cudaStream_t stream) {
-  selftest_timeout_kernel<<<1, 32, 0, stream>>>(limit_ns, err, waited_ns);
+  selftest_timeout_kernel<<<1, 96, 0, stream>>>(limit_ns, err, waited_ns);
   return cudaGetLastError();
 }
 

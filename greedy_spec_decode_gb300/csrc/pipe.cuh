@@ -11,7 +11,8 @@ namespace {
 // Bounded wait (as mbar_wait) that sleeps in the barrier unit (try_wait with a
 // time hint) between looks at the clock and the abort flag.
 __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity,
-                                          const volatile int *abort_flag) {
+                                          const volatile int *abort_flag,
+                                          unsigned long long limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   unsigned long long t0 = 0;
   while (true) {
@@ -27,14 +28,15 @@ __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity,
     if (*abort_flag) return false;
     const unsigned long long t = global_timer_ns();
     if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitLimitNs) return false;
+    if (t - t0 > limit_ns) return false;
   }
 }
 
 // The same, agreed on by the whole (converged) warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
-                                          const volatile int *abort_flag) {
-  return __all_sync(0xffffffffu, pipe_wait(bar, parity, abort_flag)) != 0;
+                                          const volatile int *abort_flag,
+                                          unsigned long long limit_ns = kWaitLimitNs) {
+  return __all_sync(0xffffffffu, pipe_wait(bar, parity, abort_flag, limit_ns)) != 0;
 }
 
 // True in one lane of a converged warp.  Producer and MMA warps run their

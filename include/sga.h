@@ -652,13 +652,15 @@ int sga_device_error(uint32_t *out_word);
 int sga_clear_device_error(void);
 
 /*
- * sga_selftest_wait_timeout -- exercises the bounded-wait path that every
- * pipelined kernel of this library uses (the pages have no counterpart): one
- * thread waits on a shared-memory mbarrier that nothing arrives at; after
- * limit_ns (1 us .. 1 s) the wait gives up, SGA_DEVERR_TIMEOUT is OR-ed into
- * the device error word and the kernel returns normally.  waited_ns (device,
- * nullable, 8-byte aligned) receives the time the wait took.  The context stays
- * usable: no trap, no fault.
+ * sga_selftest_wait_timeout -- exercises the bounded waits that the
+ * pipelined kernels of this library use (the pages have no counterpart): a
+ * thread and a warp, in the two forms of the wait, wait on a shared-memory
+ * mbarrier that nothing arrives at; after limit_ns (1 us .. 1 s) they give up,
+ * and a second warp leaves its wait on the abort flag that the first raises.
+ * If all did, none before limit_ns, SGA_DEVERR_TIMEOUT is OR-ed into the device
+ * error word; the kernel returns normally.  waited_ns (device, nullable, 8-byte
+ * aligned) receives the time the longest wait took.  The context stays usable:
+ * no trap, no fault.
  */
 int sga_selftest_wait_timeout(uint64_t limit_ns, uint64_t *waited_ns, sga_stream stream);
 
