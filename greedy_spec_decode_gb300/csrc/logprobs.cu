@@ -225,7 +225,9 @@ __device__ __forceinline__ Lse sums_total(const ThreadSums &a) {
 // only has to stay within 2^12 of the maximum).
 __device__ __forceinline__ void sums_rebase(ThreadSums &a, float m) {
   if (!(m > a.limit)) return;
-  const float r = m * kLog2e;
+  // (rounded by itself: were it contracted into the difference below, the sums so far
+  // would be restated to the unrounded reference, up to 2^0.03 off at 5e5)
+  const float r = __fmul_rn(m, kLog2e);
   if (a.limit > kUnset) {
     const Lse b = sums_total(a);
     const float d = a.r - r, f = ex2(d);

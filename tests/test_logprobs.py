@@ -195,6 +195,33 @@ def test_logprobs_match_64_bits(sga_lib, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("offset", [0.0, -1e4, 1e5, -4.9e5, 4.9e5, 3e6])
+@pytest.mark.parametrize("rows,vocab,shards", [(1, 40000, 1), (60, 40000, 1), (955, 5455, 1),
+                                               (40, 5455, 3)])
+def test_entropy_of_rows_far_from_zero(sga_lib, rows, vocab, shards, offset):
+    """The entropy does not depend on where the logits lie.  Sixteen ulps of the
+    sum of 2^t and as many of the sum of t 2^t (2e-6 each), relative to a size of
+    1 + log(vocab) at most."""
+    x = torch.from_numpy(wl.normal_matrix(vocab + rows, rows, vocab, 3.0, dtype="f32")).cuda()
+    x += offset
+    ent, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    if shards == 1:
+        sga_lib.sga_token_logprobs(x, vocab, None, None, ent, lse)
+    else:
+        parts = torch.empty((shards, rows, 4), device="cuda")
+        for s, (o, w) in enumerate(wl.even_shards(vocab, shards)):
+            sga_lib.sga_local_logprobs(x[:, o:o + w], o, w, vocab, None, parts[s])
+        sga_lib.sga_logprob_reduce(parts, None, shards, None, None, ent, lse)
+    m = x.amax(1, keepdim=True).double()
+    d = x.double() - m
+    total = torch.logsumexp(d, 1, keepdim=True)
+    exp = -(torch.exp(d - total) * (d - total)).sum(1)
+    assert ((ent.double() - exp).abs() <= 4e-6 * (1 + math.log(vocab))).all()
+    want = (m + total)[:, 0]
+    assert ((lse.double() - want).abs() <= 4e-6 * (1 + math.log(vocab)) + 2.0 ** -23 * want.abs()).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shards", [1, 2, 5])
 @pytest.mark.parametrize("case", [CASES[4], CASES[6], CASES[8], CASES[3]], ids=str)
 def test_sharded_parts_reduce_to_the_same(sga_lib, case, shards):
