@@ -535,6 +535,8 @@ def sga_logprob_reduce(parts, tops, num_shards, tokens=None, out_logprob=None, o
     [num_shards, rows, 4]) and lists (int32 [num_shards, rows, top_k, 2] or
     None)."""
     num_shards = int(num_shards)
+    if num_shards < 1:
+        raise ValueError("num_shards must be at least 1")
     rows = parts.numel() // (4 * num_shards)
     k, (tok, *outs) = _row_outputs(rows, tokens, out_logprob, out_entropy, out_lse, out_top_ids,
                                    out_top_logprobs)

@@ -630,3 +630,10 @@ def test_binding_refuses_host_tensors(sga_lib):
         sga_lib.sga_logprob_reduce(torch.zeros(1, 3, 4), None, 1, i32, f32)
     with pytest.raises(ValueError, match="CUDA"):
         sga_lib.sga_token_logprobs_grad(x, 0, 8, i32, f32, f32, f32, torch.zeros(3, 8))
+
+
+def test_binding_refuses_numbers_of_shards_below_one(sga_lib):
+    parts, f32 = torch.zeros(2, 3, 4), torch.zeros(3)
+    for n in (0, -1):
+        with pytest.raises(ValueError, match="num_shards"):
+            sga_lib.sga_logprob_reduce(parts, None, n, None, f32)
