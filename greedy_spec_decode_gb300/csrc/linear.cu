@@ -11,16 +11,17 @@
 // either into 128-byte swizzled tiles and the matrix descriptor tells the
 // tensor core which way they run, so nothing is transposed in memory.
 //   gemm_kernel      CTA pairs (cta_group::2), 256 x 256 / 128 / 64 tiles,
-//                    persistent.  Tensor-bound: 4096 x 8192 x 4096 140.5 us =
-//                    1.96 PFLOP/s (cuBLAS, without an epilogue, 136 to 142 us in
-//                    the same processes); the gradient of 4096^3 without an
-//                    activation 147 us.
+//                    persistent.  Tensor-bound, in runs too short for the power
+//                    cap: 4096 x 8192 x 4096 without an epilogue 140.5 us = 1.96
+//                    PFLOP/s (cuBLAS 136 to 142 us in the same processes; after a
+//                    second of load 165, cuBLAS 150 to 160); the gradient of 4096^3
+//                    without an activation 147 us.
 //   few_rows_kernel  few rows or tiles: the weight is the MMA's 128-row operand
 //                    and a cluster splits the summed dimension, joined through
 //                    distributed shared memory.  Bound by the weight's stream and
 //                    the join: 96 x 8192 x 4096 16.5 us, weight from HBM.
 //   dot_kernel       at most four rows, on CUDA cores.  HBM- and latency-bound:
-//                    1 x 4096 x 4096 7.0 us, 1 x 152064 x 2048 85.5 us = 7.3 TB/s.
+//                    1 x 4096 x 4096 7.0 us in a graph, 1 x 152064 x 2048 85.5 us = 7.3 TB/s.
 //   dz_kernel        dz and db, HBM-bound.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -116,12 +117,6 @@ __device__ __forceinline__ float ld_bias(const void *bias, int f32, int64_t c) {
   if (bias == nullptr) return 0.0f;
   return f32 ? static_cast<const float *>(bias)[c]
              : ld_bf16(static_cast<const __nv_bfloat16 *>(bias) + c);
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // What happens to an accumulator: out[r, c] = act(acc + bias[c]) + res[r, c],
@@ -283,21 +278,6 @@ __device__ __forceinline__ void tile_at(const Product &p, int t, int &tr, int &t
 // by 350 to 750 cycles, the eight 16-byte stores a lane by about 250.)
 __device__ __forceinline__ uint4 *box_piece(uint8_t *box, int r, int j) {
   return reinterpret_cast<uint4 *>(box + r * ROW_BYTES + ((j ^ (r & 7)) << 4));
-}
-
-// Bytes s .. s + 15 (s even, 0 .. 16) of two 16-byte pieces in a row.
-__device__ __forceinline__ uint4 bytes_of(const uint4 a, const uint4 b, int s) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = (s & 8) ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = (s & 4) ? w[i + 1] : w[i];
-  uint4 r;
-  r.x = __funnelshift_r(w[0], w[1], (s & 2) * 8);
-  r.y = __funnelshift_r(w[1], w[2], (s & 2) * 8);
-  r.z = __funnelshift_r(w[2], w[3], (s & 2) * 8);
-  r.w = __funnelshift_r(w[3], w[4], (s & 2) * 8);
-  return (s & 16) ? b : r;
 }
 
 __device__ __forceinline__ unsigned short *box_elem(uint8_t *box, int r, int c) {
@@ -1182,7 +1162,10 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---------------------------------------------------------------------------
 // dz = g * act'(z) in bf16 (dz nullable) and db = the column sums of dz in
-// fp32, before the rounding (db nullable).  HBM-bound: g and z are read once
+// fp32, before the rounding (db nullable).  dz is rounded because the tensor cores
+// take 16 bits from both operands: the products' error in the 2-norm is 0.0023, of
+// which the rounding of the results alone is 0.0017; a second product of what the
+// rounding leaves out would take the tensor time twice.  HBM-bound: g and z are read once
 // and dz written once.  A cluster covers a strip of columns, its CTAs
 // contiguous ranges of rows; their column sums meet in the first CTA through
 // distributed shared memory, in a fixed order, so db needs no second launch.

@@ -130,7 +130,7 @@ struct PieceShared {
   uint64_t full[kRing], empty[kRing];
   int abort, num_vecs, num_keys;
   uint32_t threshold;
-  float max, sum, wsum;
+  float sum, wsum;
   Stats piece[kMaxChunks];  // the row's pieces, in its first CTA
   Lse warp_lse[kMaxWarps];
   float warp_max[kMaxWarps];
@@ -1013,12 +1013,6 @@ __device__ __forceinline__ void store_elem(char *p, int j, float v) {
     reinterpret_cast<float *>(p)[j] = v;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 template <bool kBf16>
 __device__ __forceinline__ float read_elem(const char *p, int j) {  // the buffer may be the output
   if (kBf16)
@@ -1121,27 +1115,15 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (v + u * kThreads >= ve) continue;
-      uint32_t wd[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-      if (kShift && offset != 0) {
-        uint32_t w[8] = {q[u].x, q[u].y, q[u].z, q[u].w, q1[u].x, q1[u].y, q1[u].z, q1[u].w};
-        if (offset & 8) {
-#pragma unroll
-          for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-        }
-        if (offset & 4) {
-#pragma unroll
-          for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) wd[i] = __funnelshift_r(w[i], w[i + 1], (offset & 2) * 8);
-      }
+      const uint4 xq = kShift && offset != 0 ? bytes_of(q[u], q1[u], offset) : q[u];
+      uint32_t wd[4] = {xq.x, xq.y, xq.z, xq.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (!live) {
           wd[i] = 0u;
         } else if (kBf16) {
-          wd[i] = pack_bf16(grad_term(bf16_lo(wd[i]), lse, a, bh, b),
-                            grad_term(bf16_hi(wd[i]), lse, a, bh, b));
+          wd[i] = pack2(grad_term(bf16_lo(wd[i]), lse, a, bh, b),
+                        grad_term(bf16_hi(wd[i]), lse, a, bh, b));
         } else {
           wd[i] = __float_as_uint(grad_term(__uint_as_float(wd[i]), lse, a, bh, b));
         }

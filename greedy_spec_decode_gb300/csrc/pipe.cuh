@@ -1,6 +1,7 @@
 // pipe.cuh -- pieces shared by linear.cu and logprobs.cu: bounded mbarrier waits
-// that sleep in the barrier unit, single-lane issue from a converged warp, and
-// paired fp32 arithmetic.
+// that sleep in the barrier unit, single-lane issue from a converged warp, paired
+// fp32 arithmetic, and bf16 pairs and byte shifts of 16-byte pieces.  (The
+// self-test of the waits in lmhead.cu runs them out.)
 #pragma once
 
 #include "tcgen05.cuh"
@@ -84,6 +85,28 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// Two values rounded to bf16, lo in the low half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Bytes s .. s + 15 (s even, 0 .. 16) of two 16-byte pieces that follow each other.
+__device__ __forceinline__ uint4 bytes_of(const uint4 a, const uint4 b, int s) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = (s & 8) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = (s & 4) ? w[i + 1] : w[i];
+  uint4 r;
+  r.x = __funnelshift_r(w[0], w[1], (s & 2) * 8);
+  r.y = __funnelshift_r(w[1], w[2], (s & 2) * 8);
+  r.z = __funnelshift_r(w[2], w[3], (s & 2) * 8);
+  r.w = __funnelshift_r(w[3], w[4], (s & 2) * 8);
+  return (s & 16) ? b : r;
 }
 
 // Untiled copy of global memory into shared memory (16-byte aligned, size a

@@ -1,5 +1,6 @@
 // tcgen05.cuh -- pieces shared by the LM-head kernels (lmhead.cu: the 2-SM
-// GEMM kernel, lmhead_decode.cu: the decode-size kernels): tile and
+// GEMM kernel, lmhead_decode.cu: the decode-size kernels) and, through
+// pipe.cuh, by linear.cu and logprobs.cu: tile and
 // thread constants, inline PTX for mbarriers, TMA (cp.async.bulk.tensor),
 // tcgen05 fences, shared-memory matrix descriptors, the MMA instruction
 // descriptor and tensor-memory loads, and the host-side tensor-map encoding,
