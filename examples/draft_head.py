@@ -25,7 +25,8 @@ import greedy_spec_decode_gb300 as sga  # noqa: E402
 class DraftHead:
     """weight: bf16 [H, H], bias: float32 [H], lm_weight: bf16 [V, H] (ids past
     org_vocab are padding); at most max_rows rows a call.  Buffers are kept, so
-    the calls can be captured in a CUDA graph."""
+    the calls can be captured in a CUDA graph; what a call returns lies in them
+    and holds until the next call."""
 
     def __init__(self, weight, bias, lm_weight, max_rows, top_k=5, org_vocab=None):
         self.weight, self.bias, self.lm_weight = weight, bias, lm_weight

@@ -22,7 +22,7 @@
 //                    the join: 96 x 8192 x 4096 16.5 us, weight from HBM.
 //   dot_kernel       at most four rows, on CUDA cores.  HBM- and latency-bound:
 //                    1 x 4096 x 4096 7.0 us in a graph, 1 x 152064 x 2048 85.5 us = 7.3 TB/s.
-//   dz_kernel        dz and db, HBM-bound.
+//   dz_kernel        dz and db, 81 % of the copy rate.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -1165,8 +1165,9 @@ __global__ void __launch_bounds__(kThreads)
 // fp32, before the rounding (db nullable).  dz is rounded because the tensor cores
 // take 16 bits from both operands: the products' error in the 2-norm is 0.0023, of
 // which the rounding of the results alone is 0.0017; a second product of what the
-// rounding leaves out would take the tensor time twice.  HBM-bound: g and z are read once
-// and dz written once.  A cluster covers a strip of columns, its CTAs
+// rounding leaves out would take the tensor time twice.  g and z are read once and dz
+// written once: 8192 x 8192 73 us, 5.5 TB/s of a copy's 6.8, with four rows in flight a
+// thread and 44 % of the warps.  A cluster covers a strip of columns, its CTAs
 // contiguous ranges of rows; their column sums meet in the first CTA through
 // distributed shared memory, in a fixed order, so db needs no second launch.
 // A strip has 64 columns, or 32 or 16 where that leaves SMs idle; a thread takes

@@ -55,10 +55,11 @@ __device__ __forceinline__ void lse_restate(Lse &a, float r) {
 
 // ---------------------------------------------------------------- forward
 // HBM-bound, with little issue to spare: 4096 x 202048 bf16 231 us without
-// alternatives (7.15 TB/s), 265 with 5, 310 with 20; one row of
-// 152064 3.8 us without and 7.7 with 20, latency.  The 2^x of every logit and the
-// packed fp32 sums take 65 % of the issue slots, which is why the reference is
-// only moved when it has to be and candidates are tested a vector at a time.
+// alternatives (7.2 TB/s), 265 with 5, 308 with 20; 2048 x 202048 fp32 229, 239,
+// 345; one row of 152064 3.8 us without and 7.7 with 20, latency.  The 2^x of every
+// logit and the packed fp32 sums take 65 % of the issue slots, which is why the
+// reference is only moved when it has to be and candidates are tested a vector at a
+// time.
 //
 // A row is read once through a shared-memory ring (cp.async.bulk by a copy
 // warp; the row's unaligned ends element by element), three stages of 16 KB in
