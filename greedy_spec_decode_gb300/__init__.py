@@ -28,6 +28,7 @@ SGA_F32, SGA_BF16 = 0, 1
 SGA_MAX_K = 15
 SGA_MAX_VOCAB = 1 << 24
 SGA_MAX_TOP = 32
+SGA_MAX_TEACHER = 128
 SGA_ACT_NONE, SGA_ACT_RELU, SGA_ACT_SILU, SGA_ACT_GELU, SGA_ACT_GELU_TANH = 0, 1, 2, 3, 4
 SGA_DEVERR_K_RANGE, SGA_DEVERR_D2T_RANGE, SGA_DEVERR_TIMEOUT, SGA_DEVERR_LAYOUT = 1, 2, 4, 8
 
@@ -83,6 +84,13 @@ def lib():
             "sga_logprob_reduce": ([vp, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp], i32),
             "sga_token_logprobs_grad": ([vp, i32, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp,
                                          i32, vp, vp, vp, i64, vp], i32),
+            "sga_probs": ([vp, i32, i64, i64, i64, i64, vp, vp, i64, vp], i32),
+            "sga_sampled_verify": ([vp, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, vp, i32, vp,
+                                    vp, vp, vp, vp], i32),
+            "sga_distill": ([vp, i32, i64, i64, i64, i64, vp, vp, i32, vp, ctypes.c_float, vp,
+                             vp, vp, vp, vp, i64, vp], i32),
+            "sga_distill_grad": ([vp, i32, i64, i64, i64, i64, vp, vp, i32, vp, ctypes.c_float,
+                                  vp, vp, vp, vp, i64, vp], i32),
             "sga_device_error": ([ctypes.POINTER(ctypes.c_uint32)], i32),
             "sga_clear_device_error": ([], i32),
             "sga_selftest_wait_timeout": ([ctypes.c_uint64, vp, vp], i32),
@@ -575,6 +583,128 @@ def sga_token_logprobs_grad(logits, shard_start, org_vocab, tokens, lse, entropy
         _check_out(top_ids, i32, rows * k, "top_ids"),
         _check_out(grad_top, f32, rows * k, "grad_top"), out_grad.data_ptr(), ldg,
         _raw_stream(stream)))
+    return out_grad
+
+
+def _probs_2d(t, name):
+    """(rows, columns, row stride, address) of fp32 probabilities."""
+    if t.dtype is not _F32 or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D float32 tensor")
+    rows, width = t.shape
+    ld, col = t.stride()
+    if col != 1 and width > 1:
+        raise ValueError(f"{name} must have unit stride along the vocab")
+    return rows, width, ld if rows > 1 else max(ld, width), t.data_ptr()
+
+
+def sga_probs(logits, org_vocab, out_probs, temperature=None, stream=None):
+    """Probabilities of logits rows at a temperature (float32 [rows], 0 = one at
+    the argmax; None = 1).  logits: 2-D, unit stride along the vocab; out_probs:
+    float32 of the same shape, or float32 logits themselves; ids past org_vocab
+    get 0 (see include/sga.h)."""
+    rows, width, ld, code = _logits_2d(logits)
+    out_rows, out_width, ldp, out = _probs_2d(out_probs, "out_probs")
+    if out_rows != rows or out_width != width:
+        raise ValueError("out_probs must have the shape of logits")
+    _on_gpu(logits, out_probs, temperature)
+    _check("sga_probs", lib().sga_probs(
+        logits.data_ptr(), code, rows, ld, width, int(org_vocab),
+        _check_out(temperature, _F32, rows, "temperature"), out, ldp, _raw_stream(stream)))
+    return out_probs
+
+
+def sga_sampled_verify(target_probs, draft_probs, cu_num_draft, draft_tokens, accept_u, sample_u,
+                       max_k, out_sampled, out_num_sampled, out_num_rejected, out_last,
+                       in_prefill=None, stream=None):
+    """Verification of drafted tokens by rejection sampling.  target_probs:
+    float32 [D + num_reqs, vocab] (rows as sga_greedy_verify's), draft_probs:
+    float32 [D, vocab], or None for drafts without probabilities; draft_tokens
+    int32 [D], accept_u float32 [D], sample_u float32 [num_reqs] (uniform in
+    [0, 1)); in_prefill: uint8 / bool [num_reqs] or None.  Outputs: int32
+    [num_reqs, max_k + 1] and int32 [num_reqs] (see include/sga.h)."""
+    rows, vocab, ldt, target = _probs_2d(target_probs, "target_probs")
+    n, max_k = cu_num_draft.numel() - 1, int(max_k)
+    drafts = rows - n
+    if n < 0 or drafts < 0:
+        raise ValueError("target_probs must have a row per draft and one per request")
+    ldd, draft = 0, None
+    if draft_probs is not None:
+        d_rows, d_width, ldd, draft = _probs_2d(draft_probs, "draft_probs")
+        if d_rows != drafts or d_width != vocab:
+            raise ValueError("draft_probs must have a row per draft, as wide as target_probs")
+        if drafts == 0:
+            draft = None
+    if in_prefill is not None and in_prefill.dtype not in (torch.uint8, torch.bool):
+        raise ValueError("in_prefill must be a uint8 or bool tensor")
+    f32, i32 = _F32, _I32
+    _on_gpu(target_probs, draft_probs, cu_num_draft, draft_tokens, accept_u, sample_u,
+            out_sampled, out_num_sampled, out_num_rejected, out_last, in_prefill)
+    _check("sga_sampled_verify", lib().sga_sampled_verify(
+        target, rows, ldt, draft, ldd, vocab, n,
+        _check_out(cu_num_draft, i32, n + 1, "cu_num_draft"),
+        _check_out(draft_tokens, i32, drafts, "draft_tokens"),
+        _check_out(in_prefill, in_prefill.dtype, n, "in_prefill")
+        if in_prefill is not None else None,
+        _check_out(accept_u, f32, drafts, "accept_u"), _check_out(sample_u, f32, n, "sample_u"),
+        max_k, _check_out(out_sampled, i32, n * (max_k + 1), "out_sampled"),
+        _check_out(out_num_sampled, i32, n, "out_num_sampled"),
+        _check_out(out_num_rejected, i32, n, "out_num_rejected"),
+        _check_out(out_last, i32, n, "out_last"), _raw_stream(stream)))
+
+
+def _teacher_lists(rows, teacher_ids, teacher_logits, teacher_lse):
+    """Addresses of a teacher's lists, and k."""
+    k = teacher_ids.size(-1)
+    return (_check_out(teacher_ids, _I32, rows * k, "teacher_ids"),
+            _check_out(teacher_logits, _F32, rows * k, "teacher_logits"), k,
+            _check_out(teacher_lse, _F32, rows, "teacher_lse"))
+
+
+def _grad_2d(logits, out_grad, rows, width):
+    """Address and row stride of a gradient like logits."""
+    if out_grad is None:
+        return None, 0
+    if out_grad.dtype != logits.dtype or out_grad.shape != logits.shape or (
+            width > 1 and out_grad.stride(1) != 1):
+        raise ValueError("out_grad must match logits, unit stride along the vocab")
+    return out_grad.data_ptr(), out_grad.stride(0) if rows > 1 else max(out_grad.stride(0), width)
+
+
+def sga_distill(logits, org_vocab, teacher_ids, teacher_logits, out_loss=None, teacher_lse=None,
+                temperature=1.0, out_lse=None, out_lse_rest=None, grad_loss=None, out_grad=None,
+                stream=None):
+    """Divergence of each row of a draft model's logits from a teacher's top
+    logits: teacher_ids int32 / teacher_logits float32 [rows, k] (-1: no entry),
+    teacher_lse float32 [rows], or None for the list by itself.  out_loss,
+    out_lse, out_lse_rest: float32 [rows] or None; out_grad: the gradient with
+    respect to logits times grad_loss (float32 [rows] or None), like logits, or
+    logits itself, or None (see include/sga.h)."""
+    rows, width, ld, code = _logits_2d(logits)
+    lists = _teacher_lists(rows, teacher_ids, teacher_logits, teacher_lse)
+    grad, ldg = _grad_2d(logits, out_grad, rows, width)
+    f32 = _F32
+    _on_gpu(logits, teacher_ids, teacher_logits, teacher_lse, out_loss, out_lse, out_lse_rest,
+            grad_loss, out_grad)
+    _check("sga_distill", lib().sga_distill(
+        logits.data_ptr(), code, rows, ld, width, int(org_vocab), *lists, float(temperature),
+        _check_out(out_loss, f32, rows, "out_loss"), _check_out(out_lse, f32, rows, "out_lse"),
+        _check_out(out_lse_rest, f32, rows, "out_lse_rest"),
+        _check_out(grad_loss, f32, rows, "grad_loss"), grad, ldg, _raw_stream(stream)))
+
+
+def sga_distill_grad(logits, org_vocab, teacher_ids, teacher_logits, lse, lse_rest, out_grad,
+                     teacher_lse=None, temperature=1.0, grad_loss=None, stream=None):
+    """Gradient of sga_distill from the lse and lse_rest (float32 [rows]) that
+    it gave; lse_rest may be None without teacher_lse.  out_grad: like logits, or
+    logits itself."""
+    rows, width, ld, code = _logits_2d(logits)
+    lists = _teacher_lists(rows, teacher_ids, teacher_logits, teacher_lse)
+    grad, ldg = _grad_2d(logits, out_grad, rows, width)
+    _on_gpu(logits, teacher_ids, teacher_logits, teacher_lse, lse, lse_rest, grad_loss, out_grad)
+    _check("sga_distill_grad", lib().sga_distill_grad(
+        logits.data_ptr(), code, rows, ld, width, int(org_vocab), *lists, float(temperature),
+        _check_out(lse, _F32, rows, "lse"), _check_out(lse_rest, _F32, rows, "lse_rest"),
+        _check_out(grad_loss, _F32, rows, "grad_loss"), grad, ldg, _raw_stream(stream)))
     return out_grad
 
 

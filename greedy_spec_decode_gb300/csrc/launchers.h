@@ -137,6 +137,37 @@ cudaError_t launch_logprobs_grad(const void *logits, int dtype, int64_t rows, in
                                  const int32_t *top_ids, const float *g_top, void *grad,
                                  int64_t ldg, cudaStream_t stream);
 
+// Probabilities at a temperature (probs.cu).
+cudaError_t launch_probs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t width,
+                         int64_t valid, const float *temperature, float *probs, int64_t ldp,
+                         int num_sms, uint32_t *err, cudaStream_t stream);
+
+// Verification by rejection sampling (sampled_verify.cu).
+cudaError_t launch_sampled_verify(const float *target, int64_t rows, int64_t ldt,
+                                  const float *draft, int64_t ldd, int64_t vocab, int num_reqs,
+                                  const int32_t *cu_num_draft, const int32_t *draft_tokens,
+                                  const uint8_t *in_prefill, const float *accept_u,
+                                  const float *sample_u, int max_k, int32_t *out_sampled,
+                                  int32_t *out_num_sampled, int32_t *out_num_rejected,
+                                  int32_t *out_last, int num_sms, uint32_t *err,
+                                  cudaStream_t stream);
+
+// Divergence from a teacher's top logits and its gradient (distill.cu).  With
+// `in_lse` set only the gradient, from those sums.
+struct DistillArgs {
+  const int32_t *ids;
+  const float *logits, *lse;  // the teacher's
+  int k;
+  float temperature;
+  float *out_loss, *out_lse, *out_lse_rest;
+  const float *in_lse, *in_lse_rest;  // the row's, from the forward pass
+  const float *grad_loss;
+  void *grad;
+};
+cudaError_t launch_distill(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t width,
+                           int64_t valid, const DistillArgs &args, int64_t ldg, int num_sms,
+                           uint32_t *err, cudaStream_t stream);
+
 // Bounded-wait self-test (lmhead.cu).
 cudaError_t launch_selftest_timeout(unsigned long long limit_ns, uint32_t *err,
                                     unsigned long long *waited_ns, cudaStream_t stream);

@@ -13,7 +13,6 @@
 // are restated relative to that maximum (sga_logprob_part), which is how CTAs
 // and vocab shards are joined.
 #include <cooperative_groups.h>
-#include <cuda_bf16.h>
 
 #include "pipe.cuh"
 #include "scan.cuh"
@@ -1004,23 +1003,6 @@ struct GradIn {
 __device__ __forceinline__ float grad_term(float x, float lse, float a, float bh, float b) {
   const float lp = max_nan(x - lse, -256.0f);  // p is 0 from there on: times a finite factor
   return ex2(lp * kLog2e) * fmaf(b, lp, fmaf(b, bh, a));
-}
-
-template <bool kBf16>
-__device__ __forceinline__ void store_elem(char *p, int j, float v) {
-  if (kBf16)
-    reinterpret_cast<__nv_bfloat16 *>(p)[j] = __float2bfloat16_rn(v);
-  else
-    reinterpret_cast<float *>(p)[j] = v;
-}
-
-template <bool kBf16>
-__device__ __forceinline__ float read_elem(const char *p, int j) {  // the buffer may be the output
-  if (kBf16)
-    return __uint_as_float(static_cast<uint32_t>(
-                               reinterpret_cast<const volatile unsigned short *>(p)[j])
-                           << 16);
-  return reinterpret_cast<const volatile float *>(p)[j];
 }
 
 // kShift: some rows of the logits and of the gradient lie at different 16-byte

@@ -1,7 +1,10 @@
 // scan.cuh -- element and 16-byte-vector steps of the argmax scan over a
 // contiguous run of logits (fp32 or bf16), shared by the per-shard kernel
-// (argmax.cu) and the block-granular kernel (blocks.cu).
+// (argmax.cu) and the block-granular kernel (blocks.cu), and single elements of
+// rows that are read and written (logprobs.cu, probs.cu, distill.cu).
 #pragma once
+
+#include <cuda_bf16.h>
 
 #include "common.cuh"
 
@@ -16,6 +19,23 @@ __device__ __forceinline__ float load_elem(const char *p, int j) {
   } else {
     return __ldg(reinterpret_cast<const float *>(p) + j);
   }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void store_elem(char *p, int j, float v) {
+  if (kBf16)
+    reinterpret_cast<__nv_bfloat16 *>(p)[j] = __float2bfloat16_rn(v);
+  else
+    reinterpret_cast<float *>(p)[j] = v;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float read_elem(const char *p, int j) {  // the buffer may be the output
+  if (kBf16)
+    return __uint_as_float(static_cast<uint32_t>(
+                               reinterpret_cast<const volatile unsigned short *>(p)[j])
+                           << 16);
+  return reinterpret_cast<const volatile float *>(p)[j];
 }
 
 // NaN-propagating maximum of the elements of one 16-byte vector.

@@ -647,6 +647,116 @@ int sga_token_logprobs_grad(const void *logits, int dtype, int64_t rows, int64_t
       grad_entropy, top_k, top_ids, grad_top, out_grad, ldg, static_cast<cudaStream_t>(stream)));
 }
 
+int sga_probs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+              int64_t org_vocab, const float *temperature, float *out_probs, int64_t ldp,
+              sga_stream stream) {
+  if (dtype != SGA_F32 && dtype != SGA_BF16) return SGA_ERR_DTYPE;
+  if (rows < 0 || rows > (int64_t(1) << 28)) return SGA_ERR_SIZE;
+  int st = check_shard(0, vocab, org_vocab);
+  if (st != SGA_OK) return st;
+  if (ld < vocab || ldp < vocab) return SGA_ERR_SHARD;
+  if (rows == 0) return SGA_OK;
+  if (logits == nullptr || out_probs == nullptr) return SGA_ERR_NULL;
+  if (misaligned(logits, dtype == SGA_BF16 ? 2 : 4) || misaligned(temperature, 4) ||
+      misaligned(out_probs, 4))
+    return SGA_ERR_ALIGN;
+  DeviceInfo d;
+  if ((st = current_device(&d)) != SGA_OK) return st;
+  return launch_status(sga::launch_probs(logits, dtype, rows, ld, vocab,
+                                         valid_ids(0, vocab, org_vocab), temperature, out_probs,
+                                         ldp, d.num_sms, d.err,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int sga_sampled_verify(const float *target_probs, int64_t rows, int64_t ldt,
+                       const float *draft_probs, int64_t ldd, int64_t vocab, int num_reqs,
+                       const int32_t *cu_num_draft, const int32_t *draft_tokens,
+                       const uint8_t *in_prefill, const float *accept_u, const float *sample_u,
+                       int max_k, int32_t *out_sampled, int32_t *out_num_sampled,
+                       int32_t *out_num_rejected, int32_t *out_last, sga_stream stream) {
+  if (max_k < 1 || max_k > SGA_MAX_K) return SGA_ERR_MAXK;
+  if (num_reqs < 0 || num_reqs > (1 << 24) || rows < num_reqs || rows > (int64_t(1) << 28))
+    return SGA_ERR_SIZE;
+  if (vocab <= 0 || vocab > SGA_MAX_VOCAB) return SGA_ERR_VOCAB;
+  if (ldt < vocab || (draft_probs != nullptr && ldd < vocab)) return SGA_ERR_SHARD;
+  if (num_reqs == 0) return SGA_OK;
+  if (target_probs == nullptr || cu_num_draft == nullptr || sample_u == nullptr ||
+      out_sampled == nullptr || out_num_sampled == nullptr || out_num_rejected == nullptr ||
+      out_last == nullptr ||
+      (rows > num_reqs && (draft_tokens == nullptr || accept_u == nullptr)))
+    return SGA_ERR_NULL;
+  if (misaligned(target_probs, 4) || misaligned(draft_probs, 4) || misaligned(cu_num_draft, 4) ||
+      misaligned(draft_tokens, 4) || misaligned(accept_u, 4) || misaligned(sample_u, 4) ||
+      misaligned(out_sampled, 4) || misaligned(out_num_sampled, 4) ||
+      misaligned(out_num_rejected, 4) || misaligned(out_last, 4))
+    return SGA_ERR_ALIGN;
+  DeviceInfo d;
+  const int st = current_device(&d);
+  if (st != SGA_OK) return st;
+  return launch_status(sga::launch_sampled_verify(
+      target_probs, rows, ldt, draft_probs, ldd, vocab, num_reqs, cu_num_draft, draft_tokens,
+      in_prefill, accept_u, sample_u, max_k, out_sampled, out_num_sampled, out_num_rejected,
+      out_last, d.num_sms, d.err, static_cast<cudaStream_t>(stream)));
+}
+
+static int check_distill(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+                         int64_t org_vocab, const sga::DistillArgs &a, int64_t ldg) {
+  if (dtype != SGA_F32 && dtype != SGA_BF16) return SGA_ERR_DTYPE;
+  if (rows < 0 || rows > (int64_t(1) << 28)) return SGA_ERR_SIZE;
+  if (a.k < 1 || a.k > SGA_MAX_TEACHER) return SGA_ERR_SIZE;
+  if (!(a.temperature >= 1e-6f && a.temperature <= 1e6f)) return SGA_ERR_SIZE;
+  const int st = check_shard(0, vocab, org_vocab);
+  if (st != SGA_OK) return st;
+  if (ld < vocab || (a.grad != nullptr && ldg < vocab)) return SGA_ERR_SHARD;
+  if (rows == 0) return SGA_OK;
+  if (logits == nullptr || a.ids == nullptr || a.logits == nullptr) return SGA_ERR_NULL;
+  const uintptr_t elt = dtype == SGA_BF16 ? 2 : 4;
+  if (misaligned(logits, elt) || misaligned(a.grad, elt) || misaligned(a.ids, 4) ||
+      misaligned(a.logits, 4) || misaligned(a.lse, 4) || misaligned(a.out_loss, 4) ||
+      misaligned(a.out_lse, 4) || misaligned(a.out_lse_rest, 4) || misaligned(a.in_lse, 4) ||
+      misaligned(a.in_lse_rest, 4) || misaligned(a.grad_loss, 4))
+    return SGA_ERR_ALIGN;
+  return SGA_OK;
+}
+
+int sga_distill(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+                int64_t org_vocab, const int32_t *teacher_ids, const float *teacher_logits, int k,
+                const float *teacher_lse, float temperature, float *out_loss, float *out_lse,
+                float *out_lse_rest, const float *grad_loss, void *out_grad, int64_t ldg,
+                sga_stream stream) {
+  const sga::DistillArgs a = {teacher_ids, teacher_logits, teacher_lse, k,         temperature,
+                              out_loss,    out_lse,        out_lse_rest, nullptr,  nullptr,
+                              grad_loss,   out_grad};
+  int st = check_distill(logits, dtype, rows, ld, vocab, org_vocab, a, ldg);
+  if (st != SGA_OK || rows == 0) return st;
+  if (out_loss == nullptr && out_lse == nullptr && out_lse_rest == nullptr && out_grad == nullptr)
+    return SGA_OK;
+  DeviceInfo d;
+  if ((st = current_device(&d)) != SGA_OK) return st;
+  return launch_status(sga::launch_distill(logits, dtype, rows, ld, vocab,
+                                           valid_ids(0, vocab, org_vocab), a, ldg, d.num_sms,
+                                           d.err, static_cast<cudaStream_t>(stream)));
+}
+
+int sga_distill_grad(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+                     int64_t org_vocab, const int32_t *teacher_ids, const float *teacher_logits,
+                     int k, const float *teacher_lse, float temperature, const float *lse,
+                     const float *lse_rest, const float *grad_loss, void *out_grad, int64_t ldg,
+                     sga_stream stream) {
+  const sga::DistillArgs a = {teacher_ids, teacher_logits, teacher_lse, k,        temperature,
+                              nullptr,     nullptr,        nullptr,     lse,      lse_rest,
+                              grad_loss,   out_grad};
+  int st = check_distill(logits, dtype, rows, ld, vocab, org_vocab, a, ldg);
+  if (st != SGA_OK || rows == 0) return st;
+  if (lse == nullptr || out_grad == nullptr || (teacher_lse != nullptr && lse_rest == nullptr))
+    return SGA_ERR_NULL;
+  DeviceInfo d;
+  if ((st = current_device(&d)) != SGA_OK) return st;
+  return launch_status(sga::launch_distill(logits, dtype, rows, ld, vocab,
+                                           valid_ids(0, vocab, org_vocab), a, ldg, d.num_sms,
+                                           d.err, static_cast<cudaStream_t>(stream)));
+}
+
 int sga_selftest_wait_timeout(uint64_t limit_ns, uint64_t *waited_ns, sga_stream stream) {
   if (limit_ns < 1000 || limit_ns > 1000000000ull) return SGA_ERR_SIZE;
   if (misaligned(waited_ns, 8)) return SGA_ERR_ALIGN;

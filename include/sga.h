@@ -633,8 +633,146 @@ int sga_token_logprobs_grad(const void *logits, int dtype, int64_t rows, int64_t
                             int64_t ldg, sga_stream stream);
 
 /*
+ * sga_probs -- the probabilities of logits rows at a temperature, over a whole
+ * vocabulary: what sga_sampled_verify reads, of the target's rows and of the
+ * draft model's.  (The pages verify greedily; this is the library's extension.)
+ *   p_j = e^((x_j - max) / T) / sum_i e^((x_i - max) / T)
+ *
+ *   logits, dtype, rows, ld, vocab, org_vocab   as sga_token_logprobs.
+ *   temperature  device fp32 [rows], finite, or NULL (1 everywhere).  0 is a
+ *                greedy row: 1 at its argmax (see "argmax order" above), 0
+ *                elsewhere.  A negative or NaN temperature makes the row NaN.
+ *   out_probs    device fp32, rows x vocab elements, row stride ldp >= vocab,
+ *                4-byte aligned; padding ids get 0.  May be the buffer of fp32
+ *                logits itself (ldp == ld); any other overlap is not allowed.
+ * At a temperature above 0 a row with no logit above -inf is 0 everywhere, and
+ * a row holding a NaN or +inf is NaN (but for its padding ids).  One launch.
+ * Errors: SGA_ERR_DTYPE, SGA_ERR_SIZE (rows), SGA_ERR_VOCAB, SGA_ERR_SHARD
+ * (ld or ldp < vocab), SGA_ERR_NULL, SGA_ERR_ALIGN.
+ */
+int sga_probs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+              int64_t org_vocab, const float *temperature, float *out_probs, int64_t ldp,
+              sga_stream stream);
+
+/*
+ * sga_sampled_verify -- verification of drafted tokens by rejection sampling:
+ * sga_greedy_verify for requests that are sampled, from the target's and the
+ * draft model's probabilities and given uniform random numbers.  The emitted
+ * tokens are distributed as the target's.  (The pages verify greedily; this is
+ * the library's extension, on the same request layout and outputs.)
+ *
+ * Draft t of a row with target probabilities p, draft probabilities q and
+ * uniform u is accepted when fl(u q_t) < p_t (fp32), up to the first one that
+ * is not.  There a token is drawn from w_j = max(fl(p_j - q_j), 0), or from w = p
+ * where those are all 0; with every draft accepted it is drawn from the bonus
+ * row's p.  Drawing: weights count in whole units of 2^-38 (w clamped to [0, 1]
+ * and rounded to the nearest unit, NaN counts as 0), S_j = w_0 + ... + w_j in
+ * 64-bit integers, and the token is the first j with S_j > min(floor(u S), S - 1),
+ * S the total and u S a product of doubles (u = sample_u below, counted as 0 when
+ * it is negative or NaN).  The sums are exact, so the ids do not depend on how
+ * the row is split, and tokens of weight 0 are never drawn.
+ * A row of ones and zeros (sga_probs at temperature 0) gives the greedy result
+ * of sga_greedy_verify where the draft's rows are of that kind as well (or
+ * draft_probs is NULL).
+ *
+ *   target_probs  device fp32, rows x vocab, row stride ldt >= vocab: row
+ *                 cu[i] + i + j is position j of request i, as sga_greedy_verify.
+ *   rows          D + num_reqs, D = cu_num_draft[num_reqs] the number of drafts;
+ *                 num_reqs .. 2^28.
+ *   draft_probs   device fp32, D x vocab, row stride ldd >= vocab: row cu[i] + j
+ *                 is what draft j of request i was sampled from.  NULL: drafts
+ *                 proposed without probabilities, q = 1 at the draft, 0 elsewhere.
+ *   vocab         1 .. SGA_MAX_VOCAB (leave out padding ids, or give them 0).
+ *   num_reqs      >= 0 (0: nothing enqueued).
+ *   cu_num_draft  device int32 [num_reqs + 1], as sga_greedy_verify.  A request
+ *                 with K_i outside [0, max_k] or with rows outside of `rows` emits
+ *                 nothing and sets SGA_DEVERR_K_RANGE.
+ *   draft_tokens  device int32 [D] (may be NULL when D is 0).  An id outside
+ *                 [0, vocab) is a placeholder: not accepted, and q counts as 0.
+ *   in_prefill    device uint8 [num_reqs] or NULL, as sga_greedy_verify_prefill.
+ *   accept_u      device fp32 [D], uniform in [0, 1) (may be NULL when D is 0).
+ *   sample_u      device fp32 [num_reqs], uniform in [0, 1).
+ *   max_k         1 .. SGA_MAX_K.
+ *   out_sampled   device int32 [num_reqs, max_k + 1]: the a_i accepted drafts,
+ *                 the drawn token, then -1.  A row without any weight draws -1.
+ *   out_num_sampled, out_num_rejected, out_last   device int32 [num_reqs]:
+ *                 a_i + 1, K_i - a_i and the drawn token.
+ * All pointers must be 4-byte aligned (in_prefill: none).  One launch.
+ * Errors: SGA_ERR_MAXK, SGA_ERR_SIZE (num_reqs, rows), SGA_ERR_VOCAB,
+ * SGA_ERR_SHARD (ldt or ldd < vocab), SGA_ERR_NULL, SGA_ERR_ALIGN.
+ */
+int sga_sampled_verify(const float *target_probs, int64_t rows, int64_t ldt,
+                       const float *draft_probs, int64_t ldd, int64_t vocab, int num_reqs,
+                       const int32_t *cu_num_draft, const int32_t *draft_tokens,
+                       const uint8_t *in_prefill, const float *accept_u, const float *sample_u,
+                       int max_k, int32_t *out_sampled, int32_t *out_num_sampled,
+                       int32_t *out_num_rejected, int32_t *out_last, sga_stream stream);
+
+/*
+ * sga_distill -- the divergence of a draft model's rows from a teacher's top
+ * logits (of a target model, as sga_token_logprobs lists them), with or without
+ * its gradient with respect to the draft's logits in the same pass.  (The pages
+ * take trained draft models as given; this is the library's extension.)
+ *
+ * With y = x / T of the row's logits x, s_j = e^(y_j - lse) (lse the log-sum-exp
+ * of y over ids below org_vocab), and the teacher's entries (id_i, z_i):
+ *   without teacher_lse: p_i = e^(z_i / T) / sum of those of the list, p_r = 0;
+ *   with teacher_lse:    p_i = e^(z_i / T - teacher_lse), p_r = max(0, 1 - sum p_i),
+ *                        the teacher's probability of all ids off the list;
+ *   loss = sum_i p_i (log p_i - log s_id_i) + p_r (log p_r - log s_r),
+ *   s_r = e^(lse_rest - lse), lse_rest the log-sum-exp of y over ids off the list;
+ *   grad_j = grad_loss / T ((sum_i p_i + p_r) s_j - sum over id_i = j of p_i
+ *            - [j off the list] p_r e^(y_j - lse_rest)).
+ * (Soft targets at T > 1 are often weighted by T^2: give that in grad_loss.)
+ *
+ *   logits, dtype, rows, ld, vocab, org_vocab   as sga_token_logprobs.
+ *   teacher_ids, teacher_logits   device int32 / fp32 [rows, k]: ids in any
+ *                order.  An id outside [0, org_vocab) is no entry (it counts to
+ *                the rest).  Entries of the same id each count.  A row without
+ *                an entry (or whose list has no weight, without teacher_lse)
+ *                has loss 0 and gradient 0 whatever its logits are.
+ *   k            1 .. SGA_MAX_TEACHER.
+ *   teacher_lse  device fp32 [rows] or NULL: log-sum-exp of the teacher's
+ *                logits / T (zeros where teacher_logits are log probabilities
+ *                and T is 1).
+ *   temperature  T, 1e-6 .. 1e6.
+ *   out_loss, out_lse, out_lse_rest   device fp32 [rows], each nullable.
+ *   grad_loss    device fp32 [rows] or NULL (ones): upstream gradients.
+ *   out_grad     device, rows x vocab elements of `dtype`, row stride ldg >=
+ *                vocab, or NULL; padding ids get 0.  May be the logits buffer
+ *                itself (ldg == ld); any other overlap is not allowed.
+ * An entry with p_i > 0 on a logit of -inf makes the loss +inf (its gradient
+ * stays finite); p_r is left out (0) where the row has no logit above -inf off
+ * the list.  A row with no logit above -inf has lse -inf and gradient 0; one
+ * holding a NaN or +inf has NaN for its lse, loss and gradient.  One launch.
+ * Errors: SGA_ERR_DTYPE, SGA_ERR_SIZE (rows, k, temperature), SGA_ERR_VOCAB,
+ * SGA_ERR_SHARD (ld or ldg < vocab), SGA_ERR_NULL, SGA_ERR_ALIGN.
+ */
+#define SGA_MAX_TEACHER 128
+int sga_distill(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+                int64_t org_vocab, const int32_t *teacher_ids, const float *teacher_logits, int k,
+                const float *teacher_lse, float temperature, float *out_loss, float *out_lse,
+                float *out_lse_rest, const float *grad_loss, void *out_grad, int64_t ldg,
+                sga_stream stream);
+
+/*
+ * sga_distill_grad -- the gradient of sga_distill from the lse and lse_rest
+ * that it gave, for losses whose upstream gradient is known later.
+ *   lse          device fp32 [rows].
+ *   lse_rest     device fp32 [rows]; may be NULL iff teacher_lse is.
+ *   out_grad     as sga_distill, not NULL.
+ * Other arguments, results and errors as sga_distill.
+ */
+int sga_distill_grad(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,
+                     int64_t org_vocab, const int32_t *teacher_ids, const float *teacher_logits,
+                     int k, const float *teacher_lse, float temperature, const float *lse,
+                     const float *lse_rest, const float *grad_loss, void *out_grad, int64_t ldg,
+                     sga_stream stream);
+
+/*
  * Device error word of the current device.  Kernels OR bits into it instead
- * of trapping: SGA_DEVERR_K_RANGE (a request's K_i outside [0, max_k]),
+ * of trapping: SGA_DEVERR_K_RANGE (a request's K_i outside [0, max_k], or in
+ * sga_sampled_verify its rows outside of the given ones),
  * SGA_DEVERR_D2T_RANGE (a winning id outside the d2t table),
  * SGA_DEVERR_TIMEOUT (a bounded wait inside a pipelined kernel gave up; its
  * outputs are not valid), SGA_DEVERR_LAYOUT (sga_local_argmax_blocks[_shards]:
