@@ -1,75 +1,271 @@
 // probs.cu -- probabilities of logits rows at a temperature.
 //
-// p_j = 2^((x_j - max) log2e / T) / sum_i 2^(...): the difference to the row's
-// maximum is formed first, so that the largest term is exactly 1 at any
-// temperature and offset.  A greedy row (T = 0) is 1 at its argmax.
-#include "scan.cuh"
+// p_j = 2^((x_j - m) log2e / T) / sum_i 2^(...), m a logit within 2^12 (in terms)
+// of the row's maximum, by which the exponents are exact differences at any
+// offset and temperature.  A greedy row (T = 0) is 1 at its argmax.
+#include "rowring.cuh"
 
 namespace sga {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 512;
+template <int kT>
+struct ProbsShared {
+  Ring ring;
+  Exchange<1> ex;
+  Sum warp_sum[kT / 32];
+  int32_t warp_id[kT / 32];
+};
 
-__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
-
+// Unit of the output: 16 bytes, four probabilities.
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads)
-    probs_kernel(const char *logits, int64_t ld_bytes, int valid, int width,
-                 const float *temperature, float *probs, int64_t ldp) {
-  __shared__ float part[32];
-  __shared__ int32_t part_id[32];
+__device__ __forceinline__ void load4(const uint4 *stage, int unit, float (&x)[4]) {
+  if constexpr (kBf16) {
+    const uint2 q = reinterpret_cast<const uint2 *>(stage)[unit];
+    x[0] = bf16_lo(q.x);
+    x[1] = bf16_hi(q.x);
+    x[2] = bf16_lo(q.y);
+    x[3] = bf16_hi(q.y);
+  } else {
+    const uint4 q = stage[unit];
+    x[0] = __uint_as_float(q.x);
+    x[1] = __uint_as_float(q.y);
+    x[2] = __uint_as_float(q.z);
+    x[3] = __uint_as_float(q.w);
+  }
+}
+
+template <bool kBf16, int kT>
+__global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
+    probs_kernel(const char *logits, int64_t ld_bytes, int64_t num_rows, int valid, int width,
+                 const float *temperature, float *probs, int64_t ldp, int chunks, uint32_t *err) {
+  constexpr int slots = kSlots<kT>;
+  constexpr int kElt = kBf16 ? 2 : 4;
+  constexpr int kVec = 16 / kElt;
+  constexpr int kWarps = kT / 32;
+  constexpr uint32_t kMasked = kBf16 ? 0xff80ff80u : 0xff800000u;  // -inf
+  extern __shared__ __align__(128) uint4 buf[];
+  __shared__ ProbsShared<kT> sh;
+  const int chunk = static_cast<int>(blockIdx.x % chunks);
+  const int64_t row0 = blockIdx.x / chunks, row_step = gridDim.x / chunks;
+  const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
+  const volatile int *abort_flag = &sh.ring.abort;
+  if (tid == 0) {
+    for (int i = 0; i < slots; ++i) {
+      mbar_init(smem_u32(&sh.ring.full[i]), 1);
+      mbar_init(smem_u32(&sh.ring.empty[i]), kWarps);
+    }
+    sh.ring.abort = 0;
+    exchange_init(sh.ex, chunks);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  if (chunks > 1) {  // every CTA's barriers are ready
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  }
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x;
-  const char *x = logits + row * ld_bytes;
-  float *out = probs + row * ldp;
-  const float t = temperature != nullptr ? temperature[row] : 1.0f;
-  float m = neg_inf();
-  int32_t id = kNoId;
-  for (int j = tid; j < valid; j += kThreads) {
-    const float v = read_elem<kBf16>(x, j);
-    if (id == kNoId || scan_better(v, m)) {
-      m = v;
-      id = j;
-    }
-  }
-  warp_argmax(m, id);
-  if (lane == 0) {
-    part[warp] = m;
-    part_id[warp] = id;
-  }
-  __syncthreads();
-  m = neg_inf();
-  id = kNoId;
-  for (int w = 0; w < kThreads / 32; ++w)
-    if (pair_beats(part[w], part_id[w], m, id)) {
-      m = part[w];
-      id = part_id[w];
-    }
-  __syncthreads();
-  const bool greedy = t == 0.0f;
-  const float scale = t > 0.0f ? fminf(kLog2e / t, 3e38f) : __int_as_float(0x7fc00000);
-  auto term = [&](int j) { return exp2f((read_elem<kBf16>(x, j) - m) * scale); };
-  float s = 0.0f;
-  if (!greedy && m != neg_inf()) {
-    for (int j = tid; j < valid; j += kThreads) s += term(j);
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (lane == 0) part[warp] = s;
-    __syncthreads();
-    s = 0.0f;
-    for (int w = 0; w < kThreads / 32; ++w) s += part[w];
-  }
-  for (int j = tid; j < width; j += kThreads) {
-    float p = 0.0f;
-    if (j < valid) {
+
+  if (warp == kWarps) {
+    copy_rows<kBf16, kT>(sh.ring, buf, slots, true, logits, ld_bytes, row0, row_step, num_rows,
+                         valid, chunk, chunks, lane, err);
+    pdl_launch_dependents();
+  } else {
+    Place at = {0, 0};
+    bool ok = true;
+    int64_t it = 0;
+    float t_next = temperature != nullptr && row0 < num_rows ? temperature[row0] : 1.0f;
+    for (int64_t row = row0; row < num_rows; row += row_step, ++it) {
+      const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
+      const float t = t_next;
+      if (temperature != nullptr && row + row_step < num_rows) t_next = temperature[row + row_step];
+      const bool greedy = t == 0.0f;
+      const float scale = t > 0.0f ? fminf(kLog2e / t, 3e38f) : nan_f32();
+      const float room = 12.0f / scale;
+      RunSum a = {0.0f, neg_inf(), 0u};
+      float best = neg_inf();
+      int32_t best_id = kNoId;
+      // the single elements at the row's ends
+      float end_x[2] = {neg_inf(), neg_inf()};
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int j = end_column(pc, side, tid);
+        if (j >= 0) end_x[side] = read_elem<kBf16>(pc.p, j);
+      }
+      // ---- the row's sum (a greedy row's argmax)
+      Place r = at;
+      const int kept = max(0, pc.stages - slots);  // the first stage that stays
+      for (int j = 0; j < pc.stages; ++j) {
+        ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+        if (!ok) break;
+        const uint4 *st = buf + r.slot * kStageVec<kT>;
+        const int c = pc.b0 + j * kStageVec<kT> * kVec;
+        const int n = min(kStageVec<kT>, (pc.b1 - c) / kVec);
+        uint4 q[kVecPerThread];
+#pragma unroll
+        for (int u = 0; u < kVecPerThread; ++u) {
+          const int i = u * kT + tid;
+          q[u] = i < n ? st[i] : make_uint4(kMasked, kMasked, kMasked, kMasked);
+        }
+        if (greedy) {
+#pragma unroll
+          for (int u = 0; u < kVecPerThread; ++u)
+            if (u * kT + tid < n && (best_id == kNoId || scan_better(vec_max<kBf16>(q[u]), best))) {
+              const int32_t id = c + (u * kT + tid) * kVec;
+              if (best_id == kNoId) best_id = id;  // (a first id, if nothing is above -inf)
+              scan_vec<kBf16>(q[u], id, best, best_id);
+            }
+        } else {
+          uint4 most = q[0];
+#pragma unroll
+          for (int u = 1; u < kVecPerThread; ++u) most = vec_larger<kBf16>(most, q[u]);
+          sum_rebase(a, vec_max<kBf16>(most), scale, room);
+#pragma unroll
+          for (int u = 0; u < kVecPerThread; ++u) sum_vector<kBf16>(a, q[u], scale);
+        }
+        if (j < kept) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
+        }
+        step(r, slots);
+      }
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int j = end_column(pc, side, tid);
+        if (j < 0) continue;
+        if (greedy) {
+          if (best_id == kNoId || pair_beats(end_x[side], j, best, best_id)) {
+            best = end_x[side];
+            best_id = j;
+          }
+        } else {
+          sum_rebase(a, end_x[side], scale, room);
+          sum_add(a, end_x[side], neg_inf(), scale);
+        }
+      }
+      // ---- joined over the warps and the cluster
+      Sum total = {best, 0.0f};
       if (greedy)
-        p = j == id ? 1.0f : 0.0f;
-      else if (m != neg_inf() || t != t || t < 0.0f)
-        p = term(j) / s;
+        warp_argmax(total.m, best_id);
+      else
+        total = sum_warp(sum_result(a), scale);
+      if (lane == 0) {
+        sh.warp_sum[warp] = total;
+        sh.warp_id[warp] = best_id;
+      }
+      consumers_sync<kT>();
+      if (warp == 0) {
+        total = lane < kWarps ? sh.warp_sum[lane] : Sum{neg_inf(), 0.0f};
+        best_id = lane < kWarps ? sh.warp_id[lane] : kNoId;
+        if (greedy)
+          warp_argmax(total.m, best_id);
+        else
+          total = sum_warp(total, scale);
+      }
+      const uint4 mine[1] = {make_uint4(__float_as_uint(total.m), __float_as_uint(total.s),
+                                        static_cast<uint32_t>(best_id), 0u)};
+      ok = exchange<kT>(sh.ex, mine, it, chunk, chunks, tid, ok, abort_flag);
+      total = {neg_inf(), 0.0f};
+      best_id = kNoId;
+      for (int c = 0; c < chunks; ++c) {
+        const uint4 q = sh.ex.part[it & 1][c][0];
+        const Sum o = {__uint_as_float(q.x), __uint_as_float(q.y)};
+        if (!greedy) {
+          total = sum_merge(total, o, scale);
+        } else if (pair_beats(o.m, static_cast<int32_t>(q.z), total.m, best_id)) {
+          total.m = o.m;
+          best_id = static_cast<int32_t>(q.z);
+        }
+      }
+      // a row without terms is 0 (its sum is 0; a NaN stays)
+      const float m = total.m == neg_inf() ? 0.0f : total.m;
+      const float inv = total.s == 0.0f ? 0.0f : 1.0f / total.s;
+
+      // ---- the probabilities
+      float *out = probs + row * ldp;
+      auto value = [&](float x) { return ex2((x - m) * scale) * inv; };
+      const bool aligned = (reinterpret_cast<uintptr_t>(out + pc.b0) & 15u) == 0;
+      r = later(at, kept, slots);
+      for (int i = 0; i < pc.stages; ++i) {
+        const bool again = i >= pc.stages - kept;  // loaded a second time
+        const int j = again ? i - (pc.stages - kept) : kept + i;
+        if (again) ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+        if (!ok) break;
+        const uint4 *st = buf + r.slot * kStageVec<kT>;
+        const int c = pc.b0 + j * kStageVec<kT> * kVec;
+        const int n = min(kStageVec<kT> * kVec, pc.b1 - c);
+        float *o = out + c;
+        if (aligned) {
+          const int hot = best_id - c;
+#pragma unroll
+          for (int u = 0; u < kVecPerThread * kVec / 4; ++u) {
+            const int unit = u * kT + tid;
+            if (unit * 4 >= n) continue;
+            float4 p;
+            if (greedy) {
+              const int e = hot - unit * 4;
+              p = make_float4(e == 0 ? 1.0f : 0.0f, e == 1 ? 1.0f : 0.0f, e == 2 ? 1.0f : 0.0f,
+                              e == 3 ? 1.0f : 0.0f);
+            } else {
+              float x[4];
+              load4<kBf16>(st, unit, x);
+              p = make_float4(value(x[0]), value(x[1]), value(x[2]), value(x[3]));
+            }
+            reinterpret_cast<float4 *>(o)[unit] = p;
+          }
+        } else {
+          for (int e = tid; e < n; e += kT)
+            o[e] = greedy ? (c + e == best_id ? 1.0f : 0.0f)
+                          : value(read_elem<kBf16>(reinterpret_cast<const char *>(st), e));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
+        step(r, slots);
+      }
+      if (!ok) {  // (every warp keeps to the rows' barriers)
+        if (lane == 0) raise_abort(&sh.ring.abort, err);
+        continue;
+      }
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int j = end_column(pc, side, tid);
+        if (j >= 0) out[j] = greedy ? (j == best_id ? 1.0f : 0.0f) : value(end_x[side]);
+      }
+      if (chunk == chunks - 1)
+        for (int j = valid + tid; j < width; j += kT) out[j] = 0.0f;
+      at = later(at, num_loads(pc.stages, slots, true), slots);
     }
-    out[j] = p;
   }
+  if (chunks > 1) {  // no CTA ends while another may write to it
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  }
+}
+
+template <bool kBf16, int kT>
+cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t width, int64_t valid,
+                        const float *temperature, float *probs, int64_t ldp, int chunks,
+                        int num_sms, uint32_t *err, cudaStream_t stream) {
+  auto kern = probs_kernel<kBf16, kT>;
+  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), kRingBytes<kT>,
+                                      (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2));
+  if (e != cudaSuccess) return e;
+  const int64_t resident = resident_clusters(chunks, kPerSm<kT>, num_sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows < resident ? rows : resident) * chunks));
+  cfg.blockDim = dim3(kT + 32);
+  cfg.dynamicSmemBytes = kRingBytes<kT>;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = chunks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits),
+                            ld * (kBf16 ? 2 : 4), rows, static_cast<int>(valid),
+                            static_cast<int>(width), temperature, probs, ldp, chunks, err);
 }
 
 }  // namespace
@@ -77,22 +273,13 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_probs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t width,
                          int64_t valid, const float *temperature, float *probs, int64_t ldp,
                          int num_sms, uint32_t *err, cudaStream_t stream) {
-  (void)num_sms;
-  (void)err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const bool bf16 = dtype == SGA_BF16;
-  return cudaLaunchKernelEx(&cfg, bf16 ? probs_kernel<true> : probs_kernel<false>,
-                            static_cast<const char *>(logits), ld * (bf16 ? 2 : 4),
-                            static_cast<int>(valid), static_cast<int>(width), temperature, probs,
-                            ldp);
+  const int64_t bytes = valid * (dtype == SGA_BF16 ? 2 : 4);
+  const bool small = small_rows(rows, bytes, num_sms);
+  const int chunks = small ? 1 : pick_chunks(rows, bytes, num_sms);
+  auto launch = dtype == SGA_BF16 ? (small ? launch_rows<true, 64> : launch_rows<true, 256>)
+                                  : (small ? launch_rows<false, 64> : launch_rows<false, 256>);
+  return launch(logits, rows, ld, width, valid, temperature, probs, ldp, chunks, num_sms, err,
+                stream);
 }
 
 }  // namespace sga

@@ -1,0 +1,343 @@
+// rowring.cuh -- rows of logits held in the shared memory of a cluster, shared by
+// probs.cu and distill.cu: what a row is split into, the ring that a copy warp
+// fills, the running sum of exponentials, and the exchange of a row's pieces.
+//
+// Both kernels read a row twice, for its sum and then to write something of each
+// of its logits.  A cluster of CTAs (one for short rows) shares a row, and each
+// keeps its piece in a ring of stages until it has been written: the logits come
+// from HBM once.  As a stage is written out it is filled with the next row, so the
+// loads of one row run under the stores of another.  A piece with more stages than
+// the ring keeps its last ones; the others are loaded a second time.
+#pragma once
+
+#include "pipe.cuh"
+#include "scan.cuh"
+
+namespace sga {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kVecPerThread = 4;  // 16-byte vectors of a stage per thread
+constexpr int kMaxCluster = 8;
+template <int kT>
+constexpr int kStageVec = kT * kVecPerThread;
+// 256 threads: two CTAs per SM with seven stages of 16 KB, the most that fits;
+// 64 threads (short rows): eight with six of 4 KB.
+template <int kT>
+constexpr int kPerSm = 512 / kT;
+template <int kT>
+constexpr int kSlots = kT == 256 ? 7 : 6;
+template <int kT>
+constexpr int kRingBytes = kSlots<kT> * kStageVec<kT> * 16;
+constexpr int kMaxSlots = 7;
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ float nan_f32() { return __int_as_float(0x7fc00000); }
+
+__device__ __forceinline__ float ex2(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+template <int kT>
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kT) : "memory");
+}
+
+// ------------------------------------------------------------------ pieces
+
+// A CTA's piece of a row: columns [c0, c1), of which [b0, b1) are whole 16-byte
+// vectors (loaded in stages) and at most seven at either end of the row are not.
+struct Piece {
+  const char *p;
+  int c0, b0, b1, c1, stages;
+};
+
+template <bool kBf16, int kT>
+__device__ __forceinline__ Piece piece_of(const char *p, int valid, int chunk, int chunks) {
+  constexpr int kElt = kBf16 ? 2 : 4, kVec = 16 / kElt;
+  Piece q;
+  q.p = p;
+  int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / kElt);
+  if (head > valid) head = valid;
+  const int nvec = (valid - head) / kVec;  // < 2^22, chunks <= 8
+  const int v0 = static_cast<int>(static_cast<uint32_t>(nvec * chunk) / chunks);
+  const int v1 = static_cast<int>(static_cast<uint32_t>(nvec * (chunk + 1)) / chunks);
+  q.b0 = head + v0 * kVec;
+  q.b1 = head + v1 * kVec;
+  q.c0 = chunk == 0 ? 0 : q.b0;
+  q.c1 = chunk == chunks - 1 ? valid : q.b1;
+  q.stages = (v1 - v0 + kStageVec<kT> - 1) / kStageVec<kT>;
+  return q;
+}
+
+// Column of the single element that a thread takes at one end (0: before b0, 1:
+// from b1) of its piece, or -1.
+__device__ __forceinline__ int end_column(const Piece &q, int side, int tid) {
+  const int j = (side == 0 ? q.c0 : q.b1) + tid;
+  return j < (side == 0 ? q.b0 : q.c1) ? j : -1;
+}
+
+// -------------------------------------------------------------------- ring
+
+struct Ring {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  int abort;
+};
+
+// A load's place: its slot, and the parity of the slot's use.
+struct Place {
+  int slot;
+  uint32_t phase;
+};
+__device__ __forceinline__ void step(Place &a, int slots) {
+  if (++a.slot == slots) {
+    a.slot = 0;
+    a.phase ^= 1;
+  }
+}
+__device__ __forceinline__ Place later(const Place &a, int by, int slots) {
+  const int s = a.slot + by, q = s / slots;
+  return {s - q * slots, a.phase ^ (q & 1)};
+}
+
+// Loads of a row's piece: its stages, and (kept) those again that the ring could not keep.
+__device__ __forceinline__ int num_loads(int stages, int slots, bool kept) {
+  return stages + (kept && stages > slots ? stages - slots : 0);
+}
+
+// The copy warp: every piece's stages into the ring.
+template <bool kBf16, int kT>
+__device__ __forceinline__ void copy_rows(Ring &ring, uint4 *buf, int slots, bool kept,
+                                          const char *logits, int64_t ld_bytes, int64_t row0,
+                                          int64_t row_step, int64_t num_rows, int valid, int chunk,
+                                          int chunks, int lane, uint32_t *err) {
+  constexpr int kElt = kBf16 ? 2 : 4, kVec = 16 / kElt;
+  const volatile int *abort_flag = &ring.abort;
+  Place at = {0, 0};
+  int filled = 0;
+  bool ok = true;
+  for (int64_t row = row0; row < num_rows && ok; row += row_step) {
+    const Piece q = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
+    const int loads = num_loads(q.stages, slots, kept);
+    for (int j = 0; j < loads; ++j) {
+      if (filled < slots) {
+        ++filled;
+      } else if (!warp_wait(smem_u32(&ring.empty[at.slot]), at.phase ^ 1, abort_flag)) {
+        if (lane == 0) raise_abort(&ring.abort, err);
+        ok = false;
+        break;
+      }
+      if (elect_one()) {
+        const int c = q.b0 + (j < q.stages ? j : j - q.stages) * kStageVec<kT> * kVec;
+        const uint32_t bytes = static_cast<uint32_t>(min(kStageVec<kT> * kVec, q.b1 - c)) * kElt;
+        mbar_expect_tx(smem_u32(&ring.full[at.slot]), bytes);
+        bulk_load(smem_u32(buf + at.slot * kStageVec<kT>), q.p + static_cast<int64_t>(c) * kElt,
+                  bytes, smem_u32(&ring.full[at.slot]));
+      }
+      __syncwarp();
+      step(at, slots);
+    }
+  }
+  // every copy has landed before the CTA ends
+  const int zero = 0;
+  for (int i = 0; i < filled; ++i) {
+    if (at.slot == 0) {
+      at.slot = slots;
+      at.phase ^= 1;
+    }
+    --at.slot;
+    pipe_wait(smem_u32(&ring.full[at.slot]), at.phase, &zero);
+  }
+}
+
+// --------------------------------------------------- sum of exponentials
+
+// A thread's running sum of 2^((x - m) scale), in two halves; m is one of its
+// logits, moved up when a logit passes `limit` (2^12 above it; -inf: there is
+// none yet, m = 0).  The difference is taken before it is scaled, so neither
+// offset nor scale of the logits costs accuracy or range.
+struct RunSum {
+  float m, limit;
+  uint64_t s;
+};
+
+__device__ __forceinline__ float sum_total(const RunSum &a) {
+  float lo, hi;
+  unpack_f32(a.s, lo, hi);
+  return lo + hi;
+}
+
+// Before logits whose maximum is `most` join.
+__device__ __forceinline__ void sum_rebase(RunSum &a, float most, float scale, float room) {
+  if (!(most > a.limit)) return;
+  const float s = sum_total(a);
+  a.s = pack_f32(s == 0.0f ? 0.0f : s * ex2((a.m - most) * scale), 0.0f);
+  a.m = most;
+  a.limit = most + room;
+}
+
+__device__ __forceinline__ void sum_add(RunSum &a, float lo, float hi, float scale) {
+  const uint64_t t = mul2(add2(pack_f32(lo, hi), pack_f32(-a.m, -a.m)), pack_f32(scale, scale));
+  float t0, t1;
+  unpack_f32(t, t0, t1);
+  a.s = add2(a.s, pack_f32(ex2(t0), ex2(t1)));
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void sum_vector(RunSum &a, const uint4 q, float scale) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (kBf16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum_add(a, bf16_lo(w[i]), bf16_hi(w[i]), scale);
+  } else {
+    sum_add(a, __uint_as_float(w[0]), __uint_as_float(w[1]), scale);
+    sum_add(a, __uint_as_float(w[2]), __uint_as_float(w[3]), scale);
+  }
+}
+
+// The larger of each pair of logits of two vectors (NaN wins).
+template <bool kBf16>
+__device__ __forceinline__ uint4 vec_larger(const uint4 a, const uint4 b) {
+  auto larger = [](uint32_t x, uint32_t y) {
+    return kBf16 ? max_nan_bf16x2(x, y)
+                 : __float_as_uint(max_nan(__uint_as_float(x), __uint_as_float(y)));
+  };
+  return make_uint4(larger(a.x, b.x), larger(a.y, b.y), larger(a.z, b.z), larger(a.w, b.w));
+}
+
+// A sum and its reference; one without terms has m = -inf, s = 0.  A NaN in
+// either row stays in the sum.
+struct Sum {
+  float m, s;
+};
+
+__device__ __forceinline__ Sum sum_result(const RunSum &a) {
+  return {a.limit == neg_inf() ? neg_inf() : a.m, sum_total(a)};
+}
+
+__device__ __forceinline__ float sum_at(const Sum &a, float m, float scale) {
+  return a.s == 0.0f ? 0.0f : a.s * ex2((a.m - m) * scale);
+}
+
+__device__ __forceinline__ Sum sum_merge(const Sum &a, const Sum &b, float scale) {
+  const float m = fmaxf(a.m, b.m);
+  return {m, sum_at(a, m, scale) + sum_at(b, m, scale)};
+}
+
+// Over the lanes of a warp (or its first `lanes`).
+__device__ __forceinline__ Sum sum_warp(Sum a, float scale) {
+  float m = a.m;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  float s = sum_at(a, m, scale);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return {m, s};
+}
+
+// ---------------------------------------------------------------- exchange
+
+// What the CTAs of a cluster tell each other about a row, kQ 16-byte words each;
+// by turns in two buffers: a CTA tells of row r + 2 when all have told of row r + 1,
+// so all have read row r.
+template <int kQ>
+struct Exchange {
+  uint64_t bar[2];
+  alignas(16) uint4 part[2][kMaxCluster][kQ];
+};
+
+template <int kQ>
+__device__ __forceinline__ void exchange_init(Exchange<kQ> &ex, int chunks) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(smem_u32(&ex.bar[i]), 1);
+    mbar_expect_tx(smem_u32(&ex.bar[i]), static_cast<uint32_t>(chunks) * kQ * 16);
+  }
+}
+
+__device__ __forceinline__ void st_async(uint32_t addr, const uint4 v, uint32_t bar, int rank) {
+  uint32_t a, b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(bar), "r"(rank));
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, "
+      "[%5];" ::"r"(a),
+      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(b)
+      : "memory");
+}
+
+// The consumers' exchange for their it-th row; `mine` is that of warp 0, the same
+// in all lanes.  The parts are then in ex.part[it & 1].  A warp that has given up
+// (ok false) tells and waits no more.
+template <int kT, int kQ>
+__device__ __forceinline__ bool exchange(Exchange<kQ> &ex, const uint4 (&mine)[kQ], int64_t it,
+                                         int chunk, int chunks, int tid, bool ok,
+                                         const volatile int *abort_flag) {
+  const int par = static_cast<int>(it & 1);
+  if (chunks == 1) {
+    if (tid == 0)
+      for (int q = 0; q < kQ; ++q) ex.part[par][0][q] = mine[q];
+    consumers_sync<kT>();
+    return ok;
+  }
+  if (ok && tid < chunks)
+    for (int q = 0; q < kQ; ++q)
+      st_async(smem_u32(&ex.part[par][chunk][q]), mine[q], smem_u32(&ex.bar[par]), tid);
+  __syncwarp();
+  ok = ok && warp_wait(smem_u32(&ex.bar[par]), static_cast<uint32_t>(it >> 1) & 1, abort_flag);
+  if (ok && tid == 0)
+    mbar_expect_tx(smem_u32(&ex.bar[par]), static_cast<uint32_t>(chunks) * kQ * 16);
+  return ok;
+}
+
+// ------------------------------------------------------------------- host
+
+// Clusters of `chunks` CTAs that run at once: a cluster lies in one GPC, whose SMs
+// are not all a multiple of it (as cudaOccupancyMaxActiveClusters counts them on
+// 152 SMs; a grid with more would leave its last clusters a second round).
+inline int64_t resident_clusters(int chunks, int per_sm, int num_sms) {
+  const int64_t ctas = static_cast<int64_t>(per_sm) * num_sms;
+  switch (chunks) {
+    case 1: return ctas;
+    case 2: return ctas / 2;
+    case 3: return ctas * 97 / 304;
+    case 4: return ctas * 74 / 304;
+    case 6: return ctas * 46 / 304;
+    default: return ctas * 36 / 304;
+  }
+}
+
+// Many rows of up to 48 KB: small CTAs, eight per SM, a row each (bf16
+// probabilities, small / wide: 4096 rows of 1000 ids 17 / 27 us, 4096 of 8000 38 / 48,
+// 700 of 20000 23 / 25).
+inline bool small_rows(int64_t rows, int64_t bytes, int num_sms) {
+  return bytes <= (48 << 10) && rows > 2 * num_sms;
+}
+
+// CTAs that share a row.  Few rows: as many as let all rows run at once, with at
+// least 4 KB each (96 rows of 200064 bf16 ids: 3 CTAs 27 us, in rounds 4 33 us).
+// Otherwise the fewest whose pieces leave the ring room for the next row's loads (2048
+// rows of 202048: 6 CTAs 403 us, 4 408; 2000 rows of 50257 fp32 ids: 3 138, 2 148).
+inline int pick_chunks(int64_t rows, int64_t bytes, int num_sms) {
+  constexpr int kWidths[6] = {8, 6, 4, 3, 2, 1};
+  constexpr int64_t kRing = kRingBytes<256>;
+  for (int c : kWidths)
+    if (c == 1 || (rows <= resident_clusters(c, 2, num_sms) && bytes >= 4096 * c)) {
+      if (rows <= resident_clusters(c, 2, num_sms) && bytes <= kRing * 5 / 4 * c) return c;
+      break;
+    }
+  int best = kMaxCluster;
+  for (int c : kWidths)
+    if (bytes <= kRing * 5 / 8 * c) best = c;
+  return best;
+}
+
+}  // namespace
+}  // namespace sga

@@ -11,16 +11,21 @@
 // 2^-38: 64-bit sums of up to 2^24 weights of at most 1 are exact (< 2^62), and
 // any split of the row draws the same id.  An id of probability 1e-9 still has
 // 275 units.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace sga {
 namespace {
 
 using Units = unsigned long long;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kSegments = 64;  // sums kept of a row
+constexpr int kBatch = 8;           // loads in flight per thread and row
+constexpr int kStep = 32 * kBatch;  // ids that a warp takes at once
+constexpr int kMaxSegments = 256;   // sums kept of a CTA's ids
+constexpr int kMaxCtas = 8;         // CTAs per request
 
 // A weight in units of 2^-38 (a NaN counts as 0).
 __device__ __forceinline__ Units units(float w) {
@@ -30,6 +35,16 @@ __device__ __forceinline__ Units units(float w) {
 __device__ __forceinline__ Units warp_sum(Units v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// The sums up to and with each lane.
+__device__ __forceinline__ Units warp_prefix(Units v, int lane) {
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const Units o = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += o;
+  }
   return v;
 }
 
@@ -43,33 +58,124 @@ struct VerifyArgs {
   int32_t *sampled, *num_sampled, *num_rejected, *last;
 };
 
-__global__ void __launch_bounds__(kThreads) sampled_verify_kernel(VerifyArgs in, uint32_t *err) {
-  __shared__ Units seg[kSegments];
-  __shared__ Units sums[kWarps];
-  __shared__ int s_accepted;
-  __shared__ int32_t s_token;
-  pdl_wait();
+// A running sum of weights w = max(x - y, 0) in units, for one thread: w 2^38 is
+// split into hi 2^23 + lo, hi = rint(w 2^15) and lo the rounded rest (in -2^22 ..
+// 2^22), both read off the mantissa of a sum with 1.5 2^23.  The integers carry that
+// constant's bits once per weight; at most 2^9 weights, then `take`.  (A conversion
+// to 64 bits per weight takes 4 x the time of these eight operations.)
+struct UnitSum {
+  uint32_t hi, lo;
+};
+constexpr float kMagic = 12582912.0f;       // 1.5 2^23
+constexpr uint32_t kMagicBits = 0x4b400000u;
+
+__device__ __forceinline__ void unit_add(UnitSum &a, float x, float y) {
+  float w;  // rounded once, clamped to [0, 1], a NaN becomes 0
+  asm("sub.rn.sat.f32 %0, %1, %2;" : "=f"(w) : "f"(x), "f"(y));
+  const float t = __fmaf_rn(w, 32768.0f, kMagic);
+  const float rest = __fmaf_rn(w, 32768.0f, -__fsub_rn(t, kMagic));
+  a.hi += __float_as_uint(t);
+  a.lo += __float_as_uint(__fmaf_rn(rest, 8388608.0f, kMagic));
+}
+
+__device__ __forceinline__ Units unit_total(const UnitSum &a, uint32_t weights) {
+  const uint32_t hi = a.hi - weights * kMagicBits;
+  const int32_t lo = static_cast<int32_t>(a.lo - weights * kMagicBits);
+  return (static_cast<Units>(hi) << 23) + static_cast<Units>(static_cast<int64_t>(lo));
+}
+
+// The sum of the weights of ids [j0, j1), for one warp.  kRow: q is a row of draft
+// probabilities; otherwise the one id `hot` (or none) has all of them.  kVec: rows
+// and j0 are 16-byte aligned.
+template <bool kRow, bool kVec>
+__device__ __forceinline__ Units warp_units(const float *p, const float *q, int32_t hot, int j0,
+                                            int j1, int lane) {
+  Units sum = 0;
+  int j = j0;
+  for (; j + kStep <= j1; j += kStep) {
+    float x[kBatch], y[kBatch];
+    if (kVec) {
+#pragma unroll
+      for (int u = 0; u < kBatch; u += 4) {
+        const int at = j + u * 32 + lane * 4;
+        *reinterpret_cast<float4 *>(x + u) = __ldcs(reinterpret_cast<const float4 *>(p + at));
+        if (kRow)
+          *reinterpret_cast<float4 *>(y + u) = __ldcs(reinterpret_cast<const float4 *>(q + at));
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        x[u] = __ldcs(p + j + u * 32 + lane);
+        if (kRow) y[u] = __ldcs(q + j + u * 32 + lane);
+      }
+    }
+    UnitSum a = {0u, 0u};
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int at = kVec ? j + (u & ~3) * 32 + lane * 4 + (u & 3) : j + u * 32 + lane;
+      if (!kRow) y[u] = at == hot ? 1.0f : 0.0f;
+      unit_add(a, x[u], y[u]);
+    }
+    sum += unit_total(a, kBatch);
+  }
+  if (j < j1) {
+    UnitSum a = {0u, 0u};
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int at = j + u * 32 + lane;
+      const float x = at < j1 ? __ldcs(p + at) : 0.0f;
+      unit_add(a, x, kRow ? (at < j1 ? __ldcs(q + at) : 0.0f) : (at == hot ? 1.0f : 0.0f));
+    }
+    sum += unit_total(a, kBatch);
+  }
+  return warp_sum(sum);
+}
+
+// A cluster of CTAs per request, each with a run of the row's ids.  Bound by HBM
+// where requests are many (512 of 152064 ids, half of them with a rejection: 467 MB
+// in 87 us = 5.4 TB/s), by the chain of dependent steps where they are few: offsets,
+// drafts, their probabilities, the row's sum (segment sums stay in shared memory),
+// the totals' exchange, the segment of the drawn id once more (from L2).
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    sampled_verify_kernel(VerifyArgs in, int ctas, uint32_t *err) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ Units seg[kMaxSegments];
+  __shared__ Units totals[2][kMaxCtas];  // of the request's CTAs, by pass
+  __shared__ Units warp_sums[kWarps];
+  __shared__ int s_accepted, s_segment;
+  __shared__ int32_t s_draft[32], s_token;
+  __shared__ Units s_below;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t req = blockIdx.x;
+  const int rank = static_cast<int>(blockIdx.x % ctas);
+  const int64_t req = blockIdx.x / ctas;
+  // (every CTA of the cluster has begun: its memory may be written)
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+  pdl_wait();
   const int64_t c = in.cu[req];
   const int64_t k = in.cu[req + 1] - c;
   int32_t *sampled = in.sampled + req * (in.max_k + 1);
   const bool bad = k < 0 || k > in.max_k || c < 0 || c + k > in.rows - in.num_reqs;
   if (bad || (in.in_prefill != nullptr && in.in_prefill[req] != 0)) {
-    if (tid <= in.max_k) sampled[tid] = -1;
-    if (tid == 0) {
-      in.num_sampled[req] = 0;
-      in.num_rejected[req] = 0;
-      in.last[req] = -1;
-      if (bad) atomicOr(err, SGA_DEVERR_K_RANGE);
+    if (rank == 0) {
+      if (tid <= in.max_k) sampled[tid] = -1;
+      if (tid == 0) {
+        in.num_sampled[req] = 0;
+        in.num_rejected[req] = 0;
+        in.last[req] = -1;
+        if (bad) atomicOr(err, SGA_DEVERR_K_RANGE);
+      }
     }
+    if (ctas > 1) asm volatile("barrier.cluster.wait;" ::: "memory");
     return;
   }
-  // the first draft that is not accepted
+  // the first draft that is not accepted (every CTA finds it by itself)
+  const float u = in.sample_u[req];
   if (warp == 0) {
     bool fails = false;
     if (lane < k) {
       const int32_t t = in.tokens[c + lane];
+      s_draft[lane] = t;
       fails = true;
       if (t >= 0 && t < in.vocab) {
         const float p = in.target[(c + req + lane) * in.ldt + t];
@@ -86,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) sampled_verify_kernel(VerifyArgs in,
   const float *q = nullptr;  // the draft's row, where there is one
   int32_t hot = -1;          // or the id that has all of its probability
   if (a < k) {
-    const int32_t t = in.tokens[c + a];
+    const int32_t t = s_draft[a];
     if (t >= 0 && t < in.vocab) {
       if (in.draft != nullptr)
         q = in.draft + (c + a) * in.ldd;
@@ -94,53 +200,98 @@ __global__ void __launch_bounds__(kThreads) sampled_verify_kernel(VerifyArgs in,
         hot = t;
     }
   }
-  auto weight = [&](int j) {
-    const float w = p[j];
-    return units(q != nullptr ? __fsub_rn(w, q[j]) : (j == hot ? __fsub_rn(w, 1.0f) : w));
-  };
-  const int len = (in.vocab + kSegments - 1) / kSegments;
-  Units total = 0;
-  while (true) {
-    for (int s = warp; s < kSegments; s += kWarps) {
-      const int64_t j1 = min(static_cast<int64_t>(in.vocab), static_cast<int64_t>(s + 1) * len);
-      Units sum = 0;
-      for (int64_t j = static_cast<int64_t>(s) * len + lane; j < j1; j += 32)
-        sum += weight(static_cast<int>(j));
-      sum = warp_sum(sum);
+  // this CTA's ids, in segments of whole steps
+  const int share = ((in.vocab + ctas - 1) / ctas + 3) & ~3;
+  const int c0 = min(in.vocab, rank * share), c1 = min(in.vocab, c0 + share);
+  int len = 2 * kStep;
+  while (static_cast<int64_t>(len) * kMaxSegments < share) len *= 2;
+  const int segments = (c1 - c0 + len - 1) / len;
+  const bool vec = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
+
+  Units total = 0, own = 0, before = 0;  // the row's, this CTA's, those of the CTAs before it
+  bool found = false;
+  for (int pass = 0;; ++pass) {
+    for (int s = warp; s < segments; s += kWarps) {
+      const int j0 = c0 + s * len, j1 = min(c1, j0 + len);
+      const Units sum =
+          vec ? (q != nullptr ? warp_units<true, true>(p, q, hot, j0, j1, lane)
+                              : warp_units<false, true>(p, q, hot, j0, j1, lane))
+              : (q != nullptr ? warp_units<true, false>(p, q, hot, j0, j1, lane)
+                              : warp_units<false, false>(p, q, hot, j0, j1, lane));
       if (lane == 0) seg[s] = sum;
     }
     __syncthreads();
-    total = 0;
-    for (int s = 0; s < kSegments; ++s) total += seg[s];
-    if (total != 0 || (q == nullptr && hot < 0)) break;
+    if (warp == 0) {
+      Units sum = 0;
+      for (int s = lane; s < segments; s += 32) sum += seg[s];
+      sum = warp_sum(sum);
+      if (ctas == 1) {
+        if (lane == 0) totals[pass][0] = sum;
+      } else {
+        if (pass == 0) asm volatile("barrier.cluster.wait;" ::: "memory");
+        if (lane < ctas) *cg::this_cluster().map_shared_rank(&totals[pass][rank], lane) = sum;
+        __syncwarp();
+      }
+    } else if (ctas > 1 && pass == 0) {
+      asm volatile("barrier.cluster.wait;" ::: "memory");
+    }
+    if (ctas > 1)
+      asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    else
+      __syncthreads();
+    total = before = 0;
+    own = totals[pass][rank];
+    for (int i = 0; i < ctas; ++i) {
+      if (i < rank) before += totals[pass][i];
+      total += totals[pass][i];
+    }
+    found = total != 0;
+    if (found || (q == nullptr && hot < 0)) break;
     q = nullptr;  // p nowhere above q: from p itself
     hot = -1;
-    __syncthreads();
   }
-  if (tid == 0) s_token = -1;
-  if (total != 0) {
-    const float u = in.sample_u[req];
-    Units edge = u > 0.0f ? __double2ull_rd(__dmul_rn(u, __ull2double_rn(total))) : 0;
+  pdl_launch_dependents();
+  Units edge = 0;
+  if (found) {
+    edge = u > 0.0f ? __double2ull_rd(__dmul_rn(u, __ull2double_rn(total))) : 0;
     if (edge > total - 1) edge = total - 1;
-    int s = 0;
-    Units below = 0;
-    while (below + seg[s] <= edge) below += seg[s++];
-    // the segment again, a run of ids per thread
-    const int j0 = s * len, n = min(len, in.vocab - j0), run = (n + kThreads - 1) / kThreads;
-    const int b0 = j0 + min(n, tid * run), b1 = j0 + min(n, (tid + 1) * run);
-    Units own = 0;
-    for (int j = b0; j < b1; ++j) own += weight(j);
-    Units upto = own;  // with the lanes before
+  }
+  // the CTA whose ids hold the edge goes on alone
+  if (found ? edge < before || edge - before >= own : rank != 0) return;
+  if (tid == 0) s_token = -1;
+  if (found) {
+    edge -= before;
+    if (warp == 0) {  // its segment
+      constexpr int kPer = kMaxSegments / 32;
+      Units part = 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const Units o = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += o;
+      for (int i = 0; i < kPer; ++i) part += lane * kPer + i < segments ? seg[lane * kPer + i] : 0;
+      const Units upto = warp_prefix(part, lane);
+      Units below = upto - part;
+      if (below <= edge && edge < upto) {
+        int s = lane * kPer;
+        while (below + seg[s] <= edge) below += seg[s++];
+        s_segment = s;
+        s_below = below;
+      }
     }
-    if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    Units sum = below + upto - own;
-    for (int w = 0; w < warp; ++w) sum += sums[w];
-    if (sum <= edge && edge < sum + own) {
+    edge -= s_below;
+    // the segment again, a run of ids per thread
+    const int j0 = c0 + s_segment * len, n = min(len, c1 - j0);
+    const int run = (n + kThreads - 1) / kThreads;
+    const int b0 = j0 + min(n, tid * run), b1 = j0 + min(n, (tid + 1) * run);
+    auto weight = [&](int j) {
+      return units(__fsub_rn(__ldg(p + j), q != nullptr ? __ldg(q + j) : (j == hot ? 1.0f : 0.0f)));
+    };
+    Units part = 0;
+    for (int j = b0; j < b1; ++j) part += weight(j);
+    const Units upto = warp_prefix(part, lane);
+    if (lane == 31) warp_sums[warp] = upto;
+    __syncthreads();
+    Units sum = upto - part;
+    for (int w = 0; w < warp; ++w) sum += warp_sums[w];
+    if (sum <= edge && edge < sum + part) {
       int j = b0;
       while ((sum += weight(j)) <= edge) ++j;
       s_token = j;
@@ -148,12 +299,36 @@ __global__ void __launch_bounds__(kThreads) sampled_verify_kernel(VerifyArgs in,
   }
   __syncthreads();
   if (tid <= in.max_k)
-    sampled[tid] = tid < a ? in.tokens[c + tid] : (tid == a ? s_token : -1);
+    sampled[tid] = tid < a ? s_draft[tid] : (tid == a ? s_token : -1);
   if (tid == 0) {
     in.num_sampled[req] = a + 1;
     in.num_rejected[req] = static_cast<int32_t>(k) - a;
     in.last[req] = s_token;
   }
+}
+
+// Threads per CTA and CTAs per request, 1024 threads per SM: as many CTAs as let all
+// requests run at once (a few too many do no harm: about half of them read one row
+// instead of two), with at least 4096 ids each.  A CTA's loads in flight bound its
+// rate, so up to as many requests as fill the SMs in eights have CTAs of 512.  24 requests
+// of 200064 ids with 512 threads x 8 19 us, 256 x 8 23; 96 of 152064 with 256 x 6
+// 27, x 4 31, x 8 33; 512 with x 1 87, x 2 93, x 4 103, 512 x 1 95.
+void pick_ctas(int num_reqs, int64_t vocab, int num_sms, int *threads, int *ctas) {
+  constexpr int kWidths[3] = {8, 6, 4};
+  constexpr int kClusters[3] = {36, 46, 74};  // at once, of 304 CTAs (GPCs hold whole clusters)
+  auto fit = [&](int i, int per_sm) {
+    return vocab >= 4096 * kWidths[i] &&
+           num_reqs * 20ll <= kClusters[i] * 21ll * per_sm * num_sms / 304;
+  };
+  *threads = fit(0, 2) ? 512 : 256;
+  if (fit(0, 4))
+    *ctas = 8;
+  else if (fit(1, 4))
+    *ctas = 6;
+  else if (fit(2, 4))
+    *ctas = 4;
+  else
+    *ctas = num_reqs <= 2ll * num_sms && vocab >= 8192 ? 2 : 1;
 }
 
 }  // namespace
@@ -171,17 +346,23 @@ cudaError_t launch_sampled_verify(const float *target, int64_t rows, int64_t ldt
                          cu_num_draft, draft_tokens, in_prefill, accept_u,
                          sample_u,   out_sampled, out_num_sampled, out_num_rejected,
                          out_last};
-  (void)num_sms;
+  int threads, ctas;
+  pick_ctas(num_reqs, vocab, num_sms, &threads, &ctas);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(num_reqs));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(num_reqs * ctas));
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sampled_verify_kernel, in, err);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(
+      &cfg, threads == 512 ? sampled_verify_kernel<512> : sampled_verify_kernel<256>, in, ctas, err);
 }
 
 }  // namespace sga
