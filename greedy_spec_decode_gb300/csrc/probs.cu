@@ -8,6 +8,12 @@
 namespace sga {
 namespace {
 
+// Stages of the ring: the most that fits two CTAs per SM (16 KB), or eight (4 KB).
+template <int kT>
+constexpr int kSlots = kT == 256 ? 7 : 6;
+template <int kT>
+constexpr int kRingBytes = kSlots<kT> * kStageVec<kT> * 16;
+
 template <int kT>
 struct ProbsShared {
   Ring ring;
@@ -275,7 +281,7 @@ cudaError_t launch_probs(const void *logits, int dtype, int64_t rows, int64_t ld
                          int num_sms, uint32_t *err, cudaStream_t stream) {
   const int64_t bytes = valid * (dtype == SGA_BF16 ? 2 : 4);
   const bool small = small_rows(rows, bytes, num_sms);
-  const int chunks = small ? 1 : pick_chunks(rows, bytes, num_sms);
+  const int chunks = small ? 1 : pick_chunks(rows, bytes, kRingBytes<256>, num_sms);
   auto launch = dtype == SGA_BF16 ? (small ? launch_rows<true, 64> : launch_rows<true, 256>)
                                   : (small ? launch_rows<false, 64> : launch_rows<false, 256>);
   return launch(logits, rows, ld, width, valid, temperature, probs, ldp, chunks, num_sms, err,

@@ -21,14 +21,9 @@ constexpr int kVecPerThread = 4;  // 16-byte vectors of a stage per thread
 constexpr int kMaxCluster = 8;
 template <int kT>
 constexpr int kStageVec = kT * kVecPerThread;
-// 256 threads: two CTAs per SM with seven stages of 16 KB, the most that fits;
-// 64 threads (short rows): eight with six of 4 KB.
+// CTAs per SM: two with 256 consumers, eight with 64 (short rows).
 template <int kT>
 constexpr int kPerSm = 512 / kT;
-template <int kT>
-constexpr int kSlots = kT == 256 ? 7 : 6;
-template <int kT>
-constexpr int kRingBytes = kSlots<kT> * kStageVec<kT> * 16;
 constexpr int kMaxSlots = 7;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -323,19 +318,20 @@ inline bool small_rows(int64_t rows, int64_t bytes, int num_sms) {
 
 // CTAs that share a row.  Few rows: as many as let all rows run at once, with at
 // least 4 KB each (96 rows of 200064 bf16 ids: 3 CTAs 27 us, in rounds 4 33 us).
-// Otherwise the fewest whose pieces leave the ring room for the next row's loads (2048
-// rows of 202048: 6 CTAs 403 us, 4 408; 2000 rows of 50257 fp32 ids: 3 138, 2 148).
-inline int pick_chunks(int64_t rows, int64_t bytes, int num_sms) {
+// Otherwise one, or where rows are kept in a ring of `ring` bytes per CTA the fewest
+// whose pieces leave it room for the next row's loads (2048 rows of 202048: 6 CTAs
+// 403 us, 4 408; 2000 rows of 50257 fp32 ids: 3 138, 2 148).
+inline int pick_chunks(int64_t rows, int64_t bytes, int64_t ring, int num_sms) {
   constexpr int kWidths[6] = {8, 6, 4, 3, 2, 1};
-  constexpr int64_t kRing = kRingBytes<256>;
   for (int c : kWidths)
     if (c == 1 || (rows <= resident_clusters(c, 2, num_sms) && bytes >= 4096 * c)) {
-      if (rows <= resident_clusters(c, 2, num_sms) && bytes <= kRing * 5 / 4 * c) return c;
+      if (ring == 0) return c;
+      if (rows <= resident_clusters(c, 2, num_sms) && bytes <= ring * 5 / 4 * c) return c;
       break;
     }
   int best = kMaxCluster;
   for (int c : kWidths)
-    if (bytes <= kRing * 5 / 8 * c) best = c;
+    if (bytes <= ring * 5 / 8 * c) best = c;
   return best;
 }
 

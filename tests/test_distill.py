@@ -243,6 +243,7 @@ def test_the_gradient_may_take_the_logits_place(sga_lib, rows, vocab, dtype):
     org, temp = vocab - 2, 1.0
     _, x, lists, up = make(7, rows, vocab, org, dtype, 20, True, temp, 1, 1)
     a, b = x.clone(), x.clone()
+    x = x.clone()      # laid out like them: at other alignments sums have another order
     grad = torch.empty_like(x)
     got = run_forward(sga_lib, x, org, lists, temp, up, True, grad)
     here = run_forward(sga_lib, a, org, lists, temp, up, True, a)
