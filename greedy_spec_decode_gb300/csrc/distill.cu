@@ -20,14 +20,20 @@
 namespace sga {
 namespace {
 
+// The call's arguments, and what follows from the temperature (a 64-bit division per
+// thread would take some us of every CTA).
+struct Args : DistillArgs {
+  double inv_t;          // 1 / T
+  float inv_t32, scale;  // 1 / T, log2(e) / T
+};
+
 // ------------------------------------------------------------- the teacher
 
 // A row's list, and what follows from it.
-struct List {
+struct alignas(16) List {
   int32_t id[SGA_MAX_TEACHER];  // -1: no entry
-  float z[SGA_MAX_TEACHER];
   float x[SGA_MAX_TEACHER];     // the row's logits there
-  double p[SGA_MAX_TEACHER];    // probabilities; at an id's first entry those of all its entries
+  float p[SGA_MAX_TEACHER];     // at an id's first entry: the probability of all its entries
   uint8_t first[SGA_MAX_TEACHER];  // no earlier entry has the id
   Sum listed;                   // sum of exponentials of the listed ids
   double sum_p, rest_p;         // probability on and off the list
@@ -36,77 +42,128 @@ struct List {
   int any;                      // the row has a teacher
 };
 
-__device__ __forceinline__ double warp_sum_f64(double v) {
+// Sums of a and b over a warp: a's in lanes 0-15, b's in 16-31 (64-bit additions are
+// 1/64 of the 32-bit rate here, so the two share theirs).
+__device__ __forceinline__ void warp_sums_f64(double &a, double &b, int lane) {
+  const bool low = lane < 16;
+  double v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
+  for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  a = __shfl_sync(0xffffffffu, v, 0);
+  b = __shfl_sync(0xffffffffu, v, 16);
 }
 
-// One warp works out a row's list; l.id (entries only), l.z and l.x are given.
-__device__ __forceinline__ void teacher_row(List &l, int k, const float *teacher_lse, int64_t row,
-                                            double inv_t, float scale, int lane) {
-  // the normaliser, and which entries are the first of their id
-  double norm = 0.0, most = -INFINITY;
-  bool some = false, again = false;
-#pragma unroll 1
-  for (int i = lane; i < k; i += 32) {
-    const int32_t id = l.id[i];
-    bool first = id >= 0;
-    if (id >= 0) {
-      some = true;
-      const double z = l.z[i] * inv_t;
-      if (!(z <= most)) most = z;  // (a NaN goes on into the sums)
+// log of a positive normal number: that of its mantissa in [0.7, 1.4] in 32 bits (off
+// by 2^-25 of it), the exponent's part in 64.
+__device__ __forceinline__ double log_of(float v) {
+  const int e = (__float_as_int(v) - 0x3f3504f3) >> 23;
+  return fma(static_cast<double>(e), 0.69314718055994530942,
+             static_cast<double>(logf(__int_as_float(__float_as_int(v) - (e << 23)))));
+}
+
+constexpr int kPerLane = SGA_MAX_TEACHER / 32;
+
+// A lane's entries of a list: r * 32 + lane.
+struct Entries {
+  int32_t id[kPerLane];  // -1: no entry
+  float z[kPerLane], x[kPerLane];
+};
+
+// Loads a row's entries, and its logits there if they are in columns [c0, c1).
+template <bool kBf16>
+__device__ __forceinline__ void entries_load(Entries &e, const Args &in, int64_t row,
+                                             const char *x, int valid, int c0, int c1, int lane) {
+#pragma unroll
+  for (int r = 0; r < kPerLane; ++r) {
+    const int i = r * 32 + lane;
+    e.id[r] = i < in.k ? in.ids[row * in.k + i] : -1;
+    e.z[r] = i < in.k ? in.logits[row * in.k + i] : 0.0f;
+    if (e.id[r] < 0 || e.id[r] >= valid) e.id[r] = -1;
+  }
+#pragma unroll
+  for (int r = 0; r < kPerLane; ++r)
+    e.x[r] = e.id[r] >= 0 && e.id[r] >= c0 && e.id[r] < c1 ? read_elem<kBf16>(x, e.id[r]) : neg_inf();
+}
+
+// One warp works out a row's list from its entries.  The logits are needed last: their
+// loads, which hang on those of the ids, run under the rest.
+__device__ __forceinline__ void teacher_row(List &l, const Entries &e, int k, float lse,
+                                            bool with_lse, double inv_t, float scale, int lane) {
+#pragma unroll
+  for (int r = 0; r < kPerLane; ++r)
+    if (r * 32 < k) l.id[r * 32 + lane] = e.id[r];
+  __syncwarp();
+  // which entries are the first of their id
+  bool first[kPerLane], some = false, again = false;
+  const int4 *ids = reinterpret_cast<const int4 *>(l.id);
+#pragma unroll
+  for (int r = 0; r < kPerLane; ++r) {
+    if (r * 32 >= k) continue;
+    const int i = r * 32 + lane;
+    first[r] = e.id[r] >= 0;
+    some = some || first[r];
 #pragma unroll 4
-      for (int j = 0; j < i; ++j) first = first && l.id[j] != id;
-      again = again || !first;
+    for (int j = 0; j < min(k, r * 32 + 32); j += 4) {
+      const int4 o = ids[j >> 2];
+      if ((o.x == e.id[r] && j < i) || (o.y == e.id[r] && j + 1 < i) ||
+          (o.z == e.id[r] && j + 2 < i) || (o.w == e.id[r] && j + 3 < i))
+        first[r] = false;
     }
-    l.first[i] = first;
+    again = again || (e.id[r] >= 0 && !first[r]);
+    l.first[i] = first[r];
   }
   bool any = __any_sync(0xffffffffu, some);
   again = __any_sync(0xffffffffu, again);
-  if (teacher_lse != nullptr) {
-    norm = teacher_lse[row];
-  } else {
+  // the normaliser
+  double norm = lse, sum_p = 0.0, part = 0.0;
+  if (!with_lse) {
+    float most = neg_inf();
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const double o = __shfl_xor_sync(0xffffffffu, most, off);
-      if (!(o <= most)) most = o;
-    }
-    any = any && most != -INFINITY;
-    double sum = 0.0;
-#pragma unroll 1
-    for (int i = lane; i < k; i += 32)
-      if (l.id[i] >= 0) sum += exp(l.z[i] * inv_t - most);
-    norm = most + log(warp_sum_f64(sum));
+    for (int r = 0; r < kPerLane; ++r)
+      if (r * 32 < k && e.id[r] >= 0) most = max_nan(most, e.z[r]);  // (a NaN goes on)
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, off));
+    any = any && most != neg_inf();
+    double sum = 0.0, none = 0.0;
+#pragma unroll
+    for (int r = 0; r < kPerLane; ++r)
+      if (r * 32 < k && e.id[r] >= 0 && any)
+        sum += exp((static_cast<double>(e.z[r]) - most) * inv_t);
+    warp_sums_f64(sum, none, lane);
+    norm = most * inv_t + log(sum);
   }
   // probabilities, the list's part of the loss, and its sum of exponentials
-  double sum_p = 0.0, part = 0.0;
   Sum listed = {neg_inf(), 0.0f};
-#pragma unroll 1
-  for (int i = lane; i < k; i += 32) {
+#pragma unroll
+  for (int r = 0; r < kPerLane; ++r) {
+    if (r * 32 >= k) continue;
     double p = 0.0;
-    if (l.id[i] >= 0 && any) {
-      const double logp = l.z[i] * inv_t - norm;
+    if (e.id[r] >= 0 && any) {
+      const double logp = e.z[r] * inv_t - norm;
       p = exp(logp);
       sum_p += p;
-      if (!(p <= 0.0)) part += p * (logp - l.x[i] * inv_t);
+      if (!(p <= 0.0)) part += p * (logp - e.x[r] * inv_t);
     }
-    l.p[i] = p;
-    const float x = l.first[i] ? l.x[i] : neg_inf();
+    l.p[r * 32 + lane] = static_cast<float>(p);
+    l.x[r * 32 + lane] = e.x[r];
+    const float x = first[r] ? e.x[r] : neg_inf();
     if (x != neg_inf()) listed = sum_merge(listed, {is_nan(x) ? neg_inf() : x, x - x + 1.0f}, scale);
   }
   __syncwarp();
-  sum_p = warp_sum_f64(sum_p);
-  part = warp_sum_f64(part);
+  warp_sums_f64(sum_p, part, lane);
   listed = sum_warp(listed, scale);
-  if (again) {  // (entries are visited in the same order by every CTA of a row)
+  if (again) {
 #pragma unroll 1
     for (int i = lane; i < k; i += 32)
-      if (l.first[i])
+      if (l.first[i]) {
+        float p = l.p[i];
         for (int j = i + 1; j < k; ++j)
-          if (l.id[j] == l.id[i]) l.p[i] += l.p[j];
+          if (l.id[j] == l.id[i]) p += l.p[j];
+        l.p[i] = p;
+      }
   }
-  const double rest = teacher_lse != nullptr && any ? (sum_p > 1.0 ? 0.0 : 1.0 - sum_p) : 0.0;
+  const double rest = with_lse && any ? (sum_p > 1.0 ? 0.0 : 1.0 - sum_p) : 0.0;
   if (lane == 0) {
     l.listed = listed;
     l.sum_p = sum_p;
@@ -122,22 +179,26 @@ __device__ __forceinline__ void teacher_row(List &l, int k, const float *teacher
 
 // ------------------------------------------------------------ loss (and gradient)
 
-constexpr int kPerLane = SGA_MAX_TEACHER / 32;  // entries of a list per lane
+// Long rows (kT 256) and short ones (64): CTAs per SM, stages of the ring (16 or
+// 4 KB; the most that fits), and list warps.
+template <int kT, bool kGrad>
+struct Form {
+  static constexpr int kPerSm = kT == 256 ? (kGrad ? 1 : 2) : (kGrad ? 4 : 6);
+  static constexpr int kSlots = kT == 256 ? (kGrad ? 12 : 5) : (kGrad ? 9 : 5);
+  static constexpr int kLists = kT == 256 ? 4 : 2;
+  static constexpr int kRingBytes = kSlots * kStageVec<kT> * 16;
+  static constexpr int kThreads = (kGrad ? 2 : 1) * kT + 32 + 32 * kLists;
+};
 
-// Stages of the ring: the most that fits two CTAs per SM (16 KB), or eight (4 KB).
-template <int kT>
-constexpr int kSlots = kT == 256 ? 6 : 5;
-template <int kT>
-constexpr int kRingBytes = kSlots<kT> * kStageVec<kT> * 16;
-
-template <int kT>
+// kLists list warps work on rows in turn, each one ahead.
+template <int kT, int kLists>
 struct DistillShared {
+  static constexpr int kHeld = 2 * kLists;  // lists held
   Ring ring;
-  uint64_t ready[2], stored[2];  // a row's list is there; its gradient is written
-  Exchange<1> ex;
-  Sum warp_sum[kT / 32];
-  Sum total[2], rest[2];  // the row's sums, for the list warp
-  List list[2];
+  uint64_t ready[kHeld], stored[kHeld];  // a row's list is there; its gradient is written
+  Exchange<2 * kHeld> ex;
+  Sum warp_sum[2][kT / 32];
+  List list[kHeld];
 };
 
 // Gradient of 16 bytes of logits off the list: coef 2^((x - m) scale).
@@ -168,34 +229,41 @@ __device__ __forceinline__ uint4 grad_vec(const uint4 q, float m, float scale, f
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A row's piece is read once and kept (rowring.cuh) for the gradient.  Before a warp
-// sums its part of a stage it takes the listed logits out (-inf in their place), so
-// that the sum is the rest's and no other logit is compared with an id.  A list warp
-// works out the teacher's numbers a row ahead, reading the listed logits by itself,
-// and writes the loss and the listed ids' gradients a row behind.
+// Four kinds of warps: the copy warp fills the ring; the sum warps add up a row's
+// piece, taking the listed logits out of it first (-inf in their place: the sum is
+// the rest's, and no other logit is compared with an id); the gradient warps write
+// out what the ring has kept, a row or two behind; list warps work out the teacher's
+// numbers a row ahead, reading the listed logits by themselves, and write the loss
+// and the listed ids' gradients a row behind.
 template <bool kBf16, int kT, bool kGrad>
-__global__ void __launch_bounds__(kT + 64, kPerSm<kT>)
+__global__ void __launch_bounds__(Form<kT, kGrad>::kThreads, Form<kT, kGrad>::kPerSm)
     distill_kernel(const char *logits, int64_t ld_bytes, int64_t num_rows, int valid, int width,
-                   DistillArgs in, int64_t ldg_bytes, int chunks, uint32_t *err) {
+                   Args in, int64_t ldg_bytes, int chunks, uint32_t *err) {
+  using F = Form<kT, kGrad>;
+  using Shared = DistillShared<kT, F::kLists>;
   constexpr int kElt = kBf16 ? 2 : 4;
   constexpr int kVec = 16 / kElt;
   constexpr int kWarps = kT / 32;
-  constexpr int slots = kSlots<kT>;
+  constexpr int kGradWarps = kGrad ? kWarps : 0;
+  constexpr int slots = F::kSlots;
+  constexpr uint32_t kHeld = Shared::kHeld;
   constexpr uint32_t kMasked = kBf16 ? 0xff80ff80u : 0xff800000u;  // -inf
   extern __shared__ __align__(128) uint4 buf[];
-  __shared__ DistillShared<kT> sh;
+  __shared__ Shared sh;
   const int chunk = static_cast<int>(blockIdx.x % chunks);
   const int64_t row0 = blockIdx.x / chunks, row_step = gridDim.x / chunks;
+  const uint32_t num_its =
+      static_cast<uint32_t>(row0 < num_rows ? (num_rows - row0 + row_step - 1) / row_step : 0);
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const volatile int *abort_flag = &sh.ring.abort;
-  const double inv_t = 1.0 / static_cast<double>(in.temperature);
-  const float scale = static_cast<float>(1.4426950408889634 * inv_t);
+  const double inv_t = in.inv_t;
+  const float scale = in.scale;
   if (tid == 0) {
     for (int i = 0; i < slots; ++i) {
       mbar_init(smem_u32(&sh.ring.full[i]), 1);
       mbar_init(smem_u32(&sh.ring.empty[i]), kWarps);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (uint32_t i = 0; i < kHeld; ++i) {
       mbar_init(smem_u32(&sh.ready[i]), 1);
       mbar_init(smem_u32(&sh.stored[i]), kWarps);
     }
@@ -208,96 +276,15 @@ __global__ void __launch_bounds__(kT + 64, kPerSm<kT>)
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   pdl_wait();
 
-  if (warp == kWarps) {
-    copy_rows<kBf16, kT>(sh.ring, buf, slots, kGrad, logits, ld_bytes, row0, row_step, num_rows,
-                         valid, chunk, chunks, lane, err);
-    pdl_launch_dependents();
-  } else if (warp == kWarps + 1) {
-    // ------------------------------------------------------------- list warp
-    auto finish = [&](int64_t row, int64_t it) {
-      const int par = static_cast<int>(it & 1);
-      if (!warp_wait(smem_u32(&sh.stored[par]), static_cast<uint32_t>(it >> 1) & 1, abort_flag))
-        return false;
-      const List &l = sh.list[par];
-      const Sum total = sh.total[par], rest = sh.rest[par];
-      const bool bad = is_nan(total.s);
-      const double rest_p = rest.s == 0.0f ? 0.0 : l.rest_p;
-      if (chunk == 0 &&
-          (in.out_loss != nullptr || in.out_lse != nullptr || in.out_lse_rest != nullptr)) {
-        // lane 0: lse, lane 1: lse_rest, lane 2: log p_r
-        const double lg =
-            log(lane == 0 ? static_cast<double>(total.s)
-                          : (lane == 1 ? static_cast<double>(rest.s) : rest_p));
-        const Sum own = lane == 0 ? total : rest;
-        const double v = bad ? nan("") : (own.s == 0.0f ? -INFINITY : own.m * inv_t + lg);
-        const double lse = __shfl_sync(0xffffffffu, v, 0);
-        const double lse_rest = __shfl_sync(0xffffffffu, v, 1);
-        const double log_rest = __shfl_sync(0xffffffffu, lg, 2);
-        if (lane == 1 && in.out_lse_rest != nullptr)
-          in.out_lse_rest[row] = static_cast<float>(v);
-        if (lane == 0) {
-          if (in.out_lse != nullptr) in.out_lse[row] = static_cast<float>(v);
-          double loss = l.part;
-          if (lse != -INFINITY) loss += l.sum_p * lse;  // (else it is +inf or 0)
-          if (!(rest_p <= 0.0)) loss += rest_p * (log_rest - (lse_rest - lse));
-          if (!l.any) loss = 0.0;
-          if (in.out_loss != nullptr) in.out_loss[row] = static_cast<float>(loss);
-        }
-      }
-      if (kGrad && l.any && total.s != 0.0f) {
-        const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
-        char *g = static_cast<char *>(in.grad) + row * ldg_bytes;
-        const float up = (in.grad_loss != nullptr ? in.grad_loss[row] : 1.0f) *
-                         static_cast<float>(inv_t);
-        const float of = (rest.s == 0.0f ? l.on_list : l.total) / total.s;
-        for (int i = lane; i < in.k; i += 32) {
-          const int32_t id = l.id[i];
-          if (!l.first[i] || id < pc.c0 || id >= pc.c1) continue;
-          const float s = of * ex2((l.x[i] - total.m) * scale);
-          store_elem<kBf16>(g, id, up * (s - static_cast<float>(l.p[i])));
-        }
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = true;
-    int64_t it = 0;
-    int32_t id[kPerLane];
-    float z[kPerLane];
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-      for (int r = 0; r < kPerLane; ++r) {
-        const int i = r * 32 + lane;
-        id[r] = i < in.k ? in.ids[row * in.k + i] : -1;
-        z[r] = i < in.k ? in.logits[row * in.k + i] : 0.0f;
-      }
-    };
-    if (row0 < num_rows) fetch(row0);
-    for (int64_t row = row0; row < num_rows && ok; row += row_step, ++it) {
-      List &l = sh.list[it & 1];
-#pragma unroll
-      for (int r = 0; r < kPerLane; ++r) {
-        const int i = r * 32 + lane;
-        if (i >= in.k) continue;
-        const bool entry = id[r] >= 0 && id[r] < valid;
-        l.id[i] = entry ? id[r] : -1;
-        l.z[i] = z[r];
-        l.x[i] = entry ? read_elem<kBf16>(logits + row * ld_bytes, id[r]) : neg_inf();
-      }
-      if (row + row_step < num_rows) fetch(row + row_step);
-      __syncwarp();
-      teacher_row(l, in.k, in.lse, row, inv_t, scale, lane);
-      if (lane == 0) mbar_arrive(smem_u32(&sh.ready[it & 1]));
-      if (it > 0) ok = finish(row - row_step, it - 1);
-    }
-    if (ok && it > 0) ok = finish(row0 + (it - 1) * row_step, it - 1);
-    if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
-  } else {
-    // ------------------------------------------------------------- consumers
+  // waits for the it-th row's list, or its stored gradient
+  auto wait_held = [&](uint64_t (&bar)[kHeld], uint32_t it) {
+    return warp_wait(smem_u32(&bar[it % kHeld]), (it / kHeld) & 1, abort_flag);
+  };
+  bool ok = true;
+  if (warp < kWarps) {
+    // ------------------------------------------------------------- sum warps
     const float room = 12.0f / scale;
     Place at = {0, 0};
-    bool ok = true;
-    int64_t it = 0;
     int32_t next_id[kPerLane];
     auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -306,16 +293,14 @@ __global__ void __launch_bounds__(kT + 64, kPerSm<kT>)
         if (r * 32 + lane < in.k) next_id[r] = in.ids[row * in.k + r * 32 + lane];
       }
     };
-    if (row0 < num_rows) fetch(row0);
-    for (int64_t row = row0; row < num_rows; row += row_step, ++it) {
-      const int par = static_cast<int>(it & 1);
+    if (num_its > 0) fetch(row0);
+    for (uint32_t it = 0; it < num_its; ++it) {
+      const int64_t row = row0 + it * row_step;
       const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
       int32_t id[kPerLane];
 #pragma unroll
       for (int r = 0; r < kPerLane; ++r) id[r] = next_id[r];
-      if (row + row_step < num_rows) fetch(row + row_step);
-      float up = static_cast<float>(inv_t);
-      if (kGrad && in.grad_loss != nullptr) up *= in.grad_loss[row];
+      if (it + 1 < num_its) fetch(row + row_step);
       // the single elements at the piece's ends (warp 0), without listed ones
       float end_x[2] = {neg_inf(), neg_inf()};
       if (warp == 0 && (pc.c0 < pc.b0 || pc.b1 < pc.c1)) {
@@ -332,7 +317,16 @@ __global__ void __launch_bounds__(kT + 64, kPerSm<kT>)
           if (j >= 0 && !((mask >> (side * 8 + tid)) & 1)) end_x[side] = read_elem<kBf16>(pc.p, j);
         }
       }
-      // ---- the sum off the list
+      // the stages (mod 32) with listed logits among this warp's vectors
+      auto owns = [&](int c) {
+        return c >= pc.b0 && c < pc.b1 &&
+               static_cast<int>(static_cast<uint32_t>(c - pc.b0) / (32 * kVec)) % kWarps == warp;
+      };
+      uint32_t listed = 0;
+#pragma unroll
+      for (int s = 0; s < kPerLane; ++s)
+        if (owns(id[s])) listed |= 1u << ((id[s] - pc.b0) / (kStageVec<kT> * kVec) % 32);
+      listed = __reduce_or_sync(0xffffffffu, listed);
       RunSum a = {0.0f, neg_inf(), 0u};
       Place r = at;
       const int kept = kGrad ? max(0, pc.stages - slots) : pc.stages;  // the first that stays
@@ -342,30 +336,25 @@ __global__ void __launch_bounds__(kT + 64, kPerSm<kT>)
         uint4 *st = buf + r.slot * kStageVec<kT>;
         const int c = pc.b0 + j * kStageVec<kT> * kVec;
         const int n = min(kStageVec<kT>, (pc.b1 - c) / kVec);
-        // listed logits among this warp's vectors
-        bool mine[kPerLane], here = false;
-#pragma unroll
-        for (int s = 0; s < kPerLane; ++s) {
-          mine[s] = false;
-          if (s * 32 >= in.k) continue;
-          const uint32_t e = static_cast<uint32_t>(id[s] - c);
-          mine[s] = e < static_cast<uint32_t>(n * kVec) &&
-                    static_cast<int>(e / (32 * kVec)) % kWarps == warp;
-          here = here || mine[s];
-        }
-        if (__any_sync(0xffffffffu, here)) {
+        if ((listed >> (j % 32)) & 1) {
 #pragma unroll
           for (int s = 0; s < kPerLane; ++s)
-            if (mine[s]) store_elem<kBf16>(reinterpret_cast<char *>(st), id[s] - c, neg_inf());
+            if (owns(id[s]) && id[s] >= c && id[s] < c + n * kVec)
+              store_elem<kBf16>(reinterpret_cast<char *>(st), id[s] - c, neg_inf());
           // (the slot's next copy is ordered behind these writes)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
         uint4 q[kVecPerThread];
+        if (n == kStageVec<kT>) {
 #pragma unroll
-        for (int u = 0; u < kVecPerThread; ++u) {
-          const int i = u * kT + tid;
-          q[u] = i < n ? st[i] : make_uint4(kMasked, kMasked, kMasked, kMasked);
+          for (int u = 0; u < kVecPerThread; ++u) q[u] = st[u * kT + tid];
+        } else {
+#pragma unroll
+          for (int u = 0; u < kVecPerThread; ++u) {
+            const int i = u * kT + tid;
+            q[u] = i < n ? st[i] : make_uint4(kMasked, kMasked, kMasked, kMasked);
+          }
         }
         uint4 most = q[0];
 #pragma unroll
@@ -384,125 +373,198 @@ __global__ void __launch_bounds__(kT + 64, kPerSm<kT>)
         sum_rebase(a, end_x[side], scale, room);
         sum_add(a, end_x[side], neg_inf(), scale);
       }
-      // ---- joined over the warps and the cluster
       Sum rest = sum_warp(sum_result(a), scale);
-      if (lane == 0) sh.warp_sum[warp] = rest;
-      consumers_sync<kT>();
-      if (warp == 0)
-        rest = sum_warp(lane < kWarps ? sh.warp_sum[lane] : Sum{neg_inf(), 0.0f}, scale);
-      // (the list warp has read its logits before any CTA of the row may write over them)
-      ok = ok && warp_wait(smem_u32(&sh.ready[par]), static_cast<uint32_t>(it >> 1) & 1, abort_flag);
-      const uint4 part[1] = {make_uint4(__float_as_uint(rest.m), __float_as_uint(rest.s), 0u, 0u)};
-      ok = exchange<kT>(sh.ex, part, it, chunk, chunks, tid, ok, abort_flag);
-      if (!ok) {  // (every warp keeps to the rows' barriers)
-        if (lane == 0) raise_abort(&sh.ring.abort, err);
-        continue;
+      if (lane == 0) sh.warp_sum[it & 1][warp] = rest;
+      consumers_sync<kT>();  // (every warp keeps to the rows' barriers)
+      if (warp == static_cast<int>(it % kWarps)) {
+        rest = sum_warp(lane < kWarps ? sh.warp_sum[it & 1][lane] : Sum{neg_inf(), 0.0f}, scale);
+        // (the list warp has read its logits before any CTA of the row may write over
+        // them, and the row kHeld before this one is done with)
+        ok = ok && wait_held(sh.ready, it);
+        if (ok)
+          exchange_tell(sh.ex, it, make_uint4(__float_as_uint(rest.m), __float_as_uint(rest.s), 0u, 0u),
+                        chunk, chunks, lane);
       }
-      rest = {neg_inf(), 0.0f};
-      for (int c = 0; c < chunks; ++c) {
-        const uint4 q = sh.ex.part[par][c][0];
-        rest = sum_merge(rest, {__uint_as_float(q.x), __uint_as_float(q.y)}, scale);
-      }
-      const List &l = sh.list[par];
-      const Sum total = sum_merge(l.listed, rest, scale);
-      if (tid == 0) {
-        sh.total[par] = total;
-        sh.rest[par] = rest;
-      }
-      if (kGrad) {
-        // ---- the gradient off the list
-        const bool bad = is_nan(total.s);
-        const bool live = l.any && total.s != 0.0f;
-        const float m = rest.m == neg_inf() ? 0.0f : rest.m;
-        float coef = nan_f32();
-        if (!bad) {
-          const float share = sum_at(rest, total.m, scale) / total.s;  // s_r
-          coef = rest.s == 0.0f ? 0.0f : up * fmaf(l.total, share, -l.rest) / rest.s;
-        }
-        char *g = static_cast<char *>(in.grad) + row * ldg_bytes;
-        auto value = [&](float x) { return live ? coef * ex2((x - m) * scale) : 0.0f; };
-        r = later(at, kept, slots);
-        for (int i = 0; i < pc.stages; ++i) {
-          const bool again = i >= pc.stages - kept;  // loaded a second time
-          const int j = again ? i - (pc.stages - kept) : kept + i;
-          if (again) ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
-          if (!ok) break;
-          const uint4 *st = buf + r.slot * kStageVec<kT>;
-          const int c = pc.b0 + j * kStageVec<kT> * kVec;
-          const int n = min(kStageVec<kT>, (pc.b1 - c) / kVec);
-          char *o = g + static_cast<int64_t>(c) * kElt;
-          // bytes of the stage before the output's first whole vector
-          const int skip = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(o) & 15u)) & 15u);
-          uint4 *ov = reinterpret_cast<uint4 *>(o + skip);
-          if (skip == 0) {
-#pragma unroll
-            for (int u = 0; u < kVecPerThread; ++u) {
-              const int v = u * kT + tid;
-              if (v < n)
-                __stcs(ov + v, live ? grad_vec<kBf16>(st[v], m, scale, coef) : make_uint4(0, 0, 0, 0));
-            }
-          } else {
-            for (int v = tid; v < n - 1; v += kT)
-              __stcs(ov + v, live ? grad_vec<kBf16>(bytes_of(st[v], st[v + 1], skip), m, scale, coef)
-                                  : make_uint4(0, 0, 0, 0));
-            // the vector's worth of elements at both ends
-            if (tid < kVec) {
-              const int e = tid * kElt < skip ? tid : (n - 1) * kVec + tid;
-              store_elem<kBf16>(o, e, value(read_elem<kBf16>(reinterpret_cast<const char *>(st), e)));
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
-          step(r, slots);
-        }
-        if (!ok) {
-          if (lane == 0) raise_abort(&sh.ring.abort, err);
-          continue;
-        }
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          const int j = end_column(pc, side, tid);
-          if (j >= 0) store_elem<kBf16>(g, j, value(end_x[side]));
-        }
-        if (chunk == chunks - 1)
-          for (int j = valid + tid; j < width; j += kT) store_elem<kBf16>(g, j, 0.0f);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.stored[par]));
+      // (a slot's uses are waited for one by one: a wait tells only even from odd ones)
+      for (int j = 0; kGrad && j < kept; ++j, step(r, slots))
+        ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+      if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
       at = later(at, num_loads(pc.stages, slots, kGrad), slots);
     }
+  } else if (warp < kWarps + kGradWarps) {
+    // -------------------------------------------------------- gradient warps
+    Place at = {0, 0};
+    const int gtid = tid - kT;
+    float next_up = in.grad_loss != nullptr && num_its > 0 ? in.grad_loss[row0] : 1.0f;
+    for (uint32_t it = 0; it < num_its; ++it) {
+      const int64_t row = row0 + it * row_step;
+      const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
+      const float up = next_up * in.inv_t32;
+      if (in.grad_loss != nullptr && it + 1 < num_its) next_up = in.grad_loss[row + row_step];
+      float end_x[2] = {neg_inf(), neg_inf()};
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int j = end_column(pc, side, gtid);
+        if (j >= 0) end_x[side] = read_elem<kBf16>(pc.p, j);
+      }
+      ok = exchange_wait(sh.ex, it, abort_flag) && wait_held(sh.ready, it);
+      if (!ok) break;
+      const Sum rest = exchange_sum(sh.ex, it, chunks, lane, scale);
+      const List &l = sh.list[it % kHeld];
+      const Sum total = sum_merge(l.listed, rest, scale);
+      const bool live = l.any && total.s != 0.0f;
+      const float m = rest.m == neg_inf() ? 0.0f : rest.m;
+      float coef = nan_f32();
+      if (!is_nan(total.s)) {
+        const float share = sum_at(rest, total.m, scale) / total.s;  // s_r
+        coef = rest.s == 0.0f ? 0.0f : up * fmaf(l.total, share, -l.rest) / rest.s;
+      }
+      char *g = static_cast<char *>(in.grad) + row * ldg_bytes;
+      auto value = [&](float x) { return live ? coef * ex2((x - m) * scale) : 0.0f; };
+      const int kept = max(0, pc.stages - slots);
+      Place r = later(at, kept, slots);
+      for (int i = 0; i < pc.stages; ++i) {
+        // (stages that stayed are there since the row's sum; waiting again costs nothing)
+        const bool again = i >= pc.stages - kept;  // loaded a second time
+        const int j = again ? i - (pc.stages - kept) : kept + i;
+        ok = warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+        if (!ok) break;
+        const uint4 *st = buf + r.slot * kStageVec<kT>;
+        const int c = pc.b0 + j * kStageVec<kT> * kVec;
+        const int n = min(kStageVec<kT>, (pc.b1 - c) / kVec);
+        char *o = g + static_cast<int64_t>(c) * kElt;
+        // bytes of the stage before the output's first whole vector
+        const int skip = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(o) & 15u)) & 15u);
+        uint4 *ov = reinterpret_cast<uint4 *>(o + skip);
+        if (skip == 0 && live && n == kStageVec<kT>) {
+          uint4 q[kVecPerThread];
+#pragma unroll
+          for (int u = 0; u < kVecPerThread; ++u) q[u] = st[u * kT + gtid];
+#pragma unroll
+          for (int u = 0; u < kVecPerThread; ++u)
+            __stcs(ov + u * kT + gtid, grad_vec<kBf16>(q[u], m, scale, coef));
+        } else if (skip == 0) {
+          for (int v = gtid; v < n; v += kT)
+            __stcs(ov + v, live ? grad_vec<kBf16>(st[v], m, scale, coef) : make_uint4(0, 0, 0, 0));
+        } else {
+          for (int v = gtid; v < n - 1; v += kT)
+            __stcs(ov + v, live ? grad_vec<kBf16>(bytes_of(st[v], st[v + 1], skip), m, scale, coef)
+                                : make_uint4(0, 0, 0, 0));
+          // the vector's worth of elements at both ends
+          if (gtid < kVec) {
+            const int e = gtid * kElt < skip ? gtid : (n - 1) * kVec + gtid;
+            store_elem<kBf16>(o, e, value(read_elem<kBf16>(reinterpret_cast<const char *>(st), e)));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
+        step(r, slots);
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int j = end_column(pc, side, gtid);
+        if (j >= 0) store_elem<kBf16>(g, j, value(end_x[side]));
+      }
+      if (chunk == chunks - 1)
+        for (int j = valid + gtid; j < width; j += kT) store_elem<kBf16>(g, j, 0.0f);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.stored[it % kHeld]));
+      at = later(at, num_loads(pc.stages, slots, true), slots);
+    }
+    if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
+  } else if (warp == kWarps + kGradWarps) {
+    copy_rows<kBf16, kT>(sh.ring, buf, slots, kGrad, logits, ld_bytes, row0, row_step, num_rows,
+                         valid, chunk, chunks, lane, err);
+    pdl_launch_dependents();
+  } else {
+    // ------------------------------------------------------------ list warps
+    auto finish = [&](uint32_t it) {
+      const int64_t row = row0 + it * row_step;
+      if (!exchange_wait(sh.ex, it, abort_flag)) return false;
+      exchange_rearm(sh.ex, it, chunks, lane);
+      const List &l = sh.list[it % kHeld];
+      const Sum rest = exchange_sum(sh.ex, it, chunks, lane, scale);
+      const Sum total = sum_merge(l.listed, rest, scale);
+      if (chunk == 0 &&
+          (in.out_loss != nullptr || in.out_lse != nullptr || in.out_lse_rest != nullptr)) {
+        // lane 0: lse, lane 1: lse_rest, lane 2: log p_r
+        const double rest_p = rest.s == 0.0f ? 0.0 : l.rest_p;
+        const float of = lane == 0 ? total.s : (lane == 1 ? rest.s : static_cast<float>(rest_p));
+        const Sum own = lane == 0 ? total : rest;
+        const double lg = log_of(of);
+        const double v = is_nan(total.s) ? nan("") : (own.s == 0.0f ? -INFINITY
+                                                                    : own.m * inv_t + lg);
+        const double lse = __shfl_sync(0xffffffffu, v, 0);
+        const double lse_rest = __shfl_sync(0xffffffffu, v, 1);
+        const double log_rest = __shfl_sync(0xffffffffu, lg, 2);
+        if (lane == 1 && in.out_lse_rest != nullptr)
+          in.out_lse_rest[row] = static_cast<float>(v);
+        if (lane == 0) {
+          if (in.out_lse != nullptr) in.out_lse[row] = static_cast<float>(v);
+          double loss = l.part;
+          if (lse != -INFINITY) loss += l.sum_p * lse;  // (else it is +inf or 0)
+          if (!(rest_p <= 0.0)) loss += rest_p * (log_rest - (lse_rest - lse));
+          if (!l.any) loss = 0.0;
+          if (in.out_loss != nullptr) in.out_loss[row] = static_cast<float>(loss);
+        }
+      }
+      if (kGrad) {
+        float up = in.inv_t32;
+        if (in.grad_loss != nullptr) up *= in.grad_loss[row];
+        if (!wait_held(sh.stored, it)) return false;
+        if (l.any && total.s != 0.0f) {
+          const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
+          char *g = static_cast<char *>(in.grad) + row * ldg_bytes;
+          const float of = (rest.s == 0.0f ? l.on_list : l.total) / total.s;
+          for (int i = lane; i < in.k; i += 32) {
+            const int32_t id = l.id[i];
+            if (!l.first[i] || id < pc.c0 || id >= pc.c1) continue;
+            store_elem<kBf16>(g, id, up * (of * ex2((l.x[i] - total.m) * scale) - l.p[i]));
+          }
+        }
+      }
+      __syncwarp();
+      return true;
+    };
+    const uint32_t first = static_cast<uint32_t>(warp - kWarps - kGradWarps - 1);
+    Entries next;
+    float next_lse = 0.0f;
+    auto fetch = [&](int64_t row) {
+      entries_load<kBf16>(next, in, row, logits + row * ld_bytes, valid, 0, valid, lane);
+      if (in.lse != nullptr) next_lse = in.lse[row];
+    };
+    if (first < num_its) fetch(row0 + first * row_step);
+    uint32_t it = first;
+    for (; it < num_its && ok; it += F::kLists) {
+      const int64_t row = row0 + it * row_step;
+      teacher_row(sh.list[it % kHeld], next, in.k, next_lse, in.lse != nullptr, inv_t, scale, lane);
+      if (lane == 0) mbar_arrive(smem_u32(&sh.ready[it % kHeld]));
+      if (it + F::kLists < num_its) fetch(row + F::kLists * row_step);
+      if (it >= F::kLists) ok = finish(it - F::kLists);
+    }
+    if (ok && it >= F::kLists && it != first) ok = finish(it - F::kLists);
+    if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
   }
-  if (chunks > 1) {  // no CTA ends while another may write to it
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-  }
+  leave(sh.ring, chunks);
 }
 
 template <bool kBf16, int kT, bool kGrad>
 cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t width, int64_t valid,
-                        const DistillArgs &in, int64_t ldg, int chunks, int num_sms, uint32_t *err,
-                        cudaStream_t stream) {
+                        const Args &in, int64_t ldg, uint32_t *err, cudaStream_t stream) {
+  using F = Form<kT, kGrad>;
   constexpr int kElt = kBf16 ? 2 : 4;
   auto kern = distill_kernel<kBf16, kT, kGrad>;
-  const cudaError_t e =
-      set_smem_once(reinterpret_cast<const void *>(kern), kRingBytes<kT>,
-                    (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2) + (kGrad ? 0 : 4));
+  const RowKernel k = {reinterpret_cast<const void *>(kern), F::kThreads, F::kRingBytes,
+                       (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2) + (kGrad ? 0 : 4)};
+  int64_t resident[6];
+  const cudaError_t e = resident_clusters(k, resident);
   if (e != cudaSuccess) return e;
-  const int64_t resident = resident_clusters(chunks, kPerSm<kT>, num_sms);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows < resident ? rows : resident) * chunks));
-  cfg.blockDim = dim3(kT + 64);
-  cfg.dynamicSmemBytes = kRingBytes<kT>;
-  cfg.stream = stream;
+  int chunks =
+      kT == 256 ? pick_chunks(rows, valid * kElt, kGrad ? F::kRingBytes : 0, 0.85, resident) : 1;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = chunks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cudaLaunchConfig_t cfg = {};
+  row_launch(k, rows, chunks, resident, stream, attr, cfg);
   return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits), ld * kElt, rows,
                             static_cast<int>(valid), static_cast<int>(width), in, ldg * kElt,
                             chunks, err);
@@ -519,7 +581,7 @@ constexpr int kBatch = 4;  // loads in flight per thread
 // different 16-byte offsets.
 template <bool kBf16, bool kShift>
 __global__ void __launch_bounds__(kThreads)
-    distill_grad_kernel(const char *logits, int64_t ld_bytes, int valid, int width, DistillArgs in,
+    distill_grad_kernel(const char *logits, int64_t ld_bytes, int valid, int width, Args in,
                         int chunks, int64_t ldg_bytes) {
   constexpr int kElt = kBf16 ? 2 : 4;
   constexpr int kVec = 16 / kElt;
@@ -566,23 +628,18 @@ __global__ void __launch_bounds__(kThreads)
   };
   load(vs + tid);
 
-  const double inv_t = 1.0 / static_cast<double>(in.temperature);
-  const float scale = static_cast<float>(1.4426950408889634 * inv_t);
+  const double inv_t = in.inv_t;
+  const float scale = in.scale;
   const float lse = in.in_lse[row];
   const float lse_rest = in.in_lse_rest != nullptr ? in.in_lse_rest[row] : neg_inf();
   const float up =
-      (in.grad_loss != nullptr ? in.grad_loss[row] : 1.0f) * static_cast<float>(inv_t);
+      (in.grad_loss != nullptr ? in.grad_loss[row] : 1.0f) * in.inv_t32;
   if (tid < 32) {
-    for (int i = tid; i < in.k; i += 32) {
-      const int32_t id = in.ids[row * in.k + i];
-      const bool entry = id >= 0 && id < valid;
-      l.id[i] = entry ? id : -1;
-      l.z[i] = in.logits[row * in.k + i];
-      // (read before the pass may write over it)
-      l.x[i] = entry && id >= c0 && id < c1 ? read_elem<kBf16>(x, id) : neg_inf();
-    }
-    __syncwarp();
-    teacher_row(l, in.k, in.lse, row, inv_t, scale, tid);
+    // (its logits are read before the pass may write over them)
+    Entries e;
+    entries_load<kBf16>(e, in, row, x, valid, c0, c1, tid);
+    teacher_row(l, e, in.k, in.lse != nullptr ? in.lse[row] : 0.0f, in.lse != nullptr, inv_t, scale,
+                tid);
   }
   __syncthreads();
   const bool live = l.any && lse != neg_inf();
@@ -624,12 +681,12 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   if (live && tid < in.k && l.first[tid] && l.id[tid] >= c0 && l.id[tid] < c1) {
     const float s = total * ex2(fmaf(l.x[tid], scale, -lse * kLog2e));
-    store_elem<kBf16>(g, l.id[tid], up * (s - static_cast<float>(l.p[tid])));
+    store_elem<kBf16>(g, l.id[tid], up * (s - l.p[tid]));
   }
 }
 
 cudaError_t launch_grad(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t width,
-                        int64_t valid, const DistillArgs &in, int64_t ldg, int num_sms,
+                        int64_t valid, const Args &in, int64_t ldg, int num_sms,
                         cudaStream_t stream) {
   const int elt = dtype == SGA_BF16 ? 2 : 4;
   // pieces of 64 KB, or down to 16 KB where the SMs would not have eight each
@@ -661,18 +718,19 @@ cudaError_t launch_grad(const void *logits, int dtype, int64_t rows, int64_t ld,
 }  // namespace
 
 cudaError_t launch_distill(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t width,
-                           int64_t valid, const DistillArgs &args, int64_t ldg, int num_sms,
+                           int64_t valid, const DistillArgs &in, int64_t ldg, int num_sms,
                            uint32_t *err, cudaStream_t stream) {
+  const double inv_t = 1.0 / static_cast<double>(in.temperature);
+  const Args args = {in, inv_t, static_cast<float>(inv_t),
+                     static_cast<float>(1.4426950408889634 * inv_t)};
   if (args.in_lse != nullptr)
     return launch_grad(logits, dtype, rows, ld, width, valid, args, ldg, num_sms, stream);
-  const int64_t bytes = valid * (dtype == SGA_BF16 ? 2 : 4);
   const bool kept = args.grad != nullptr;
-  const bool small = small_rows(rows, bytes, num_sms);
-  const int chunks = small ? 1 : pick_chunks(rows, bytes, kept ? kRingBytes<256> : 0, num_sms);
+  const bool small = small_rows(rows, valid * (dtype == SGA_BF16 ? 2 : 4), num_sms);
   auto launch = [&](auto bf16, auto grad) {
     constexpr bool kBf16 = decltype(bf16)::value, kGrad = decltype(grad)::value;
     return (small ? launch_rows<kBf16, 64, kGrad> : launch_rows<kBf16, 256, kGrad>)(
-        logits, rows, ld, width, valid, args, ldg, chunks, num_sms, err, stream);
+        logits, rows, ld, width, valid, args, ldg, err, stream);
   };
   if (dtype == SGA_BF16)
     return kept ? launch(std::true_type{}, std::true_type{})

@@ -17,7 +17,7 @@ constexpr int kRingBytes = kSlots<kT> * kStageVec<kT> * 16;
 template <int kT>
 struct ProbsShared {
   Ring ring;
-  Exchange<1> ex;
+  Exchange<2> ex;
   Sum warp_sum[kT / 32];
   int32_t warp_id[kT / 32];
 };
@@ -166,13 +166,17 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
         else
           total = sum_warp(total, scale);
       }
-      const uint4 mine[1] = {make_uint4(__float_as_uint(total.m), __float_as_uint(total.s),
-                                        static_cast<uint32_t>(best_id), 0u)};
-      ok = exchange<kT>(sh.ex, mine, it, chunk, chunks, tid, ok, abort_flag);
+      if (warp == 0 && ok)
+        exchange_tell(sh.ex, static_cast<uint32_t>(it),
+                      make_uint4(__float_as_uint(total.m), __float_as_uint(total.s),
+                                 static_cast<uint32_t>(best_id), 0u),
+                      chunk, chunks, lane);
+      ok = ok && exchange_wait(sh.ex, static_cast<uint32_t>(it), abort_flag);
+      if (ok && warp == 0) exchange_rearm(sh.ex, static_cast<uint32_t>(it), chunks, lane);
       total = {neg_inf(), 0.0f};
       best_id = kNoId;
       for (int c = 0; c < chunks; ++c) {
-        const uint4 q = sh.ex.part[it & 1][c][0];
+        const uint4 q = sh.ex.part[it & 1][c];
         const Sum o = {__uint_as_float(q.x), __uint_as_float(q.y)};
         if (!greedy) {
           total = sum_merge(total, o, scale);
@@ -240,35 +244,24 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
       at = later(at, num_loads(pc.stages, slots, true), slots);
     }
   }
-  if (chunks > 1) {  // no CTA ends while another may write to it
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-  }
+  leave(sh.ring, chunks);
 }
 
 template <bool kBf16, int kT>
 cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t width, int64_t valid,
-                        const float *temperature, float *probs, int64_t ldp, int chunks,
-                        int num_sms, uint32_t *err, cudaStream_t stream) {
+                        const float *temperature, float *probs, int64_t ldp, uint32_t *err,
+                        cudaStream_t stream) {
   auto kern = probs_kernel<kBf16, kT>;
-  const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kern), kRingBytes<kT>,
-                                      (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2));
+  const RowKernel k = {reinterpret_cast<const void *>(kern), kT + 32, kRingBytes<kT>,
+                       (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2)};
+  int64_t resident[6];
+  const cudaError_t e = resident_clusters(k, resident);
   if (e != cudaSuccess) return e;
-  const int64_t resident = resident_clusters(chunks, kPerSm<kT>, num_sms);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows < resident ? rows : resident) * chunks));
-  cfg.blockDim = dim3(kT + 32);
-  cfg.dynamicSmemBytes = kRingBytes<kT>;
-  cfg.stream = stream;
+  const int chunks =
+      kT == 256 ? pick_chunks(rows, valid * (kBf16 ? 2 : 4), kRingBytes<kT>, 0.625, resident) : 1;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = chunks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cudaLaunchConfig_t cfg = {};
+  row_launch(k, rows, chunks, resident, stream, attr, cfg);
   return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits),
                             ld * (kBf16 ? 2 : 4), rows, static_cast<int>(valid),
                             static_cast<int>(width), temperature, probs, ldp, chunks, err);
@@ -279,13 +272,10 @@ cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t wi
 cudaError_t launch_probs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t width,
                          int64_t valid, const float *temperature, float *probs, int64_t ldp,
                          int num_sms, uint32_t *err, cudaStream_t stream) {
-  const int64_t bytes = valid * (dtype == SGA_BF16 ? 2 : 4);
-  const bool small = small_rows(rows, bytes, num_sms);
-  const int chunks = small ? 1 : pick_chunks(rows, bytes, kRingBytes<256>, num_sms);
+  const bool small = small_rows(rows, valid * (dtype == SGA_BF16 ? 2 : 4), num_sms);
   auto launch = dtype == SGA_BF16 ? (small ? launch_rows<true, 64> : launch_rows<true, 256>)
                                   : (small ? launch_rows<false, 64> : launch_rows<false, 256>);
-  return launch(logits, rows, ld, width, valid, temperature, probs, ldp, chunks, num_sms, err,
-                stream);
+  return launch(logits, rows, ld, width, valid, temperature, probs, ldp, err, stream);
 }
 
 }  // namespace sga

@@ -10,6 +10,8 @@
 // the ring keeps its last ones; the others are loaded a second time.
 #pragma once
 
+#include <mutex>
+
 #include "pipe.cuh"
 #include "scan.cuh"
 
@@ -24,7 +26,7 @@ constexpr int kStageVec = kT * kVecPerThread;
 // CTAs per SM: two with 256 consumers, eight with 64 (short rows).
 template <int kT>
 constexpr int kPerSm = 512 / kT;
-constexpr int kMaxSlots = 7;
+constexpr int kMaxSlots = 13;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ float nan_f32() { return __int_as_float(0x7fc00000); }
@@ -227,33 +229,33 @@ __device__ __forceinline__ Sum sum_merge(const Sum &a, const Sum &b, float scale
   return {m, sum_at(a, m, scale) + sum_at(b, m, scale)};
 }
 
-// Over the lanes of a warp (or its first `lanes`).
+// Over groups of kN lanes of a warp.
+template <int kN = 32>
 __device__ __forceinline__ Sum sum_warp(Sum a, float scale) {
   float m = a.m;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  for (int off = kN / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   float s = sum_at(a, m, scale);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  for (int off = kN / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   return {m, s};
 }
 
 // ---------------------------------------------------------------- exchange
 
-// What the CTAs of a cluster tell each other about a row, kQ 16-byte words each;
-// by turns in two buffers: a CTA tells of row r + 2 when all have told of row r + 1,
-// so all have read row r.
-template <int kQ>
+// What the CTAs of a cluster tell each other about their it-th row, 16 bytes each,
+// by turns in kN buffers (a power of two).
+template <int kN>
 struct Exchange {
-  uint64_t bar[2];
-  alignas(16) uint4 part[2][kMaxCluster][kQ];
+  uint64_t bar[kN];
+  alignas(16) uint4 part[kN][kMaxCluster];
 };
 
-template <int kQ>
-__device__ __forceinline__ void exchange_init(Exchange<kQ> &ex, int chunks) {
-  for (int i = 0; i < 2; ++i) {
+template <int kN>
+__device__ __forceinline__ void exchange_init(Exchange<kN> &ex, int chunks) {
+  for (int i = 0; i < kN; ++i) {
     mbar_init(smem_u32(&ex.bar[i]), 1);
-    mbar_expect_tx(smem_u32(&ex.bar[i]), static_cast<uint32_t>(chunks) * kQ * 16);
+    mbar_expect_tx(smem_u32(&ex.bar[i]), static_cast<uint32_t>(chunks) * 16);
   }
 }
 
@@ -268,45 +270,124 @@ __device__ __forceinline__ void st_async(uint32_t addr, const uint4 v, uint32_t 
       : "memory");
 }
 
-// The consumers' exchange for their it-th row; `mine` is that of warp 0, the same
-// in all lanes.  The parts are then in ex.part[it & 1].  A warp that has given up
-// (ok false) tells and waits no more.
-template <int kT, int kQ>
-__device__ __forceinline__ bool exchange(Exchange<kQ> &ex, const uint4 (&mine)[kQ], int64_t it,
-                                         int chunk, int chunks, int tid, bool ok,
-                                         const volatile int *abort_flag) {
-  const int par = static_cast<int>(it & 1);
-  if (chunks == 1) {
-    if (tid == 0)
-      for (int q = 0; q < kQ; ++q) ex.part[par][0][q] = mine[q];
-    consumers_sync<kT>();
-    return ok;
-  }
-  if (ok && tid < chunks)
-    for (int q = 0; q < kQ; ++q)
-      st_async(smem_u32(&ex.part[par][chunk][q]), mine[q], smem_u32(&ex.bar[par]), tid);
+// One warp tells every CTA (its own too).
+template <int kN>
+__device__ __forceinline__ void exchange_tell(Exchange<kN> &ex, uint32_t it, const uint4 mine,
+                                              int chunk, int chunks, int lane) {
+  if (lane < chunks)
+    st_async(smem_u32(&ex.part[it % kN][chunk]), mine, smem_u32(&ex.bar[it % kN]), lane);
   __syncwarp();
-  ok = ok && warp_wait(smem_u32(&ex.bar[par]), static_cast<uint32_t>(it >> 1) & 1, abort_flag);
-  if (ok && tid == 0)
-    mbar_expect_tx(smem_u32(&ex.bar[par]), static_cast<uint32_t>(chunks) * kQ * 16);
-  return ok;
+}
+
+template <int kN>
+__device__ __forceinline__ bool exchange_wait(Exchange<kN> &ex, uint32_t it,
+                                              const volatile int *abort_flag) {
+  return warp_wait(smem_u32(&ex.bar[it % kN]), (it / kN) & 1, abort_flag);
+}
+
+// The buffer's next use; by one warp that has waited for this one.
+template <int kN>
+__device__ __forceinline__ void exchange_rearm(Exchange<kN> &ex, uint32_t it, int chunks, int lane) {
+  if (lane == 0) mbar_expect_tx(smem_u32(&ex.bar[it % kN]), static_cast<uint32_t>(chunks) * 16);
+}
+
+// The sum of the parts, whose first two words are a Sum (in every lane; the same in
+// every CTA).
+template <int kN>
+__device__ __forceinline__ Sum exchange_sum(const Exchange<kN> &ex, uint32_t it, int chunks,
+                                            int lane, float scale) {
+  Sum s = {neg_inf(), 0.0f};
+  const int c = lane % kMaxCluster;
+  if (c < chunks) {
+    const uint4 q = ex.part[it % kN][c];
+    s = {__uint_as_float(q.x), __uint_as_float(q.y)};
+  }
+  return sum_warp<kMaxCluster>(s, scale);
+}
+
+// The end of a kernel: no CTA ends while another may write to it.  After a wait that
+// gave up, what was told may still be on its way (some us).
+__device__ __forceinline__ void leave(const Ring &ring, int chunks) {
+  __syncwarp();
+  if (chunks > 1)
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  if (*static_cast<const volatile int *>(&ring.abort) != 0) {
+    const unsigned long long t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 100000) {
+    }
+  }
 }
 
 // ------------------------------------------------------------------- host
 
-// Clusters of `chunks` CTAs that run at once: a cluster lies in one GPC, whose SMs
-// are not all a multiple of it (as cudaOccupancyMaxActiveClusters counts them on
-// 152 SMs; a grid with more would leave its last clusters a second round).
-inline int64_t resident_clusters(int chunks, int per_sm, int num_sms) {
-  const int64_t ctas = static_cast<int64_t>(per_sm) * num_sms;
-  switch (chunks) {
-    case 1: return ctas;
-    case 2: return ctas / 2;
-    case 3: return ctas * 97 / 304;
-    case 4: return ctas * 74 / 304;
-    case 6: return ctas * 46 / 304;
-    default: return ctas * 36 / 304;
+// A kernel of this kind and how it is launched.
+struct RowKernel {
+  const void *kern;
+  int threads, smem;  // dynamic shared memory
+  int slot;           // of this file's kernels, 0 .. 7
+};
+
+constexpr int kWidths[6] = {8, 6, 4, 3, 2, 1};  // CTAs that may share a row
+
+// Clusters of each width that run at once (a cluster lies in one GPC, whose SMs are
+// not all a multiple of it: of 152 SMs 8 x 15, 6 x 23, 4 x 36, 3 x 46, 2 x 76, or with
+// two CTAs per SM 36, 46, 74, 97, 152).  A grid with more would leave its last clusters
+// a second round.  Asked once per device.
+inline cudaError_t resident_clusters(const RowKernel &k, int64_t (&out)[6]) {
+  struct Entry {
+    uintptr_t ctx;
+    int n[6];
+  };
+  static std::mutex mu;
+  static Entry cache[8][64] = {};
+  cudaError_t e = set_smem_once(k.kern, k.smem, k.slot);
+  int dev = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uintptr_t ctx = current_context_key();
+  std::lock_guard<std::mutex> lock(mu);
+  Entry &c = cache[k.slot][dev];
+  if (ctx == 0 || c.ctx != ctx) {
+    for (int i = 0; i < 6; ++i) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(kWidths[i]));
+      cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
+      cfg.dynamicSmemBytes = k.smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = kWidths[i];
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&c.n[i], k.kern, &cfg);
+      if (e != cudaSuccess) return e;
+    }
+    c.ctx = current_context_key();
   }
+  for (int i = 0; i < 6; ++i) out[i] = c.n[i] > 0 ? c.n[i] : 1;
+  return cudaSuccess;
+}
+
+// The launch of rows, `chunks` CTAs each, as a persistent grid.
+inline void row_launch(const RowKernel &k, int64_t rows, int chunks, const int64_t (&resident)[6],
+                       cudaStream_t stream, cudaLaunchAttribute (&attr)[2],
+                       cudaLaunchConfig_t &cfg) {
+  int64_t n = rows;
+  for (int i = 0; i < 6; ++i)
+    if (kWidths[i] == chunks && resident[i] < n) n = resident[i];
+  cfg.gridDim = dim3(static_cast<unsigned>(n * chunks));
+  cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
+  cfg.dynamicSmemBytes = k.smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = chunks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
 }
 
 // Many rows of up to 48 KB: small CTAs, eight per SM, a row each (bf16
@@ -319,19 +400,17 @@ inline bool small_rows(int64_t rows, int64_t bytes, int num_sms) {
 // CTAs that share a row.  Few rows: as many as let all rows run at once, with at
 // least 4 KB each (96 rows of 200064 bf16 ids: 3 CTAs 27 us, in rounds 4 33 us).
 // Otherwise one, or where rows are kept in a ring of `ring` bytes per CTA the fewest
-// whose pieces leave it room for the next row's loads (2048 rows of 202048: 6 CTAs
-// 403 us, 4 408; 2000 rows of 50257 fp32 ids: 3 138, 2 148).
-inline int pick_chunks(int64_t rows, int64_t bytes, int64_t ring, int num_sms) {
-  constexpr int kWidths[6] = {8, 6, 4, 3, 2, 1};
-  for (int c : kWidths)
-    if (c == 1 || (rows <= resident_clusters(c, 2, num_sms) && bytes >= 4096 * c)) {
-      if (ring == 0) return c;
-      if (rows <= resident_clusters(c, 2, num_sms) && bytes <= ring * 5 / 4 * c) return c;
+// whose pieces are at most `share` of it.
+inline int pick_chunks(int64_t rows, int64_t bytes, int64_t ring, double share,
+                       const int64_t (&resident)[6]) {
+  for (int i = 0; i < 6; ++i)
+    if (kWidths[i] == 1 || (rows <= resident[i] && bytes >= 4096 * kWidths[i])) {
+      if (ring == 0 || (rows <= resident[i] && bytes <= ring * 5 / 4 * kWidths[i])) return kWidths[i];
       break;
     }
   int best = kMaxCluster;
   for (int c : kWidths)
-    if (bytes <= ring * 5 / 8 * c) best = c;
+    if (bytes <= share * ring * c) best = c;
   return best;
 }
 
