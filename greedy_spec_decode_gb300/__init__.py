@@ -588,9 +588,10 @@ def sga_token_logprobs_grad(logits, shard_start, org_vocab, tokens, lse, entropy
 
 def _probs_2d(t, name):
     """(rows, columns, row stride, address) of fp32 probabilities."""
-    if t.dtype is not _F32 or t.dim() != 2:
+    shape = t.shape
+    if t.dtype is not _F32 or len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D float32 tensor")
-    rows, width = t.shape
+    rows, width = shape
     ld, col = t.stride()
     if col != 1 and width > 1:
         raise ValueError(f"{name} must have unit stride along the vocab")
@@ -654,7 +655,7 @@ def sga_sampled_verify(target_probs, draft_probs, cu_num_draft, draft_tokens, ac
 
 def _teacher_lists(rows, teacher_ids, teacher_logits, teacher_lse):
     """Addresses of a teacher's lists, and k."""
-    k = teacher_ids.size(-1)
+    k = teacher_ids.shape[-1]
     return (_check_out(teacher_ids, _I32, rows * k, "teacher_ids"),
             _check_out(teacher_logits, _F32, rows * k, "teacher_logits"), k,
             _check_out(teacher_lse, _F32, rows, "teacher_lse"))
@@ -664,10 +665,12 @@ def _grad_2d(logits, out_grad, rows, width):
     """Address and row stride of a gradient like logits."""
     if out_grad is None:
         return None, 0
-    if out_grad.dtype != logits.dtype or out_grad.shape != logits.shape or (
-            width > 1 and out_grad.stride(1) != 1):
-        raise ValueError("out_grad must match logits, unit stride along the vocab")
-    return out_grad.data_ptr(), out_grad.stride(0) if rows > 1 else max(out_grad.stride(0), width)
+    if out_grad.dtype is not logits.dtype or out_grad.shape != (rows, width):
+        raise ValueError("out_grad must match logits")
+    ldg, col = out_grad.stride()
+    if col != 1 and width > 1:
+        raise ValueError("out_grad must have unit stride along the vocab")
+    return out_grad.data_ptr(), ldg if rows > 1 else max(ldg, width)
 
 
 def sga_distill(logits, org_vocab, teacher_ids, teacher_logits, out_loss=None, teacher_lse=None,

@@ -40,6 +40,7 @@ struct alignas(16) List {
   double part;                  // sum of p_i (log p_i - y_i)
   float total, on_list, rest;   // sum_p + rest_p, sum_p, rest_p
   int any;                      // the row has a teacher
+  float m, coef, of;            // (kBackward) off the list the gradient is coef 2^((x - m) scale)
 };
 
 // Sums of a and b over a warp: a's in lanes 0-15, b's in 16-31 (64-bit additions are
@@ -179,15 +180,19 @@ __device__ __forceinline__ void teacher_row(List &l, const Entries &e, int k, fl
 
 // ------------------------------------------------------------ loss (and gradient)
 
+// The loss; the loss and its gradient; the gradient from the saved sums.
+enum Mode { kLoss, kBoth, kBackward };
+
 // Long rows (kT 256) and short ones (64): CTAs per SM, stages of the ring (16 or
 // 4 KB; the most that fits), and list warps.
-template <int kT, bool kGrad>
+template <int kT, Mode kMode>
 struct Form {
-  static constexpr int kPerSm = kT == 256 ? (kGrad ? 1 : 2) : (kGrad ? 4 : 6);
-  static constexpr int kSlots = kT == 256 ? (kGrad ? 12 : 5) : (kGrad ? 9 : 5);
+  static constexpr bool kSum = kMode != kBackward, kGrad = kMode != kLoss;
+  static constexpr int kPerSm = kT == 256 ? (kMode == kBoth ? 1 : 2) : (kMode == kBoth ? 4 : 6);
+  static constexpr int kSlots = kT == 256 ? (kMode == kBoth ? 12 : 5) : (kMode == kBoth ? 9 : 5);
   static constexpr int kLists = kT == 256 ? 4 : 2;
   static constexpr int kRingBytes = kSlots * kStageVec<kT> * 16;
-  static constexpr int kThreads = (kGrad ? 2 : 1) * kT + 32 + 32 * kLists;
+  static constexpr int kThreads = (kMode == kBoth ? 2 : 1) * kT + 32 + 32 * kLists;
 };
 
 // kLists list warps work on rows in turn, each one ahead.
@@ -234,26 +239,26 @@ __device__ __forceinline__ uint4 grad_vec(const uint4 q, float m, float scale, f
 // the rest's, and no other logit is compared with an id); the gradient warps write
 // out what the ring has kept, a row or two behind; list warps work out the teacher's
 // numbers a row ahead, reading the listed logits by themselves, and write the loss
-// and the listed ids' gradients a row behind.
-template <bool kBf16, int kT, bool kGrad>
-__global__ void __launch_bounds__(Form<kT, kGrad>::kThreads, Form<kT, kGrad>::kPerSm)
+// and the listed ids' gradients a row behind.  kBackward has no sum warps: a row's
+// pieces have nothing in common but the teacher's numbers, and are rows of their own.
+template <bool kBf16, int kT, Mode kMode>
+__global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kPerSm)
     distill_kernel(const char *logits, int64_t ld_bytes, int64_t num_rows, int valid, int width,
                    Args in, int64_t ldg_bytes, int chunks, uint32_t *err) {
-  using F = Form<kT, kGrad>;
+  using F = Form<kT, kMode>;
   using Shared = DistillShared<kT, F::kLists>;
+  constexpr bool kGrad = F::kGrad;
   constexpr int kElt = kBf16 ? 2 : 4;
   constexpr int kVec = 16 / kElt;
   constexpr int kWarps = kT / 32;
-  constexpr int kGradWarps = kGrad ? kWarps : 0;
+  constexpr int kSumWarps = F::kSum ? kWarps : 0, kGradWarps = kGrad ? kWarps : 0;
   constexpr int slots = F::kSlots;
   constexpr uint32_t kHeld = Shared::kHeld;
   constexpr uint32_t kMasked = kBf16 ? 0xff80ff80u : 0xff800000u;  // -inf
   extern __shared__ __align__(128) uint4 buf[];
   __shared__ Shared sh;
-  const int chunk = static_cast<int>(blockIdx.x % chunks);
-  const int64_t row0 = blockIdx.x / chunks, row_step = gridDim.x / chunks;
-  const uint32_t num_its =
-      static_cast<uint32_t>(row0 < num_rows ? (num_rows - row0 + row_step - 1) / row_step : 0);
+  const auto walk = walk_of<kMode == kBackward>(num_rows, chunks);
+  const uint32_t num_its = walk.n;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const volatile int *abort_flag = &sh.ring.abort;
   const double inv_t = in.inv_t;
@@ -272,16 +277,19 @@ __global__ void __launch_bounds__(Form<kT, kGrad>::kThreads, Form<kT, kGrad>::kP
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  if (chunks > 1)  // every CTA's barriers are ready
+  if (F::kSum && chunks > 1)  // every CTA's barriers are ready
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   pdl_wait();
 
+  auto piece = [&](uint32_t it) {
+    return piece_of<kBf16, kT>(logits + walk.row(it) * ld_bytes, valid, walk.chunk_of(it), chunks);
+  };
   // waits for the it-th row's list, or its stored gradient
   auto wait_held = [&](uint64_t (&bar)[kHeld], uint32_t it) {
     return warp_wait(smem_u32(&bar[it % kHeld]), (it / kHeld) & 1, abort_flag);
   };
   bool ok = true;
-  if (warp < kWarps) {
+  if (warp < kSumWarps) {
     // ------------------------------------------------------------- sum warps
     const float room = 12.0f / scale;
     Place at = {0, 0};
@@ -293,14 +301,13 @@ __global__ void __launch_bounds__(Form<kT, kGrad>::kThreads, Form<kT, kGrad>::kP
         if (r * 32 + lane < in.k) next_id[r] = in.ids[row * in.k + r * 32 + lane];
       }
     };
-    if (num_its > 0) fetch(row0);
+    if (num_its > 0) fetch(walk.row(0));
     for (uint32_t it = 0; it < num_its; ++it) {
-      const int64_t row = row0 + it * row_step;
-      const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
+      const Piece pc = piece(it);
       int32_t id[kPerLane];
 #pragma unroll
       for (int r = 0; r < kPerLane; ++r) id[r] = next_id[r];
-      if (it + 1 < num_its) fetch(row + row_step);
+      if (it + 1 < num_its) fetch(walk.row(it + 1));
       // the single elements at the piece's ends (warp 0), without listed ones
       float end_x[2] = {neg_inf(), neg_inf()};
       if (warp == 0 && (pc.c0 < pc.b0 || pc.b1 < pc.c1)) {
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(Form<kT, kGrad>::kThreads, Form<kT, kGrad>::kP
       listed = __reduce_or_sync(0xffffffffu, listed);
       RunSum a = {0.0f, neg_inf(), 0u};
       Place r = at;
-      const int kept = kGrad ? max(0, pc.stages - slots) : pc.stages;  // the first that stays
+      const int kept = kMode == kBoth ? max(0, pc.stages - slots) : pc.stages;  // the first that stays
       for (int j = 0; j < pc.stages; ++j) {
         ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
         if (!ok) break;
@@ -383,45 +390,50 @@ __global__ void __launch_bounds__(Form<kT, kGrad>::kThreads, Form<kT, kGrad>::kP
         ok = ok && wait_held(sh.ready, it);
         if (ok)
           exchange_tell(sh.ex, it, make_uint4(__float_as_uint(rest.m), __float_as_uint(rest.s), 0u, 0u),
-                        chunk, chunks, lane);
+                        walk.chunk, chunks, lane);
       }
       // (a slot's uses are waited for one by one: a wait tells only even from odd ones)
-      for (int j = 0; kGrad && j < kept; ++j, step(r, slots))
+      for (int j = 0; kMode == kBoth && j < kept; ++j, step(r, slots))
         ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
       if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
-      at = later(at, num_loads(pc.stages, slots, kGrad), slots);
+      at = later(at, num_loads(pc.stages, slots, kMode == kBoth), slots);
     }
-  } else if (warp < kWarps + kGradWarps) {
+  } else if (warp < kSumWarps + kGradWarps) {
     // -------------------------------------------------------- gradient warps
     Place at = {0, 0};
-    const int gtid = tid - kT;
-    float next_up = in.grad_loss != nullptr && num_its > 0 ? in.grad_loss[row0] : 1.0f;
+    const int gtid = tid - kSumWarps * 32;
+    const bool with_up = kMode == kBoth && in.grad_loss != nullptr;
+    float next_up = with_up && num_its > 0 ? in.grad_loss[walk.row(0)] : 1.0f;
     for (uint32_t it = 0; it < num_its; ++it) {
-      const int64_t row = row0 + it * row_step;
-      const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
+      const int64_t row = walk.row(it);
+      const Piece pc = piece(it);
       const float up = next_up * in.inv_t32;
-      if (in.grad_loss != nullptr && it + 1 < num_its) next_up = in.grad_loss[row + row_step];
+      if (with_up && it + 1 < num_its) next_up = in.grad_loss[walk.row(it + 1)];
       float end_x[2] = {neg_inf(), neg_inf()};
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         const int j = end_column(pc, side, gtid);
         if (j >= 0) end_x[side] = read_elem<kBf16>(pc.p, j);
       }
-      ok = exchange_wait(sh.ex, it, abort_flag) && wait_held(sh.ready, it);
+      ok = (kMode != kBoth || exchange_wait(sh.ex, it, abort_flag)) && wait_held(sh.ready, it);
       if (!ok) break;
-      const Sum rest = exchange_sum(sh.ex, it, chunks, lane, scale);
       const List &l = sh.list[it % kHeld];
-      const Sum total = sum_merge(l.listed, rest, scale);
-      const bool live = l.any && total.s != 0.0f;
-      const float m = rest.m == neg_inf() ? 0.0f : rest.m;
-      float coef = nan_f32();
-      if (!is_nan(total.s)) {
-        const float share = sum_at(rest, total.m, scale) / total.s;  // s_r
-        coef = rest.s == 0.0f ? 0.0f : up * fmaf(l.total, share, -l.rest) / rest.s;
+      bool live = l.any;
+      float m = l.m, coef = l.coef;
+      if (kMode == kBoth) {
+        const Sum rest = exchange_sum(sh.ex, it, chunks, lane, scale);
+        const Sum total = sum_merge(l.listed, rest, scale);
+        live = live && total.s != 0.0f;
+        m = rest.m == neg_inf() ? 0.0f : rest.m;
+        coef = nan_f32();
+        if (!is_nan(total.s)) {
+          const float share = sum_at(rest, total.m, scale) / total.s;  // s_r
+          coef = rest.s == 0.0f ? 0.0f : up * fmaf(l.total, share, -l.rest) / rest.s;
+        }
       }
       char *g = static_cast<char *>(in.grad) + row * ldg_bytes;
       auto value = [&](float x) { return live ? coef * ex2((x - m) * scale) : 0.0f; };
-      const int kept = max(0, pc.stages - slots);
+      const int kept = kMode == kBoth ? max(0, pc.stages - slots) : 0;
       Place r = later(at, kept, slots);
       for (int i = 0; i < pc.stages; ++i) {
         // (stages that stayed are there since the row's sum; waiting again costs nothing)
@@ -466,27 +478,90 @@ __global__ void __launch_bounds__(Form<kT, kGrad>::kThreads, Form<kT, kGrad>::kP
         const int j = end_column(pc, side, gtid);
         if (j >= 0) store_elem<kBf16>(g, j, value(end_x[side]));
       }
-      if (chunk == chunks - 1)
+      if (walk.chunk_of(it) == chunks - 1)
         for (int j = valid + gtid; j < width; j += kT) store_elem<kBf16>(g, j, 0.0f);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.stored[it % kHeld]));
-      at = later(at, num_loads(pc.stages, slots, true), slots);
+      at = later(at, num_loads(pc.stages, slots, kMode == kBoth), slots);
     }
     if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
-  } else if (warp == kWarps + kGradWarps) {
-    copy_rows<kBf16, kT>(sh.ring, buf, slots, kGrad, logits, ld_bytes, row0, row_step, num_rows,
-                         valid, chunk, chunks, lane, err);
+  } else if (warp == kSumWarps + kGradWarps) {
+    copy_rows<kBf16, kT>(sh.ring, buf, slots, kMode == kBoth, logits, ld_bytes, walk, valid, lane,
+                         err);
     pdl_launch_dependents();
   } else {
     // ------------------------------------------------------------ list warps
-    auto finish = [&](uint32_t it) {
-      const int64_t row = row0 + it * row_step;
-      if (!exchange_wait(sh.ex, it, abort_flag)) return false;
-      exchange_rearm(sh.ex, it, chunks, lane);
+    auto fix = [&](uint32_t it, float up, float m, float of) {
       const List &l = sh.list[it % kHeld];
-      const Sum rest = exchange_sum(sh.ex, it, chunks, lane, scale);
+      const Piece pc = piece(it);
+      char *g = static_cast<char *>(in.grad) + walk.row(it) * ldg_bytes;
+      for (int i = lane; i < in.k; i += 32) {
+        const int32_t id = l.id[i];
+        if (!l.first[i] || id < pc.c0 || id >= pc.c1) continue;
+        store_elem<kBf16>(g, id, up * (of * ex2((l.x[i] - m) * scale) - l.p[i]));
+      }
+    };
+    const uint32_t first = static_cast<uint32_t>(warp - kSumWarps - kGradWarps - 1);
+    Entries next;
+    float next_lse = 0.0f, next_own = 0.0f, next_rest = neg_inf(), next_up = 1.0f;
+    auto fetch = [&](uint32_t it) {
+      const int64_t row = walk.row(it);
+      int c0 = 0, c1 = valid;
+      if (kMode == kBackward) {  // (other pieces may be written already)
+        const Piece pc = piece(it);
+        c0 = pc.c0;
+        c1 = pc.c1;
+        next_own = in.in_lse[row];
+        if (in.in_lse_rest != nullptr) next_rest = in.in_lse_rest[row];
+        if (in.grad_loss != nullptr) next_up = in.grad_loss[row];
+      }
+      if (in.lse != nullptr) next_lse = in.lse[row];
+      entries_load<kBf16>(next, in, row, logits + row * ld_bytes, valid, c0, c1, lane);
+    };
+    if (first < num_its) fetch(first);
+    for (uint32_t it = first; ok && it < num_its + F::kLists; it += F::kLists) {
+      if (it < num_its) {
+        List &l = sh.list[it % kHeld];
+        teacher_row(l, next, in.k, next_lse, in.lse != nullptr, inv_t, scale, lane);
+        if (kMode == kBackward && lane == 0) {
+          // relative to lse_rest, where there is a rest: s_r <= 1 times e^(y_j - lse_rest), where
+          // s_j itself may vanish (a rest that is masked by a low value).  m is rounded; what the
+          // exponents lose by that is in the factors.
+          const bool by_rest = l.rest > 0.0f && next_rest != neg_inf();
+          const float total = by_rest ? l.total : l.on_list, base = by_rest ? next_rest : next_own;
+          auto lost = [&](float lse) {
+            return 1.0f - static_cast<float>(lse - (lse * in.temperature) * inv_t);
+          };
+          l.m = base * in.temperature;
+          l.coef = next_up * in.inv_t32 * lost(base) *
+                   (by_rest ? fmaf(total, ex2((next_rest - next_own) * kLog2e), -l.rest) : total);
+          l.of = total * lost(next_own);
+          if (next_own == neg_inf()) l.any = 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.ready[it % kHeld]));
+        if (it + F::kLists < num_its) fetch(it + F::kLists);
+      }
+      if (it < F::kLists || it - F::kLists >= num_its) continue;
+      // the row before it
+      const uint32_t last = it - F::kLists;
+      const int64_t row = walk.row(last);
+      const List &l = sh.list[last % kHeld];
+      float up = in.inv_t32;
+      if (kGrad && in.grad_loss != nullptr) up *= in.grad_loss[row];
+      if (kMode == kBackward) {
+        const float lse = in.in_lse[row];
+        ok = wait_held(sh.stored, last);
+        if (ok && l.any) fix(last, up, lse * in.temperature, l.of);
+        __syncwarp();
+        continue;
+      }
+      ok = exchange_wait(sh.ex, last, abort_flag);
+      if (!ok) continue;
+      exchange_rearm(sh.ex, last, chunks, lane);
+      const Sum rest = exchange_sum(sh.ex, last, chunks, lane, scale);
       const Sum total = sum_merge(l.listed, rest, scale);
-      if (chunk == 0 &&
+      if (walk.chunk == 0 &&
           (in.out_loss != nullptr || in.out_lse != nullptr || in.out_lse_rest != nullptr)) {
         // lane 0: lse, lane 1: lse_rest, lane 2: log p_r
         const double rest_p = rest.s == 0.0f ? 0.0 : l.rest_p;
@@ -510,209 +585,54 @@ __global__ void __launch_bounds__(Form<kT, kGrad>::kThreads, Form<kT, kGrad>::kP
         }
       }
       if (kGrad) {
-        float up = in.inv_t32;
-        if (in.grad_loss != nullptr) up *= in.grad_loss[row];
-        if (!wait_held(sh.stored, it)) return false;
-        if (l.any && total.s != 0.0f) {
-          const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
-          char *g = static_cast<char *>(in.grad) + row * ldg_bytes;
-          const float of = (rest.s == 0.0f ? l.on_list : l.total) / total.s;
-          for (int i = lane; i < in.k; i += 32) {
-            const int32_t id = l.id[i];
-            if (!l.first[i] || id < pc.c0 || id >= pc.c1) continue;
-            store_elem<kBf16>(g, id, up * (of * ex2((l.x[i] - total.m) * scale) - l.p[i]));
-          }
-        }
+        ok = wait_held(sh.stored, last);
+        if (ok && l.any && total.s != 0.0f)
+          fix(last, up, total.m, (rest.s == 0.0f ? l.on_list : l.total) / total.s);
       }
       __syncwarp();
-      return true;
-    };
-    const uint32_t first = static_cast<uint32_t>(warp - kWarps - kGradWarps - 1);
-    Entries next;
-    float next_lse = 0.0f;
-    auto fetch = [&](int64_t row) {
-      entries_load<kBf16>(next, in, row, logits + row * ld_bytes, valid, 0, valid, lane);
-      if (in.lse != nullptr) next_lse = in.lse[row];
-    };
-    if (first < num_its) fetch(row0 + first * row_step);
-    uint32_t it = first;
-    for (; it < num_its && ok; it += F::kLists) {
-      const int64_t row = row0 + it * row_step;
-      teacher_row(sh.list[it % kHeld], next, in.k, next_lse, in.lse != nullptr, inv_t, scale, lane);
-      if (lane == 0) mbar_arrive(smem_u32(&sh.ready[it % kHeld]));
-      if (it + F::kLists < num_its) fetch(row + F::kLists * row_step);
-      if (it >= F::kLists) ok = finish(it - F::kLists);
     }
-    if (ok && it >= F::kLists && it != first) ok = finish(it - F::kLists);
     if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
   }
-  leave(sh.ring, chunks);
+  leave(sh.ring, F::kSum ? chunks : 1);
 }
 
-template <bool kBf16, int kT, bool kGrad>
+// Pieces of a row in the gradient from saved sums: few rows are split over all CTAs, in
+// pieces of 8 KB or more; many into pieces of at most 128 KB (333 rows of 50257 fp32 ids: 100 KB
+// 37 us, 50 KB 43; 2048 of 200064 bf16 ids: 50 to 200 KB 260, 400 KB 264).
+int backward_pieces(int64_t rows, int64_t bytes, int64_t ctas) {
+  int64_t n = rows < ctas ? ctas / rows : (bytes + 131071) / 131072;
+  if (n > bytes / 8192) n = bytes / 8192;
+  if (n > 1024) n = 1024;  // (piece_of)
+  if (rows * n > (int64_t(1) << 30)) n = (int64_t(1) << 30) / rows;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+template <bool kBf16, int kT, Mode kMode>
 cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t width, int64_t valid,
                         const Args &in, int64_t ldg, uint32_t *err, cudaStream_t stream) {
-  using F = Form<kT, kGrad>;
+  using F = Form<kT, kMode>;
   constexpr int kElt = kBf16 ? 2 : 4;
-  auto kern = distill_kernel<kBf16, kT, kGrad>;
+  auto kern = distill_kernel<kBf16, kT, kMode>;
   const RowKernel k = {reinterpret_cast<const void *>(kern), F::kThreads, F::kRingBytes,
-                       (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2) + (kGrad ? 0 : 4)};
+                       (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2) + 4 * kMode};
   int64_t resident[6];
   const cudaError_t e = resident_clusters(k, resident);
   if (e != cudaSuccess) return e;
-  int chunks =
-      kT == 256 ? pick_chunks(rows, valid * kElt, kGrad ? F::kRingBytes : 0, 0.85, resident) : 1;
+  int chunks = 1, width_of = 1;
+  int64_t walks = rows;
+  if (kMode == kBackward) {
+    chunks = backward_pieces(rows, valid * kElt, resident[5]);
+    walks = rows * chunks;
+  } else if (kT == 256) {
+    width_of = chunks =
+        pick_chunks(rows, valid * kElt, kMode == kBoth ? F::kRingBytes : 0, 0.85, resident);
+  }
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
-  row_launch(k, rows, chunks, resident, stream, attr, cfg);
+  row_launch(k, walks, width_of, resident, stream, attr, cfg);
   return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits), ld * kElt, rows,
                             static_cast<int>(valid), static_cast<int>(width), in, ldg * kElt,
                             chunks, err);
-}
-
-// ---------------------------------------------------------- gradient alone
-
-constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // loads in flight per thread
-
-// One pass from the saved sums, a CTA per piece of a row (nothing but the teacher's
-// few numbers is shared along it).  The first loads are under way while one warp
-// works those out.  kShift: some rows of the logits and of the gradient lie at
-// different 16-byte offsets.
-template <bool kBf16, bool kShift>
-__global__ void __launch_bounds__(kThreads)
-    distill_grad_kernel(const char *logits, int64_t ld_bytes, int valid, int width, Args in,
-                        int chunks, int64_t ldg_bytes) {
-  constexpr int kElt = kBf16 ? 2 : 4;
-  constexpr int kVec = 16 / kElt;
-  __shared__ List l;
-  const int chunk = static_cast<int>(blockIdx.x % chunks);
-  const int64_t row = blockIdx.x / chunks;
-  const int tid = threadIdx.x;
-  const char *x = logits + row * ld_bytes;
-  char *g = static_cast<char *>(in.grad) + row * ldg_bytes;
-  pdl_wait();
-  // this CTA's columns: whole 16-byte groups of the output row
-  int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(g) & 15u)) & 15u) / kElt);
-  if (head > width) head = width;
-  const int nvec = (width - head) / kVec;
-  const int v0 = static_cast<int>(static_cast<int64_t>(nvec) * chunk / chunks);
-  const int v1 = static_cast<int>(static_cast<int64_t>(nvec) * (chunk + 1) / chunks);
-  const int c0 = chunk == 0 ? 0 : head + v0 * kVec;
-  const int c1 = chunk == chunks - 1 ? width : head + v1 * kVec;
-  // whole vectors of the output without padding ids.  Where the logits' row
-  // lies at another 16-byte offset, a vector is put together from the two
-  // aligned ones that hold it; the row's first and last vectors are left to
-  // the single columns, so that no load leaves the row.
-  const int offset = kShift ? static_cast<int>((reinterpret_cast<uintptr_t>(x) -
-                                                reinterpret_cast<uintptr_t>(g)) & 15u)
-                            : 0;
-  const int full = valid > head ? (valid - head) / kVec : 0;
-  const int vs = offset != 0 && v0 == 0 ? min(1, v1) : v0;
-  const int ve = max(vs, min(v1, offset != 0 ? full - 1 : full));
-  const char *xv = x + head * kElt - offset;  // 16-byte aligned
-  char *gv = g + head * kElt;
-  uint4 q[kBatch], q1[kBatch];
-  auto load = [&](int v) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (v + u * kThreads >= ve) continue;
-      const uint4 *src = reinterpret_cast<const uint4 *>(xv) + v + u * kThreads;
-      if (!kShift || offset == 0) {
-        q[u] = __ldcs(src);
-      } else {
-        q[u] = src[0];
-        q1[u] = src[1];
-      }
-    }
-  };
-  load(vs + tid);
-
-  const double inv_t = in.inv_t;
-  const float scale = in.scale;
-  const float lse = in.in_lse[row];
-  const float lse_rest = in.in_lse_rest != nullptr ? in.in_lse_rest[row] : neg_inf();
-  const float up =
-      (in.grad_loss != nullptr ? in.grad_loss[row] : 1.0f) * in.inv_t32;
-  if (tid < 32) {
-    // (its logits are read before the pass may write over them)
-    Entries e;
-    entries_load<kBf16>(e, in, row, x, valid, c0, c1, tid);
-    teacher_row(l, e, in.k, in.lse != nullptr ? in.lse[row] : 0.0f, in.lse != nullptr, inv_t, scale,
-                tid);
-  }
-  __syncthreads();
-  const bool live = l.any && lse != neg_inf();
-  // off the list relative to lse_rest: s_r <= 1 times e^(y_j - lse_rest), where s_j itself may
-  // vanish (a rest that is masked by a low value)
-  const bool by_rest = l.rest > 0.0f && lse_rest != neg_inf();
-  const float total = by_rest ? l.total : l.on_list;
-  const float base = -(by_rest ? lse_rest : lse) * kLog2e;
-  const float coef =
-      up * (by_rest ? fmaf(total, ex2((lse_rest - lse) * kLog2e), -l.rest) : total);
-  auto value = [&](float v) { return coef * ex2(fmaf(v, scale, base)); };
-  auto one = [&](int j) {
-    store_elem<kBf16>(g, j, live && j < valid ? value(read_elem<kBf16>(x, j)) : 0.0f);
-  };
-  if (chunk == 0 && tid < head) one(tid);
-  for (int v = vs + tid; v < ve; v += kBatch * kThreads) {
-    if (v != vs + tid) load(v);
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (v + u * kThreads >= ve) continue;
-      const uint4 xq = kShift && offset != 0 ? bytes_of(q[u], q1[u], offset) : q[u];
-      uint32_t w[4] = {xq.x, xq.y, xq.z, xq.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!live)
-          w[i] = 0u;
-        else if (kBf16)
-          w[i] = pack2(value(bf16_lo(w[i])), value(bf16_hi(w[i])));
-        else
-          w[i] = __float_as_uint(value(__uint_as_float(w[i])));
-      }
-      __stcs(reinterpret_cast<uint4 *>(gv) + v + u * kThreads, make_uint4(w[0], w[1], w[2], w[3]));
-    }
-  }
-  if (vs > v0)
-    for (int j = head + v0 * kVec + tid; j < head + vs * kVec; j += kThreads) one(j);
-  for (int j = head + ve * kVec + tid; j < c1; j += kThreads) one(j);
-  pdl_launch_dependents();
-  __syncthreads();
-  if (live && tid < in.k && l.first[tid] && l.id[tid] >= c0 && l.id[tid] < c1) {
-    const float s = total * ex2(fmaf(l.x[tid], scale, -lse * kLog2e));
-    store_elem<kBf16>(g, l.id[tid], up * (s - l.p[tid]));
-  }
-}
-
-cudaError_t launch_grad(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t width,
-                        int64_t valid, const Args &in, int64_t ldg, int num_sms,
-                        cudaStream_t stream) {
-  const int elt = dtype == SGA_BF16 ? 2 : 4;
-  // pieces of 64 KB, or down to 16 KB where the SMs would not have eight each
-  const int64_t bytes = width * elt;
-  int64_t piece = 65536;
-  while (piece > 16384 && rows * ((bytes + piece - 1) / piece) < 8 * num_sms) piece /= 2;
-  int64_t chunks = (bytes + piece - 1) / piece;
-  if (rows * chunks > (int64_t(1) << 30)) chunks = (int64_t(1) << 30) / rows;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * chunks));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const bool shift =
-      ((reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(in.grad)) |
-       ((ld - ldg) * elt)) % 16 != 0;
-  auto kern = dtype == SGA_BF16
-                  ? (shift ? distill_grad_kernel<true, true> : distill_grad_kernel<true, false>)
-                  : (shift ? distill_grad_kernel<false, true> : distill_grad_kernel<false, false>);
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<const char *>(logits), ld * elt,
-                            static_cast<int>(valid), static_cast<int>(width), in,
-                            static_cast<int>(chunks), ldg * elt);
 }
 
 }  // namespace
@@ -723,20 +643,19 @@ cudaError_t launch_distill(const void *logits, int dtype, int64_t rows, int64_t 
   const double inv_t = 1.0 / static_cast<double>(in.temperature);
   const Args args = {in, inv_t, static_cast<float>(inv_t),
                      static_cast<float>(1.4426950408889634 * inv_t)};
-  if (args.in_lse != nullptr)
-    return launch_grad(logits, dtype, rows, ld, width, valid, args, ldg, num_sms, stream);
-  const bool kept = args.grad != nullptr;
   const bool small = small_rows(rows, valid * (dtype == SGA_BF16 ? 2 : 4), num_sms);
-  auto launch = [&](auto bf16, auto grad) {
-    constexpr bool kBf16 = decltype(bf16)::value, kGrad = decltype(grad)::value;
-    return (small ? launch_rows<kBf16, 64, kGrad> : launch_rows<kBf16, 256, kGrad>)(
+  auto launch = [&](auto bf16, auto mode) {
+    constexpr bool kBf16 = decltype(bf16)::value;
+    constexpr Mode kMode = static_cast<Mode>(decltype(mode)::value);
+    return (small ? launch_rows<kBf16, 64, kMode> : launch_rows<kBf16, 256, kMode>)(
         logits, rows, ld, width, valid, args, ldg, err, stream);
   };
-  if (dtype == SGA_BF16)
-    return kept ? launch(std::true_type{}, std::true_type{})
-                : launch(std::true_type{}, std::false_type{});
-  return kept ? launch(std::false_type{}, std::true_type{})
-              : launch(std::false_type{}, std::false_type{});
+  auto by_mode = [&](auto bf16) {
+    if (in.in_lse != nullptr) return launch(bf16, std::integral_constant<int, kBackward>{});
+    return in.grad != nullptr ? launch(bf16, std::integral_constant<int, kBoth>{})
+                              : launch(bf16, std::integral_constant<int, kLoss>{});
+  };
+  return dtype == SGA_BF16 ? by_mode(std::true_type{}) : by_mode(std::false_type{});
 }
 
 }  // namespace sga

@@ -51,8 +51,9 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
   constexpr uint32_t kMasked = kBf16 ? 0xff80ff80u : 0xff800000u;  // -inf
   extern __shared__ __align__(128) uint4 buf[];
   __shared__ ProbsShared<kT> sh;
-  const int chunk = static_cast<int>(blockIdx.x % chunks);
-  const int64_t row0 = blockIdx.x / chunks, row_step = gridDim.x / chunks;
+  const auto walk = walk_of<false>(num_rows, chunks);
+  const int chunk = walk.chunk;
+  const int64_t row0 = walk.first, row_step = walk.step;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const volatile int *abort_flag = &sh.ring.abort;
   if (tid == 0) {
@@ -71,8 +72,7 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
   pdl_wait();
 
   if (warp == kWarps) {
-    copy_rows<kBf16, kT>(sh.ring, buf, slots, true, logits, ld_bytes, row0, row_step, num_rows,
-                         valid, chunk, chunks, lane, err);
+    copy_rows<kBf16, kT>(sh.ring, buf, slots, true, logits, ld_bytes, walk, valid, lane, err);
     pdl_launch_dependents();
   } else {
     Place at = {0, 0};

@@ -64,9 +64,9 @@ __device__ __forceinline__ Piece piece_of(const char *p, int valid, int chunk, i
   q.p = p;
   int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / kElt);
   if (head > valid) head = valid;
-  const int nvec = (valid - head) / kVec;  // < 2^22, chunks <= 8
-  const int v0 = static_cast<int>(static_cast<uint32_t>(nvec * chunk) / chunks);
-  const int v1 = static_cast<int>(static_cast<uint32_t>(nvec * (chunk + 1)) / chunks);
+  const uint32_t nvec = static_cast<uint32_t>((valid - head) / kVec);  // <= 2^22, chunks <= 2^10
+  const int v0 = static_cast<int>(nvec * chunk / chunks);
+  const int v1 = static_cast<int>(nvec * (chunk + 1) / chunks);
   q.b0 = head + v0 * kVec;
   q.b1 = head + v1 * kVec;
   q.c0 = chunk == 0 ? 0 : q.b0;
@@ -80,6 +80,36 @@ __device__ __forceinline__ Piece piece_of(const char *p, int valid, int chunk, i
 __device__ __forceinline__ int end_column(const Piece &q, int side, int tid) {
   const int j = (side == 0 ? q.c0 : q.b1) + tid;
   return j < (side == 0 ? q.b0 : q.c1) ? j : -1;
+}
+
+// What a CTA goes over: every step-th row from `first`, its chunk of each (the CTAs of
+// a cluster share rows), or every step-th piece of all rows' `chunks` pieces.
+template <bool kPieces>
+struct Walk {
+  int64_t first, step;
+  uint32_t n;
+  int chunks, chunk;
+  __device__ __forceinline__ int64_t row(uint32_t it) const {
+    const int64_t i = first + it * step;
+    return kPieces ? static_cast<uint32_t>(i) / static_cast<uint32_t>(chunks) : i;
+  }
+  __device__ __forceinline__ int chunk_of(uint32_t it) const {
+    return kPieces ? static_cast<int>(static_cast<uint32_t>(first + it * step) %
+                                     static_cast<uint32_t>(chunks))
+                  : chunk;
+  }
+};
+
+template <bool kPieces>
+__device__ __forceinline__ Walk<kPieces> walk_of(int64_t rows, int chunks) {
+  Walk<kPieces> w;
+  const int64_t all = kPieces ? rows * chunks : rows;  // (pieces: at most 2^30)
+  w.first = kPieces ? blockIdx.x : blockIdx.x / chunks;
+  w.step = kPieces ? gridDim.x : gridDim.x / chunks;
+  w.n = static_cast<uint32_t>(w.first < all ? (all - w.first + w.step - 1) / w.step : 0);
+  w.chunks = chunks;
+  w.chunk = kPieces ? 0 : static_cast<int>(blockIdx.x % chunks);
+  return w;
 }
 
 // -------------------------------------------------------------------- ring
@@ -111,18 +141,18 @@ __device__ __forceinline__ int num_loads(int stages, int slots, bool kept) {
 }
 
 // The copy warp: every piece's stages into the ring.
-template <bool kBf16, int kT>
+template <bool kBf16, int kT, class W>
 __device__ __forceinline__ void copy_rows(Ring &ring, uint4 *buf, int slots, bool kept,
-                                          const char *logits, int64_t ld_bytes, int64_t row0,
-                                          int64_t row_step, int64_t num_rows, int valid, int chunk,
-                                          int chunks, int lane, uint32_t *err) {
+                                          const char *logits, int64_t ld_bytes, const W &w,
+                                          int valid, int lane, uint32_t *err) {
   constexpr int kElt = kBf16 ? 2 : 4, kVec = 16 / kElt;
   const volatile int *abort_flag = &ring.abort;
   Place at = {0, 0};
   int filled = 0;
   bool ok = true;
-  for (int64_t row = row0; row < num_rows && ok; row += row_step) {
-    const Piece q = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
+  for (uint32_t it = 0; it < w.n && ok; ++it) {
+    const Piece q =
+        piece_of<kBf16, kT>(logits + w.row(it) * ld_bytes, valid, w.chunk_of(it), w.chunks);
     const int loads = num_loads(q.stages, slots, kept);
     for (int j = 0; j < loads; ++j) {
       if (filled < slots) {
@@ -324,7 +354,7 @@ __device__ __forceinline__ void leave(const Ring &ring, int chunks) {
 struct RowKernel {
   const void *kern;
   int threads, smem;  // dynamic shared memory
-  int slot;           // of this file's kernels, 0 .. 7
+  int slot;           // of this file's kernels, 0 .. 11
 };
 
 constexpr int kWidths[6] = {8, 6, 4, 3, 2, 1};  // CTAs that may share a row
@@ -339,15 +369,17 @@ inline cudaError_t resident_clusters(const RowKernel &k, int64_t (&out)[6]) {
     int n[6];
   };
   static std::mutex mu;
-  static Entry cache[8][64] = {};
-  cudaError_t e = set_smem_once(k.kern, k.smem, k.slot);
+  static Entry cache[12][64] = {};
   int dev = 0;
-  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   const uintptr_t ctx = current_context_key();
   std::lock_guard<std::mutex> lock(mu);
   Entry &c = cache[k.slot][dev];
   if (ctx == 0 || c.ctx != ctx) {
+    e = cudaFuncSetAttribute(k.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
+    if (e != cudaSuccess) return e;
     for (int i = 0; i < 6; ++i) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(kWidths[i]));
