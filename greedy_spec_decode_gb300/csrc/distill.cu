@@ -625,7 +625,7 @@ cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t wi
     walks = rows * chunks;
   } else if (kT == 256) {
     width_of = chunks =
-        pick_chunks(rows, valid * kElt, kMode == kBoth ? F::kRingBytes : 0, 0.85, resident);
+        pick_chunks(rows, valid * kElt, kMode == kBoth ? F::kRingBytes : 0, resident);
   }
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};

@@ -8,31 +8,47 @@
 namespace sga {
 namespace {
 
-// Stages of the ring: the most that fits two CTAs per SM (16 KB), or eight (4 KB).
+// Long rows (kT 256) and short ones (64): CTAs per SM and stages of the ring (16 or
+// 4 KB), the most that fits.
 template <int kT>
-constexpr int kSlots = kT == 256 ? 7 : 6;
-template <int kT>
-constexpr int kRingBytes = kSlots<kT> * kStageVec<kT> * 16;
+struct Form {
+  static constexpr int kPerSm = kT == 256 ? 1 : 6;
+  static constexpr int kSlots = kT == 256 ? 13 : 8;
+  static constexpr int kRingBytes = kSlots * kStageVec<kT> * 16;
+  static constexpr int kThreads = 2 * kT + 32;
+};
+
+constexpr uint32_t kHeld = 4;  // rows between a sum and its output
 
 template <int kT>
 struct ProbsShared {
   Ring ring;
-  Exchange<2> ex;
-  Sum warp_sum[kT / 32];
-  int32_t warp_id[kT / 32];
+  uint64_t stored[kHeld];  // a row's probabilities are written
+  Exchange<2 * kHeld> ex;
+  Sum warp_sum[2][kT / 32];
+  int32_t warp_id[2][kT / 32];
 };
 
-// Unit of the output: 16 bytes, four probabilities.
-template <bool kBf16>
-__device__ __forceinline__ void load4(const uint4 *stage, int unit, float (&x)[4]) {
+// Logits 4 unit + shift .. 4 unit + shift + 3 of a stage.
+template <bool kBf16, bool kShift>
+__device__ __forceinline__ void load4(const uint4 *stage, int unit, int shift, float (&x)[4]) {
   if constexpr (kBf16) {
-    const uint2 q = reinterpret_cast<const uint2 *>(stage)[unit];
+    const uint2 *p = reinterpret_cast<const uint2 *>(stage);
+    uint2 q = p[unit];
+    if constexpr (kShift) {
+      const uint2 r = p[unit + 1];
+      const uint32_t w0 = (shift & 2) ? q.y : q.x, w1 = (shift & 2) ? r.x : q.y,
+                     w2 = (shift & 2) ? r.y : r.x;
+      q = make_uint2(__funnelshift_r(w0, w1, (shift & 1) * 16),
+                     __funnelshift_r(w1, w2, (shift & 1) * 16));
+    }
     x[0] = bf16_lo(q.x);
     x[1] = bf16_hi(q.x);
     x[2] = bf16_lo(q.y);
     x[3] = bf16_hi(q.y);
   } else {
-    const uint4 q = stage[unit];
+    uint4 q = stage[unit];
+    if constexpr (kShift) q = bytes_of(q, stage[unit + 1], shift * 4);
     x[0] = __uint_as_float(q.x);
     x[1] = __uint_as_float(q.y);
     x[2] = __uint_as_float(q.z);
@@ -40,11 +56,14 @@ __device__ __forceinline__ void load4(const uint4 *stage, int unit, float (&x)[4
   }
 }
 
+// Three kinds of warps: the copy warp fills the ring, the sum warps add up a row's
+// piece (a greedy row: find its argmax), the output warps write the probabilities of
+// what the ring has kept, up to kHeld rows behind.
 template <bool kBf16, int kT>
-__global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
+__global__ void __launch_bounds__(Form<kT>::kThreads, Form<kT>::kPerSm)
     probs_kernel(const char *logits, int64_t ld_bytes, int64_t num_rows, int valid, int width,
                  const float *temperature, float *probs, int64_t ldp, int chunks, uint32_t *err) {
-  constexpr int slots = kSlots<kT>;
+  constexpr int slots = Form<kT>::kSlots;
   constexpr int kElt = kBf16 ? 2 : 4;
   constexpr int kVec = 16 / kElt;
   constexpr int kWarps = kT / 32;
@@ -52,8 +71,7 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
   extern __shared__ __align__(128) uint4 buf[];
   __shared__ ProbsShared<kT> sh;
   const auto walk = walk_of<false>(num_rows, chunks);
-  const int chunk = walk.chunk;
-  const int64_t row0 = walk.first, row_step = walk.step;
+  const uint32_t num_its = walk.n;
   const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
   const volatile int *abort_flag = &sh.ring.abort;
   if (tid == 0) {
@@ -61,33 +79,37 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
       mbar_init(smem_u32(&sh.ring.full[i]), 1);
       mbar_init(smem_u32(&sh.ring.empty[i]), kWarps);
     }
+    for (uint32_t i = 0; i < kHeld; ++i) mbar_init(smem_u32(&sh.stored[i]), kWarps);
     sh.ring.abort = 0;
     exchange_init(sh.ex, chunks);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  if (chunks > 1) {  // every CTA's barriers are ready
+  if (chunks > 1)  // every CTA's barriers are ready
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-  }
   pdl_wait();
 
-  if (warp == kWarps) {
-    copy_rows<kBf16, kT>(sh.ring, buf, slots, true, logits, ld_bytes, walk, valid, lane, err);
-    pdl_launch_dependents();
-  } else {
+  auto piece = [&](uint32_t it) {
+    return piece_of<kBf16, kT>(logits + walk.row(it) * ld_bytes, valid, walk.chunk, chunks);
+  };
+  auto temp = [&](uint32_t it) {
+    return temperature != nullptr && it < num_its ? temperature[walk.row(it)] : 1.0f;
+  };
+  auto scale_of = [](float t) { return t > 0.0f ? fminf(kLog2e / t, 3e38f) : nan_f32(); };
+  bool ok = true;
+  float t_next = temp(0);
+  if (warp < kWarps) {
+    // ------------------------------------------------------------- sum warps
     Place at = {0, 0};
-    bool ok = true;
-    int64_t it = 0;
-    float t_next = temperature != nullptr && row0 < num_rows ? temperature[row0] : 1.0f;
-    for (int64_t row = row0; row < num_rows; row += row_step, ++it) {
-      const Piece pc = piece_of<kBf16, kT>(logits + row * ld_bytes, valid, chunk, chunks);
+    for (uint32_t it = 0; it < num_its; ++it) {
+      const Piece pc = piece(it);
       const float t = t_next;
-      if (temperature != nullptr && row + row_step < num_rows) t_next = temperature[row + row_step];
+      t_next = temp(it + 1);
       const bool greedy = t == 0.0f;
-      const float scale = t > 0.0f ? fminf(kLog2e / t, 3e38f) : nan_f32();
-      const float room = 12.0f / scale;
+      const float scale = scale_of(t), room = 12.0f / scale;
       RunSum a = {0.0f, neg_inf(), 0u};
       float best = neg_inf();
+      int best_stage = -1;
       int32_t best_id = kNoId;
       // the single elements at the row's ends
       float end_x[2] = {neg_inf(), neg_inf()};
@@ -96,7 +118,6 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
         const int j = end_column(pc, side, tid);
         if (j >= 0) end_x[side] = read_elem<kBf16>(pc.p, j);
       }
-      // ---- the row's sum (a greedy row's argmax)
       Place r = at;
       const int kept = max(0, pc.stages - slots);  // the first stage that stays
       for (int j = 0; j < pc.stages; ++j) {
@@ -106,23 +127,26 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
         const int c = pc.b0 + j * kStageVec<kT> * kVec;
         const int n = min(kStageVec<kT>, (pc.b1 - c) / kVec);
         uint4 q[kVecPerThread];
+        if (n == kStageVec<kT>) {
 #pragma unroll
-        for (int u = 0; u < kVecPerThread; ++u) {
-          const int i = u * kT + tid;
-          q[u] = i < n ? st[i] : make_uint4(kMasked, kMasked, kMasked, kMasked);
-        }
-        if (greedy) {
-#pragma unroll
-          for (int u = 0; u < kVecPerThread; ++u)
-            if (u * kT + tid < n && (best_id == kNoId || scan_better(vec_max<kBf16>(q[u]), best))) {
-              const int32_t id = c + (u * kT + tid) * kVec;
-              if (best_id == kNoId) best_id = id;  // (a first id, if nothing is above -inf)
-              scan_vec<kBf16>(q[u], id, best, best_id);
-            }
+          for (int u = 0; u < kVecPerThread; ++u) q[u] = st[u * kT + tid];
         } else {
-          uint4 most = q[0];
 #pragma unroll
-          for (int u = 1; u < kVecPerThread; ++u) most = vec_larger<kBf16>(most, q[u]);
+          for (int u = 0; u < kVecPerThread; ++u) {
+            const int i = u * kT + tid;
+            q[u] = i < n ? st[i] : make_uint4(kMasked, kMasked, kMasked, kMasked);
+          }
+        }
+        uint4 most = q[0];
+#pragma unroll
+        for (int u = 1; u < kVecPerThread; ++u) most = vec_larger<kBf16>(most, q[u]);
+        if (greedy) {
+          const float v = vec_max<kBf16>(most);
+          if (scan_better(v, best)) {
+            best = v;
+            best_stage = j;
+          }
+        } else {
           sum_rebase(a, vec_max<kBf16>(most), scale, room);
 #pragma unroll
           for (int u = 0; u < kVecPerThread; ++u) sum_vector<kBf16>(a, q[u], scale);
@@ -132,6 +156,26 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
           if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
         }
         step(r, slots);
+      }
+      if (greedy && ok) {
+        // where the warp's best logit is (a first id, if nothing is above -inf)
+        float top = best;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
+        if (best_stage < 0) {
+          if (tid < (pc.b1 - pc.b0) / kVec) best_id = pc.b0 + tid * kVec;
+        } else if (best == top || is_nan(best)) {
+          const int c = pc.b0 + best_stage * kStageVec<kT> * kVec;
+          const uint4 *st = best_stage >= kept
+                                ? buf + later(at, best_stage, slots).slot * kStageVec<kT>
+                                : reinterpret_cast<const uint4 *>(pc.p + static_cast<int64_t>(c) * kElt);
+          best = neg_inf();
+          for (int u = 0; u < kVecPerThread; ++u) {
+            const int i = u * kT + tid;
+            if (i < (pc.b1 - c) / kVec) scan_vec<kBf16>(st[i], c + i * kVec, best, best_id);
+          }
+        }
       }
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
@@ -147,102 +191,157 @@ __global__ void __launch_bounds__(kT + 32, kPerSm<kT>)
           sum_add(a, end_x[side], neg_inf(), scale);
         }
       }
-      // ---- joined over the warps and the cluster
+      // ---- joined over the warps, and told
       Sum total = {best, 0.0f};
-      if (greedy)
-        warp_argmax(total.m, best_id);
-      else
-        total = sum_warp(sum_result(a), scale);
-      if (lane == 0) {
-        sh.warp_sum[warp] = total;
-        sh.warp_id[warp] = best_id;
-      }
-      consumers_sync<kT>();
-      if (warp == 0) {
-        total = lane < kWarps ? sh.warp_sum[lane] : Sum{neg_inf(), 0.0f};
-        best_id = lane < kWarps ? sh.warp_id[lane] : kNoId;
+      auto join = [&] {
         if (greedy)
           warp_argmax(total.m, best_id);
         else
           total = sum_warp(total, scale);
+      };
+      if (!greedy) total = sum_result(a);
+      join();
+      if (lane == 0) {
+        sh.warp_sum[it & 1][warp] = total;
+        sh.warp_id[it & 1][warp] = best_id;
       }
-      if (warp == 0 && ok)
-        exchange_tell(sh.ex, static_cast<uint32_t>(it),
-                      make_uint4(__float_as_uint(total.m), __float_as_uint(total.s),
-                                 static_cast<uint32_t>(best_id), 0u),
-                      chunk, chunks, lane);
-      ok = ok && exchange_wait(sh.ex, static_cast<uint32_t>(it), abort_flag);
-      if (ok && warp == 0) exchange_rearm(sh.ex, static_cast<uint32_t>(it), chunks, lane);
-      total = {neg_inf(), 0.0f};
-      best_id = kNoId;
-      for (int c = 0; c < chunks; ++c) {
-        const uint4 q = sh.ex.part[it & 1][c];
-        const Sum o = {__uint_as_float(q.x), __uint_as_float(q.y)};
-        if (!greedy) {
-          total = sum_merge(total, o, scale);
-        } else if (pair_beats(o.m, static_cast<int32_t>(q.z), total.m, best_id)) {
-          total.m = o.m;
-          best_id = static_cast<int32_t>(q.z);
+      consumers_sync<kT>();  // (every warp keeps to the rows' barriers)
+      if (warp == static_cast<int>(it % kWarps)) {
+        total = lane < kWarps ? sh.warp_sum[it & 1][lane] : Sum{neg_inf(), 0.0f};
+        best_id = lane < kWarps ? sh.warp_id[it & 1][lane] : kNoId;
+        join();
+        if (it >= kHeld)  // the buffer's last row has been read everywhere
+          ok = ok && warp_wait(smem_u32(&sh.stored[it % kHeld]), (it / kHeld - 1) & 1, abort_flag);
+        if (ok)
+          exchange_tell(sh.ex, it,
+                        make_uint4(__float_as_uint(total.m), __float_as_uint(total.s),
+                                   static_cast<uint32_t>(best_id), 0u),
+                        walk.chunk, chunks, lane);
+      }
+      // (a slot's uses are waited for one by one: a wait tells only even from odd ones)
+      for (int j = 0; j < kept; ++j, step(r, slots))
+        ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+      if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
+      at = later(at, num_loads(pc.stages, slots, true), slots);
+    }
+  } else if (warp < 2 * kWarps) {
+    // ---------------------------------------------------------- output warps
+    Place at = {0, 0};
+    const int otid = tid - kT;
+    for (uint32_t it = 0; it < num_its; ++it) {
+      const Piece pc = piece(it);
+      const float t = t_next;
+      t_next = temp(it + 1);
+      const bool greedy = t == 0.0f;
+      const float scale = scale_of(t);
+      float end_x[2] = {neg_inf(), neg_inf()};
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int j = end_column(pc, side, otid);
+        if (j >= 0) end_x[side] = read_elem<kBf16>(pc.p, j);
+      }
+      ok = exchange_wait(sh.ex, it, abort_flag);
+      if (!ok) break;
+      Sum total = {neg_inf(), 0.0f};
+      int32_t best_id = kNoId;
+      if (greedy) {
+        for (int c = 0; c < chunks; ++c) {
+          const uint4 q = sh.ex.part[it % (2 * kHeld)][c];
+          const float v = __uint_as_float(q.x);
+          if (pair_beats(v, static_cast<int32_t>(q.z), total.m, best_id)) {
+            total.m = v;
+            best_id = static_cast<int32_t>(q.z);
+          }
         }
+      } else {
+        total = exchange_sum(sh.ex, it, chunks, lane, scale);
       }
+      if (warp == kWarps) exchange_rearm(sh.ex, it, chunks, lane);
       // a row without terms is 0 (its sum is 0; a NaN stays)
       const float m = total.m == neg_inf() ? 0.0f : total.m;
       const float inv = total.s == 0.0f ? 0.0f : 1.0f / total.s;
-
-      // ---- the probabilities
-      float *out = probs + row * ldp;
+      float *out = probs + walk.row(it) * ldp;
       auto value = [&](float x) { return ex2((x - m) * scale) * inv; };
-      const bool aligned = (reinterpret_cast<uintptr_t>(out + pc.b0) & 15u) == 0;
-      r = later(at, kept, slots);
+      const uint64_t m2 = pack_f32(-m, -m), s2 = pack_f32(scale, scale), i2 = pack_f32(inv, inv);
+      auto values = [&](const float (&x)[4]) {
+        float4 p;
+        unpack_f32(mul2(add2(pack_f32(x[0], x[1]), m2), s2), p.x, p.y);
+        unpack_f32(mul2(add2(pack_f32(x[2], x[3]), m2), s2), p.z, p.w);
+        unpack_f32(mul2(pack_f32(ex2(p.x), ex2(p.y)), i2), p.x, p.y);
+        unpack_f32(mul2(pack_f32(ex2(p.z), ex2(p.w)), i2), p.z, p.w);
+        return p;
+      };
+      const int kept = max(0, pc.stages - slots);
+      Place r = later(at, kept, slots);
       for (int i = 0; i < pc.stages; ++i) {
         const bool again = i >= pc.stages - kept;  // loaded a second time
         const int j = again ? i - (pc.stages - kept) : kept + i;
-        if (again) ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+        ok = warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
         if (!ok) break;
         const uint4 *st = buf + r.slot * kStageVec<kT>;
         const int c = pc.b0 + j * kStageVec<kT> * kVec;
         const int n = min(kStageVec<kT> * kVec, pc.b1 - c);
         float *o = out + c;
-        if (aligned) {
-          const int hot = best_id - c;
+        // elements of the stage before the output's first whole vector
+        const int skip = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(o) & 15u)) & 15u) / 4);
+        const int units = (n - skip) / 4;
+        float4 *ov = reinterpret_cast<float4 *>(o + skip);
+        if (greedy) {
+          const int hot = best_id - c - skip;
+          for (int u = otid; u < units; u += kT) {
+            const int e = hot - u * 4;
+            __stcs(ov + u, make_float4(e == 0 ? 1.0f : 0.0f, e == 1 ? 1.0f : 0.0f,
+                                       e == 2 ? 1.0f : 0.0f, e == 3 ? 1.0f : 0.0f));
+          }
+        } else if (skip == 0 && n == kStageVec<kT> * kVec) {
+          constexpr int kUnits = kVecPerThread * kVec / 4;
 #pragma unroll
-          for (int u = 0; u < kVecPerThread * kVec / 4; ++u) {
-            const int unit = u * kT + tid;
-            if (unit * 4 >= n) continue;
-            float4 p;
-            if (greedy) {
-              const int e = hot - unit * 4;
-              p = make_float4(e == 0 ? 1.0f : 0.0f, e == 1 ? 1.0f : 0.0f, e == 2 ? 1.0f : 0.0f,
-                              e == 3 ? 1.0f : 0.0f);
-            } else {
-              float x[4];
-              load4<kBf16>(st, unit, x);
-              p = make_float4(value(x[0]), value(x[1]), value(x[2]), value(x[3]));
-            }
-            reinterpret_cast<float4 *>(o)[unit] = p;
+          for (int h = 0; h < kUnits; h += 4) {
+            float x[4][4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) load4<kBf16, false>(st, (h + u) * kT + otid, 0, x[u]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) __stcs(ov + (h + u) * kT + otid, values(x[u]));
+          }
+        } else if (skip == 0) {
+          for (int u = otid; u < units; u += kT) {
+            float x[4];
+            load4<kBf16, false>(st, u, 0, x);
+            __stcs(ov + u, values(x));
           }
         } else {
-          for (int e = tid; e < n; e += kT)
-            o[e] = greedy ? (c + e == best_id ? 1.0f : 0.0f)
-                          : value(read_elem<kBf16>(reinterpret_cast<const char *>(st), e));
+#pragma unroll 4
+          for (int u = otid; u < units; u += kT) {
+            float x[4];
+            load4<kBf16, true>(st, u, skip, x);
+            __stcs(ov + u, values(x));
+          }
+        }
+        if (otid < n - units * 4) {  // both ends (at most six)
+          const int e = otid < skip ? otid : units * 4 + otid;
+          o[e] = greedy ? (c + e == best_id ? 1.0f : 0.0f)
+                        : value(read_elem<kBf16>(reinterpret_cast<const char *>(st), e));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
         step(r, slots);
       }
-      if (!ok) {  // (every warp keeps to the rows' barriers)
-        if (lane == 0) raise_abort(&sh.ring.abort, err);
-        continue;
-      }
+      if (!ok) break;
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
-        const int j = end_column(pc, side, tid);
+        const int j = end_column(pc, side, otid);
         if (j >= 0) out[j] = greedy ? (j == best_id ? 1.0f : 0.0f) : value(end_x[side]);
       }
-      if (chunk == chunks - 1)
-        for (int j = valid + tid; j < width; j += kT) out[j] = 0.0f;
+      if (walk.chunk == chunks - 1)
+        for (int j = valid + otid; j < width; j += kT) out[j] = 0.0f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.stored[it % kHeld]));
       at = later(at, num_loads(pc.stages, slots, true), slots);
     }
+    if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
+  } else {
+    copy_rows<kBf16, kT>(sh.ring, buf, slots, true, logits, ld_bytes, walk, valid, lane, err);
+    pdl_launch_dependents();
   }
   leave(sh.ring, chunks);
 }
@@ -252,13 +351,13 @@ cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t wi
                         const float *temperature, float *probs, int64_t ldp, uint32_t *err,
                         cudaStream_t stream) {
   auto kern = probs_kernel<kBf16, kT>;
-  const RowKernel k = {reinterpret_cast<const void *>(kern), kT + 32, kRingBytes<kT>,
+  const RowKernel k = {reinterpret_cast<const void *>(kern), Form<kT>::kThreads, Form<kT>::kRingBytes,
                        (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2)};
   int64_t resident[6];
   const cudaError_t e = resident_clusters(k, resident);
   if (e != cudaSuccess) return e;
   const int chunks =
-      kT == 256 ? pick_chunks(rows, valid * (kBf16 ? 2 : 4), kRingBytes<kT>, 0.625, resident) : 1;
+      kT == 256 ? pick_chunks(rows, valid * (kBf16 ? 2 : 4), Form<kT>::kRingBytes, resident) : 1;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   row_launch(k, rows, chunks, resident, stream, attr, cfg);

@@ -429,20 +429,30 @@ inline bool small_rows(int64_t rows, int64_t bytes, int num_sms) {
   return bytes <= (48 << 10) && rows > 2 * num_sms;
 }
 
-// CTAs that share a row.  Few rows: as many as let all rows run at once, with at
-// least 4 KB each (96 rows of 200064 bf16 ids: 3 CTAs 27 us, in rounds 4 33 us).
-// Otherwise one, or where rows are kept in a ring of `ring` bytes per CTA the fewest
-// whose pieces are at most `share` of it.
-inline int pick_chunks(int64_t rows, int64_t bytes, int64_t ring, double share,
-                       const int64_t (&resident)[6]) {
-  for (int i = 0; i < 6; ++i)
-    if (kWidths[i] == 1 || (rows <= resident[i] && bytes >= 4096 * kWidths[i])) {
-      if (ring == 0 || (rows <= resident[i] && bytes <= ring * 5 / 4 * kWidths[i])) return kWidths[i];
-      break;
-    }
+// CTAs that share a row: the width with the least rounds of rows x time of a piece, in
+// bytes, 16 KB standing for what a row costs besides (pieces of 4 KB or more).  With
+// rows kept in a ring of `ring` bytes per CTA a piece leaves some of it for the next
+// row's loads, unless there is one round, and clusters of 4 or 8 cost more than their
+// share of the SMs says (probabilities of 2048 rows of 202048 bf16 ids: 3 CTAs 382 us,
+// 4 399, 2 403; 96 of 200064 4 29, 3 33-35; 333 of 50257 fp32 ids 2 33, 1 39, 4 35).
+// Without (0) a row is split only if all run at once (loss of 333 rows of 50257 fp32
+// ids: 1 CTA 30 us, 4 39).
+inline int pick_chunks(int64_t rows, int64_t bytes, int64_t ring, const int64_t (&resident)[6]) {
   int best = kMaxCluster;
-  for (int c : kWidths)
-    if (bytes <= share * ring * c) best = c;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 6; ++i) {
+    const int c = kWidths[i];
+    const int64_t rounds = (rows + resident[i] - 1) / resident[i], piece = bytes / c;
+    if (c > 1 && (piece < 4096 || (ring == 0 && rounds > 1))) continue;
+    int64_t cost = rounds * (piece + 16384);
+    if (c % 4 == 0 && rounds > 1) cost += cost / 16;
+    if (ring > 0 && 10 * piece > 7 * ring) cost += cost / 12;
+    if (ring > 0 && (rounds > 1 ? 10 * piece > 9 * ring : 4 * piece > 5 * ring)) cost *= 4;
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  }
   return best;
 }
 

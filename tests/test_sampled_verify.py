@@ -116,6 +116,9 @@ PROBS = [  # rows, vocab, org, dtype, temperature, pad, offset
     # longer than the shared memory of a cluster, at aligned and odd rows
     (3, 900001, 900001, "bf16", "row", 0, 0), (11, 480003, 480000, "f32", "mixed", 1, 1),
     (2000, 333, 333, "bf16", "mixed", 1, 0),
+    # several such rows per cluster, and short rows longer than a small ring
+    (60, 900001, 900001, "bf16", "mixed", 0, 0), (2000, 24001, 24000, "bf16", "mixed", 0, 0),
+    (2000, 12001, 12001, "f32", "row", 1, 1),
 ]
 
 
