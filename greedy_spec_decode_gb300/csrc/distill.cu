@@ -13,8 +13,6 @@
 // lse_rest is summed without the listed ids: as a difference of sums it would
 // lose what a draft that agrees with its teacher leaves off the list.  The
 // teacher's few numbers are kept in 64 bits, p_r being 1 less a sum near 1.
-#include <type_traits>
-
 #include "rowring.cuh"
 
 namespace sga {
@@ -86,20 +84,21 @@ __device__ __forceinline__ void entries_load(Entries &e, const Args &in, int64_t
     e.x[r] = e.id[r] >= 0 && e.id[r] >= c0 && e.id[r] < c1 ? read_elem<kBf16>(x, e.id[r]) : neg_inf();
 }
 
-// One warp works out a row's list from its entries.  The logits are needed last: their
-// loads, which hang on those of the ids, run under the rest.
-__device__ __forceinline__ void teacher_row(List &l, const Entries &e, int k, float lse,
-                                            bool with_lse, double inv_t, float scale, int lane) {
+// One warp works out a row's list from its entries, in kN rounds of 32 (their
+// exponentials side by side: one takes 1100 cycles, mostly of latency).  The logits are
+// needed last: their loads, which hang on those of the ids, run under the rest.
+template <int kN>
+__device__ __forceinline__ void teacher_rounds(List &l, const Entries &e, int k, float lse,
+                                               bool with_lse, double inv_t, float scale,
+                                               int lane) {
 #pragma unroll
-  for (int r = 0; r < kPerLane; ++r)
-    if (r * 32 < k) l.id[r * 32 + lane] = e.id[r];
+  for (int r = 0; r < kN; ++r) l.id[r * 32 + lane] = e.id[r];
   __syncwarp();
   // which entries are the first of their id
-  bool first[kPerLane], some = false, again = false;
+  bool first[kN], some = false, again = false;
   const int4 *ids = reinterpret_cast<const int4 *>(l.id);
 #pragma unroll
-  for (int r = 0; r < kPerLane; ++r) {
-    if (r * 32 >= k) continue;
+  for (int r = 0; r < kN; ++r) {
     const int i = r * 32 + lane;
     first[r] = e.id[r] >= 0;
     some = some || first[r];
@@ -115,67 +114,80 @@ __device__ __forceinline__ void teacher_row(List &l, const Entries &e, int k, fl
   }
   bool any = __any_sync(0xffffffffu, some);
   again = __any_sync(0xffffffffu, again);
-  // the normaliser
-  double norm = lse, sum_p = 0.0, part = 0.0;
+  // terms relative to the teacher's log-sum-exp, or to the list's largest
+  double base = lse;
   if (!with_lse) {
     float most = neg_inf();
 #pragma unroll
-    for (int r = 0; r < kPerLane; ++r)
-      if (r * 32 < k && e.id[r] >= 0) most = max_nan(most, e.z[r]);  // (a NaN goes on)
+    for (int r = 0; r < kN; ++r)
+      if (e.id[r] >= 0) most = max_nan(most, e.z[r]);  // (a NaN goes on into the sums)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
       most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, off));
     any = any && most != neg_inf();
-    double sum = 0.0, none = 0.0;
-#pragma unroll
-    for (int r = 0; r < kPerLane; ++r)
-      if (r * 32 < k && e.id[r] >= 0 && any)
-        sum += exp((static_cast<double>(e.z[r]) - most) * inv_t);
-    warp_sums_f64(sum, none, lane);
-    norm = most * inv_t + log(sum);
+    base = most * inv_t;
   }
-  // probabilities, the list's part of the loss, and its sum of exponentials
-  Sum listed = {neg_inf(), 0.0f};
+  double t[kN], p[kN], sum = 0.0, part = 0.0;  // sum of p, of p (t - y)
 #pragma unroll
-  for (int r = 0; r < kPerLane; ++r) {
-    if (r * 32 >= k) continue;
-    double p = 0.0;
-    if (e.id[r] >= 0 && any) {
-      const double logp = e.z[r] * inv_t - norm;
-      p = exp(logp);
-      sum_p += p;
-      if (!(p <= 0.0)) part += p * (logp - e.x[r] * inv_t);
-    }
-    l.p[r * 32 + lane] = static_cast<float>(p);
+  for (int r = 0; r < kN; ++r) t[r] = e.z[r] * inv_t - base;
+#pragma unroll
+  for (int r = 0; r < kN; ++r) p[r] = exp(t[r]);
+  Sum listed = {neg_inf(), 0.0f};  // the list's sum of exponentials
+#pragma unroll
+  for (int r = 0; r < kN; ++r) {
+    if (e.id[r] < 0 || !any) p[r] = 0.0;
+    sum += p[r];
+    if (!(p[r] <= 0.0)) part += p[r] * (t[r] - e.x[r] * inv_t);
     l.x[r * 32 + lane] = e.x[r];
     const float x = first[r] ? e.x[r] : neg_inf();
     if (x != neg_inf()) listed = sum_merge(listed, {is_nan(x) ? neg_inf() : x, x - x + 1.0f}, scale);
   }
-  __syncwarp();
-  warp_sums_f64(sum_p, part, lane);
+  warp_sums_f64(sum, part, lane);
   listed = sum_warp(listed, scale);
+  float norm = 1.0f;
+  if (!with_lse && any) {  // p_i = p / sum, log p_i = t - log sum
+    const float s = static_cast<float>(sum);
+    double inv = 1.0f / s;
+    inv *= 2.0 - sum * inv;
+    part = part * inv - (log_of(s) + (sum - s) * inv);
+    norm = static_cast<float>(inv);
+    sum = is_nan(s) ? sum : 1.0;
+  }
+#pragma unroll
+  for (int r = 0; r < kN; ++r) l.p[r * 32 + lane] = static_cast<float>(p[r]) * norm;
+  __syncwarp();
   if (again) {
 #pragma unroll 1
     for (int i = lane; i < k; i += 32)
       if (l.first[i]) {
-        float p = l.p[i];
+        float q = l.p[i];
         for (int j = i + 1; j < k; ++j)
-          if (l.id[j] == l.id[i]) p += l.p[j];
-        l.p[i] = p;
+          if (l.id[j] == l.id[i]) q += l.p[j];
+        l.p[i] = q;
       }
   }
-  const double rest = with_lse && any ? (sum_p > 1.0 ? 0.0 : 1.0 - sum_p) : 0.0;
+  const double rest = with_lse && any ? (sum > 1.0 ? 0.0 : 1.0 - sum) : 0.0;
   if (lane == 0) {
     l.listed = listed;
-    l.sum_p = sum_p;
+    l.sum_p = sum;
     l.rest_p = rest;
     l.part = part;
-    l.total = static_cast<float>(sum_p + rest);
-    l.on_list = static_cast<float>(sum_p);
+    l.total = static_cast<float>(sum + rest);
+    l.on_list = static_cast<float>(sum);
     l.rest = static_cast<float>(rest);
     l.any = any;
   }
   __syncwarp();
+}
+
+__device__ __forceinline__ void teacher_row(List &l, const Entries &e, int k, float lse,
+                                            bool with_lse, double inv_t, float scale, int lane) {
+  if (k <= 32)
+    teacher_rounds<1>(l, e, k, lse, with_lse, inv_t, scale, lane);
+  else if (k <= 64)
+    teacher_rounds<2>(l, e, k, lse, with_lse, inv_t, scale, lane);
+  else
+    teacher_rounds<kPerLane>(l, e, k, lse, with_lse, inv_t, scale, lane);
 }
 
 // ------------------------------------------------------------ loss (and gradient)
@@ -188,8 +200,8 @@ enum Mode { kLoss, kBoth, kBackward };
 template <int kT, Mode kMode>
 struct Form {
   static constexpr bool kSum = kMode != kBackward, kGrad = kMode != kLoss;
-  static constexpr int kPerSm = kT == 256 ? (kMode == kBoth ? 1 : 2) : (kMode == kBoth ? 4 : 6);
-  static constexpr int kSlots = kT == 256 ? (kMode == kBoth ? 12 : 5) : (kMode == kBoth ? 9 : 5);
+  static constexpr int kPerSm = kT == 256 ? (kMode == kBoth ? 1 : 2) : (kMode == kBoth ? 5 : 6);
+  static constexpr int kSlots = kT == 256 ? (kMode == kBoth ? 12 : 5) : (kMode == kBoth ? 7 : 5);
   static constexpr int kLists = kT == 256 ? 4 : 2;
   static constexpr int kRingBytes = kSlots * kStageVec<kT> * 16;
   static constexpr int kThreads = (kMode == kBoth ? 2 : 1) * kT + 32 + 32 * kLists;
@@ -459,12 +471,22 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
           for (int v = gtid; v < n; v += kT)
             __stcs(ov + v, live ? grad_vec<kBf16>(st[v], m, scale, coef) : make_uint4(0, 0, 0, 0));
         } else {
-          for (int v = gtid; v < n - 1; v += kT)
-            __stcs(ov + v, live ? grad_vec<kBf16>(bytes_of(st[v], st[v + 1], skip), m, scale, coef)
-                                : make_uint4(0, 0, 0, 0));
-          // the vector's worth of elements at both ends
-          if (gtid < kVec) {
-            const int e = gtid * kElt < skip ? gtid : (n - 1) * kVec + gtid;
+          with_shift<kElt>(skip, [&](auto by) {
+            uint4 q[kVecPerThread];
+#pragma unroll
+            for (int u = 0; u < kVecPerThread; ++u) {
+              const int v = min(u * kT + gtid, max(0, n - 2));
+              q[u] = shifted<decltype(by)::value>(st[v], st[v + 1]);
+            }
+#pragma unroll
+            for (int u = 0; u < kVecPerThread; ++u) {
+              const uint4 d = live ? grad_vec<kBf16>(q[u], m, scale, coef) : make_uint4(0, 0, 0, 0);
+              if (u * kT + gtid < n - 1) __stcs(ov + u * kT + gtid, d);
+            }
+          });
+          // the vector's worth of elements at both ends, a warp after the other
+          if (gtid / 32 == j % kWarps && lane < kVec) {
+            const int e = lane * kElt < skip ? lane : (n - 1) * kVec + lane;
             store_elem<kBf16>(o, e, value(read_elem<kBf16>(reinterpret_cast<const char *>(st), e)));
           }
         }

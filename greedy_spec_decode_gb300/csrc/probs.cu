@@ -29,18 +29,16 @@ struct ProbsShared {
   int32_t warp_id[2][kT / 32];
 };
 
-// Logits 4 unit + shift .. 4 unit + shift + 3 of a stage.
-template <bool kBf16, bool kShift>
-__device__ __forceinline__ void load4(const uint4 *stage, int unit, int shift, float (&x)[4]) {
+// Logits 4 unit + kShift .. 4 unit + kShift + 3 of a stage.
+template <bool kBf16, int kShift>
+__device__ __forceinline__ void load4(const uint4 *stage, int unit, float (&x)[4]) {
   if constexpr (kBf16) {
     const uint2 *p = reinterpret_cast<const uint2 *>(stage);
     uint2 q = p[unit];
-    if constexpr (kShift) {
+    if constexpr (kShift != 0) {
       const uint2 r = p[unit + 1];
-      const uint32_t w0 = (shift & 2) ? q.y : q.x, w1 = (shift & 2) ? r.x : q.y,
-                     w2 = (shift & 2) ? r.y : r.x;
-      q = make_uint2(__funnelshift_r(w0, w1, (shift & 1) * 16),
-                     __funnelshift_r(w1, w2, (shift & 1) * 16));
+      const uint4 v = shifted<2 * kShift>(make_uint4(q.x, q.y, r.x, r.y), make_uint4(0, 0, 0, 0));
+      q = make_uint2(v.x, v.y);
     }
     x[0] = bf16_lo(q.x);
     x[1] = bf16_hi(q.x);
@@ -48,7 +46,7 @@ __device__ __forceinline__ void load4(const uint4 *stage, int unit, int shift, f
     x[3] = bf16_hi(q.y);
   } else {
     uint4 q = stage[unit];
-    if constexpr (kShift) q = bytes_of(q, stage[unit + 1], shift * 4);
+    if constexpr (kShift != 0) q = shifted<4 * kShift>(q, stage[unit + 1]);
     x[0] = __uint_as_float(q.x);
     x[1] = __uint_as_float(q.y);
     x[2] = __uint_as_float(q.z);
@@ -299,26 +297,36 @@ __global__ void __launch_bounds__(Form<kT>::kThreads, Form<kT>::kPerSm)
           for (int h = 0; h < kUnits; h += 4) {
             float x[4][4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) load4<kBf16, false>(st, (h + u) * kT + otid, 0, x[u]);
+            for (int u = 0; u < 4; ++u) load4<kBf16, 0>(st, (h + u) * kT + otid, x[u]);
 #pragma unroll
             for (int u = 0; u < 4; ++u) __stcs(ov + (h + u) * kT + otid, values(x[u]));
           }
         } else if (skip == 0) {
           for (int u = otid; u < units; u += kT) {
             float x[4];
-            load4<kBf16, false>(st, u, 0, x);
+            load4<kBf16, 0>(st, u, x);
             __stcs(ov + u, values(x));
           }
         } else {
-#pragma unroll 4
-          for (int u = otid; u < units; u += kT) {
-            float x[4];
-            load4<kBf16, true>(st, u, skip, x);
-            __stcs(ov + u, values(x));
-          }
+          with_shift<4>(skip * 4, [&](auto by) {
+            constexpr int kUnits = kVecPerThread * kVec / 4;
+            for (int h = 0; h < kUnits; h += 4) {
+              float x[4][4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                load4<kBf16, decltype(by)::value / 4>(
+                    st, min((h + u) * kT + otid, max(0, units - 1)), x[u]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float4 p = values(x[u]);
+                if ((h + u) * kT + otid < units) __stcs(ov + (h + u) * kT + otid, p);
+              }
+            }
+          });
         }
-        if (otid < n - units * 4) {  // both ends (at most six)
-          const int e = otid < skip ? otid : units * 4 + otid;
+        // both ends (at most six), a warp after the other
+        if (otid / 32 == j % kWarps && lane < n - units * 4) {
+          const int e = lane < skip ? lane : units * 4 + lane;
           o[e] = greedy ? (c + e == best_id ? 1.0f : 0.0f)
                         : value(read_elem<kBf16>(reinterpret_cast<const char *>(st), e));
         }

@@ -11,6 +11,7 @@
 #pragma once
 
 #include <mutex>
+#include <type_traits>
 
 #include "pipe.cuh"
 #include "scan.cuh"
@@ -41,6 +42,30 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// Bytes kS .. kS + 15 (kS even, below 16) of two 16-byte pieces that follow each other.
+template <int kS>
+__device__ __forceinline__ uint4 shifted(const uint4 a, const uint4 b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  constexpr int i = kS / 4;
+  if constexpr (kS % 4 == 0) return make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  return make_uint4(__funnelshift_r(w[i], w[i + 1], 16), __funnelshift_r(w[i + 1], w[i + 2], 16),
+                    __funnelshift_r(w[i + 2], w[i + 3], 16),
+                    __funnelshift_r(w[i + 3], w[i + 4], 16));
+}
+
+// f with the shift that an output's alignment needs, in steps of kStep bytes below 16,
+// as a constant (loss and gradient of 333 x 50257 fp32 ids into rows of another
+// alignment: 36 us with the shift as a variable, 32 so, 29 at the same alignment).
+template <int kStep, int kS = kStep, class F>
+__device__ __forceinline__ void with_shift(int s, F &&f) {
+  if constexpr (kS < 16) {
+    if (s == kS)
+      f(std::integral_constant<int, kS>{});
+    else
+      with_shift<kStep, kS + kStep>(s, f);
+  }
 }
 
 template <int kT>
