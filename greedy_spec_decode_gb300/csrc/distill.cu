@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
 int backward_pieces(int64_t rows, int64_t bytes, int64_t ctas) {
   int64_t n = rows < ctas ? ctas / rows : (bytes + 131071) / 131072;
   if (n > bytes / 8192) n = bytes / 8192;
-  if (n > 1024) n = 1024;  // (piece_of)
+  if (n > 512) n = 512;  // (what piece_of multiplies stays below 2^32)
   if (rows * n > (int64_t(1) << 30)) n = (int64_t(1) << 30) / rows;
   return n < 1 ? 1 : static_cast<int>(n);
 }

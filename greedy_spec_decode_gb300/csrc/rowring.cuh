@@ -89,7 +89,7 @@ __device__ __forceinline__ Piece piece_of(const char *p, int valid, int chunk, i
   q.p = p;
   int head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / kElt);
   if (head > valid) head = valid;
-  const uint32_t nvec = static_cast<uint32_t>((valid - head) / kVec);  // <= 2^22, chunks <= 2^10
+  const uint32_t nvec = static_cast<uint32_t>((valid - head) / kVec);  // <= 2^22, chunks <= 2^9
   const int v0 = static_cast<int>(nvec * chunk / chunks);
   const int v1 = static_cast<int>(nvec * (chunk + 1) / chunks);
   q.b0 = head + v0 * kVec;

@@ -398,6 +398,91 @@ def test_own_stream_and_graph_replay(sga_lib):
         check()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("temp", [1e-6, 1e-2, 50.0, 1e6])
+@pytest.mark.parametrize("rest", [False, True])
+def test_temperatures_far_from_one(sga_lib, temp, rest):
+    """Logits of the temperature's size, so that the softmax is one of spread 3.
+    The row is drawn before it is scaled, in fp32: an exponent of size |y| is then
+    off by the roundings that grad_tol counts."""
+    rows, vocab, k = 8, 5003, 12
+    x = torch.randn((rows, vocab), generator=gen(21), device="cuda") * 3.0
+    ids = torch.randint(0, vocab, (rows, k), generator=gen(22), device="cuda").to(torch.int32)
+    z = torch.randn((rows, k), generator=gen(23), device="cuda") * 3.0
+    x *= temp
+    z *= temp
+    tlse = torch.logsumexp(z.double() / temp, 1).float() + 0.3 if rest else None
+    up = torch.randn(rows, generator=gen(24), device="cuda") * temp
+    grad, back = torch.empty_like(x), torch.empty_like(x)
+    temp = float(torch.tensor(temp))                 # as the call takes it
+    got = run_forward(sga_lib, x, vocab, (ids, z, tlse), temp, up, True, grad)
+    got["grad"] = grad
+    check_all(x, vocab, (ids, z, tlse), temp, up, got, torch.float32)
+    sga_lib.sga_distill_grad(x, vocab, ids, z, got["lse"], got["rest"], back, teacher_lse=tlse,
+                             temperature=temp, grad_loss=up)
+    got["grad"] = back
+    check_all(x, vocab, (ids, z, tlse), temp, up, got, torch.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_vocabulary(sga_lib, dtype):
+    vocab, k = sga_lib.SGA_MAX_VOCAB, 128
+    x = torch.empty((2, vocab), dtype=DT[dtype], device="cuda").normal_(0.0, 3.0, generator=gen(31))
+    ids = torch.randint(0, vocab, (2, k), generator=gen(32), device="cuda")
+    ids[:, 0], ids[:, 1] = vocab - 1, 0
+    z = torch.randn((2, k), generator=gen(33), device="cuda") + 8.0
+    x.scatter_(1, ids, (z + 4.0).to(x.dtype))
+    lists = (ids.to(torch.int32), z, torch.logsumexp(z, 1) + 0.2)
+    up = torch.randn(2, generator=gen(34), device="cuda")
+    grad, back = torch.empty_like(x), torch.empty_like(x)
+    got = run_forward(sga_lib, x, vocab, lists, 1.0, up, True, grad)
+    got["grad"] = grad
+    check_all(x, vocab, lists, 1.0, up, got, DT[dtype])
+    sga_lib.sga_distill_grad(x, vocab, lists[0], z, got["lse"], got["rest"], back,
+                             teacher_lse=lists[2], grad_loss=up)
+    got["grad"] = back
+    check_all(x, vocab, lists, 1.0, up, got, DT[dtype])
+
+
+@pytest.mark.gpu
+def test_two_graphs_at_once(sga_lib):
+    """Two graphs of the same calls on other data, replayed on two streams at the
+    same time: each has its own results every time."""
+    work = []
+    for seed in (41, 42):
+        rows, vocab = 40, 30011
+        _, x, lists, up = make(seed, rows, vocab, vocab, "bf16", 40, True, 1.0, 0, 0)
+        ids, z, tlse = lists
+        out = [torch.empty(rows, device="cuda") for _ in range(3)]
+        out += [torch.empty_like(x), torch.empty_like(x)]
+
+        def step(x=x, ids=ids, z=z, tlse=tlse, up=up, out=out):
+            sga_lib.sga_distill(x, vocab, ids, z, out[0], teacher_lse=tlse, out_lse=out[1],
+                                out_lse_rest=out[2], grad_loss=up, out_grad=out[3])
+            sga_lib.sga_distill_grad(x, vocab, ids, z, out[1], out[2], out[4], teacher_lse=tlse,
+                                     grad_loss=up)
+
+        step()
+        torch.cuda.synchronize()
+        want = [t.nan_to_num(9.0) for t in out]
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=stream):
+            for _ in range(20):
+                step()
+        for t in out:
+            t.fill_(GUARD)
+        work.append((graph, stream, want, out, step))      # (step holds the inputs)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream, *_ in work:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, want, out, _ in work:
+            assert all(torch.equal(a, b.nan_to_num(9.0)) for a, b in zip(want, out))
+
+
 # ------------------------------------------------------------------ refusals
 
 

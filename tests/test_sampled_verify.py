@@ -164,6 +164,47 @@ def test_probs_at_extreme_temperatures(sga_lib, dtype, t):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,vocab,dtype,pad", [
+    (64, 5, "bf16", 1), (64, 1003, "f32", 1), (700, 9001, "bf16", 0), (40, 70001, "bf16", 3),
+    (40, 70001, "f32", 1), (30, 900001, "bf16", 1), (30, 480003, "f32", 0)])
+def test_greedy_rows_take_the_lowest_of_equal_logits(sga_lib, rows, vocab, dtype, pad):
+    """Logits of four values, NaN among them in some rows, -inf alone in others."""
+    g = gen(vocab)
+    _, x = guarded(rows, vocab, pad, 1, DT[dtype])
+    x.copy_(torch.randint(-2, 2, (rows, vocab), generator=g, device="cuda"))
+    x[1::4] = torch.where(torch.rand((len(x[1::4]), vocab), generator=g, device="cuda") < 3 / vocab,
+                          5.0, x[1::4].float()).to(x.dtype)
+    x[2::8, vocab // 3:] = math.nan
+    x[3::8] = NEG
+    x[5::8, :-1] = NEG
+    out = torch.empty((rows, vocab), device="cuda")
+    sga_lib.sga_probs(x, vocab, out, temperature=torch.zeros(rows, device="cuda"))
+    xf = x.float()
+    nan = torch.isnan(xf)
+    best = xf.masked_fill(nan, NEG).amax(1, keepdim=True)
+    hit = torch.where(nan.any(1, keepdim=True), nan, xf == best)
+    first = hit.to(torch.uint8).argmax(1)      # the first of equal ones
+    exp = torch.zeros_like(out)
+    exp[torch.arange(rows, device="cuda"), first] = 1.0
+    assert torch.equal(out, exp)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_probs_of_the_largest_vocabulary(sga_lib, dtype):
+    vocab = sga_lib.SGA_MAX_VOCAB
+    x = torch.empty((2, vocab), dtype=DT[dtype], device="cuda").normal_(0.0, 4.0, generator=gen(3))
+    x[1, vocab - 1] = 50.0
+    out = torch.full((2, vocab), GUARD, device="cuda")
+    for t in (None, torch.tensor([0.7, 0.0], device="cuda")):
+        sga_lib.sga_probs(x, vocab, out, temperature=t)
+        check_probs(out, x, vocab, t)
+    with pytest.raises(sga_lib.SgaError):
+        sga_lib.sga_probs(torch.empty((1, vocab + 1), dtype=DT[dtype], device="cuda"), vocab + 1,
+                          torch.empty((1, vocab + 1), device="cuda"))
+
+
+@pytest.mark.gpu
 def test_a_negative_or_nan_temperature_makes_the_row_nan(sga_lib):
     x = torch.randn((4, 100), device="cuda")
     x[3] = NEG
@@ -513,6 +554,47 @@ def test_logits_to_tokens_on_a_stream_and_in_a_graph(sga_lib):
         torch.cuda.synchronize()
         check()
     del g
+
+
+@pytest.mark.gpu
+def test_two_graphs_at_once(sga_lib):
+    """Two graphs of the same calls on other data, replayed on two streams at the
+    same time, again and again: each has its own results every time."""
+    steps = []
+    for seed in (1, 2):
+        g = gen(seed)
+        n, k, vocab = 6, 3, 30011
+        logits = torch.empty((n * (k + 1), vocab), device="cuda").normal_(0.0, 3.0, generator=g)
+        target = torch.empty_like(logits)
+        draft = torch.softmax(torch.randn((n * k, vocab), generator=g, device="cuda") * 3.0, 1)
+        cu = torch.arange(n + 1, device="cuda", dtype=torch.int32) * k
+        tokens = torch.randint(0, vocab, (n * k,), generator=g, device="cuda").to(torch.int32)
+        au, su = (torch.rand(m, generator=g, device="cuda") for m in (n * k, n))
+        out = [torch.empty(m, dtype=torch.int32, device="cuda") for m in (n * (k + 1), n, n, n)]
+
+        def step(logits=logits, target=target, draft=draft, cu=cu, tokens=tokens, au=au, su=su,
+                 out=out):
+            sga_lib.sga_probs(logits, vocab, target)
+            sga_lib.sga_sampled_verify(target, draft, cu, tokens, au, su, k, *out)
+
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (target, *out)]
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=stream):
+            for _ in range(20):
+                step()
+        for t in (target, *out):
+            t.fill_(-7)
+        steps.append((graph, stream, want, (target, *out), step))    # (step holds the inputs)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream, *_ in steps:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, want, got, _ in steps:
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
 # ------------------------------------------------------------------ refusals
