@@ -9,7 +9,8 @@ x the target model's hidden states, E the LM head's weight.  Serving
 probability, the row's entropy and the best alternatives.  Training
 (`loss_and_grads`): the mean negative log probability of given tokens, less an
 entropy bonus, and its gradients with respect to W and b, through the logits,
-the LM head (frozen) and the block.
+the LM head (frozen) and the block; or (`distill_and_grads`) the same of the mean
+divergence from the target model's top logits.
 
     python examples/draft_head.py        (needs a GB300; trains a small head)
 """
@@ -79,12 +80,32 @@ class DraftHead:
         # the logits are not needed again: their gradient takes their place
         sga.sga_token_logprobs_grad(logits, 0, self.org_vocab, tokens, lse, entropy, g_logprob,
                                     logits, grad_entropy=g_entropy)
-        sga.sga_linear_grad(logits, self.h[:n], self.lm_weight, self.workspace,
+        self._block_grads(x, logits)
+        return -logprob - entropy_bonus * entropy * live, self.grad_weight, self.grad_bias
+
+    def distill_and_grads(self, x, teacher_ids, teacher_logits, teacher_lse=None,
+                          temperature=1.0):
+        """teacher_ids / teacher_logits: int32 / float32 [n, k], the target's top
+        logits (-1: no entry), teacher_lse [n] the log-sum-exp of all of them over
+        the temperature, or None for the list by itself.  The divergence of each row
+        ([n]), and the gradients of their mean with respect to weight and bias."""
+        n = x.size(0)
+        logits = self._logits(x, self.preact[:n])
+        mean = torch.full((n,), 1.0 / n, device="cuda")
+        # loss and gradient in one pass; the gradient takes the logits' place
+        sga.sga_distill(logits, self.org_vocab, teacher_ids, teacher_logits, self.logprob[:n],
+                        teacher_lse=teacher_lse, temperature=temperature, grad_loss=mean,
+                        out_grad=logits)
+        self._block_grads(x, logits)
+        return self.logprob[:n], self.grad_weight, self.grad_bias
+
+    def _block_grads(self, x, grad_logits):
+        n = x.size(0)
+        sga.sga_linear_grad(grad_logits, self.h[:n], self.lm_weight, self.workspace,
                             grad_x=self.grad_h[:n])
         sga.sga_linear_grad(self.grad_h[:n], x, self.weight, self.workspace, sga.SGA_ACT_SILU,
                             self.preact[:n], grad_weight=self.grad_weight,
                             grad_bias=self.grad_bias)
-        return -logprob - entropy_bonus * entropy * live, self.grad_weight, self.grad_bias
 
 
 def main(steps=30, rows=256, hidden=512, vocab=8000):

@@ -446,6 +446,59 @@ def test_the_largest_vocabulary(sga_lib, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rest", [False, True])
+def test_a_draft_head_learns_from_a_targets_list(sga_lib, rest):
+    """Target logits -> their best log probabilities -> the draft head's step
+    (examples/draft_head.py), against automatic differentiation in 64 bits."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "draft_head.py")
+    spec = importlib.util.spec_from_file_location("draft_head_distill", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    rows, hidden, vocab, org, k, g = 150, 256, 1000, 990, 16, gen(51)
+
+    def normal(*shape, sigma):
+        return torch.empty(shape, device="cuda").normal_(0.0, sigma, generator=g)
+
+    head = example.DraftHead(normal(hidden, hidden, sigma=hidden ** -0.5).bfloat16(),
+                             normal(hidden, sigma=0.3),
+                             normal(vocab, hidden, sigma=2 * hidden ** -0.5).bfloat16(), rows,
+                             org_vocab=org)
+    x, target = normal(rows, hidden, sigma=1.0).bfloat16(), normal(rows, vocab, sigma=3.0)
+    ids = torch.empty((rows, k), dtype=torch.int32, device="cuda")
+    z = torch.empty((rows, k), device="cuda")
+    sga_lib.sga_token_logprobs(target, org, None, None, None, None, ids, z)
+    ids[::10] = -1                                # prompt rows: no teacher
+    loss, gw, gb = head.distill_and_grads(x, ids, z, torch.zeros(rows, device="cuda")
+                                          if rest else None)
+    weight = head.weight.double().requires_grad_()
+    bias = head.bias.double().requires_grad_()
+    h = x.double() @ weight.T + bias
+    h = x.double() + h * torch.sigmoid(h)
+    y = h @ head.lm_weight.double()[:org].T
+    live = (ids >= 0).any(1)
+    e = ids.clamp(min=0).long()
+    logp = z.double() if rest else torch.log_softmax(z.double(), 1)
+    p = logp.exp()
+    lse = torch.logsumexp(y, 1)
+    exp = (p * (logp - torch.gather(y, 1, e) + lse[:, None])).sum(1)
+    if rest:
+        pr = 1.0 - p.sum(1)
+        off = torch.ones_like(y, dtype=torch.bool).scatter_(1, e, False)
+        exp = exp + pr * (pr.log() - torch.logsumexp(y.masked_fill(~off, NEG), 1) + lse)
+    exp = torch.where(live, exp, 0.0)
+    exp.mean().backward()
+    # logits of size up to about 8 went through two roundings to bf16 (2^-8 of 8 each, and
+    # 2^-8 of h summed over the LM head): 0.1 covers both
+    assert ((loss.double() - exp).abs() <= 0.1).all()
+    # h, the logits, their gradient, dh and dz are each rounded to bf16 (about 2e-3 of the
+    # value in the 2-norm), the logits' rounding also moves s by up to 2^-8 * 8: below 3 %
+    for got, want in ((gw, weight.grad), (gb, bias.grad)):
+        rel = (got.double() - want).norm() / want.norm()
+        assert rel < 0.03, float(rel)
+
+
+@pytest.mark.gpu
 def test_two_graphs_at_once(sga_lib):
     """Two graphs of the same calls on other data, replayed on two streams at the
     same time: each has its own results every time."""

@@ -384,6 +384,32 @@ def test_every_end_of_the_uniforms(sga_lib, seed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fill", ["ones", "sparse"])
+def test_verify_of_the_largest_vocabulary(sga_lib, fill):
+    """Sums of 2^62 units (every weight 1), and weights at both ends alone."""
+    vocab = sga_lib.SGA_MAX_VOCAB
+    target = torch.zeros((3, vocab), device="cuda")
+    if fill == "ones":
+        target += 1.0
+    else:
+        target[:, 0], target[:, vocab - 1] = 0.25, 0.5
+    cu = torch.tensor([0, 0, 0, 0], dtype=torch.int32, device="cuda")
+    none_i = torch.empty(0, dtype=torch.int32, device="cuda")
+    none_f = torch.empty(0, device="cuda")
+    su = torch.tensor([0.0, 0.4, 1.0 - 2.0 ** -24], device="cuda")
+    out = [torch.empty(m, dtype=torch.int32, device="cuda") for m in (6, 3, 3, 3)]
+    sga_lib.sga_sampled_verify(target, None, cu, none_i, none_f, su, 1, *out)
+    u = [float(v) for v in su]
+    if fill == "ones":
+        # the first j with (j + 1) 2^38 > floor(u 2^62): floor(u 2^24)
+        want = [int(math.floor(v * 2.0 ** 24)) for v in u]
+    else:
+        want = [0 if v * 0.75 < 0.25 else vocab - 1 for v in u]
+    assert out[3].tolist() == want
+    assert out[1].tolist() == [1, 1, 1] and out[2].tolist() == [0, 0, 0]
+
+
+@pytest.mark.gpu
 def test_nan_and_negative_weights_are_not_drawn(sga_lib):
     p = torch.full((3, 100), math.nan, device="cuda")
     p[0, 50] = 0.5
