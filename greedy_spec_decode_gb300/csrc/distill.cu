@@ -196,13 +196,17 @@ __device__ __forceinline__ void teacher_row(List &l, const Entries &e, int k, fl
 enum Mode { kLoss, kBoth, kBackward };
 
 // Long rows (kT 256) and short ones (64): CTAs per SM, stages of the ring (16 or
-// 4 KB; the most that fits), and list warps.
+// 4 KB; the most that fits), and list warps.  The loss alone keeps nothing, so more
+// CTAs serve it better than longer rings (3 CTAs, 3 stages, 3 lists: 4096 x 152064 bf16
+// 175 us, 4096 x 32000 45; 2, 5, 4: 183 and 50), and the gradient alone is like it
+// (700 x 50257 fp32 51 us, 53).  Short rows, loss and gradient: 5, 7, 2 4096 x 8000 bf16
+// with 64 entries 55 us, 4, 9, 2 72; 6, 6, 1 71.
 template <int kT, Mode kMode>
 struct Form {
   static constexpr bool kSum = kMode != kBackward, kGrad = kMode != kLoss;
-  static constexpr int kPerSm = kT == 256 ? (kMode == kBoth ? 1 : 2) : (kMode == kBoth ? 5 : 6);
-  static constexpr int kSlots = kT == 256 ? (kMode == kBoth ? 12 : 5) : (kMode == kBoth ? 7 : 5);
-  static constexpr int kLists = kT == 256 ? 4 : 2;
+  static constexpr int kPerSm = kT == 256 ? (kMode == kBoth ? 1 : 3) : (kMode == kBoth ? 5 : 6);
+  static constexpr int kSlots = kT == 256 ? (kMode == kBoth ? 12 : 3) : (kMode == kBoth ? 7 : 5);
+  static constexpr int kLists = kT == 256 ? (kMode == kBoth ? 4 : 3) : 2;
   static constexpr int kRingBytes = kSlots * kStageVec<kT> * 16;
   static constexpr int kThreads = (kMode == kBoth ? 2 : 1) * kT + 32 + 32 * kLists;
 };

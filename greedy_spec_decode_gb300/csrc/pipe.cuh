@@ -1,4 +1,4 @@
-// pipe.cuh -- pieces shared by linear.cu and logprobs.cu: bounded mbarrier waits
+// pipe.cuh -- pieces shared by linear.cu, logprobs.cu and rowring.cuh: bounded mbarrier waits
 // that sleep in the barrier unit, single-lane issue from a converged warp, paired
 // fp32 arithmetic, and bf16 pairs and byte shifts of 16-byte pieces.  (The
 // self-test of the waits in lmhead.cu runs them out.)

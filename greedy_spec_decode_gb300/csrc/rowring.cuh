@@ -5,9 +5,11 @@
 // Both kernels read a row twice, for its sum and then to write something of each
 // of its logits.  A cluster of CTAs (one for short rows) shares a row, and each
 // keeps its piece in a ring of stages until it has been written: the logits come
-// from HBM once.  As a stage is written out it is filled with the next row, so the
-// loads of one row run under the stores of another.  A piece with more stages than
-// the ring keeps its last ones; the others are loaded a second time.
+// from HBM once.  Summing and writing are done by warps of their own, so that one
+// row is summed while another is written and a third is loaded (in turns by the
+// same warps, two CTAs per SM: probabilities of 2048 x 202048 bf16 460 us instead of
+// 382, loss and gradient of 4096 x 152064 bf16 651 instead of 396).  A piece with more
+// stages than the ring keeps its last ones; the others are loaded a second time.
 #pragma once
 
 #include <mutex>
@@ -24,9 +26,6 @@ constexpr int kVecPerThread = 4;  // 16-byte vectors of a stage per thread
 constexpr int kMaxCluster = 8;
 template <int kT>
 constexpr int kStageVec = kT * kVecPerThread;
-// CTAs per SM: two with 256 consumers, eight with 64 (short rows).
-template <int kT>
-constexpr int kPerSm = 512 / kT;
 constexpr int kMaxSlots = 13;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -299,7 +298,7 @@ __device__ __forceinline__ Sum sum_warp(Sum a, float scale) {
 // ---------------------------------------------------------------- exchange
 
 // What the CTAs of a cluster tell each other about their it-th row, 16 bytes each,
-// by turns in kN buffers (a power of two).
+// by turns in kN buffers.
 template <int kN>
 struct Exchange {
   uint64_t bar[kN];
