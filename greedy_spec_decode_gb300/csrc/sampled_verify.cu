@@ -61,7 +61,7 @@ struct VerifyArgs {
 // A running sum of weights w = max(x - y, 0) in units, for one thread: w 2^38 is
 // split into hi 2^23 + lo, hi = rint(w 2^15) and lo the rounded rest (in -2^22 ..
 // 2^22), both read off the mantissa of a sum with 1.5 2^23.  The integers carry that
-// constant's bits once per weight; at most 2^9 weights, then `take`.  (A conversion
+// constant's bits once per weight; at most 2^9 weights, then unit_total.  (A conversion
 // to 64 bits per weight takes 4 x the time of these eight operations.)
 struct UnitSum {
   uint32_t hi, lo;
@@ -133,7 +133,7 @@ __device__ __forceinline__ Units warp_units(const float *p, const float *q, int3
 
 // A cluster of CTAs per request, each with a run of the row's ids.  Bound by HBM
 // where requests are many (512 of 152064 ids, half of them with a rejection: 467 MB
-// in 87 us = 5.4 TB/s), by the chain of dependent steps where they are few: offsets,
+// in 76 us = 6.1 TB/s), by the chain of dependent steps where they are few: offsets,
 // drafts, their probabilities, the row's sum (segment sums stay in shared memory),
 // the totals' exchange, the segment of the drawn id once more (from L2).
 template <int kThreads>
