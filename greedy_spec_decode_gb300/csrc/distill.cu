@@ -200,13 +200,15 @@ enum Mode { kLoss, kBoth, kBackward };
 // CTAs serve it better than longer rings (3 CTAs, 3 stages, 3 lists: 4096 x 152064 bf16
 // 175 us, 4096 x 32000 45; 2, 5, 4: 183 and 50), and the gradient alone is like it
 // (700 x 50257 fp32 51 us, 53).  Short rows, loss and gradient: 5, 7, 2 4096 x 8000 bf16
-// with 64 entries 55 us, 4, 9, 2 72; 6, 6, 1 71.
+// with 64 entries 55 us, 4, 9, 2 72; 6, 6, 1 71.  Between them (128, of 8 KB): 4096 x 32000
+// 3, 7, 3 92 us (256: 100), 2, 12, 3 92, 2, 11, 4 95; 4096 x 24000 73 (64: 79).
 template <int kT, Mode kMode>
 struct Form {
   static constexpr bool kSum = kMode != kBackward, kGrad = kMode != kLoss;
-  static constexpr int kPerSm = kT == 256 ? (kMode == kBoth ? 1 : 3) : (kMode == kBoth ? 5 : 6);
-  static constexpr int kSlots = kT == 256 ? (kMode == kBoth ? 12 : 3) : (kMode == kBoth ? 7 : 5);
-  static constexpr int kLists = kT == 256 ? (kMode == kBoth ? 4 : 3) : 2;
+  static constexpr bool kKeeps = kMode == kBoth;
+  static constexpr int kPerSm = kT == 256 ? (kKeeps ? 1 : 3) : kT == 128 ? 3 : (kKeeps ? 5 : 6);
+  static constexpr int kSlots = kT == 256 ? (kKeeps ? 12 : 3) : kT == 128 ? 7 : (kKeeps ? 7 : 5);
+  static constexpr int kLists = kT == 256 ? (kKeeps ? 4 : 3) : kT == 128 ? 3 : 2;
   static constexpr int kRingBytes = kSlots * kStageVec<kT> * 16;
   static constexpr int kThreads = (kMode == kBoth ? 2 : 1) * kT + 32 + 32 * kLists;
 };
@@ -640,7 +642,7 @@ cudaError_t launch_rows(const void *logits, int64_t rows, int64_t ld, int64_t wi
   constexpr int kElt = kBf16 ? 2 : 4;
   auto kern = distill_kernel<kBf16, kT, kMode>;
   const RowKernel k = {reinterpret_cast<const void *>(kern), F::kThreads, F::kRingBytes,
-                       (kBf16 ? 0 : 1) + (kT == 256 ? 0 : 2) + 4 * kMode};
+                       (kBf16 ? 0 : 1) + 2 * (kT == 128 ? 6 : (kT == 256 ? 0 : 1) + 2 * kMode)};
   int64_t resident[6];
   const cudaError_t e = resident_clusters(k, resident);
   if (e != cudaSuccess) return e;
@@ -669,10 +671,15 @@ cudaError_t launch_distill(const void *logits, int dtype, int64_t rows, int64_t 
   const double inv_t = 1.0 / static_cast<double>(in.temperature);
   const Args args = {in, inv_t, static_cast<float>(inv_t),
                      static_cast<float>(1.4426950408889634 * inv_t)};
-  const bool small = small_rows(rows, valid * (dtype == SGA_BF16 ? 2 : 4), num_sms);
+  const int64_t bytes = valid * (dtype == SGA_BF16 ? 2 : 4);
+  const bool small = small_rows(rows, bytes, num_sms);
+  // (many rows of 36 to 72 KB: see Form)
+  const bool middle = bytes > (36 << 10) && bytes <= (72 << 10) && rows > 3 * num_sms;
   auto launch = [&](auto bf16, auto mode) {
     constexpr bool kBf16 = decltype(bf16)::value;
     constexpr Mode kMode = static_cast<Mode>(decltype(mode)::value);
+    if (kMode == kBoth && middle)
+      return launch_rows<kBf16, 128, kBoth>(logits, rows, ld, width, valid, args, ldg, err, stream);
     return (small ? launch_rows<kBf16, 64, kMode> : launch_rows<kBf16, 256, kMode>)(
         logits, rows, ld, width, valid, args, ldg, err, stream);
   };

@@ -396,7 +396,7 @@ __device__ __forceinline__ void leave(const Ring &ring, int chunks) {
 struct RowKernel {
   const void *kern;
   int threads, smem;  // dynamic shared memory
-  int slot;           // of this file's kernels, 0 .. 11
+  int slot;           // of this file's kernels, 0 .. 13
 };
 
 constexpr int kWidths[6] = {8, 6, 4, 3, 2, 1};  // CTAs that may share a row
@@ -411,7 +411,7 @@ inline cudaError_t resident_clusters(const RowKernel &k, int64_t (&out)[6]) {
     int n[6];
   };
   static std::mutex mu;
-  static Entry cache[12][64] = {};
+  static Entry cache[14][64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

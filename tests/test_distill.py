@@ -201,7 +201,8 @@ CASES = [  # rows, vocab, org, dtype, k, rest, temperature, pad, offset
     (900, 300, 290, "bf16", 8, True, 1.0, 1, 0),
     # several such rows per cluster, and short rows longer than a small ring
     (60, 900001, 900001, "bf16", 20, True, 1.0, 0, 0), (900, 24001, 24000, "bf16", 20, True, 1.0, 0, 0),
-    (900, 12001, 12001, "f32", 40, False, 1.0, 1, 1),
+    (900, 12001, 12001, "f32", 40, False, 1.0, 1, 1), (900, 17001, 17000, "bf16", 40, True, 1.0, 0, 0),
+    (900, 33001, 33001, "bf16", 20, True, 1.0, 1, 1),
 ]
 
 
