@@ -22,10 +22,11 @@ namespace {
 
 using Units = unsigned long long;
 
-constexpr int kBatch = 8;           // loads in flight per thread and row
+constexpr int kBatch = 16;          // loads in flight per thread and row
 constexpr int kStep = 32 * kBatch;  // ids that a warp takes at once
 constexpr int kMaxSegments = 256;   // sums kept of a CTA's ids
 constexpr int kMaxCtas = 8;         // CTAs per request
+constexpr int kThreads = 256;
 
 // A weight in units of 2^-38 (a NaN counts as 0).
 __device__ __forceinline__ Units units(float w) {
@@ -133,11 +134,11 @@ __device__ __forceinline__ Units warp_units(const float *p, const float *q, int3
 
 // A cluster of CTAs per request, each with a run of the row's ids.  Bound by HBM
 // where requests are many (512 of 152064 ids, half of them with a rejection: 467 MB
-// in 76 us = 6.1 TB/s), by the chain of dependent steps where they are few: offsets,
-// drafts, their probabilities, the row's sum (segment sums stay in shared memory),
-// the totals' exchange, the segment of the drawn id once more (from L2).
-template <int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+// in 69 us = 6.8 TB/s; with 8 loads of a row in flight per thread instead of 16 76),
+// by the chain of dependent steps where they are few: offsets, drafts, their
+// probabilities, the row's sum (segment sums stay in shared memory), the totals'
+// exchange, the segment of the drawn id once more (from L2).
+__global__ void __launch_bounds__(kThreads, 4)
     sampled_verify_kernel(VerifyArgs in, int ctas, uint32_t *err) {
   constexpr int kWarps = kThreads / 32;
   __shared__ Units seg[kMaxSegments];
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   // this CTA's ids, in segments of whole steps
   const int share = ((in.vocab + ctas - 1) / ctas + 3) & ~3;
   const int c0 = min(in.vocab, rank * share), c1 = min(in.vocab, c0 + share);
-  int len = 2 * kStep;
+  int len = kStep;
   while (static_cast<int64_t>(len) * kMaxSegments < share) len *= 2;
   const int segments = (c1 - c0 + len - 1) / len;
   const bool vec = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q)) & 15u) == 0;
@@ -307,28 +308,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   }
 }
 
-// Threads per CTA and CTAs per request, 1024 threads per SM: as many CTAs as let all
-// requests run at once (a few too many do no harm: about half of them read one row
-// instead of two), with at least 4096 ids each.  A CTA's loads in flight bound its
-// rate, so up to as many requests as fill the SMs in eights have CTAs of 512.  24 requests
-// of 200064 ids with 512 threads x 8 19 us, 256 x 8 23; 96 of 152064 with 256 x 6
-// 27, x 4 31, x 8 33; 512 with x 1 87, x 2 93, x 4 103, 512 x 1 95.
-void pick_ctas(int num_reqs, int64_t vocab, int num_sms, int *threads, int *ctas) {
+// CTAs per request, four per SM: as many as let all requests run at once, with at least
+// 4096 ids each (requests of 152064 ids: 76 x 6 13.7 us, x 8, of which 74 run at once, 17.5;
+// 100 x 4 15.0, x 6 17.8; 154 x 2 28.6, x 4 33.6; 512 x 1 69, x 2 74.  24 of 200064 x 8 9.2,
+// x 6 10.3; CTAs of 512 threads x 8 9.4).
+int pick_ctas(int num_reqs, int64_t vocab, int num_sms) {
   constexpr int kWidths[3] = {8, 6, 4};
-  constexpr int kClusters[3] = {36, 46, 74};  // at once, of 304 CTAs (GPCs hold whole clusters)
-  auto fit = [&](int i, int per_sm) {
-    return vocab >= 4096 * kWidths[i] &&
-           num_reqs * 20ll <= kClusters[i] * 21ll * per_sm * num_sms / 304;
-  };
-  *threads = fit(0, 2) ? 512 : 256;
-  if (fit(0, 4))
-    *ctas = 8;
-  else if (fit(1, 4))
-    *ctas = 6;
-  else if (fit(2, 4))
-    *ctas = 4;
-  else
-    *ctas = num_reqs <= 2ll * num_sms && vocab >= 8192 ? 2 : 1;
+  constexpr int kClusters[3] = {74, 97, 148};  // at once, of 608 CTAs (GPCs hold whole clusters)
+  for (int i = 0; i < 3; ++i)
+    if (vocab >= 4096 * kWidths[i] && num_reqs <= kClusters[i] * num_sms / 152) return kWidths[i];
+  return num_reqs <= 2ll * num_sms && vocab >= 8192 ? 2 : 1;
 }
 
 }  // namespace
@@ -346,11 +335,10 @@ cudaError_t launch_sampled_verify(const float *target, int64_t rows, int64_t ldt
                          cu_num_draft, draft_tokens, in_prefill, accept_u,
                          sample_u,   out_sampled, out_num_sampled, out_num_rejected,
                          out_last};
-  int threads, ctas;
-  pick_ctas(num_reqs, vocab, num_sms, &threads, &ctas);
+  const int ctas = pick_ctas(num_reqs, vocab, num_sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(num_reqs * ctas));
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -361,8 +349,7 @@ cudaError_t launch_sampled_verify(const float *target, int64_t rows, int64_t ldt
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(
-      &cfg, threads == 512 ? sampled_verify_kernel<512> : sampled_verify_kernel<256>, in, ctas, err);
+  return cudaLaunchKernelEx(&cfg, sampled_verify_kernel, in, ctas, err);
 }
 
 }  // namespace sga
