@@ -647,6 +647,8 @@ int sga_token_logprobs_grad(const void *logits, int dtype, int64_t rows, int64_t
  *                logits itself (ldp == ld); any other overlap is not allowed.
  * At a temperature above 0 a row with no logit above -inf is 0 everywhere, and
  * a row holding a NaN or +inf is NaN (but for its padding ids).  One launch.
+ * Equal calls give equal results; the order of a row's sum, and so its last bits,
+ * goes by the sizes and alignments.
  * Errors: SGA_ERR_DTYPE, SGA_ERR_SIZE (rows), SGA_ERR_VOCAB, SGA_ERR_SHARD
  * (ld or ldp < vocab), SGA_ERR_NULL, SGA_ERR_ALIGN.
  */
@@ -745,6 +747,8 @@ int sga_sampled_verify(const float *target_probs, int64_t rows, int64_t ldt,
  * stays finite); p_r is left out (0) where the row has no logit above -inf off
  * the list.  A row with no logit above -inf has lse -inf and gradient 0; one
  * holding a NaN or +inf has NaN for its lse, loss and gradient.  One launch.
+ * Equal calls give equal results; the order of a row's sums, and so their last
+ * bits, goes by the sizes and alignments and by whether a gradient is asked for.
  * Errors: SGA_ERR_DTYPE, SGA_ERR_SIZE (rows, k, temperature), SGA_ERR_VOCAB,
  * SGA_ERR_SHARD (ld or ldg < vocab), SGA_ERR_NULL, SGA_ERR_ALIGN.
  */
