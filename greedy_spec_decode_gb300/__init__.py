@@ -586,7 +586,24 @@ def sga_token_logprobs_grad(logits, shard_start, org_vocab, tokens, lse, entropy
     return out_grad
 
 
-def _probs_2d(t, name):
+# The calls below take up to 13 tensors, so each is looked at once: its layout, and that
+# it lies where the call's first one does, which _stream_on then finds to be the current
+# device (looked at apart, as above, a call takes 0.5 us longer).
+
+
+def _vec(t, dtype, numel, name, here):
+    """Address of a contiguous tensor of `dtype` with `numel` elements on device
+    `here`, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements")
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be on the device of the first tensor")
+    return t.data_ptr()
+
+
+def _probs_2d(t, name, here):
     """(rows, columns, row stride, address) of fp32 probabilities."""
     shape = t.shape
     if t.dtype is not _F32 or len(shape) != 2:
@@ -595,7 +612,19 @@ def _probs_2d(t, name):
     ld, col = t.stride()
     if col != 1 and width > 1:
         raise ValueError(f"{name} must have unit stride along the vocab")
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be on the device of the first tensor")
     return rows, width, ld if rows > 1 else max(ld, width), t.data_ptr()
+
+
+def _stream_on(here, stream):
+    """The raw handle of `stream`, or of the current one of device `here`, which has to be
+    the current device."""
+    if here < 0:
+        raise ValueError("CUDA tensors are needed")
+    if here != _current_device():
+        raise ValueError("CUDA tensors of the current device are needed")
+    return _current_raw_stream(here) if stream is None else _raw_stream(stream)
 
 
 def sga_probs(logits, org_vocab, out_probs, temperature=None, stream=None):
@@ -604,13 +633,14 @@ def sga_probs(logits, org_vocab, out_probs, temperature=None, stream=None):
     float32 of the same shape, or float32 logits themselves; ids past org_vocab
     get 0 (see include/sga.h)."""
     rows, width, ld, code = _logits_2d(logits)
-    out_rows, out_width, ldp, out = _probs_2d(out_probs, "out_probs")
+    here = logits.get_device()
+    out_rows, out_width, ldp, out = _probs_2d(out_probs, "out_probs", here)
     if out_rows != rows or out_width != width:
         raise ValueError("out_probs must have the shape of logits")
-    _on_gpu(logits, out_probs, temperature)
+    temps = _vec(temperature, _F32, rows, "temperature", here)
     _check("sga_probs", lib().sga_probs(
-        logits.data_ptr(), code, rows, ld, width, int(org_vocab),
-        _check_out(temperature, _F32, rows, "temperature"), out, ldp, _raw_stream(stream)))
+        logits.data_ptr(), code, rows, ld, width, int(org_vocab), temps, out, ldp,
+        _stream_on(here, stream)))
     return out_probs
 
 
@@ -623,54 +653,74 @@ def sga_sampled_verify(target_probs, draft_probs, cu_num_draft, draft_tokens, ac
     int32 [D], accept_u float32 [D], sample_u float32 [num_reqs] (uniform in
     [0, 1)); in_prefill: uint8 / bool [num_reqs] or None.  Outputs: int32
     [num_reqs, max_k + 1] and int32 [num_reqs] (see include/sga.h)."""
-    rows, vocab, ldt, target = _probs_2d(target_probs, "target_probs")
+    here = target_probs.get_device()
+    rows, vocab, ldt, target = _probs_2d(target_probs, "target_probs", here)
     n, max_k = cu_num_draft.numel() - 1, int(max_k)
     drafts = rows - n
     if n < 0 or drafts < 0:
         raise ValueError("target_probs must have a row per draft and one per request")
     ldd, draft = 0, None
     if draft_probs is not None:
-        d_rows, d_width, ldd, draft = _probs_2d(draft_probs, "draft_probs")
+        d_rows, d_width, ldd, draft = _probs_2d(draft_probs, "draft_probs", here)
         if d_rows != drafts or d_width != vocab:
             raise ValueError("draft_probs must have a row per draft, as wide as target_probs")
         if drafts == 0:
             draft = None
-    if in_prefill is not None and in_prefill.dtype not in (torch.uint8, torch.bool):
-        raise ValueError("in_prefill must be a uint8 or bool tensor")
+    prefill = None
+    if in_prefill is not None:
+        if in_prefill.dtype not in (torch.uint8, torch.bool):
+            raise ValueError("in_prefill must be a uint8 or bool tensor")
+        prefill = _vec(in_prefill, in_prefill.dtype, n, "in_prefill", here)
     f32, i32 = _F32, _I32
-    _on_gpu(target_probs, draft_probs, cu_num_draft, draft_tokens, accept_u, sample_u,
-            out_sampled, out_num_sampled, out_num_rejected, out_last, in_prefill)
     _check("sga_sampled_verify", lib().sga_sampled_verify(
         target, rows, ldt, draft, ldd, vocab, n,
-        _check_out(cu_num_draft, i32, n + 1, "cu_num_draft"),
-        _check_out(draft_tokens, i32, drafts, "draft_tokens"),
-        _check_out(in_prefill, in_prefill.dtype, n, "in_prefill")
-        if in_prefill is not None else None,
-        _check_out(accept_u, f32, drafts, "accept_u"), _check_out(sample_u, f32, n, "sample_u"),
-        max_k, _check_out(out_sampled, i32, n * (max_k + 1), "out_sampled"),
-        _check_out(out_num_sampled, i32, n, "out_num_sampled"),
-        _check_out(out_num_rejected, i32, n, "out_num_rejected"),
-        _check_out(out_last, i32, n, "out_last"), _raw_stream(stream)))
+        _vec(cu_num_draft, i32, n + 1, "cu_num_draft", here),
+        _vec(draft_tokens, i32, drafts, "draft_tokens", here), prefill,
+        _vec(accept_u, f32, drafts, "accept_u", here), _vec(sample_u, f32, n, "sample_u", here),
+        max_k, _vec(out_sampled, i32, n * (max_k + 1), "out_sampled", here),
+        _vec(out_num_sampled, i32, n, "out_num_sampled", here),
+        _vec(out_num_rejected, i32, n, "out_num_rejected", here),
+        _vec(out_last, i32, n, "out_last", here), _stream_on(here, stream)))
 
 
-def _teacher_lists(rows, teacher_ids, teacher_logits, teacher_lse):
-    """Addresses of a teacher's lists, and k."""
-    k = teacher_ids.shape[-1]
-    return (_check_out(teacher_ids, _I32, rows * k, "teacher_ids"),
-            _check_out(teacher_logits, _F32, rows * k, "teacher_logits"), k,
-            _check_out(teacher_lse, _F32, rows, "teacher_lse"))
-
-
-def _grad_2d(logits, out_grad, rows, width):
-    """Address and row stride of a gradient like logits."""
-    if out_grad is None:
-        return None, 0
-    if out_grad.dtype is not logits.dtype or out_grad.shape != (rows, width):
-        raise ValueError("out_grad must match logits")
-    ldg, col = out_grad.stride()
-    if col != 1 and width > 1:
-        raise ValueError("out_grad must have unit stride along the vocab")
-    return out_grad.data_ptr(), ldg if rows > 1 else max(ldg, width)
+def _distill(name, logits, org_vocab, teacher_ids, teacher_logits, teacher_lse, temperature,
+             loss, lse, lse_rest, lse_names, grad_loss, out_grad, stream):
+    """The two distillation calls, which differ in the sums that they give or take."""
+    rows, width, ld, code = _logits_2d(logits)
+    here = logits.get_device()
+    f32 = _F32
+    shape = teacher_ids.shape
+    if not shape:
+        raise ValueError("teacher_ids must have a row per row of logits")
+    k = shape[-1]
+    ids = _vec(teacher_ids, _I32, rows * k, "teacher_ids", here)
+    z = _vec(teacher_logits, f32, rows * k, "teacher_logits", here)
+    t_lse = _vec(teacher_lse, f32, rows, "teacher_lse", here)
+    lse = _vec(lse, f32, rows, lse_names[0], here)
+    rest = _vec(lse_rest, f32, rows, lse_names[1], here)
+    up = _vec(grad_loss, f32, rows, "grad_loss", here)
+    grad, ldg = None, 0
+    if out_grad is not None:
+        if out_grad.dtype is not logits.dtype or out_grad.shape != (rows, width):
+            raise ValueError("out_grad must match logits")
+        ldg, col = out_grad.stride()
+        if col != 1 and width > 1:
+            raise ValueError("out_grad must have unit stride along the vocab")
+        if out_grad.get_device() != here:
+            raise ValueError("out_grad must be on the device of the first tensor")
+        grad = out_grad.data_ptr()
+        if rows == 1 and ldg < width:
+            ldg = width
+    x, org_vocab, temperature = logits.data_ptr(), int(org_vocab), float(temperature)
+    if name == "sga_distill":
+        loss = _vec(loss, f32, rows, "out_loss", here)
+        _check(name, lib().sga_distill(x, code, rows, ld, width, org_vocab, ids, z, k, t_lse,
+                                       temperature, loss, lse, rest, up, grad, ldg,
+                                       _stream_on(here, stream)))
+    else:
+        _check(name, lib().sga_distill_grad(x, code, rows, ld, width, org_vocab, ids, z, k, t_lse,
+                                            temperature, lse, rest, up, grad, ldg,
+                                            _stream_on(here, stream)))
 
 
 def sga_distill(logits, org_vocab, teacher_ids, teacher_logits, out_loss=None, teacher_lse=None,
@@ -682,17 +732,9 @@ def sga_distill(logits, org_vocab, teacher_ids, teacher_logits, out_loss=None, t
     out_lse, out_lse_rest: float32 [rows] or None; out_grad: the gradient with
     respect to logits times grad_loss (float32 [rows] or None), like logits, or
     logits itself, or None (see include/sga.h)."""
-    rows, width, ld, code = _logits_2d(logits)
-    lists = _teacher_lists(rows, teacher_ids, teacher_logits, teacher_lse)
-    grad, ldg = _grad_2d(logits, out_grad, rows, width)
-    f32 = _F32
-    _on_gpu(logits, teacher_ids, teacher_logits, teacher_lse, out_loss, out_lse, out_lse_rest,
-            grad_loss, out_grad)
-    _check("sga_distill", lib().sga_distill(
-        logits.data_ptr(), code, rows, ld, width, int(org_vocab), *lists, float(temperature),
-        _check_out(out_loss, f32, rows, "out_loss"), _check_out(out_lse, f32, rows, "out_lse"),
-        _check_out(out_lse_rest, f32, rows, "out_lse_rest"),
-        _check_out(grad_loss, f32, rows, "grad_loss"), grad, ldg, _raw_stream(stream)))
+    _distill("sga_distill", logits, org_vocab, teacher_ids, teacher_logits, teacher_lse,
+             temperature, out_loss, out_lse, out_lse_rest, ("out_lse", "out_lse_rest"), grad_loss,
+             out_grad, stream)
 
 
 def sga_distill_grad(logits, org_vocab, teacher_ids, teacher_logits, lse, lse_rest, out_grad,
@@ -700,14 +742,8 @@ def sga_distill_grad(logits, org_vocab, teacher_ids, teacher_logits, lse, lse_re
     """Gradient of sga_distill from the lse and lse_rest (float32 [rows]) that
     it gave; lse_rest may be None without teacher_lse.  out_grad: like logits, or
     logits itself."""
-    rows, width, ld, code = _logits_2d(logits)
-    lists = _teacher_lists(rows, teacher_ids, teacher_logits, teacher_lse)
-    grad, ldg = _grad_2d(logits, out_grad, rows, width)
-    _on_gpu(logits, teacher_ids, teacher_logits, teacher_lse, lse, lse_rest, grad_loss, out_grad)
-    _check("sga_distill_grad", lib().sga_distill_grad(
-        logits.data_ptr(), code, rows, ld, width, int(org_vocab), *lists, float(temperature),
-        _check_out(lse, _F32, rows, "lse"), _check_out(lse_rest, _F32, rows, "lse_rest"),
-        _check_out(grad_loss, _F32, rows, "grad_loss"), grad, ldg, _raw_stream(stream)))
+    _distill("sga_distill_grad", logits, org_vocab, teacher_ids, teacher_logits, teacher_lse,
+             temperature, None, lse, lse_rest, ("lse", "lse_rest"), grad_loss, out_grad, stream)
     return out_grad
 
 

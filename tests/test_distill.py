@@ -571,6 +571,36 @@ def test_validation(sga_lib, grad_call):
         assert call(a=None, b=None, c=None, grad=None) == 0      # nothing asked for
 
 
+def test_binding_says_what_is_wrong(sga_lib):
+    """The specific refusal comes before that of host memory."""
+    i32 = torch.int32
+    ok = dict(logits=torch.zeros(2, 8), org_vocab=8, teacher_ids=torch.zeros(2, 3, dtype=i32),
+              teacher_logits=torch.zeros(2, 3))
+    for wrong, word in ((dict(teacher_ids=torch.zeros(2, 3, dtype=torch.int64)), "teacher_ids"),
+                        (dict(teacher_ids=torch.tensor(1, dtype=i32)), "teacher_ids"),
+                        (dict(teacher_logits=torch.zeros(2, 4)), "teacher_logits"),
+                        (dict(teacher_lse=torch.zeros(3)), "teacher_lse"),
+                        (dict(out_loss=torch.zeros(4)[::2]), "out_loss"),
+                        (dict(out_grad=torch.zeros(8, 2).t()), "out_grad"), (dict(), "CUDA")):
+        with pytest.raises(ValueError, match=word):
+            sga_lib.sga_distill(**dict(ok, **wrong))
+
+
+@pytest.mark.gpu
+def test_binding_refuses_host_tensors_among_others(sga_lib):
+    i32 = torch.int32
+
+    def t(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    ok = dict(logits=t(2, 8), org_vocab=8, teacher_ids=t(2, 3, dtype=i32), teacher_logits=t(2, 3),
+              teacher_lse=t(2), out_loss=t(2), out_grad=t(2, 8))
+    sga_lib.sga_distill(**ok)
+    for name in ("logits", "teacher_ids", "teacher_logits", "teacher_lse", "out_loss", "out_grad"):
+        with pytest.raises(ValueError):
+            sga_lib.sga_distill(**dict(ok, **{name: ok[name].cpu()}))
+
+
 def test_binding_refuses_wrong_tensors(sga_lib):
     def t(*shape, dtype=torch.float32):
         return torch.zeros(shape, dtype=dtype)
