@@ -153,11 +153,14 @@ __global__ void __launch_bounds__(kThreads, 4)
   // (every CTA of the cluster has begun: its memory may be written)
   if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   pdl_wait();
+  // (not after the offsets: a dependent load is 1 us)
+  const uint8_t prefill = in.in_prefill != nullptr ? in.in_prefill[req] : 0;
+  const float u = in.sample_u[req];
   const int64_t c = in.cu[req];
   const int64_t k = in.cu[req + 1] - c;
   int32_t *sampled = in.sampled + req * (in.max_k + 1);
   const bool bad = k < 0 || k > in.max_k || c < 0 || c + k > in.rows - in.num_reqs;
-  if (bad || (in.in_prefill != nullptr && in.in_prefill[req] != 0)) {
+  if (bad || prefill != 0) {
     if (rank == 0) {
       if (tid <= in.max_k) sampled[tid] = -1;
       if (tid == 0) {
@@ -171,17 +174,17 @@ __global__ void __launch_bounds__(kThreads, 4)
     return;
   }
   // the first draft that is not accepted (every CTA finds it by itself)
-  const float u = in.sample_u[req];
   if (warp == 0) {
     bool fails = false;
     if (lane < k) {
       const int32_t t = in.tokens[c + lane];
+      const float accept = in.accept_u[c + lane];
       s_draft[lane] = t;
       fails = true;
       if (t >= 0 && t < in.vocab) {
         const float p = in.target[(c + req + lane) * in.ldt + t];
         const float q = in.draft != nullptr ? in.draft[(c + lane) * in.ldd + t] : 1.0f;
-        fails = !(__fmul_rn(in.accept_u[c + lane], q) < p);
+        fails = !(__fmul_rn(accept, q) < p);
       }
     }
     const unsigned votes = __ballot_sync(0xffffffffu, fails);
