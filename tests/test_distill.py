@@ -5,8 +5,11 @@ masks and alignments where the kernels change path, and the refusals.
 Tolerances, by counting roundings: a term 2^t, t = (x - max) log2(e) / T, is off by
 5 ln2 2^-24 |t| + 2^-22 of itself; weighted by the terms themselves, |t| is at most
 some 40 on average (log2 of the largest vocabulary, and spread), and the sums of
-n terms, by 256 threads or more, have at most n / 256 + 64 additions along any
-path.  So lse and lse_rest are within
+n terms have at most n / 256 + 64 additions along any path: 256 threads or more add
+up two halves each (rows of up to 72 KB 128, of up to 48 KB 64 threads: at most n / 128
++ 16 there, which is less up to n = 12288, and from there to the 24576 ids of such a
+row at most 48 roundings of 2^-24 more, if all went the same way).  So lse and lse_rest
+are within
 
     tol(n) = (5 ln2 40 + 4 + n / 256 + 64) 2^-24
 

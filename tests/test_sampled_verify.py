@@ -5,8 +5,9 @@ kernels change path, and the entry points' refusals.
 The probabilities' tolerance, by counting roundings: t = (x - max) log2(e) / T has
 five of 2^-24 relative to itself (the difference, the constant, its quotient,
 the product, and bf16's none), so 2^t is off by 5 ln2 2^-24 |t|, and by 2^-22 as
-computed; the row's sum of n positive terms, taken by 256 threads or more, has
-at most n / 256 + 64 additions along any path, 2^-24 each; the last product and
+computed; the row's sum of n positive terms, taken by 256 threads or more in two
+halves each, has at most n / 256 + 64 additions along any path, 2^-24 each (rows of up
+to 48 KB by 64 threads: n / 128 + 16, less up to n = 12288); the last product and
 the reciprocal add 2^-22.  Terms below 2^-126 may be flushed.
 
 What sga_sampled_verify emits is whole numbers defined exactly (units of 2^-38,
