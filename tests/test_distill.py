@@ -15,8 +15,8 @@ are within
 
 of the exact ones, plus half a step of what they are rounded to (2^-24 of their
 size).  The loss holds lse once with the list's weight (at most 1) and lse_rest -
-lse with the rest's; the teacher's own numbers are exact to 64 bits: 3 tol(n), and
-its own rounding.  A gradient's parts are s_j and p_r e^(y_j - lse_rest), each off
+lse with the rest's; the teacher's own numbers are in 64 bits, with logarithms to
+2^-25: 3 tol(n), and its own rounding.  A gradient's parts are s_j and p_r e^(y_j - lse_rest), each off
 by the error of its exponent (that of its sum; of t, 5 ln2 2^-24 |t|; of y = x / T,
 2^-23 |y|; of the rounded sums, 2^-23 of theirs) and a few products; the output
 rounding is half a step.
