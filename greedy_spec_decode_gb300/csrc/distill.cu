@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
   if (tid == 0) {
     for (int i = 0; i < slots; ++i) {
       mbar_init(smem_u32(&sh.ring.full[i]), 1);
-      mbar_init(smem_u32(&sh.ring.empty[i]), kWarps);
+      mbar_init(smem_u32(&sh.ring.empty[i]), F::kKeeps ? ring_arrivals(kWarps) : kWarps);
     }
     for (uint32_t i = 0; i < kHeld; ++i) {
       mbar_init(smem_u32(&sh.ready[i]), 1);
@@ -354,7 +354,6 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
       listed = __reduce_or_sync(0xffffffffu, listed);
       RunSum a = {0.0f, neg_inf(), 0u};
       Place r = at;
-      const int kept = kMode == kBoth ? max(0, pc.stages - slots) : pc.stages;  // the first that stays
       for (int j = 0; j < pc.stages; ++j) {
         ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
         if (!ok) break;
@@ -387,7 +386,9 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
         sum_rebase(a, vec_max<kBf16>(most), scale, room);
 #pragma unroll
         for (int u = 0; u < kVecPerThread; ++u) sum_vector<kBf16>(a, q[u], scale);
-        if (j < kept) {
+        if (kMode == kBoth) {
+          sum_frees(sh.ring, r, j, pc.stages, slots, lane);
+        } else {
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
         }
@@ -410,9 +411,11 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
           exchange_tell(sh.ex, it, make_uint4(__float_as_uint(rest.m), __float_as_uint(rest.s), 0u, 0u),
                         walk.chunk, chunks, lane);
       }
-      // (a slot's uses are waited for one by one: a wait tells only even from odd ones)
-      for (int j = 0; kMode == kBoth && j < kept; ++j, step(r, slots))
-        ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+      // (every use of a slot is waited for, the second loads' too: see ring_arrivals)
+      for (int j = slots; kMode == kBoth && j < pc.stages && ok; ++j, step(r, slots)) {
+        ok = warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+        if (ok) sum_frees(sh.ring, r, pc.stages + j - slots, pc.stages, slots, lane);
+      }
       if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
       at = later(at, num_loads(pc.stages, slots, kMode == kBoth), slots);
     }

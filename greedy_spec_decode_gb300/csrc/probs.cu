@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(Form<kT>::kThreads, Form<kT>::kPerSm)
   if (tid == 0) {
     for (int i = 0; i < slots; ++i) {
       mbar_init(smem_u32(&sh.ring.full[i]), 1);
-      mbar_init(smem_u32(&sh.ring.empty[i]), kWarps);
+      mbar_init(smem_u32(&sh.ring.empty[i]), ring_arrivals(kWarps));
     }
     for (uint32_t i = 0; i < kHeld; ++i) mbar_init(smem_u32(&sh.stored[i]), kWarps);
     sh.ring.abort = 0;
@@ -149,10 +149,7 @@ __global__ void __launch_bounds__(Form<kT>::kThreads, Form<kT>::kPerSm)
 #pragma unroll
           for (int u = 0; u < kVecPerThread; ++u) sum_vector<kBf16>(a, q[u], scale);
         }
-        if (j < kept) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
-        }
+        sum_frees(sh.ring, r, j, pc.stages, slots, lane);
         step(r, slots);
       }
       if (greedy && ok) {
@@ -216,9 +213,11 @@ __global__ void __launch_bounds__(Form<kT>::kThreads, Form<kT>::kPerSm)
                                    static_cast<uint32_t>(best_id), 0u),
                         walk.chunk, chunks, lane);
       }
-      // (a slot's uses are waited for one by one: a wait tells only even from odd ones)
-      for (int j = 0; j < kept; ++j, step(r, slots))
-        ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+      // (every use of a slot is waited for, the second loads' too: see ring_arrivals)
+      for (int j = 0; j < kept && ok; ++j, step(r, slots)) {
+        ok = warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+        if (ok) sum_frees(sh.ring, r, pc.stages + j, pc.stages, slots, lane);
+      }
       if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
       at = later(at, num_loads(pc.stages, slots, true), slots);
     }

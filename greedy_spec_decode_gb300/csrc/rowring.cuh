@@ -9,13 +9,15 @@
 // row is summed while another is written and a third is loaded (in turns by the
 // same warps, two CTAs per SM: probabilities of 2048 x 202048 bf16 460 us instead of
 // 382, loss and gradient of 4096 x 152064 bf16 651 instead of 396).  A piece with more
-// stages than the ring keeps its last ones; the others are loaded a second time.
+// stages than the ring keeps its last ones; the others are loaded a second time (in
+// which order, and who frees a slot: ringorder.h).
 #pragma once
 
 #include <mutex>
 #include <type_traits>
 
 #include "pipe.cuh"
+#include "ringorder.h"
 #include "scan.cuh"
 
 namespace sga {
@@ -143,25 +145,11 @@ struct Ring {
   int abort;
 };
 
-// A load's place: its slot, and the parity of the slot's use.
-struct Place {
-  int slot;
-  uint32_t phase;
-};
-__device__ __forceinline__ void step(Place &a, int slots) {
-  if (++a.slot == slots) {
-    a.slot = 0;
-    a.phase ^= 1;
-  }
-}
-__device__ __forceinline__ Place later(const Place &a, int by, int slots) {
-  const int s = a.slot + by, q = s / slots;
-  return {s - q * slots, a.phase ^ (q & 1)};
-}
-
-// Loads of a row's piece: its stages, and (kept) those again that the ring could not keep.
-__device__ __forceinline__ int num_loads(int stages, int slots, bool kept) {
-  return stages + (kept && stages > slots ? stages - slots : 0);
+// A sum warp has seen a load of a kept row (and read it): its part in freeing the slot.
+__device__ __forceinline__ void sum_frees(Ring &ring, const Place &at, int load, int stages,
+                                          int slots, int lane) {
+  __syncwarp();
+  if (lane < sum_arrivals(load, stages, slots)) mbar_arrive(smem_u32(&ring.empty[at.slot]));
 }
 
 // bulk_load of what is read once: first to leave L2.  (Rows that are not kept: loss of
