@@ -39,7 +39,21 @@ struct alignas(16) List {
   float total, on_list, rest;   // sum_p + rest_p, sum_p, rest_p
   int any;                      // the row has a teacher
   float m, coef, of;            // (kBackward) off the list the gradient is coef 2^((x - m) scale)
+  int anew;                     // (kBackward) the row's sums are taken anew
 };
+
+// The largest log-sum-exp that a gradient is worked out from: 2^-15 of the gradient is
+// lost by its rounding to fp32.  Larger ones hold less of the sum (a rest masked by -1e9
+// nothing), and one below T = 1 may be infinite though no logit is.
+constexpr float kMostLse = 512.0f;
+
+// Whether the gradient needs more of a row's sums than its saved lse and lse_rest hold.
+__device__ __forceinline__ bool sums_lost(float lse, float lse_rest, const Args &in) {
+  auto lost = [&](float v) {
+    return fabsf(v) > kMostLse && !(v == neg_inf() && in.temperature >= 1.0f);
+  };
+  return lost(lse) || (in.lse != nullptr && lost(lse_rest));
+}
 
 // Sums of a and b over a warp: a's in lanes 0-15, b's in 16-31 (64-bit additions are
 // 1/64 of the 32-bit rate here, so the two share theirs).
@@ -68,10 +82,9 @@ struct Entries {
   float z[kPerLane], x[kPerLane];
 };
 
-// Loads a row's entries, and its logits there if they are in columns [c0, c1).
-template <bool kBf16>
-__device__ __forceinline__ void entries_load(Entries &e, const Args &in, int64_t row,
-                                             const char *x, int valid, int c0, int c1, int lane) {
+// Loads a row's entries.
+__device__ __forceinline__ void entries_load(Entries &e, const Args &in, int64_t row, int valid,
+                                             int lane) {
 #pragma unroll
   for (int r = 0; r < kPerLane; ++r) {
     const int i = r * 32 + lane;
@@ -79,6 +92,11 @@ __device__ __forceinline__ void entries_load(Entries &e, const Args &in, int64_t
     e.z[r] = i < in.k ? in.logits[row * in.k + i] : 0.0f;
     if (e.id[r] < 0 || e.id[r] >= valid) e.id[r] = -1;
   }
+}
+
+// The row's logits there, if they are in columns [c0, c1).
+template <bool kBf16>
+__device__ __forceinline__ void entries_look(Entries &e, const char *x, int c0, int c1) {
 #pragma unroll
   for (int r = 0; r < kPerLane; ++r)
     e.x[r] = e.id[r] >= 0 && e.id[r] >= c0 && e.id[r] < c1 ? read_elem<kBf16>(x, e.id[r]) : neg_inf();
@@ -220,6 +238,7 @@ struct DistillShared {
   Ring ring;
   uint64_t ready[kHeld], stored[kHeld];  // a row's list is there; its gradient is written
   Exchange<2 * kHeld> ex;
+  uint64_t joined;  // (kBackward) the parts of a row's sum are there
   Sum warp_sum[2][kT / 32];
   List list[kHeld];
 };
@@ -259,6 +278,8 @@ __device__ __forceinline__ uint4 grad_vec(const uint4 q, float m, float scale, f
 // numbers a row ahead, reading the listed logits by themselves, and write the loss
 // and the listed ids' gradients a row behind.  kBackward has no sum warps: a row's
 // pieces have nothing in common but the teacher's numbers, and are rows of their own.
+// Where the saved sums hold too little (sums_lost), the CTA of one of a row's pieces takes
+// the whole row: its gradient warps sum it, as the sum warps do, and go over it again.
 template <bool kBf16, int kT, Mode kMode>
 __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kPerSm)
     distill_kernel(const char *logits, int64_t ld_bytes, int64_t num_rows, int valid, int width,
@@ -290,6 +311,7 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
       mbar_init(smem_u32(&sh.ready[i]), 1);
       mbar_init(smem_u32(&sh.stored[i]), kWarps);
     }
+    mbar_init(smem_u32(&sh.joined), kWarps);
     sh.ring.abort = 0;
     exchange_init(sh.ex, chunks);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -302,14 +324,103 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
   auto piece = [&](uint32_t it) {
     return piece_of<kBf16, kT>(logits + walk.row(it) * ld_bytes, valid, walk.chunk_of(it), chunks);
   };
+  // the same where the row's sums are taken anew: all of it for one of its pieces (not the
+  // first one of every row, which some of the CTAs have all of: gradient of 2048 x 200064
+  // bf16 728 us where all rows are such ones, 368 so)
+  auto has_row = [&](uint32_t it) {
+    const uint32_t row = static_cast<uint32_t>(walk.row(it)), n = static_cast<uint32_t>(chunks);
+    return walk.chunk_of(it) == static_cast<int>((row + row * n / gridDim.x) % n);
+  };
+  auto whole_piece = [&](uint32_t it) {
+    Piece q = piece_of<kBf16, kT>(logits + walk.row(it) * ld_bytes, valid, 0, 1);
+    if (!has_row(it)) q.c0 = q.b0 = q.b1 = q.c1 = q.stages = 0;
+    return q;
+  };
   // waits for the it-th row's list, or its stored gradient
   auto wait_held = [&](uint64_t (&bar)[kHeld], uint32_t it) {
     return warp_wait(smem_u32(&bar[it % kHeld]), (it / kHeld) & 1, abort_flag);
   };
   bool ok = true;
+  // One warp's sum of a piece's logits off the list, from the stages at r on: the warp is
+  // the by-th, the thread the at-th of those that share the piece.
+  auto piece_sum = [&](const Piece &pc, const int32_t (&id)[kPerLane], Place &r, int at, int by) {
+    // the single elements at the piece's ends (warp 0), without listed ones
+    float end_x[2] = {neg_inf(), neg_inf()};
+    if (by == 0 && (pc.c0 < pc.b0 || pc.b1 < pc.c1)) {
+      uint32_t mask = 0;
+#pragma unroll
+      for (int r = 0; r < kPerLane; ++r) {
+        if (id[r] >= pc.c0 && id[r] < pc.b0) mask |= 1u << (id[r] - pc.c0);
+        if (id[r] >= pc.b1 && id[r] < pc.c1) mask |= 256u << (id[r] - pc.b1);
+      }
+      mask = __reduce_or_sync(0xffffffffu, mask);
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int j = end_column(pc, side, at);
+        if (j >= 0 && !((mask >> (side * 8 + at)) & 1)) end_x[side] = read_elem<kBf16>(pc.p, j);
+      }
+    }
+    // the stages (mod 32) with listed logits among this warp's vectors
+    auto owns = [&](int c) {
+      return c >= pc.b0 && c < pc.b1 &&
+             static_cast<int>(static_cast<uint32_t>(c - pc.b0) / (32 * kVec)) % kWarps == by;
+    };
+    uint32_t listed = 0;
+#pragma unroll
+    for (int s = 0; s < kPerLane; ++s)
+      if (owns(id[s])) listed |= 1u << ((id[s] - pc.b0) / (kStageVec<kT> * kVec) % 32);
+    listed = __reduce_or_sync(0xffffffffu, listed);
+    const float room = 12.0f / scale;
+    RunSum a = {0.0f, neg_inf(), 0u};
+    for (int j = 0; j < pc.stages; ++j) {
+      ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
+      if (!ok) break;
+      uint4 *st = buf + r.slot * kStageVec<kT>;
+      const int c = pc.b0 + j * kStageVec<kT> * kVec;
+      const int n = min(kStageVec<kT>, (pc.b1 - c) / kVec);
+      if ((listed >> (j % 32)) & 1) {
+#pragma unroll
+        for (int s = 0; s < kPerLane; ++s)
+          if (owns(id[s]) && id[s] >= c && id[s] < c + n * kVec)
+            store_elem<kBf16>(reinterpret_cast<char *>(st), id[s] - c, neg_inf());
+        // (the slot's next copy is ordered behind these writes)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
+      uint4 q[kVecPerThread];
+      if (n == kStageVec<kT>) {
+#pragma unroll
+        for (int u = 0; u < kVecPerThread; ++u) q[u] = st[u * kT + at];
+      } else {
+#pragma unroll
+        for (int u = 0; u < kVecPerThread; ++u) {
+          const int i = u * kT + at;
+          q[u] = i < n ? st[i] : make_uint4(kMasked, kMasked, kMasked, kMasked);
+        }
+      }
+      uint4 most = q[0];
+#pragma unroll
+      for (int u = 1; u < kVecPerThread; ++u) most = vec_larger<kBf16>(most, q[u]);
+      sum_rebase(a, vec_max<kBf16>(most), scale, room);
+#pragma unroll
+      for (int u = 0; u < kVecPerThread; ++u) sum_vector<kBf16>(a, q[u], scale);
+      if (kMode == kBoth) {
+        sum_frees(sh.ring, r, j, pc.stages, slots, lane);
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
+      }
+      step(r, slots);
+    }
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      sum_rebase(a, end_x[side], scale, room);
+      sum_add(a, end_x[side], neg_inf(), scale);
+    }
+    return sum_warp(sum_result(a), scale);
+  };
   if (warp < kSumWarps) {
     // ------------------------------------------------------------- sum warps
-    const float room = 12.0f / scale;
     Place at = {0, 0};
     int32_t next_id[kPerLane];
     auto fetch = [&](int64_t row) {
@@ -326,80 +437,8 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
 #pragma unroll
       for (int r = 0; r < kPerLane; ++r) id[r] = next_id[r];
       if (it + 1 < num_its) fetch(walk.row(it + 1));
-      // the single elements at the piece's ends (warp 0), without listed ones
-      float end_x[2] = {neg_inf(), neg_inf()};
-      if (warp == 0 && (pc.c0 < pc.b0 || pc.b1 < pc.c1)) {
-        uint32_t mask = 0;
-#pragma unroll
-        for (int r = 0; r < kPerLane; ++r) {
-          if (id[r] >= pc.c0 && id[r] < pc.b0) mask |= 1u << (id[r] - pc.c0);
-          if (id[r] >= pc.b1 && id[r] < pc.c1) mask |= 256u << (id[r] - pc.b1);
-        }
-        mask = __reduce_or_sync(0xffffffffu, mask);
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          const int j = end_column(pc, side, tid);
-          if (j >= 0 && !((mask >> (side * 8 + tid)) & 1)) end_x[side] = read_elem<kBf16>(pc.p, j);
-        }
-      }
-      // the stages (mod 32) with listed logits among this warp's vectors
-      auto owns = [&](int c) {
-        return c >= pc.b0 && c < pc.b1 &&
-               static_cast<int>(static_cast<uint32_t>(c - pc.b0) / (32 * kVec)) % kWarps == warp;
-      };
-      uint32_t listed = 0;
-#pragma unroll
-      for (int s = 0; s < kPerLane; ++s)
-        if (owns(id[s])) listed |= 1u << ((id[s] - pc.b0) / (kStageVec<kT> * kVec) % 32);
-      listed = __reduce_or_sync(0xffffffffu, listed);
-      RunSum a = {0.0f, neg_inf(), 0u};
       Place r = at;
-      for (int j = 0; j < pc.stages; ++j) {
-        ok = ok && warp_wait(smem_u32(&sh.ring.full[r.slot]), r.phase, abort_flag);
-        if (!ok) break;
-        uint4 *st = buf + r.slot * kStageVec<kT>;
-        const int c = pc.b0 + j * kStageVec<kT> * kVec;
-        const int n = min(kStageVec<kT>, (pc.b1 - c) / kVec);
-        if ((listed >> (j % 32)) & 1) {
-#pragma unroll
-          for (int s = 0; s < kPerLane; ++s)
-            if (owns(id[s]) && id[s] >= c && id[s] < c + n * kVec)
-              store_elem<kBf16>(reinterpret_cast<char *>(st), id[s] - c, neg_inf());
-          // (the slot's next copy is ordered behind these writes)
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-        uint4 q[kVecPerThread];
-        if (n == kStageVec<kT>) {
-#pragma unroll
-          for (int u = 0; u < kVecPerThread; ++u) q[u] = st[u * kT + tid];
-        } else {
-#pragma unroll
-          for (int u = 0; u < kVecPerThread; ++u) {
-            const int i = u * kT + tid;
-            q[u] = i < n ? st[i] : make_uint4(kMasked, kMasked, kMasked, kMasked);
-          }
-        }
-        uint4 most = q[0];
-#pragma unroll
-        for (int u = 1; u < kVecPerThread; ++u) most = vec_larger<kBf16>(most, q[u]);
-        sum_rebase(a, vec_max<kBf16>(most), scale, room);
-#pragma unroll
-        for (int u = 0; u < kVecPerThread; ++u) sum_vector<kBf16>(a, q[u], scale);
-        if (kMode == kBoth) {
-          sum_frees(sh.ring, r, j, pc.stages, slots, lane);
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.ring.empty[r.slot]));
-        }
-        step(r, slots);
-      }
-#pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        sum_rebase(a, end_x[side], scale, room);
-        sum_add(a, end_x[side], neg_inf(), scale);
-      }
-      Sum rest = sum_warp(sum_result(a), scale);
+      Sum rest = piece_sum(pc, id, r, tid, warp);
       if (lane == 0) sh.warp_sum[it & 1][warp] = rest;
       consumers_sync<kT>();  // (every warp keeps to the rows' barriers)
       if (warp == static_cast<int>(it % kWarps)) {
@@ -424,32 +463,62 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
     Place at = {0, 0};
     const int gtid = tid - kSumWarps * 32;
     const bool with_up = kMode == kBoth && in.grad_loss != nullptr;
+    uint32_t sums = 0;  // rows whose sums were taken anew
     float next_up = with_up && num_its > 0 ? in.grad_loss[walk.row(0)] : 1.0f;
     for (uint32_t it = 0; it < num_its; ++it) {
       const int64_t row = walk.row(it);
-      const Piece pc = piece(it);
-      const float up = next_up * in.inv_t32;
+      Piece pc = piece(it);
+      float up = next_up * in.inv_t32;
       if (with_up && it + 1 < num_its) next_up = in.grad_loss[walk.row(it + 1)];
       float end_x[2] = {neg_inf(), neg_inf()};
+      auto ends = [&] {
 #pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        const int j = end_column(pc, side, gtid);
-        if (j >= 0) end_x[side] = read_elem<kBf16>(pc.p, j);
-      }
+        for (int side = 0; side < 2; ++side) {
+          const int j = end_column(pc, side, gtid);
+          if (j >= 0) end_x[side] = read_elem<kBf16>(pc.p, j);
+        }
+      };
+      ends();
       ok = (kMode != kBoth || exchange_wait(sh.ex, it, abort_flag)) && wait_held(sh.ready, it);
       if (!ok) break;
-      const List &l = sh.list[it % kHeld];
+      List &l = sh.list[it % kHeld];
       bool live = l.any;
       float m = l.m, coef = l.coef;
-      if (kMode == kBoth) {
-        const Sum rest = exchange_sum(sh.ex, it, chunks, lane, scale);
-        const Sum total = sum_merge(l.listed, rest, scale);
+      Sum total = {neg_inf(), 0.0f};
+      auto by_sums = [&](const Sum &rest) {
+        total = sum_merge(l.listed, rest, scale);
         live = live && total.s != 0.0f;
         m = rest.m == neg_inf() ? 0.0f : rest.m;
         coef = nan_f32();
         if (!is_nan(total.s)) {
           const float share = sum_at(rest, total.m, scale) / total.s;  // s_r
           coef = rest.s == 0.0f ? 0.0f : up * fmaf(l.total, share, -l.rest) / rest.s;
+        }
+      };
+      const bool anew = kMode == kBackward && l.anew;
+      if constexpr (kMode == kBoth) by_sums(exchange_sum(sh.ex, it, chunks, lane, scale));
+      if (kMode == kBackward && anew) {
+        pc = whole_piece(it);
+        ends();
+        if (pc.c1 > 0) {
+          int32_t id[kPerLane];
+#pragma unroll
+          for (int s = 0; s < kPerLane; ++s) id[s] = s * 32 + lane < in.k ? l.id[s * 32 + lane] : -1;
+          up = coef;
+          Sum rest = piece_sum(pc, id, at, gtid, warp);
+          if (lane == 0) sh.warp_sum[sums & 1][warp] = rest;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.joined));
+          ok = ok && warp_wait(smem_u32(&sh.joined), sums & 1, abort_flag);
+          if (!ok) break;
+          rest = sum_warp(lane < kWarps ? sh.warp_sum[sums & 1][lane] : Sum{neg_inf(), 0.0f}, scale);
+          ++sums;
+          by_sums(rest);
+          if (gtid == 0) {  // (all warps have read what was there)
+            l.m = total.m;
+            l.of = (rest.s == 0.0f ? l.on_list : l.total) / total.s;
+            l.any = live;
+          }
         }
       }
       char *g = static_cast<char *>(in.grad) + row * ldg_bytes;
@@ -509,7 +578,7 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
         const int j = end_column(pc, side, gtid);
         if (j >= 0) store_elem<kBf16>(g, j, value(end_x[side]));
       }
-      if (walk.chunk_of(it) == chunks - 1)
+      if (anew ? has_row(it) : walk.chunk_of(it) == chunks - 1)
         for (int j = valid + gtid; j < width; j += kT) store_elem<kBf16>(g, j, 0.0f);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.stored[it % kHeld]));
@@ -517,14 +586,27 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
     }
     if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
   } else if (warp == kSumWarps + kGradWarps) {
-    copy_rows<kBf16, kT>(sh.ring, buf, slots, kMode == kBoth, logits, ld_bytes, walk, valid, lane,
-                         err);
+    // (kBackward) the saved sums, a row ahead: do they hold enough?
+    float next_own = 0.0f, next_rest = 0.0f;
+    auto fetch = [&](uint32_t it) {
+      if (kMode != kBackward || it >= num_its) return;
+      next_own = in.in_lse[walk.row(it)];
+      if (in.lse != nullptr) next_rest = in.in_lse_rest[walk.row(it)];
+    };
+    fetch(0);
+    auto load = [&](uint32_t it, Piece &q) {
+      const bool anew = kMode == kBackward && sums_lost(next_own, next_rest, in);
+      fetch(it + 1);
+      q = anew ? whole_piece(it) : piece(it);
+      return anew ? 2 * q.stages : num_loads(q.stages, slots, kMode == kBoth);
+    };
+    copy_rows<kBf16, kT>(sh.ring, buf, slots, kMode == kBoth, num_its, load, lane, err);
     pdl_launch_dependents();
   } else {
     // ------------------------------------------------------------ list warps
     auto fix = [&](uint32_t it, float up, float m, float of) {
       const List &l = sh.list[it % kHeld];
-      const Piece pc = piece(it);
+      const Piece pc = kMode == kBackward && l.anew ? whole_piece(it) : piece(it);
       char *g = static_cast<char *>(in.grad) + walk.row(it) * ldg_bytes;
       for (int i = lane; i < in.k; i += 32) {
         const int32_t id = l.id[i];
@@ -538,16 +620,19 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
     auto fetch = [&](uint32_t it) {
       const int64_t row = walk.row(it);
       int c0 = 0, c1 = valid;
-      if (kMode == kBackward) {  // (other pieces may be written already)
-        const Piece pc = piece(it);
-        c0 = pc.c0;
-        c1 = pc.c1;
+      if (kMode == kBackward) {
         next_own = in.in_lse[row];
         if (in.in_lse_rest != nullptr) next_rest = in.in_lse_rest[row];
         if (in.grad_loss != nullptr) next_up = in.grad_loss[row];
       }
       if (in.lse != nullptr) next_lse = in.lse[row];
-      entries_load<kBf16>(next, in, row, logits + row * ld_bytes, valid, c0, c1, lane);
+      entries_load(next, in, row, valid, lane);
+      if (kMode == kBackward) {  // (other pieces may be written already)
+        const Piece pc = sums_lost(next_own, next_rest, in) ? whole_piece(it) : piece(it);
+        c0 = pc.c0;
+        c1 = pc.c1;
+      }
+      entries_look<kBf16>(next, logits + row * ld_bytes, c0, c1);
     };
     if (first < num_its) fetch(first);
     for (uint32_t it = first; ok && it < num_its + F::kLists; it += F::kLists) {
@@ -567,7 +652,11 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
           l.coef = next_up * in.inv_t32 * lost(base) *
                    (by_rest ? fmaf(total, ex2((next_rest - next_own) * kLog2e), -l.rest) : total);
           l.of = total * lost(next_own);
-          if (next_own == neg_inf()) l.any = 0;
+          l.anew = sums_lost(next_own, next_rest, in);
+          if (l.anew)
+            l.coef = next_up * in.inv_t32;
+          else if (next_own == neg_inf())
+            l.any = 0;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.ready[it % kHeld]));
@@ -583,7 +672,7 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
       if (kMode == kBackward) {
         const float lse = in.in_lse[row];
         ok = wait_held(sh.stored, last);
-        if (ok && l.any) fix(last, up, lse * in.temperature, l.of);
+        if (ok && l.any) fix(last, up, l.anew ? l.m : lse * in.temperature, l.of);
         __syncwarp();
         continue;
       }

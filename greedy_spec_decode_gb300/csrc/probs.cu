@@ -347,7 +347,11 @@ __global__ void __launch_bounds__(Form<kT>::kThreads, Form<kT>::kPerSm)
     }
     if (!ok && lane == 0) raise_abort(&sh.ring.abort, err);
   } else {
-    copy_rows<kBf16, kT>(sh.ring, buf, slots, true, logits, ld_bytes, walk, valid, lane, err);
+    auto load = [&](uint32_t it, Piece &q) {
+      q = piece(it);
+      return num_loads(q.stages, slots, true);
+    };
+    copy_rows<kBf16, kT>(sh.ring, buf, slots, true, num_its, load, lane, err);
     pdl_launch_dependents();
   }
   leave(sh.ring, chunks);

@@ -164,11 +164,12 @@ __device__ __forceinline__ void bulk_load_once(uint32_t dst, const void *src, ui
       : "memory");
 }
 
-// The copy warp: every piece's stages into the ring.
-template <bool kBf16, int kT, class W>
+// The copy warp: the stages of `num_its` pieces into the ring.  load(it, q) says which is
+// the it-th, and how often its stages are loaded in all (those past the last one are the
+// first again).  What is loaded once is first to leave L2.
+template <bool kBf16, int kT, class F>
 __device__ __forceinline__ void copy_rows(Ring &ring, uint4 *buf, int slots, bool kept,
-                                          const char *logits, int64_t ld_bytes, const W &w,
-                                          int valid, int lane, uint32_t *err) {
+                                          uint32_t num_its, F &&load, int lane, uint32_t *err) {
   constexpr int kElt = kBf16 ? 2 : 4, kVec = 16 / kElt;
   const volatile int *abort_flag = &ring.abort;
   Place at = {0, 0};
@@ -176,10 +177,9 @@ __device__ __forceinline__ void copy_rows(Ring &ring, uint4 *buf, int slots, boo
   bool ok = true;
   uint64_t policy;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-  for (uint32_t it = 0; it < w.n && ok; ++it) {
-    const Piece q =
-        piece_of<kBf16, kT>(logits + w.row(it) * ld_bytes, valid, w.chunk_of(it), w.chunks);
-    const int loads = num_loads(q.stages, slots, kept);
+  for (uint32_t it = 0; it < num_its && ok; ++it) {
+    Piece q;
+    const int loads = load(it, q);
     for (int j = 0; j < loads; ++j) {
       if (filled < slots) {
         ++filled;
@@ -194,7 +194,7 @@ __device__ __forceinline__ void copy_rows(Ring &ring, uint4 *buf, int slots, boo
         mbar_expect_tx(smem_u32(&ring.full[at.slot]), bytes);
         const uint32_t dst = smem_u32(buf + at.slot * kStageVec<kT>);
         const char *src = q.p + static_cast<int64_t>(c) * kElt;
-        if (kept)
+        if (kept || loads > q.stages)
           bulk_load(dst, src, bytes, smem_u32(&ring.full[at.slot]));
         else
           bulk_load_once(dst, src, bytes, smem_u32(&ring.full[at.slot]), policy);

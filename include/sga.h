@@ -765,6 +765,12 @@ int sga_distill(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t
  *   lse          device fp32 [rows].
  *   lse_rest     device fp32 [rows]; may be NULL iff teacher_lse is.
  *   out_grad     as sga_distill, not NULL.
+ * The sums are rounded to fp32, which costs s_j and the rest's term up to 2^-23
+ * (|lse| + |lse_rest|) of themselves.  In a row whose lse (or, with teacher_lse,
+ * lse_rest) is above 512 in size, or infinite other than by logits of -inf, they hold too
+ * little, or nothing, of the sum of exponentials (a rest masked by -1e9, a low
+ * temperature): such a row's sums are taken anew from its logits, by one CTA,
+ * which reads the row twice.
  * Other arguments, results and errors as sga_distill.
  */
 int sga_distill_grad(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t vocab,

@@ -540,6 +540,183 @@ def test_two_graphs_at_once(sga_lib):
             assert all(torch.equal(a, b.nan_to_num(9.0)) for a, b in zip(want, out))
 
 
+# --------------------------------- sums that an fp32 log-sum-exp does not hold
+
+
+def shifted_exp(y):
+    """Softmax of each row and log2 of its terms relative to the largest one (rows
+    without a finite logit: 0)."""
+    top = y.max(1, keepdim=True).values
+    t = torch.where(y > NEG, y - top, NEG)
+    e = torch.exp(t)
+    return e / e.sum(1, keepdim=True).clamp(min=1.0), torch.nan_to_num(t, 0, 0, 0) / math.log(2.0)
+
+
+def formula(x, org, ids, z, tlse, temp, up):
+    """(gradient, tolerance) in 64 bits by the closed form, each softmax relative to
+    its own largest logit, so that no log-sum-exp has to hold a small sum beside a
+    large offset.
+
+    Tolerance: s_j and the rest's share of itself are terms 2^t over a sum.  A term is
+    off by 5 ln2 2^-24 (|t| + 24) + 2^-22 of itself (its exponent counts from a logit at
+    most 12 below the largest, the rest's from there to the row's another 12), where it
+    is not below 2^-126 altogether; a sum, and the factors of it, by 2 tol_sum.  Where the
+    saved sums are used, |lse| and |lse_rest| are at most 512 and each rounded once, and the
+    difference and product with them again: 2^-22 512.  An entry's p is rounded to fp32, and
+    its s_j is a term; the output's rounding is half a step."""
+    y = x[:, :org].double() / temp
+    rows, k = ids.shape
+    entry = (ids >= 0) & (ids < org)
+    at = torch.where(entry, ids, 0).long()
+    zt = torch.where(entry, z.double() / temp, NEG)
+    logp = zt - (torch.logsumexp(zt, 1, keepdim=True) if tlse is None else tlse.double()[:, None])
+    p = torch.where(entry, torch.exp(logp), 0.0)
+    on = torch.zeros_like(y).scatter_add_(1, at, p)
+    off = torch.zeros_like(y).scatter_add_(1, at, entry.double()) == 0
+    yr = torch.where(off, y, NEG)
+    pr = (1.0 - p.sum(1)).clamp(min=0.0) if tlse is not None else torch.zeros_like(p[:, 0])
+    pr = torch.where((yr > NEG).any(1) & entry.any(1), pr, 0.0)[:, None]
+    total = p.sum(1, keepdim=True) + pr
+    live = ((y > NEG).any(1) & entry.any(1)).double()[:, None]
+    (s, t), (r, tr) = shifted_exp(y), shifted_exp(yr)
+    scale = up.double()[:, None] / temp * live
+    grad = scale * (total * s - on - pr * r)
+    rel = 2 * tol_sum(org) + 2.0 ** -22 + 2.0 ** -22 * 512
+    ln = 5 * math.log(2.0) * 2.0 ** -24
+    tol = total * s * (rel + ln * (24 - t.clamp(min=-150))) + on * 2.0 ** -22
+    tol = scale.abs() * (tol + pr * r * (rel + ln * (24 - tr.clamp(min=-150))) + 1e-37)
+    return grad, tol + grad.abs() * torch.finfo(x.dtype).eps / 2 + 1e-38
+
+
+def both_gradients(sga_lib, x, org, lists, temp, up, pad, offset):
+    """The gradient of the loss's own pass, and that of the separate call from the sums
+    that the pass gave, each checked for what lies around it."""
+    rows, vocab = x.shape
+    ids, z, tlse = lists
+    gbuf, grad = guarded(rows, vocab, pad, offset, x.dtype)
+    got = run_forward(sga_lib, x, org, lists, temp, up, True, grad)
+    bbuf, back = guarded(rows, vocab, pad, offset, x.dtype)
+    sga_lib.sga_distill_grad(x, org, ids, z, got["lse"], got["rest"], back, teacher_lse=tlse,
+                             temperature=temp, grad_loss=up)
+    for buf in (gbuf, bbuf):
+        check_guard(buf, rows, vocab, pad, offset)
+    return grad, back, got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,vocab,dtype,k,pad,offset", [
+    (14, 4001, "f32", 5, 1, 3), (14, 3000, "bf16", 40, 0, 0), (700, 1001, "bf16", 20, 1, 1),
+    (700, 900, "f32", 70, 0, 0), (5, 200003, "bf16", 20, 0, 0), (5, 200003, "f32", 20, 1, 1),
+    (470, 30011, "bf16", 12, 1, 3)], ids=str)
+@pytest.mark.parametrize("temp", [0.5, 1.0, 1.5])
+def test_rests_that_only_low_values_mask(sga_lib, rows, vocab, dtype, k, pad, offset, temp):
+    """The rest's logits are all the same low value, or far below the listed ones: its
+    log-sum-exp in fp32 holds nothing of how many there are (and overflows, for the
+    lowest value of the type below T = 1)."""
+    org, g = vocab - 1, gen(rows + vocab)
+    _, x = guarded(rows, vocab, pad, offset, DT[dtype])
+    x.normal_(0.0, 3.0, generator=g)
+    ids = torch.randint(0, org, (rows, k), generator=g, device="cuda")
+    z = torch.randn((rows, k), generator=g, device="cuda") * 2.0
+    lowest = torch.finfo(x.dtype).min
+    kinds = [None, -1e9, lowest, -700.0, -400.0, -1e4, lowest / 2, NEG, "spread", "all", None, "up"]
+    for r in range(rows):
+        kind = kinds[r % len(kinds)]
+        own = x[r, ids[r]].clone()
+        if kind == "spread":
+            x[r] -= 2000.0
+        elif kind == "all":                      # listed logits too: lse is lost as well
+            x[r], own = lowest, torch.full_like(own, lowest)
+        elif kind == "up":                       # lse lost by logits far above 0
+            x[r] += 3000.0
+            own = own + 3000.0
+        elif kind is not None:
+            x[r] = kind
+        x[r, ids[r]] = own
+    ids = ids.to(torch.int32)
+    tlse = torch.logsumexp(z / temp, 1) + 0.3 * torch.rand(rows, generator=g, device="cuda")
+    up = torch.randn(rows, generator=g, device="cuda")
+    for t in (tlse, None):
+        grad, back, _ = both_gradients(sga_lib, x, org, (ids, z, t), temp, up, pad, offset)
+        exp, tol = formula(x, org, ids, z, t, temp, up)
+        for name, got in (("grad", grad), ("back", back)):
+            near(got[:, :org], exp, tol, name)
+            assert (got[:, org:] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("temp", [1e-6, 1e-5, 1e-3, 0.02])
+@pytest.mark.parametrize("rows,vocab", [(30, 5003), (700, 1001), (3, 150001)])
+@pytest.mark.parametrize("rest", [False, True])
+def test_low_temperatures_of_ordinary_logits(sga_lib, temp, rows, vocab, rest):
+    """Logits of 20 to 60 that differ by some T: |lse| is up to 6e7."""
+    g, k = gen(17), 12
+    x = torch.randn((rows, vocab), generator=g, device="cuda") * (3.0 * temp)
+    x += 20.0 + 40.0 * torch.rand((rows, 1), generator=g, device="cuda")
+    ids = torch.randint(0, vocab, (rows, k), generator=g, device="cuda").to(torch.int32)
+    z = torch.randn((rows, k), generator=g, device="cuda") * temp
+    temp = float(torch.tensor(temp))
+    tlse = (torch.logsumexp(z.double() / temp, 1) + 0.3).float() if rest else None
+    up = torch.randn(rows, generator=g, device="cuda") * temp
+    grad, back, _ = both_gradients(sga_lib, x, vocab, (ids, z, tlse), temp, up, 0, 0)
+    exp, tol = formula(x, vocab, ids, z, tlse, temp, up)
+    near(grad, exp, tol, "grad")
+    near(back, exp, tol, "back")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sums_that_overflow(sga_lib, dtype):
+    """Below T = 1 a finite logit's y can pass the largest fp32 number, either way."""
+    rows, vocab, k, temp, g = 8, 2001, 6, 0.5, gen(19)
+    x = torch.randn((rows, vocab), generator=g, device="cuda").to(DT[dtype])
+    big = torch.finfo(x.dtype).max
+    ids = torch.randint(0, vocab, (rows, k), generator=g, device="cuda")
+    x[0, 7], x[0, 1900] = big, big           # two ids have all the probability
+    x[1] = -big                              # all have the same
+    x[2] = NEG
+    x[3] = -big
+    x[3, ids[3]] = NEG                       # the listed ones have none
+    x[4] = NEG
+    x[4, ids[4]] = -big                      # the listed ones have all of it
+    x[5, 3] = math.nan
+    x[6, 3] = math.inf
+    ids = ids.to(torch.int32)
+    z = torch.randn((rows, k), generator=g, device="cuda")
+    tlse = torch.logsumexp(z / temp, 1) + 0.2
+    up = torch.randn(rows, generator=g, device="cuda")
+    for t in (tlse, None):
+        grad, back, _ = both_gradients(sga_lib, x, vocab, (ids, z, t), temp, up, 3, 1)
+        exp, tol = formula(x, vocab, ids, z, t, temp, up)
+        exp[5:7] = math.nan
+        near(grad, exp, tol.nan_to_num(0), "grad")
+        near(back, exp, tol.nan_to_num(0), "back")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,vocab,dtype", [(40, 3001, "bf16"), (6, 150001, "f32"),
+                                              (500, 5000, "bf16")])
+def test_lost_sums_in_the_logits_place(sga_lib, rows, vocab, dtype):
+    """Every other row is masked by a low value; the gradient is written over the logits."""
+    temp, g = 1.5, gen(23)
+    _, x = guarded(rows, vocab, 1, 3, DT[dtype])
+    x.normal_(0.0, 3.0, generator=g)
+    ids = torch.randint(0, vocab, (rows, 9), generator=g, device="cuda")
+    own = torch.gather(x, 1, ids)
+    x[::2] = -1e9
+    x.scatter_(1, ids, own)
+    ids = ids.to(torch.int32)
+    z = torch.randn((rows, 9), generator=g, device="cuda")
+    tlse = torch.logsumexp(z / temp, 1) + 0.2
+    up = torch.randn(rows, generator=g, device="cuda")
+    exp, tol = formula(x, vocab, ids, z, tlse, temp, up)
+    _, back, got = both_gradients(sga_lib, x, vocab, (ids, z, tlse), temp, up, 1, 3)
+    sga_lib.sga_distill_grad(x, vocab, ids, z, got["lse"], got["rest"], x, teacher_lse=tlse,
+                             temperature=temp, grad_loss=up)
+    near(x, exp, tol, "in place")
+    assert torch.equal(x, back)
+
+
 # ------------------------------------------------------------------ refusals
 
 
