@@ -694,6 +694,8 @@ def _distill(name, logits, org_vocab, teacher_ids, teacher_logits, teacher_lse, 
         raise ValueError("teacher_ids must have a row per row of logits")
     k = shape[-1]
     ids = _vec(teacher_ids, _I32, rows * k, "teacher_ids", here)
+    if teacher_logits.dim() > 1 and teacher_logits.shape[-1] != k:  # (of the size, not the order)
+        raise ValueError("teacher_logits must have teacher_ids' k entries per row")
     z = _vec(teacher_logits, f32, rows * k, "teacher_logits", here)
     t_lse = _vec(teacher_lse, f32, rows, "teacher_lse", here)
     lse = _vec(lse, f32, rows, lse_names[0], here)

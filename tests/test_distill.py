@@ -798,3 +798,23 @@ def test_binding_refuses_wrong_tensors(sga_lib):
     for wrong in (dict(lse=t(3)), dict(lse_rest=t(1)), dict(out_grad=t(3, 8)), dict()):
         with pytest.raises(ValueError):
             sga_lib.sga_distill_grad(**dict(ok, **wrong))
+
+
+@pytest.mark.parametrize("grad_call", [False, True])
+def test_lists_in_another_order_are_refused(sga_lib, grad_call):
+    """A contiguous [k, rows] tensor has a list's size, but not its order; lists of rows
+    in more dimensions, and flat ones, have it (and come as far as the device's check)."""
+    i32 = torch.int32
+    ok = dict(logits=torch.zeros(6, 8), org_vocab=8, teacher_ids=torch.zeros(6, 3, dtype=i32),
+              teacher_logits=torch.zeros(6, 3))
+    if grad_call:
+        ok.update(lse=torch.zeros(6), lse_rest=torch.zeros(6), out_grad=torch.zeros(6, 8))
+    call = sga_lib.sga_distill_grad if grad_call else sga_lib.sga_distill
+    for wrong, word in ((dict(teacher_logits=torch.zeros(3, 6)), "teacher_logits"),
+                        (dict(teacher_ids=torch.zeros(3, 6, dtype=i32)), "teacher_ids"),
+                        (dict(teacher_logits=torch.zeros(3, 3, 2)), "teacher_logits"),
+                        (dict(teacher_logits=torch.zeros(18)), "CUDA"),
+                        (dict(teacher_ids=torch.zeros(2, 3, 3, dtype=i32),
+                              teacher_logits=torch.zeros(2, 3, 3)), "CUDA")):
+        with pytest.raises(ValueError, match=word):
+            call(**dict(ok, **wrong))
