@@ -227,6 +227,26 @@ def test_probs_in_place(sga_lib, rows, vocab):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,vocab", [(13, 5000), (40, 50257), (12, 480003), (40, 480003),
+                                        (700, 9001), (3, 1 << 22)])
+def test_probs_in_place_at_temperatures(sga_lib, rows, vocab):
+    """Greedy rows among them, with equal best logits: in rows longer than the rings
+    their place is found by a second look at the logits, before they are written over."""
+    x = torch.randn((rows, vocab + 1), generator=gen(2), device="cuda")[:, :vocab]
+    org, g = vocab - 3, gen(4)
+    plant(x, org)
+    t = temperatures("mixed", rows, g)
+    for r in range(1, rows, 6):                          # every other greedy row
+        x[r, torch.randint(0, org, (3,), generator=g, device="cuda")] = 90.0
+    was = x.clone()
+    out = torch.empty((rows, vocab + 1), device="cuda")[:, :vocab]
+    sga_lib.sga_probs(x, org, out, temperature=t)
+    sga_lib.sga_probs(x, org, x, temperature=t)
+    assert torch.equal(x.nan_to_num(9.0), out.nan_to_num(9.0))
+    check_probs(x, was, org, t)
+
+
+@pytest.mark.gpu
 def test_probs_rows_past_32_bits(sga_lib):
     """Row offsets of 2^31 elements and more, in and out."""
     stride = (1 << 31) // 3 + 5
@@ -359,6 +379,20 @@ VERIFY = [  # requests, max_k, vocab, drafts, pad, offset
 def test_verify_matches_the_definition(sga_lib, case):
     n, max_k, vocab, drafts, pad, offset = case
     c = verify_case(n * 31 + vocab, n, max_k, vocab, drafts, pad, offset)
+    check_same(gpu_verify(sga_lib, *c), plain_verify(*host(c)))
+    assert sga_lib.sga_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,max_k,vocab", [
+    (85, 2, 40003), (6, 3, 30011), (120, 1, 20012), (100, 2, 24579), (200, 1, 9001),
+    (20, 5, 16383), (400, 1, 152064), (310, 3, 9999)])
+@pytest.mark.parametrize("drafts", ["probs", "tokens"])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 3)])
+def test_every_number_of_ctas_per_request(sga_lib, n, max_k, vocab, drafts, pad, offset):
+    """Requests that 6, 4 or 2 CTAs share, or that one takes in segments of several steps
+    (aligned rows: vocabularies of a multiple of four)."""
+    c = verify_case(n * 17 + vocab, n, max_k, vocab, drafts, pad, offset)
     check_same(gpu_verify(sga_lib, *c), plain_verify(*host(c)))
     assert sga_lib.sga_device_error() == 0
 
