@@ -8,9 +8,9 @@
 // Drawing inverts the cumulative sum in ascending id order.  A sum in fp32
 // depends on its order, and near the end of a vocabulary neighbouring sums
 // differ by less than its rounding, so weights are counted in whole units of
-// 2^-38: 64-bit sums of up to 2^24 weights of at most 1 are exact (< 2^62), and
-// any split of the row draws the same id.  An id of probability 1e-9 still has
-// 275 units.
+// 2^-38: 64-bit sums of up to 2^24 weights of at most 1 are exact (at most 2^62), and
+// any split of the row draws the same id.  How fine a draw is goes by the uniform's 24
+// bits, not by the units.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -62,13 +62,15 @@ struct VerifyArgs {
 // A running sum of weights w = max(x - y, 0) in units, for one thread: w 2^38 is
 // split into hi 2^23 + lo, hi = rint(w 2^15) and lo the rounded rest (in -2^22 ..
 // 2^22), both read off the mantissa of a sum with 1.5 2^23.  The integers carry that
-// constant's bits once per weight; at most 2^9 weights, then unit_total.  (A conversion
-// to 64 bits per weight takes 4 x the time of these eight operations.)
+// constant's bits once per weight; fewer than 2^9 weights (lo could add up to 2^31), then
+// unit_total.  (A conversion to 64 bits per weight takes 4 x the time of these eight
+// operations.)
 struct UnitSum {
   uint32_t hi, lo;
 };
 constexpr float kMagic = 12582912.0f;       // 1.5 2^23
 constexpr uint32_t kMagicBits = 0x4b400000u;
+static_assert(kBatch < 512, "weights per UnitSum");
 
 __device__ __forceinline__ void unit_add(UnitSum &a, float x, float y) {
   float w;  // rounded once, clamped to [0, 1], a NaN becomes 0
@@ -134,7 +136,7 @@ __device__ __forceinline__ Units warp_units(const float *p, const float *q, int3
 
 // A cluster of CTAs per request, each with a run of the row's ids.  Bound by HBM
 // where requests are many (512 of 152064 ids, half of them with a rejection: 467 MB
-// in 69 us = 6.8 TB/s; with 8 loads of a row in flight per thread instead of 16 76),
+// in 70 us = 6.7 TB/s; with 8 loads of a row in flight per thread instead of 16 76),
 // by the chain of dependent steps where they are few: offsets, drafts, their
 // probabilities, the row's sum (segment sums stay in shared memory), the totals'
 // exchange, the segment of the drawn id once more (from L2).
@@ -312,9 +314,11 @@ __global__ void __launch_bounds__(kThreads, 4)
 }
 
 // CTAs per request, four per SM: as many as let all requests run at once, with at least
-// 4096 ids each (requests of 152064 ids: 76 x 6 13.7 us, x 8, of which 74 run at once, 17.5;
-// 100 x 4 15.0, x 6 17.8; 154 x 2 28.6, x 4 33.6; 512 x 1 69, x 2 74.  24 of 200064 x 8 9.2,
-// x 6 10.3; CTAs of 512 threads x 8 9.4).
+// 4096 ids each.  (The three counts are what runs at once of this kernel on 152 SMs, at 64
+// registers and 256 threads: they have to be looked at again when those change.  Requests of
+// 152064 ids: 76 x 6 13.7 us, x 8, of which 74 run at once, 17.5; 100 x 4 15.0, x 6 17.8;
+// 154 x 2 28.6, x 4 33.6; 512 x 1 69, x 2 74.  24 of 200064 x 8 9.2, x 6 10.3; CTAs of 512
+// threads x 8 9.4.)
 int pick_ctas(int num_reqs, int64_t vocab, int num_sms) {
   constexpr int kWidths[3] = {8, 6, 4};
   constexpr int kClusters[3] = {74, 97, 148};  // at once, of 608 CTAs (GPCs hold whole clusters)

@@ -635,7 +635,8 @@ int sga_token_logprobs_grad(const void *logits, int dtype, int64_t rows, int64_t
 /*
  * sga_probs -- the probabilities of logits rows at a temperature, over a whole
  * vocabulary: what sga_sampled_verify reads, of the target's rows and of the
- * draft model's.  (The pages verify greedily; this is the library's extension.)
+ * draft model's.  Here and in the calls below vocab shards are gathered first.
+ * (The pages verify greedily; this is the library's extension.)
  *   p_j = e^((x_j - max) / T) / sum_i e^((x_i - max) / T)
  *
  *   logits, dtype, rows, ld, vocab, org_vocab   as sga_token_logprobs.
@@ -660,8 +661,13 @@ int sga_probs(const void *logits, int dtype, int64_t rows, int64_t ld, int64_t v
  * sga_sampled_verify -- verification of drafted tokens by rejection sampling:
  * sga_greedy_verify for requests that are sampled, from the target's and the
  * draft model's probabilities and given uniform random numbers.  The emitted
- * tokens are distributed as the target's.  (The pages verify greedily; this is
- * the library's extension, on the same request layout and outputs.)
+ * tokens are distributed as the target's, as finely as the uniforms are: fp32
+ * numbers of 24 bits step by 6e-8 of a row's sum, and ids of about that probability
+ * and less are drawn too often or never (of the 152064 ids of a softmax row with
+ * N(0, 2.5^2) logits 17 % never, which have 0.04 % of the probability; the total
+ * variation is 0.15 %).
+ * (The pages verify greedily; this is the library's extension, on the same
+ * request layout and outputs.)
  *
  * Draft t of a row with target probabilities p, draft probabilities q and
  * uniform u is accepted when fl(u q_t) < p_t (fp32), up to the first one that
