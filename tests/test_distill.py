@@ -717,6 +717,63 @@ def test_lost_sums_in_the_logits_place(sga_lib, rows, vocab, dtype):
     assert torch.equal(x, back)
 
 
+@pytest.mark.gpu
+def test_lost_sums_of_the_largest_vocabulary(sga_lib):
+    vocab, temp, g = sga_lib.SGA_MAX_VOCAB, 1.5, gen(29)
+    x = torch.full((2, vocab), -1e9, device="cuda")
+    x[1].normal_(-4000.0, 3.0, generator=g)
+    ids = torch.randint(0, vocab, (2, 100), generator=g, device="cuda")
+    ids[:, 0], ids[:, 1] = vocab - 1, 0
+    z = torch.randn((2, 100), generator=g, device="cuda")
+    x.scatter_(1, ids, z)
+    lists = (ids.to(torch.int32), z, torch.logsumexp(z / temp, 1) + 0.2)
+    up = torch.randn(2, generator=g, device="cuda")
+    grad, back, _ = both_gradients(sga_lib, x, vocab, lists, temp, up, 0, 0)
+    exp, tol = formula(x, vocab, *lists, temp, up)
+    near(grad, exp, tol, "grad")
+    near(back, exp, tol, "back")
+
+
+@pytest.mark.gpu
+def test_a_graph_of_rows_with_and_without_lost_sums(sga_lib):
+    """Which rows are summed anew is found at each replay."""
+    rows, vocab, k, temp, g = 600, 9001, 10, 1.5, gen(37)
+    x = torch.zeros((rows, vocab), dtype=torch.bfloat16, device="cuda")
+    ids = torch.zeros((rows, k), dtype=torch.int32, device="cuda")
+    z, up = torch.zeros((rows, k), device="cuda"), torch.zeros(rows, device="cuda")
+    tlse = torch.zeros(rows, device="cuda")
+    loss, lse, rest = (torch.zeros(rows, device="cuda") for _ in range(3))
+    back = torch.empty_like(x)
+
+    def step():
+        sga_lib.sga_distill(x, vocab, ids, z, loss, teacher_lse=tlse, temperature=temp,
+                            out_lse=lse, out_lse_rest=rest)
+        sga_lib.sga_distill_grad(x, vocab, ids, z, lse, rest, back, teacher_lse=tlse,
+                                 temperature=temp, grad_loss=up)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step()
+    for share in (0.0, 0.5, 1.0, 0.1):
+        x.normal_(0.0, 3.0, generator=g)
+        at = torch.randint(0, vocab, (rows, k), generator=g, device="cuda")
+        own = torch.gather(x, 1, at)
+        x[torch.rand(rows, generator=g, device="cuda") < share] = -1e9
+        x.scatter_(1, at, own)
+        ids.copy_(at)
+        z.normal_(generator=g)
+        tlse.copy_(torch.logsumexp(z / temp, 1) + 0.2)
+        up.normal_(generator=g)
+        graph.replay()
+        exp, tol = formula(x, vocab, ids, z, tlse, temp, up)
+        near(back, exp, tol, share)
+
+
 # ------------------------------------------------------------------ refusals
 
 
