@@ -216,10 +216,13 @@ enum Mode { kLoss, kBoth, kBackward };
 // Long rows (kT 256) and short ones (64): CTAs per SM, stages of the ring (16 or
 // 4 KB; the most that fits), and list warps.  The loss alone keeps nothing, so more
 // CTAs serve it better than longer rings (3 CTAs, 3 stages, 3 lists: 4096 x 152064 bf16
-// 175 us, 4096 x 32000 45; 2, 5, 4: 183 and 50), and the gradient alone is like it
-// (700 x 50257 fp32 51 us, 53).  Short rows, loss and gradient: 5, 7, 2 4096 x 8000 bf16
-// with 64 entries 55 us, 4, 9, 2 72; 6, 6, 1 71.  Between them (128, of 8 KB): 4096 x 32000
-// 3, 7, 3 92 us (256: 100), 2, 12, 3 92, 2, 11, 4 95; 4096 x 24000 73 (64: 79).
+// 173 us, 4096 x 32000 45; 2, 5, 4: 182 and 48), and the gradient alone is like it
+// (700 x 50257 fp32 47.1 us, 47.8).  Short rows, loss and gradient: 5, 7, 2 4096 x 8000 bf16
+// with 64 entries 55 us, 4, 9, 2 72; 6, 6, 1 71.  The loss and the gradient alone, six CTAs and
+// five: 4096 x 1000 / 8000 / 16000 18.9 / 21.7 / 29.7 us and 18.6 / 21.5 / 30.4 (at six the loss
+// spills 92 bytes of registers), 19.4 / 27.4 / 46.8 and 19.8 / 28.8 / 47.4.  Between them (128,
+// of 8 KB): 4096 x 32000 3, 7, 3 92 us (256: 100), 2, 12, 3 92, 2, 11, 4 95; 4096 x 24000 73.5
+// (64: 79).
 template <int kT, Mode kMode>
 struct Form {
   static constexpr bool kSum = kMode != kBackward, kGrad = kMode != kLoss;
@@ -503,7 +506,8 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
         if (pc.c1 > 0) {
           int32_t id[kPerLane];
 #pragma unroll
-          for (int s = 0; s < kPerLane; ++s) id[s] = s * 32 + lane < in.k ? l.id[s * 32 + lane] : -1;
+          for (int s = 0; s < kPerLane; ++s)
+            id[s] = s * 32 + lane < in.k ? l.id[s * 32 + lane] : -1;
           up = coef;
           Sum rest = piece_sum(pc, id, at, gtid, warp);
           if (lane == 0) sh.warp_sum[sums & 1][warp] = rest;
@@ -511,7 +515,8 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
           if (lane == 0) mbar_arrive(smem_u32(&sh.joined));
           ok = ok && warp_wait(smem_u32(&sh.joined), sums & 1, abort_flag);
           if (!ok) break;
-          rest = sum_warp(lane < kWarps ? sh.warp_sum[sums & 1][lane] : Sum{neg_inf(), 0.0f}, scale);
+          rest = lane < kWarps ? sh.warp_sum[sums & 1][lane] : Sum{neg_inf(), 0.0f};
+          rest = sum_warp(rest, scale);
           ++sums;
           by_sums(rest);
           if (gtid == 0) {  // (all warps have read what was there)
@@ -717,8 +722,11 @@ __global__ void __launch_bounds__(Form<kT, kMode>::kThreads, Form<kT, kMode>::kP
 }
 
 // Pieces of a row in the gradient from saved sums: few rows are split over all CTAs, in
-// pieces of 8 KB or more; many into pieces of at most 128 KB (333 rows of 50257 fp32 ids: 100 KB
-// 37 us, 50 KB 43; 2048 of 200064 bf16 ids: 50 to 200 KB 260, 400 KB 264).
+// pieces of 8 KB or more; many into pieces of at most 128 KB (2048 of 200064 bf16 ids: 50
+// KB 257 us, 100 to 400 KB 255-256; 700 of 50257 fp32 ids: 200 KB 47.2 us, 100 KB 47.1, 50
+// KB 46.3).  From more than half as many rows as CTAs (456 of 256 threads) up to as many, rows
+// stay whole: 333 of 50257 fp32 ids 26.2 us, in two pieces 24.0, in four 23.8; 240 19.7, 19.5,
+// 18.5; 450 31.2, 30.7, 31.0.
 int backward_pieces(int64_t rows, int64_t bytes, int64_t ctas) {
   int64_t n = rows < ctas ? ctas / rows : (bytes + 131071) / 131072;
   if (n > bytes / 8192) n = bytes / 8192;

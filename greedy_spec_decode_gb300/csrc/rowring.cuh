@@ -8,7 +8,7 @@
 // from HBM once.  Summing and writing are done by warps of their own, so that one
 // row is summed while another is written and a third is loaded (in turns by the
 // same warps, two CTAs per SM: probabilities of 2048 x 202048 bf16 460 us instead of
-// 382, loss and gradient of 4096 x 152064 bf16 651 instead of 396).  A piece with more
+// 382, loss and gradient of 4096 x 152064 bf16 651 instead of 391).  A piece with more
 // stages than the ring keeps its last ones; the others are loaded a second time (in
 // which order, and who frees a slot: ringorder.h).
 #pragma once
@@ -153,8 +153,9 @@ __device__ __forceinline__ void sum_frees(Ring &ring, const Place &at, int load,
 }
 
 // bulk_load of what is read once: first to leave L2.  (Rows that are not kept: loss of
-// 4096 x 152064 bf16 ids 176 -> 171 us, the gradient alone of 4096 x 32000 88 -> 84; of
-// rows that are, it makes loss and gradient of 4096 x 152064 395 -> 408.)
+// 4096 x 152064 bf16 ids 174.7 -> 173.1 us, the gradient alone of 4096 x 32000 88.5 -> 84, of
+// 2048 x 200064 263 -> 255; of rows that are, it makes loss and gradient of 4096 x 152064
+// 13 us slower.)
 __device__ __forceinline__ void bulk_load_once(uint32_t dst, const void *src, uint32_t bytes,
                                                uint32_t bar, uint64_t policy) {
   asm volatile(
@@ -452,9 +453,12 @@ inline void row_launch(const RowKernel &k, int64_t rows, int chunks, const int64
   cfg.numAttrs = 2;
 }
 
-// Many rows of up to 48 KB: small CTAs, several per SM, a row each (bf16, small / wide:
-// probabilities of 4096 rows of 1000 ids 16 / 49 us, of 8000 37 / 57, of 16000 72 / 72; loss
-// and gradient of 4096 of 16000 64 / 90).
+// Many rows of up to 48 KB: small CTAs, several per SM, a row each.  4096 rows of 1000 /
+// 8000 / 16000 / 24000 bf16 ids, small and wide, graphs of 20 calls: probabilities 13.5 / 34 /
+// 69 / 105 us and 44 / 51 / 66 / 99; loss and gradient 23 / 37 / 57 / 79 and 69 / 67 / 83 / 93;
+// loss 18.9 / 21.7 / 29.7 / 38.7 and 23.3 / 24.4 / 31.2 / 37.7; gradient alone 19.4 / 27.4 / 46.8 /
+// 67 and 21.9 / 28.6 / 45.7 / 65.  (One border for all four: between 32 and 48 KB the wide CTAs
+// are up to 6 % faster but for loss and gradient together.)
 inline bool small_rows(int64_t rows, int64_t bytes, int num_sms) {
   return bytes <= (48 << 10) && rows > 2 * num_sms;
 }
@@ -463,10 +467,11 @@ inline bool small_rows(int64_t rows, int64_t bytes, int num_sms) {
 // bytes, 16 KB standing for what a row costs besides (pieces of 4 KB or more).  With
 // rows kept in a ring of `ring` bytes per CTA a piece leaves some of it for the next
 // row's loads, unless there is one round, and clusters of 4 or 8 cost more than their
-// share of the SMs says (probabilities of 2048 rows of 202048 bf16 ids: 3 CTAs 382 us,
-// 4 399, 2 403; 96 of 200064 4 29, 3 33-35; 333 of 50257 fp32 ids 2 33, 1 39, 4 35).
-// Without (0) a row is split only if all run at once (loss of 333 rows of 50257 fp32
-// ids: 1 CTA 30 us, 4 39).
+// share of the SMs says.  Graphs of 20 calls, 1 / 2 / 3 / 4 CTAs: probabilities of 2048 rows of
+// 202048 bf16 ids 452 / 393 / 382 / 390 us, of 96 of 200064 28.7 / 29.9 / 28.3 / 22.4, of 333 of
+// 50257 fp32 ids 32.3 / 26.0 / 27.4 / 28.5; loss and gradient of 4096 of 152064 bf16 ids 415 / 391 /
+// - / 420, of 333 of 50257 fp32 33.7 / 29.3 / - / 33.8.  Without a ring (0) a row is split only
+// if all run at once (loss of 333 rows of 50257 fp32 ids 14.0 / 14.9 / - / 15.9).
 inline int pick_chunks(int64_t rows, int64_t bytes, int64_t ring, const int64_t (&resident)[6]) {
   int best = kMaxCluster;
   int64_t least = INT64_MAX;
